@@ -305,6 +305,193 @@ mha_status_t mha_ffn_forward(mha_dtype_t dt, const void* x,
                              void* out, void* workspace, size_t workspace_bytes,
                              void* stream);
 
+/*
+ * ======================================================================================
+ * Serving operators: rotary positions, a paged key/value cache, attention over it, attention
+ * with capped and biased scores under span masks, RMS norm with 8-bit output.
+ *
+ * Tensors here need not be contiguous: a [B, L, heads, d_k] tensor is a pointer and the three
+ * strides below, in elements; the d_k elements of one head are adjacent. So the same call takes
+ * [B, L, h, d_k], the workspace's [B, h, L, d_k], and slices of one packed projection. Strides
+ * may be 0 in an input (a broadcast); outputs must not overlap themselves. Offsets are 64-bit.
+ * Pointers are aligned to their element type; where a call needs more it says so.
+ * ======================================================================================
+ */
+typedef struct {
+    int64_t b, l, h;
+} mha_strides_t;
+
+/*
+ * Rotary positions. The first rot_dim features of a head form rot_dim / 2 pairs (x_0, x_1):
+ * features (i, i + rot_dim / 2) in the half layout, (2 i, 2 i + 1) interleaved. A token at
+ * position t turns pair i by the angle t * inv_freq[i]:
+ *   (x_0, x_1) -> scale * (x_0 cos - x_1 sin, x_1 cos + x_0 sin)
+ * Features rot_dim .. d_k - 1 pass unchanged. The angle is formed to about 2^-45 of its size and
+ * reduced before it is rounded, so far positions keep fp32 accuracy; products are in fp32,
+ * rounded once to the type of the tensor.
+ */
+typedef struct {
+    const float* inv_freq;   /* device fp32 [rot_dim / 2] */
+    int rot_dim;             /* even, 2 <= rot_dim <= d_k */
+    int interleaved;         /* 0: half layout, 1: interleaved pairs */
+    float scale;             /* multiplies cos and sin (1: none) */
+} mha_rotary_t;
+
+/*
+ * Host helper: fills inv_freq (HOST memory, rot_dim / 2 floats) and *scale for a context scaled by
+ * `factor` against the `original_length` that the model was trained with.
+ *   MHA_ROPE_PLAIN   base^(-2 i / rot_dim)
+ *   MHA_ROPE_LINEAR  plain / factor (positions interpolated)
+ *   MHA_ROPE_BASE    plain with base * factor^(rot_dim / (rot_dim - 2)) (the base stretched)
+ *   MHA_ROPE_BANDED  by wavelength w = 2 pi / f: kept below original_length / high, divided by
+ *                    factor above original_length / low, a blend linear in original_length / w between
+ *   MHA_ROPE_RAMP    by index: kept up to the pair that turns `high` times over original_length,
+ *                    divided by factor from the one that turns `low` times, linear in the index
+ *                    between; *scale = 0.1 ln(factor) + 1
+ * *scale is 1 for the others. low < high; both ignored by the first three.
+ */
+typedef enum {
+    MHA_ROPE_PLAIN = 0, MHA_ROPE_LINEAR = 1, MHA_ROPE_BASE = 2, MHA_ROPE_BANDED = 3, MHA_ROPE_RAMP = 4
+} mha_rope_scaling_t;
+mha_status_t mha_rotary_frequencies(float* inv_freq, float* scale, int rot_dim, double base,
+                                    mha_rope_scaling_t scaling, double factor, double original_length,
+                                    double low, double high);
+
+/*
+ * Turns queries and keys: q [B, T, h, d_k] -> q_out, and, unless k is NULL, k [B, T, h_kv, d_k] ->
+ * k_out. positions: device int32 [B, T] (any value, contiguous) or NULL for 0 .. T-1. An output may
+ * be its input with the same strides (in place); otherwise they must not overlap. MHA_F32 or MHA_BF16,
+ * any d_k <= 1024. h_kv, the k strides and k_out are ignored if k is NULL. One launch.
+ */
+mha_status_t mha_rotary(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                        void* q_out, const mha_strides_t* q_out_strides,
+                        const void* k, const mha_strides_t* k_strides,
+                        void* k_out, const mha_strides_t* k_out_strides,
+                        int B, int T, int h, int h_kv, int d_k, const int32_t* positions,
+                        const mha_rotary_t* rotary, void* stream);
+
+/*
+ * A paged key/value cache: n_pages pages of page_size slots, each slot h_kv heads of d_k, in two
+ * arrays with the same strides (in elements; d_k adjacent). Position t of sequence b lives in slot
+ * t % page_size of page block_table[b * table_stride + t / page_size]; max_pages entries of a row
+ * are read at most, so a sequence holds up to max_pages * page_size positions. Any page_size >= 1.
+ * Pages that a call writes must be distinct between (and within) sequences; pages only read may be
+ * shared. A page number outside [0, n_pages), or a position beyond the table, is never followed:
+ * the append skips the token, the attention leaves the position out (a length beyond the table is
+ * cut to it), and both record MHA_PAGED_BAD_PAGE in the device status word.
+ */
+typedef struct {
+    void* k_pages;
+    void* v_pages;
+    int64_t page_stride, slot_stride, head_stride;
+    int n_pages, page_size;
+    const int32_t* block_table;
+    int64_t table_stride;
+    int max_pages;
+} mha_paged_cache_t;
+#define MHA_PAGED_BAD_PAGE 0x501
+
+/*
+ * Appends T new tokens a sequence to the cache and turns queries and keys on the way, in one launch.
+ *   k, v [B, T, h_kv, d_k]; start: device int32 [B], the positions already held (token t of
+ *   sequence b goes to position start[b] + t, which is also its rotary position);
+ *   new_lens: device int32 [B] or NULL: only tokens t < new_lens[b] exist; the rest is not read and
+ *   their outputs are left as they were; rotary NULL: keys enter as they are.
+ *   k_out NULL, or [B, T, h_kv, d_k]: the turned keys, for an attention over the prompt itself.
+ *   q NULL, or [B, T, h, d_k] -> q_out turned the same way.
+ * In-place rules as for mha_rotary. start is not changed: the caller adds the counts.
+ */
+mha_status_t mha_paged_append(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                              void* q_out, const mha_strides_t* q_out_strides,
+                              const void* k, const mha_strides_t* k_strides,
+                              void* k_out, const mha_strides_t* k_out_strides,
+                              const void* v, const mha_strides_t* v_strides,
+                              int B, int T, int h, int h_kv, int d_k, const int32_t* start,
+                              const int32_t* new_lens, const mha_rotary_t* rotary,
+                              const mha_paged_cache_t* cache, void* stream);
+
+/*
+ * How a score is formed from q . k:
+ *   s = scale * q.k;  cap > 0: s = cap * tanh(s / cap);  slopes: s -= slopes[head] * |i - j|
+ * with i, j the positions of the query and the key.
+ */
+typedef struct {
+    float scale;             /* 0: 1 / sqrt(d_k) */
+    float cap;               /* 0: no cap */
+    const float* slopes;     /* device fp32 [h] or NULL */
+} mha_scores_t;
+
+/*
+ * Attention of one new token a sequence over the paged cache:
+ *   out[b, i] = sum_j softmax_j(s)[j] v[j, i / (h / h_kv)],  j = 0 .. kv_lens[b] - 1
+ * for the query q [B, h, d_k] at position kv_lens[b] - 1 (append its key and value first). q and out
+ * have strides (b, h; l is ignored). kv_lens: device int32 [B]; a length <= 0 gives zeros. scores NULL:
+ * the plain scaled scores. MHA_BF16 or MHA_F32, d_k = 64 or 128, h a multiple of h_kv. What lies in a
+ * page behind a sequence's end is not used, whatever it holds. MHA_BF16: pages and their strides
+ * aligned to 16 bytes. Weights are rounded to bf16 for the product with bf16 values.
+ * workspace >= mha_paged_attention_workspace_size(...), 256-byte aligned, contents of no matter;
+ * calls that overlap on the GPU need one each. The result does not depend on timing.
+ */
+size_t mha_paged_attention_workspace_size(mha_dtype_t dt, int B, int h, int h_kv, int d_k);
+mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                                 void* out, const mha_strides_t* out_strides,
+                                 int B, int h, int h_kv, int d_k, const int32_t* kv_lens,
+                                 const mha_scores_t* scores, const mha_paged_cache_t* cache,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The keys that a query may attend to, as the intersection of (all optional):
+ *   causal          key j <= q_offset + i, or j < prefix_lens[b] (a prefix that all may see)
+ *   key_valid_lens  key j < key_valid_lens[b]
+ *   doc_spans       doc_spans[b, i, 0] <= key j < doc_spans[b, i, 1] (mha_document_spans)
+ * Query i has position q_offset + i. A query without any key gives a row of zeros (not the uniform
+ * row of mha_forward's -1e9 fill).
+ */
+typedef struct {
+    int causal;
+    int q_offset;                   /* >= 0: keys before the first query, L_k - L_q where both end together */
+    const int32_t* key_valid_lens;  /* device [B] or NULL */
+    const int32_t* prefix_lens;     /* device [B] or NULL; read only if causal */
+    const int32_t* doc_spans;       /* device [B, L_q, 2] or NULL */
+} mha_span_mask_t;
+
+/*
+ * spans[b, i] = [first, last + 1) of the run of equal doc_ids around position i; (0, 0) where
+ * doc_ids < 0 (padding). doc_ids, device int32 [B, L]: each document is one run. spans: device
+ * int32 [B, L, 2]. Serves every layer of a batch.
+ */
+mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* spans, void* stream);
+
+/*
+ * Attention with grouped heads over strided tensors, scores and mask as above:
+ *   q [B, L_q, h, d_k], k and v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]
+ * h a multiple of h_kv (head n reads key head n / (h / h_kv)); scores, mask NULL: plain, all keys.
+ * MHA_BF16 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
+ * behind key_valid_lens[b] are not used, whatever they hold. No workspace.
+ */
+mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                           const void* k, const mha_strides_t* k_strides,
+                           const void* v, const mha_strides_t* v_strides,
+                           void* out, const mha_strides_t* out_strides,
+                           int B, int L_q, int L_k, int h, int h_kv, int d_k,
+                           const mha_scores_t* scores, const mha_span_mask_t* mask, void* stream);
+
+/*
+ * RMS norm of rows, with the residual's addition before it and, on request, 8-bit output:
+ *   z = x + residual;  y = gain * z / sqrt(mean(z^2) + eps)
+ *   x, residual, sum [rows, d] with row strides (elements), type dt; residual NULL: z = x, and sum is
+ *   ignored; sum NULL: z is not written. sum may be x or residual (same stride). The norm is of the
+ *   fp32 sum, not of its rounding. gain [d] type dt, or NULL (ones).
+ *   scales NULL: y has type dt. Otherwise y is e4m3 (1 byte an element, finite form): each group of
+ *   `group` elements of a row (0: the whole row; else 32, 64 or 128, dividing d) has
+ *   scale = max |y| / 448 (1 where that is 0), y8 = y / scale rounded to nearest even, and scales
+ *   [rows, groups], fp32, contiguous, receives it. NaN stays NaN.
+ *   d >= 1, any; rows >= 0.
+ */
+mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const void* residual,
+                         int64_t residual_stride, void* sum, int64_t sum_stride, const void* gain, float eps,
+                         int64_t rows, int d, void* y, int64_t y_stride, float* scales, int group, void* stream);
+
 /* Message for the last non-OK status returned on this thread ("" if none). */
 const char* mha_last_error(void);
 

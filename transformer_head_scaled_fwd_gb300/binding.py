@@ -7,7 +7,9 @@ if the library is missing or a call fails, an exception is raised.
 Function names match the C entry points: ``mha_forward``,
 ``mha_qkv_projection``, ``mha_attention_core``, ``mha_output_projection``,
 ``mha_forward_host``, ``mha_workspace_size``, ``mha_host_staging_size``,
-``mha_check_device_status``.
+``mha_check_device_status``; the serving operators ``mha_rotary``,
+``mha_paged_append``, ``mha_paged_attention``, ``mha_attention``,
+``mha_document_spans``, ``mha_rmsnorm`` and the ``make_*`` descriptions they take.
 """
 from __future__ import annotations
 
@@ -27,7 +29,9 @@ EXPORTS = ("mha_workspace_size", "mha_forward", "mha_qkv_projection", "mha_atten
            "mha_check_device_status", "mha_version", "mha_forward_noalloc", "mha_ffn_workspace_size",
            "mha_ffn_forward", "mha_sublayer_workspace_size", "mha_sublayer_forward",
            "mha_decode_workspace_size", "mha_kv_cache_prefill", "mha_decode_step",
-           "mha_selftest_wait_timeout")
+           "mha_selftest_wait_timeout", "mha_rotary_frequencies", "mha_rotary", "mha_paged_append",
+           "mha_paged_attention_workspace_size", "mha_paged_attention", "mha_document_spans",
+           "mha_attention", "mha_rmsnorm")
 MHA_SELFTEST_WAIT_CODE = 0x7f1
 
 
@@ -40,6 +44,31 @@ class MHAError(RuntimeError):
 class MaskT(ctypes.Structure):
     _fields_ = [("causal", ctypes.c_int), ("key_valid_lens", ctypes.c_void_p),
                 ("dense", ctypes.c_void_p), ("dense_mq", ctypes.c_int)]
+
+
+class StridesT(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("l", ctypes.c_int64), ("h", ctypes.c_int64)]
+
+
+class RotaryT(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("scale", ctypes.c_float)]
+
+
+class PagedCacheT(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("max_pages", ctypes.c_int)]
+
+
+class ScoresT(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("cap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
+
+
+class SpanMaskT(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int), ("q_offset", ctypes.c_int), ("key_valid_lens", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("doc_spans", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -97,6 +126,23 @@ def load(path: str | None = None):
         lib.mha_selftest_wait_timeout.argtypes = [vp]
         lib.mha_forward_noalloc.restype = i
         lib.mha_forward_noalloc.argtypes = [i] + [vp] * 11 + [i] * 5 + [ctypes.POINTER(MaskT), vp, vp, vp]
+        i64, f = ctypes.c_int64, ctypes.c_float
+        lib.mha_rotary_frequencies.restype = i
+        lib.mha_rotary_frequencies.argtypes = [vp, vp, i, ctypes.c_double, i] + [ctypes.c_double] * 4
+        lib.mha_rotary.restype = i
+        lib.mha_rotary.argtypes = [i] + [vp] * 8 + [i] * 5 + [vp] * 3
+        lib.mha_paged_append.restype = i
+        lib.mha_paged_append.argtypes = [i] + [vp] * 10 + [i] * 5 + [vp] * 5
+        lib.mha_paged_attention_workspace_size.restype = sz
+        lib.mha_paged_attention_workspace_size.argtypes = [i] * 5
+        lib.mha_paged_attention.restype = i
+        lib.mha_paged_attention.argtypes = [i] + [vp] * 4 + [i] * 4 + [vp] * 4 + [sz, vp]
+        lib.mha_document_spans.restype = i
+        lib.mha_document_spans.argtypes = [vp, i, i, vp, vp]
+        lib.mha_attention.restype = i
+        lib.mha_attention.argtypes = [i] + [vp] * 8 + [i] * 6 + [vp] * 3
+        lib.mha_rmsnorm.restype = i
+        lib.mha_rmsnorm.argtypes = [i, vp, i64, vp, i64, vp, i64, vp, f, i64, i, vp, i64, vp, i, vp]
         _lib = lib
         return lib
 
@@ -262,6 +308,253 @@ def mha_ffn_forward(x, w_1, b_1, w_2, b_2, *, out, workspace, stream=None):
     _check(load().mha_ffn_forward(
         _dtype_code(x), _ptr(x), _ptr(w_1), _ptr(b_1), _ptr(w_2), _ptr(b_2), B, L, d, d_ff, _ptr(out),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ------------------------------------------------------------------ serving operators
+MHA_PAGED_BAD_PAGE = 0x501
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDED, ROPE_RAMP = range(5)
+
+
+def _want(t, name, dtype, shape, device):
+    """t is a CUDA tensor of this dtype, shape and device (the current one, where the call is enqueued)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+
+
+def _here(t):
+    """t's device, which has to be the current CUDA device: work is enqueued there."""
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, not on {t.device}")
+    return t.device
+
+
+def _strided(t, name):
+    """Pointer and strides of a [B, L, H, d] tensor whose last dimension is adjacent."""
+    b, l, h, d = t.stride()
+    if d != 1 and t.shape[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be adjacent (stride {d})")
+    return t.data_ptr(), ctypes.byref(StridesT(b, l, h))
+
+
+def _ints(t, name, shape, device):
+    """Pointer of a contiguous int32 tensor, or None."""
+    import torch
+    if t is None:
+        return None
+    _want(t, name, torch.int32, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _floats(t, name, n, device):
+    import torch
+    _want(t, name, torch.float32, (n,), device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+                       original_length: float = 0.0, low: float = 1.0, high: float = 4.0):
+    """(inv_freq, scale): the rot_dim / 2 frequencies (a CPU fp32 tensor) and the factor of cos and sin
+    for a scaled context."""
+    import torch
+    table = torch.empty(max(rot_dim // 2, 1), dtype=torch.float32)
+    scale = ctypes.c_float(1.0)
+    _check(load().mha_rotary_frequencies(table.data_ptr(), ctypes.addressof(scale), rot_dim, base, scaling, factor,
+                                         original_length, low, high))
+    return table, scale.value
+
+
+def make_rotary(inv_freq, interleaved: bool = False, scale: float = 1.0):
+    """Rotary description: inv_freq is a CUDA fp32 tensor of rot_dim / 2 frequencies. Holds a reference to it."""
+    r = RotaryT(_floats(inv_freq, "inv_freq", inv_freq.numel(), _here(inv_freq)), 2 * inv_freq.numel(), int(interleaved),
+                scale)
+    r._tensors = inv_freq
+    r._ref = ctypes.byref(r)
+    return r
+
+
+def make_paged_cache(k_pages, v_pages, block_table):
+    """Cache description: k_pages and v_pages [n_pages, page_size, h_kv, d_k] with the same strides (any order of
+    the dimensions in memory but the last), block_table int32 [B, max_pages]. Holds references to the three."""
+    import torch
+    device = _here(k_pages)
+    n, size, h_kv, d = k_pages.shape
+    _dtype_code(k_pages)
+    _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape, device)
+    if k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same strides")
+    if k_pages.stride(3) != 1:
+        raise ValueError("the last dimension of the pages must be adjacent")
+    _want(block_table, "block_table", torch.int32, block_table.shape, device)
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, max_pages] with adjacent rows")
+    c = PagedCacheT(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], n, size, block_table.data_ptr(),
+                    block_table.stride(0), block_table.shape[1])
+    c._tensors = (k_pages, v_pages, block_table)
+    c._ref = ctypes.byref(c)
+    c._batch, c._heads, c._d, c._dtype, c._device = block_table.shape[0], h_kv, d, k_pages.dtype, device
+    return c
+
+
+def make_scores(scale: float = 0.0, cap: float = 0.0, slopes=None):
+    """Score description: scale (0: 1 / sqrt(d_k)), tanh cap (0: none), slopes a CUDA fp32 [h] or None."""
+    s = ScoresT(scale, cap, None if slopes is None else _floats(slopes, "slopes", slopes.numel(), _here(slopes)))
+    s._tensors = slopes
+    s._ref = ctypes.byref(s)
+    return s
+
+
+def make_span_mask(causal=False, q_offset=0, key_valid_lens=None, prefix_lens=None, doc_spans=None):
+    """Mask description for mha_attention. Holds references to the tensors."""
+    m = SpanMaskT(int(bool(causal)), q_offset, _ptr(key_valid_lens), _ptr(prefix_lens), _ptr(doc_spans))
+    m._tensors = (key_valid_lens, prefix_lens, doc_spans)
+    return m
+
+
+def _check_scores(scores, h):
+    if scores is None:
+        return None
+    if scores._tensors is not None and scores._tensors.numel() != h:
+        raise ValueError(f"slopes has {scores._tensors.numel()} entries for {h} heads")
+    return scores._ref
+
+
+def mha_rotary(q, *, rotary, q_out, k=None, k_out=None, positions=None, stream=None):
+    """Turn q [B, T, h, d_k] into q_out and k [B, T, h_kv, d_k] into k_out (an output may be its input)."""
+    device = _here(q)
+    B, T, h, d = q.shape
+    _want(q_out, "q_out", q.dtype, q.shape, device)
+    kp = ks = kop = kos = None
+    h_kv = 0
+    if k is not None:
+        h_kv = k.shape[2]
+        _want(k, "k", q.dtype, (B, T, h_kv, d), device)
+        _want(k_out, "k_out", q.dtype, k.shape, device)
+        kp, ks = _strided(k, "k")
+        kop, kos = _strided(k_out, "k_out")
+    _check(load().mha_rotary(_dtype_code(q), *_strided(q, "q"), *_strided(q_out, "q_out"), kp, ks, kop, kos, B, T, h,
+                             h_kv, d, _ints(positions, "positions", (B, T), device), rotary._ref, _stream(stream)))
+
+
+def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_lens=None, rotary=None, stream=None):
+    """Append k, v [B, T, h_kv, d_k] to the cache at positions start[b] + t, turning k (and q into q_out)."""
+    device = _here(k)
+    B, T, h_kv, d = k.shape
+    _want(v, "v", k.dtype, k.shape, device)
+    if (cache._batch, cache._heads, cache._d, cache._dtype, cache._device) != (B, h_kv, d, k.dtype, device):
+        raise ValueError("the cache's batch, heads, head width, dtype or device differ from k's")
+    qp = qs = qop = qos = kop = kos = None
+    h = 0
+    if q is not None:
+        h = q.shape[2]
+        _want(q, "q", k.dtype, (B, T, h, d), device)
+        _want(q_out, "q_out", k.dtype, q.shape, device)
+        qp, qs = _strided(q, "q")
+        qop, qos = _strided(q_out, "q_out")
+    if k_out is not None:
+        _want(k_out, "k_out", k.dtype, k.shape, device)
+        kop, kos = _strided(k_out, "k_out")
+    if start is None:
+        raise ValueError("start must be an int32 tensor [B]")
+    _check(load().mha_paged_append(_dtype_code(k), qp, qs, qop, qos, *_strided(k, "k"), kop, kos, *_strided(v, "v"), B, T,
+                                   h, h_kv, d, _ints(start, "start", (B,), device),
+                                   _ints(new_lens, "new_lens", (B,), device), rotary._ref if rotary is not None else None,
+                                   cache._ref, _stream(stream)))
+
+
+def paged_attention_workspace_size(dt: int, B: int, h: int, h_kv: int, d_k: int) -> int:
+    return int(load().mha_paged_attention_workspace_size(dt, B, h, h_kv, d_k))
+
+
+def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, stream=None):
+    """Attention of one new token a sequence, q [B, h, d_k], over the kv_lens[b] cached positions -> out."""
+    device = _here(q)
+    B, h, d = q.shape
+    _want(out, "out", q.dtype, q.shape, device)
+    if (cache._batch, cache._d, cache._dtype, cache._device) != (B, d, q.dtype, device):
+        raise ValueError("the cache's batch, head width, dtype or device differ from q's")
+    if workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not {device}")
+    if kv_lens is None:
+        raise ValueError("kv_lens must be an int32 tensor [B]")
+    qb, qh, qd = q.stride()
+    ob, oh, od = out.stride()
+    if qd != 1 or od != 1:
+        raise ValueError("the last dimension of q and out must be adjacent")
+    _check(load().mha_paged_attention(
+        _dtype_code(q), q.data_ptr(), ctypes.byref(StridesT(qb, 0, qh)), out.data_ptr(), ctypes.byref(StridesT(ob, 0, oh)),
+        B, h, cache._heads, d, _ints(kv_lens, "kv_lens", (B,), device), _check_scores(scores, h), cache._ref,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def mha_document_spans(doc_ids, *, spans, stream=None):
+    """spans int32 [B, L, 2] of the documents in doc_ids int32 [B, L] (one run each; < 0 is padding)."""
+    device = _here(doc_ids)
+    B, L = doc_ids.shape
+    _check(load().mha_document_spans(_ints(doc_ids, "doc_ids", (B, L), device), B, L,
+                                     _ints(spans, "spans", (B, L, 2), device), _stream(stream)))
+
+
+def mha_attention(q, k, v, *, out, scores=None, mask=None, stream=None):
+    """Attention of q [B, L_q, h, d_k] over k, v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]."""
+    device = _here(q)
+    B, Lq, h, d = q.shape
+    Lk, h_kv = k.shape[1], k.shape[2]
+    _want(k, "k", q.dtype, (B, Lk, h_kv, d), device)
+    _want(v, "v", q.dtype, k.shape, device)
+    _want(out, "out", q.dtype, q.shape, device)
+    ref = None
+    if mask is not None:
+        valid, prefix, spans = mask._tensors
+        _ints(valid, "key_valid_lens", (B,), device)
+        _ints(prefix, "prefix_lens", (B,), device)
+        _ints(spans, "doc_spans", (B, Lq, 2), device)
+        ref = ctypes.byref(mask)
+    _check(load().mha_attention(_dtype_code(q), *_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"),
+                                *_strided(out, "out"), B, Lq, Lk, h, h_kv, d, _check_scores(scores, h), ref,
+                                _stream(stream)))
+
+
+def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=None, stream=None):
+    """y = gain * z / rms(z), z = x + residual (written to sum_out), rows of length d = x.shape[-1], x [rows, d].
+    y has x's dtype, or torch.float8_e4m3fn with scales fp32 [rows, groups] (one group: the row)."""
+    import torch
+    device = _here(x)
+    rows, d = x.shape
+    group = 0
+    if scales is None:
+        _want(y, "y", x.dtype, x.shape, device)
+    else:
+        _want(y, "y", torch.float8_e4m3fn, x.shape, device)
+        groups = scales.shape[1]
+        _want(scales, "scales", torch.float32, (rows, groups), device)
+        if not scales.is_contiguous() or groups < 1 or d % groups != 0:
+            raise ValueError("scales must be contiguous [rows, groups] with groups dividing d")
+        group = 0 if groups == 1 else d // groups
+    for name, t in (("residual", residual), ("sum_out", sum_out)):
+        if t is not None:
+            _want(t, name, x.dtype, x.shape, device)
+    if sum_out is not None and residual is None:
+        raise ValueError("sum_out needs a residual")
+    if gain is not None:
+        _want(gain, "gain", x.dtype, (d,), device)
+    for name, t in (("x", x), ("y", y), ("residual", residual), ("sum_out", sum_out)):
+        if t is not None and d > 1 and t.stride(1) != 1:
+            raise ValueError(f"the rows of {name} must be adjacent")
+    if gain is not None and d > 1 and gain.stride(0) != 1:
+        raise ValueError("gain must be contiguous")
+    _check(load().mha_rmsnorm(
+        _dtype_code(x), x.data_ptr(), x.stride(0), _ptr(residual), residual.stride(0) if residual is not None else 0,
+        _ptr(sum_out), sum_out.stride(0) if sum_out is not None else 0, _ptr(gain), eps, rows, d, y.data_ptr(), y.stride(0),
+        _ptr(scales), group, _stream(stream)))
 
 
 def mha_selftest_wait_timeout(stream=None):

@@ -18,6 +18,7 @@
 #include "gemv.h"
 #include "convert.h"
 #include "mha_internal.h"
+#include "serve.h"
 
 namespace {
 
@@ -282,6 +283,14 @@ mha_status_t forward_bf16_on_f32(const void* query, const void* key, const void*
 }  // namespace
 
 void mha::set_last_error(const char* msg) { g_last_error = msg; }
+
+int* mha::device_status() { return device_status_ptr(); }
+
+bool mha::encode_bf16_tiled(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                            const uint64_t* strides_bytes, const uint32_t* box, bool swizzle) {
+    return get_encoder() == MHA_OK &&
+           encode_bf16(m, base, rank, dims, strides_bytes, box, "strided tensor", swizzle) == MHA_OK;
+}
 
 // ==================================================================== C ABI
 extern "C" {
