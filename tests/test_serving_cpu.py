@@ -100,7 +100,8 @@ def test_attention_refusals(lib):
     assert call(q=None) == INV and call(out=None) == INV
     assert call(qs=st(l=65)) == INV and call(q=ctypes.c_void_p(4104)) == INV
     assert call(sc=scores_t(cap=math.nan)) == INV
-    assert call(B_=4096, h=64) == UNS
+    assert call(B_=1 << 20, Lq=1 << 20) == UNS
+    assert call(qs=st(l=0)) == INV
     m = bnd.SpanMaskT(1, -1, None, None, None)
     assert call(mask=m) == INV
     m = bnd.SpanMaskT(1, 0, None, None, 4100)

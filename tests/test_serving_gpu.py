@@ -462,6 +462,16 @@ def test_attention_head_major_strides_and_spans(bnd, d):
     assert empty.any() and (got[empty] == 0).all()
 
 
+def test_attention_broadcast_inputs(bnd):
+    """Keys and values shared by all sequences, a query shared by all heads (strides of 0)."""
+    B, L, h, hk, d = 3, 140, 4, 2, 64
+    k, v = (randn(75 + i, 1, L, hk, d, dtype=BF).expand(B, L, hk, d) for i in range(2))
+    q = randn(77, B, L, 1, d, dtype=BF).expand(B, L, h, d)
+    got = run_attention(bnd, q, k, v, out=torch.empty(B, L, h, d, dtype=BF, device="cuda"), causal=True)
+    ref, tol = attention_ref(q, k, v, causal=True)
+    R.check(got, ref, tol, "broadcast")
+
+
 def test_attention_long_causal(bnd):
     """Rows sampled from a long sequence, grouped heads, cap and bias."""
     for d, sc in ((64, dict(slopes=True)), (128, dict(cap=50.0))):

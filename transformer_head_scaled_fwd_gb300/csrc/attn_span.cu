@@ -5,7 +5,6 @@
 
 #include <math_constants.h>
 
-#include "elem.cuh"
 #include "launch.h"
 #include "mha_internal.h"
 #include "ptx.cuh"
@@ -14,66 +13,620 @@
 namespace mha {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int BM = 128;          // queries of a unit
+constexpr int BN = 128;          // keys of a tile
+constexpr int kThreads = 384;
+constexpr uint32_t kHalf = 128 * 128;        // one 128-row x 64-column bf16 half tile = 16 KB
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0;                // + 128 b: score buffers S_0, S_1
+constexpr uint32_t kColP = 256;              // + 64 b + 32 h: weight buffers P_0, P_1 (two halves each)
+constexpr uint32_t kColO = 384;              // output accumulator, d_k features
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr int kHeadGroup = 8;
 
-// Keys [x, y) of query i of sequence b.
-__device__ __forceinline__ int2 interval_of(const SpanAttnParams& p, int b, int i) {
-    int lo = 0, hi = p.Lk;
-    if (p.valid_lens != nullptr) hi = min(hi, p.valid_lens[b]);
-    if (p.causal) {
-        int seen = i + p.q_offset + 1;
-        if (p.prefix_lens != nullptr) seen = max(seen, p.prefix_lens[b]);
-        hi = min(hi, seen);
-    }
-    if (p.spans != nullptr) {
-        const int2 sp = reinterpret_cast<const int2*>(p.spans)[static_cast<int64_t>(b) * p.Lq + i];
-        lo = max(lo, sp.x);
-        hi = min(hi, sp.y);
-    }
-    return make_int2(lo, max(hi, lo));
+// How scores become weights:
+//   kPlain   scale > 0, no cap, no bias: running maximum of the raw scores, one multiply-add each
+//   kCapped  a cap of at most kFixedCap, no bias: every score lies in [-cap, cap], so the weights are
+//            exp(s) with no maximum at all (2^+-87 at most, far inside fp32 and bf16): no maximum,
+//            no rescaling, no exchange between the two halves of a row
+//   kGeneral anything else: scores formed first, then as kPlain
+enum Mode { kPlain, kCapped, kGeneral };
+constexpr float kFixedCap = 60.0f;
+
+// One unit as the scheduler publishes it; n == 0 means no more work.
+struct UnitInfo {
+    int b, head, q0;
+    int j0, n;             // key tiles j0 .. j0 + n - 1
+    int lo_max, hi_min;    // keys [lo_max, hi_min) are allowed to every row of the unit
+    int valid, seen;       // valid length; prefix that all rows see
+};
+
+template <int kD>
+struct Tiles {
+    static constexpr int kSlabs = kD / 64;
+    static constexpr uint32_t kTile = kSlabs * kHalf;       // 128 x d_k bf16
+    static constexpr int kStagesK = kD == 128 ? 3 : 4;
+    static constexpr int kStagesV = kD == 128 ? 2 : 4;
+    static constexpr uint32_t kOffK = 2 * kTile;            // two Q buffers first
+    static constexpr uint32_t kOffV = kOffK + kStagesK * kTile;
+    static constexpr uint32_t kOffBar = kOffV + kStagesV * kTile;
+};
+
+struct SmemSpan {
+    uint64_t q_full[2], q_empty[2];          // Q buffer loaded / output stored from it
+    uint64_t k_full[4], k_empty[4];
+    uint64_t v_full[4], v_empty[4];
+    uint64_t v_edge;                         // the tile that holds the valid length has arrived
+    uint64_t s_full[2];                      // score buffer b holds S(j) (commit)
+    uint64_t s_free[2];                      // S(j) of buffer b loaded by both halves (256 arrivals)
+    uint64_t p_full[2];                      // P(j) of weight buffer b written by both halves (256 arrivals)
+    uint64_t p_free[2];                      // P.V(j) of weight buffer b done (commit)
+    uint64_t unit_full[2];                   // unit slot published by the scheduler
+    uint64_t steal_full[2];                  // answer to a request for another unit
+    alignas(16) uint32_t steal[2][4];
+    UnitInfo unit[2];
+    uint32_t tmem_base;
+    int abort_flag;
+    float mx[2][2][BM];                      // [tile parity][half][row]: the halves' tile maxima, exchanged
+};
+template <int kD>
+constexpr size_t smem_bytes() { return Tiles<kD>::kOffBar + sizeof(SmemSpan); }
+
+struct SpanMaps {
+    CUtensorMap q, k, v, out;   // {64, L, d_k / 64, heads, B}, box {64, 128, d_k / 64, 1, 1}
+};
+// Coordinates of a (head, sequence) in a map: a broadcast dimension (stride 0) has one entry there.
+__device__ __forceinline__ int at_h(const Strided& t, int head) { return t.h != 0 ? head : 0; }
+__device__ __forceinline__ int at_b(const Strided& t, int b) { return t.b != 0 ? b : 0; }
+
+__device__ __forceinline__ void tma_load_5d(const CUtensorMap* m, uint64_t* bar, void* dst, int c1, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c3), "r"(c4)
+        : "memory");
 }
 
-// One warp per (query, head, sequence), d / 32 features a lane.
-template <int kD>
-__global__ void __launch_bounds__(32 * kWarps) span_attn_simple_kernel(const __grid_constant__ SpanAttnParams p) {
-    constexpr int kPer = kD / 32;
-    using T = __nv_bfloat16;
+// Work stealing: the grid has one CTA a unit; a running CTA asks the hardware to cancel the launch of
+// one that has not started and does its unit instead (its set-up is paid once, and no counter in
+// memory is needed). After a refusal no further request is made.
+__device__ __forceinline__ void steal_request(void* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// blockIdx.x of the cancelled CTA, or -1
+__device__ __forceinline__ int steal_answer(const void* answer) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 x, y, z, w;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "mov.b32 x, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {x, y, z, w}, r;\n\t"
+        "mov.b32 %0, x;\n\t}"
+        : "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return x;
+}
+
+// Keys [x, y) of query i: the unit's valid length and prefix, its own span.
+__device__ __forceinline__ int2 interval_of(const SpanAttnParams& p, int valid, int seen, int2 span, int i) {
+    const int hi = p.causal ? min(valid, max(i + p.q_offset + 1, seen)) : valid;
+    return make_int2(max(span.x, 0), min(span.y, hi));
+}
+__device__ __forceinline__ int2 span_of(const SpanAttnParams& p, int b, int i) {
+    if (p.spans == nullptr || i >= p.Lq) return make_int2(0, p.Lk);
+    return reinterpret_cast<const int2*>(p.spans)[static_cast<int64_t>(b) * p.Lq + i];
+}
+
+// Unit u of the schedule (a whole warp): groups of kHeadGroup (batch, head) pairs, whose keys and values
+// stay in L2, inside a group the query tiles from the last (longest under a causal mask) to the first.
+__device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int lane) {
+    const int planes = p.B * p.h;
+    const int tiles = (p.Lq + BM - 1) / BM;
+    const int grp = u / (kHeadGroup * tiles);
+    const int g_heads = min(kHeadGroup, planes - grp * kHeadGroup);
+    const int r = u - grp * kHeadGroup * tiles;
+    const int qt = tiles - 1 - r / g_heads;
+    const int plane = grp * kHeadGroup + r % g_heads;
+    UnitInfo x;
+    x.b = plane / p.h;
+    x.head = plane - x.b * p.h;
+    x.q0 = qt * BM;
+    x.valid = p.valid_lens != nullptr ? min(max(p.valid_lens[x.b], 0), p.Lk) : p.Lk;
+    x.seen = p.prefix_lens != nullptr ? p.prefix_lens[x.b] : 0;
+    int lo_min = p.Lk, lo_max = 0, hi_min = p.Lk, hi_max = 0;
+    const int last = min(x.q0 + BM, p.Lq) - 1;
+    if (p.spans == nullptr) {   // hi grows with i
+        const int2 first = interval_of(p, x.valid, x.seen, make_int2(0, p.Lk), x.q0);
+        lo_min = 0;
+        hi_min = first.y;
+        hi_max = interval_of(p, x.valid, x.seen, make_int2(0, p.Lk), last).y;
+    } else {
+        for (int i = x.q0 + lane; i <= last; i += 32) {
+            const int2 iv = interval_of(p, x.valid, x.seen, span_of(p, x.b, i), i);
+            lo_max = max(lo_max, iv.x);
+            hi_min = min(hi_min, iv.y);
+            if (iv.y > iv.x) {
+                lo_min = min(lo_min, iv.x);
+                hi_max = max(hi_max, iv.y);
+            }
+        }
+        lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+        hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+        lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+        hi_max = __reduce_max_sync(0xffffffffu, hi_max);
+    }
+    // no row has a key: one tile all the same, which the masks leave without weight
+    const bool any = hi_max > lo_min;
+    x.j0 = any ? lo_min / BN : 0;
+    x.n = any ? (hi_max + BN - 1) / BN - x.j0 : 1;
+    x.lo_max = lo_max;
+    x.hi_min = hi_min;
+    return x;
+}
+
+// tanh(x) = x P(x^2) for |x| <= 1/2: minimax polynomial of degree 3 in x^2 (Remez exchange on the
+// relative error; 2^-21.8 of 1 in fp32 arithmetic).
+constexpr float kTanhRange2 = 0.25f;
+constexpr float kT0 = 0.999999463558197f, kT1 = -0.33326318860054016f, kT2 = 0.13190296292304993f,
+                kT3 = -0.04440222680568695f;
+
+// u[0..63] -> cap log2(e) tanh(u * a), a = scale / cap, 16 scores at a time: the polynomial where all of a
+// warp's scores allow it (two instructions and a half a score, packed), else 1 - 2 / (1 + e^2x), which is
+// good to 2^-22 of 1 over the whole range.
+__device__ __forceinline__ void cap_scores(uint32_t (&u)[64], float a, float top) {
+    const float2 a2 = make_float2(a, a);
+    const float2 c3 = make_float2(kT3 * top, kT3 * top), c2 = make_float2(kT2 * top, kT2 * top),
+                 c1 = make_float2(kT1 * top, kT1 * top), c0 = make_float2(kT0 * top, kT0 * top);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float2 x[8], y[8];
+        float far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int c = 16 * q + 2 * e;
+            x[e] = fmul2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), a2);
+            y[e] = fmul2(x[e], x[e]);
+            far = fmax3(far, y[e].x, y[e].y);
+        }
+        if (!__any_sync(0xffffffffu, far > kTanhRange2)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 r = fmul2(ffma2(ffma2(ffma2(c3, y[e], c2), y[e], c1), y[e], c0), x[e]);
+                u[16 * q + 2 * e] = __float_as_uint(r.x);
+                u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float v = (e & 1) ? x[e >> 1].y : x[e >> 1].x;
+                const float r = rcp_approx(1.0f + ex2_approx(v * (2.0f * kLog2e)));
+                u[16 * q + e] = __float_as_uint(fmaf(-2.0f * top, r, top));
+            }
+        }
+    }
+}
+
+// Scores in log2 units minus slope |i - j|: away = i - (first key of u), slope in log2 units.
+__device__ __forceinline__ void bias_scores(uint32_t (&u)[64], float away, float slope) {
+    const bool below = away >= 63.0f, above = away <= 0.0f;
+    if (__all_sync(0xffffffffu, below) || __all_sync(0xffffffffu, above)) {   // |away - c| is linear in c
+        const float s = __all_sync(0xffffffffu, below) ? slope : -slope;
+        float2 b = make_float2(-s * away, fmaf(-s, away, s));
+        const float2 step = make_float2(2.0f * s, 2.0f * s);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+            const float2 r = fadd2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])),
+                                   ffma2(step, make_float2(c, c), b));
+            u[2 * c] = __float_as_uint(r.x);
+            u[2 * c + 1] = __float_as_uint(r.y);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c])));
+    }
+}
+
+template <int kD, int kMode>
+__global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_constant__ SpanAttnParams p,
+                                                                const __grid_constant__ SpanMaps maps) {
+    using G = Tiles<kD>;
+    constexpr uint32_t kTile = G::kTile;
+    constexpr int kOut = kD / 2;      // output features of a softmax thread
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* base = smem_raw;
+    SmemSpan* sm = reinterpret_cast<SmemSpan*>(base + G::kOffBar);
     pdl_trigger();
-    pdl_wait();
+    if ((smem_u32(base) & 1023u) != 0) {
+        // the 128-byte-swizzled tiles need 1024-byte alignment: refuse rather than compute garbage
+        pdl_wait();
+        if (threadIdx.x == 0) atomicCAS(p.status, 0, 0x802);
+        return;
+    }
+    const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (i >= p.Lq) return;
-    const int head = blockIdx.y % p.h, b = blockIdx.y / p.h;
-    const int kvh = head / (p.h / p.h_kv);
-    const T* qr = static_cast<const T*>(p.q.p) + b * p.q.b + i * p.q.l + head * p.q.h + lane;
-    const T* K = static_cast<const T*>(p.k.p) + b * p.k.b + kvh * p.k.h + lane;
-    const T* V = static_cast<const T*>(p.v.p) + b * p.v.b + kvh * p.v.h + lane;
-    float q[kPer], o[kPer];
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-        q[e] = load_f(qr + 32 * e);
-        o[e] = 0.0f;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->q_full[i], 1);
+            mbar_init(&sm->q_empty[i], 1);
+            mbar_init(&sm->unit_full[i], 1);
+            mbar_init(&sm->steal_full[i], 1);
+            mbar_init(&sm->s_full[i], 1);
+            mbar_init(&sm->s_free[i], 2 * BM);
+            mbar_init(&sm->p_full[i], 2 * BM);
+            mbar_init(&sm->p_free[i], 1);
+        }
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(&sm->k_full[s], 1);
+            mbar_init(&sm->k_empty[s], 1);
+            mbar_init(&sm->v_full[s], 1);
+            mbar_init(&sm->v_empty[s], 1);
+        }
+        mbar_init(&sm->v_edge, 1);
+        sm->abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&maps.q);
+        tma_prefetch_desc(&maps.k);
+        tma_prefetch_desc(&maps.v);
+        tma_prefetch_desc(&maps.out);
     }
-    const float slope = p.slopes != nullptr ? p.slopes[head] : 0.0f;
-    const int2 range = interval_of(p, b, i);
-    float m = -CUDART_INF_F, l = 0.0f;
-    for (int j = range.x; j < range.y; ++j) {
-        float s = 0.0f;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s = fmaf(q[e], load_f(K + j * p.k.l + 32 * e), s);
-        s = warp_add(s) * p.scale;
-        if (p.cap > 0.0f) s = p.cap * tanhf(s / p.cap);
-        s -= slope * fabsf(static_cast<float>(i + p.q_offset - j));
-        const float m_new = fmaxf(m, s);
-        const float alpha = expf(m - m_new), w = expf(s - m_new);
-        l = l * alpha + w;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] = fmaf(w, load_f(V + j * p.v.l + 32 * e), o[e] * alpha);
-        m = m_new;
+    if (warp == 9) {
+        tmem_alloc(&sm->tmem_base, kTmemCols);
+        tmem_relinquish();
     }
-    T* y = static_cast<T*>(p.out.p) + b * p.out.b + i * p.out.l + head * p.out.h + lane;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    volatile int* abort_flag = &sm->abort_flag;
+    pdl_wait();   // the tensors and the mask parts come from earlier kernels
+
+    if (warp >= 8) {
+        regs_dec<64>();
+        if (warp == 8) {
+            // ------------------------------------------------ scheduler, Q and K loads
+            int u = blockIdx.x;
+            uint32_t gk = 0;   // K tiles issued so far
+            for (int k = 0;; ++k) {
+                const int qb = k & 1;
+                // unit k - 2 has stored its output from this Q buffer (and every role has read its slot)
+                if (k >= 2) mbar_wait(&sm->q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.status, 0x810);
+                if (k >= 1) {
+                    const int a = (k - 1) & 1;
+                    const bool ok = mbar_wait(&sm->steal_full[a], ((k - 1) >> 1) & 1, abort_flag, p.status, 0x811);
+                    u = ok ? steal_answer(&sm->steal[a][0]) : -1;
+                    fence_proxy_async_smem();   // the slot may take the answer after next
+                }
+                u = __shfl_sync(0xffffffffu, u, 0);
+                if (__any_sync(0xffffffffu, u < 0 || *abort_flag != 0)) {
+                    if (lane == 0) {
+                        sm->unit[qb].n = 0;
+                        mbar_arrive(&sm->unit_full[qb]);
+                    }
+                    break;
+                }
+                if (lane == 0) steal_request(&sm->steal[qb][0], &sm->steal_full[qb]);
+                const UnitInfo x = unit_of(p, u, lane);
+                if (lane == 0) {
+                    sm->unit[qb] = x;
+                    mbar_arrive(&sm->unit_full[qb]);
+                    const int kvh = x.head / (p.h / p.h_kv);
+                    mbar_arrive_expect_tx(&sm->q_full[qb], kTile);
+                    tma_load_5d(&maps.q, &sm->q_full[qb], base + qb * kTile, x.q0, at_h(p.q, x.head),
+                                at_b(p.q, x.b));
+                    for (int j = 0; j < x.n; ++j, ++gk) {
+                        const int s = gk % G::kStagesK;
+                        mbar_wait(&sm->k_empty[s], ((gk / G::kStagesK) & 1) ^ 1, abort_flag, p.status, 0x812);
+                        mbar_arrive_expect_tx(&sm->k_full[s], kTile);
+                        tma_load_5d(&maps.k, &sm->k_full[s], base + G::kOffK + s * kTile, (x.j0 + j) * BN,
+                                    at_h(p.k, kvh), at_b(p.k, x.b));
+                    }
+                }
+                __syncwarp();
+            }
+        } else if (warp == 11) {
+            // ------------------------------------------------ V loads
+            uint32_t gv = 0, edges = 0;
+            for (int k = 0;; ++k) {
+                const int qb = k & 1;
+                const bool ok = mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x813);
+                const UnitInfo x = sm->unit[qb];
+                if (!__all_sync(0xffffffffu, ok && x.n > 0)) break;
+                const int kvh = x.head / (p.h / p.h_kv);
+                for (int j = 0; j < x.n; ++j, ++gv) {
+                    const int s = gv % G::kStagesV;
+                    const int r0 = x.valid - (x.j0 + j) * BN;   // rows of the tile before the valid length
+                    uint8_t* dst = base + G::kOffV + s * kTile;
+                    mbar_wait(&sm->v_empty[s], ((gv / G::kStagesV) & 1) ^ 1, abort_flag, p.status, 0x814);
+                    __syncwarp();
+                    if (r0 >= BN || x.valid >= p.Lk) {
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sm->v_full[s], kTile);
+                            tma_load_5d(&maps.v, &sm->v_full[s], dst, (x.j0 + j) * BN, at_h(p.v, kvh), at_b(p.v, x.b));
+                        }
+                    } else {
+                        // values behind the valid length may be anything, and 0 * NaN is NaN: zeros in their place
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(&sm->v_edge, kTile);
+                            tma_load_5d(&maps.v, &sm->v_edge, dst, (x.j0 + j) * BN, at_h(p.v, kvh), at_b(p.v, x.b));
+                        }
+                        mbar_wait(&sm->v_edge, edges++ & 1, abort_flag, p.status, 0x815);
+                        __syncwarp();
+                        for (int sl = 0; sl < G::kSlabs; ++sl)
+                            for (uint32_t o = max(r0, 0) * 128 + lane * 16; o < kHalf; o += 512)
+                                st_shared_v4(smem_u32(dst + sl * kHalf) + o, 0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sm->v_full[s]);
+                    }
+                }
+            }
+        } else if (warp == 9 && lane == 0) {
+            // ------------------------------------------------ score MMAs: S(j) = Q K_j^T
+            constexpr uint32_t idesc_s = idesc_bf16(BM, BN, false, false);
+            const uint32_t k_addr = smem_u32(base + G::kOffK);
+            uint32_t gk = 0;   // score tiles issued so far
+            for (int k = 0;; ++k) {
+                const int qb = k & 1;
+                if (!mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x816)) break;
+                const int n = sm->unit[qb].n;
+                if (n == 0) break;
+                const uint32_t qa = smem_u32(base + qb * kTile);
+                mbar_wait(&sm->q_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x817);
+                for (int j = 0; j < n; ++j, ++gk) {
+                    const int s = gk % G::kStagesK;
+                    mbar_wait(&sm->k_full[s], (gk / G::kStagesK) & 1, abort_flag, p.status, 0x818);
+                    // buffer gk mod 2 is free once both halves have loaded score tile gk - 2
+                    const int sb = gk & 1;
+                    if (gk >= 2) mbar_wait(&sm->s_free[sb], ((gk >> 1) - 1) & 1, abort_flag, p.status, 0x819);
+                    tc_fence_after();
+                    const uint32_t ka = k_addr + s * kTile;
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) store_f(y + 32 * e, range.y > range.x ? o[e] / l : 0.0f);
+                    for (int kk = 0; kk < kD / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+                        mma_ss(tmem + kColS + sb * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024),
+                               idesc_s, kk > 0);
+                    }
+                    tc_commit(&sm->s_full[sb]);
+                    tc_commit(&sm->k_empty[s]);
+                }
+            }
+        } else if (warp == 10 && lane == 0) {
+            // ------------------------------------------------ P.V MMAs: O += P(j) V_j
+            constexpr uint32_t idesc_o = idesc_bf16(BM, kD, false, true);
+            const uint32_t v_addr = smem_u32(base + G::kOffV);
+            uint32_t gv = 0;   // P.V steps issued so far
+            for (int k = 0;; ++k) {
+                const int qb = k & 1;
+                if (!mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x81a)) break;
+                const int n = sm->unit[qb].n;
+                if (n == 0) break;
+                for (int j = 0; j < n; ++j, ++gv) {
+                    const int s = gv % G::kStagesV;
+                    mbar_wait(&sm->v_full[s], (gv / G::kStagesV) & 1, abort_flag, p.status, 0x81b);
+                    // P(j) written; for j = 0 also: the previous unit's output has been read out of O
+                    mbar_wait(&sm->p_full[gv & 1], (gv >> 1) & 1, abort_flag, p.status, 0x81c);
+                    tc_fence_after();
+                    const uint32_t va = v_addr + s * kTile;
+                    const uint32_t pa = tmem + kColP + (gv & 1) * 64;   // keys 16 kk .. 16 kk + 15: columns 8 kk ..
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_ts(tmem + kColO, pa + kk * 8, sdesc_sw128(va + kk * 2048, kHalf, 1024), idesc_o,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    tc_commit(&sm->p_free[gv & 1]);
+                    tc_commit(&sm->v_empty[s]);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        named_bar_sync(3, kThreads);
+        if (warp == 9) {
+            __syncwarp();
+            tc_fence_after();
+            tmem_dealloc(tmem, kTmemCols);
+        }
+    } else {
+        regs_inc<216>();
+        // ------------------------------------------------ softmax: thread (h, row), keys 64 h .. 64 h + 63
+        const int h = warp >> 2;
+        const int q = warp & 3;   // lane quarter; warps q and q + 4 hold the two halves of the same rows
+        const int row = q * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t s_tmem = tmem + lane_off + kColS + h * 64;     // + 128 b
+        const uint32_t p_tmem = tmem + lane_off + kColP + h * 32;     // + 64 b
+        const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;   // this half's output features
+        const float scale_log2 = p.scale * kLog2e;
+        const float tanh_in = p.cap > 0.0f ? p.scale / p.cap : 0.0f, tanh_out = p.cap * kLog2e;
+        uint32_t g = 0;   // score tiles consumed so far
+        bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x81d);
+        UnitInfo x = sm->unit[0];
+        int2 span = ok && x.n > 0 ? span_of(p, x.b, x.q0 + row) : make_int2(0, 0);
+        for (int k = 0;; ++k) {
+            const int qb = k & 1;
+            __syncwarp();
+            // every softmax thread takes the same decision (a give-up in one thread stops all)
+            if (!named_bar_and(1, 2 * BM, ok && x.n > 0)) break;
+            const int n = x.n, q0 = x.q0, b = x.b, head = x.head;
+            const int2 iv = interval_of(p, x.valid, x.seen, span, q0 + row);
+            const float slope = kMode == kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
+            float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to both halves
+            float l = 0.0f;            // this half's share of the row sum
+            for (int j = 0; j < n; ++j, ++g) {
+                const uint32_t sb = g & 1;
+                mbar_wait(&sm->s_full[sb], (g >> 1) & 1, abort_flag, p.status, 0x81e);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t u[64];
+                tmem_ld_x64(s_tmem + sb * 128, u);
+                tc_fence_before();
+                mbar_arrive(&sm->s_free[sb]);
+                const int k0 = (x.j0 + j) * BN + h * 64;   // first key of this half
+                const bool edge = k0 < x.lo_max || k0 + 64 > x.hi_min;
+                float sc = 1.0f;
+                if constexpr (kMode == kPlain) {
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                    } else {
+                        sc = scale_log2;
+                    }
+                } else if constexpr (kMode == kCapped) {
+                    cap_scores(u, tanh_in, tanh_out);
+                } else {
+                    if (p.cap > 0.0f) {
+                        cap_scores(u, tanh_in, tanh_out);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                    }
+                    if (slope != 0.0f) bias_scores(u, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                }
+                if (edge) {
+                    const uint32_t first = iv.x - k0, many = max(iv.y - iv.x, 0);   // keys first .. first + many - 1 of u
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        if (static_cast<uint32_t>(c) - first >= many) u[c] = __float_as_uint(-CUDART_INF_F);
+                }
+                float alpha = 1.0f;
+                bool grow = false;
+                float mref = 0.0f;
+                if constexpr (kMode != kCapped) {
+                    float a4[4];
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        float a = fmax3(__uint_as_float(u[16 * c4]), __uint_as_float(u[16 * c4 + 1]),
+                                        __uint_as_float(u[16 * c4 + 2]));
+#pragma unroll
+                        for (int e = 3; e < 15; e += 2)
+                            a = fmax3(a, __uint_as_float(u[16 * c4 + e]), __uint_as_float(u[16 * c4 + e + 1]));
+                        a4[c4] = fmaxf(a, __uint_as_float(u[16 * c4 + 15]));
+                    }
+                    // this half's tile max (log2 units), exchanged with the other half of the row
+                    const float mth = fmaxf(fmax3(a4[0], a4[1], a4[2]), a4[3]) * sc;
+                    sm->mx[sb][h][row] = mth;
+                    named_bar_sync(4 + q, 64);   // warps q and q + 4
+                    const float m_new = fmaxf(m, fmaxf(mth, sm->mx[sb][h ^ 1][row]));
+                    if (m == -CUDART_INF_F) {
+                        m = m_new;   // first keys of the row (-inf while it has none)
+                    } else {
+                        grow = (m_new - m) > kRescaleThreshold;
+                        if (grow) {
+                            alpha = ex2_approx(m - m_new);
+                            l *= alpha;
+                            m = m_new;
+                        }
+                    }
+                    // with no key of the row yet (m = -inf) every weight is exp2(-inf) = 0
+                    mref = (m == -CUDART_INF_F) ? 0.0f : m;
+                }
+                const float2 sc2 = make_float2(sc, sc);
+                const float2 nm2 = make_float2(-mref, -mref);
+                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                 make_float2(0.f, 0.f)};
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float2 e2 = make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
+                    if constexpr (kMode == kPlain) e2 = ffma2(e2, sc2, nm2);
+                    if constexpr (kMode == kGeneral) e2 = fadd2(e2, nm2);
+                    e2.x = ex2_approx(e2.x);
+                    e2.y = ex2_approx(e2.y);
+                    acc[c & 3] = fadd2(acc[c & 3], e2);
+                    // the weights are rounded to bf16 for the product; the sum takes them unrounded
+                    pk[c] = pack_bf16x2(e2.x, e2.y);
+                }
+                const float2 s4 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                l += s4.x + s4.y;
+                // weight buffer sb is free once P.V(g - 2) has read it
+                if (g >= 2) {
+                    mbar_wait(&sm->p_free[sb], ((g >> 1) - 1) & 1, abort_flag, p.status, 0x81f);
+                    __syncwarp();
+                    tc_fence_after();
+                }
+                if (kMode != kCapped && j > 0 && __any_sync(0xffffffffu, grow)) {
+                    // O is rescaled (this half's features) once P.V(g - 1) has completed; at j = 0 the first
+                    // P.V overwrites O, after the previous unit's output has been read
+                    mbar_wait(&sm->p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, p.status, 0x820);
+                    __syncwarp();
+                    tc_fence_after();
+#pragma unroll
+                    for (int q4 = 0; q4 < kOut / 16; ++q4) {
+                        uint32_t o[16];
+                        tmem_ld_x16(o_tmem + q4 * 16, o);
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                        tmem_st_x16(o_tmem + q4 * 16, o);
+                    }
+                }
+#pragma unroll
+                for (int q4 = 0; q4 < 2; ++q4)
+                    tmem_st_x16_nowait(p_tmem + sb * 64 + q4 * 16,
+                                       *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q4]));
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&sm->p_full[sb]);
+            }
+            // The next unit's slot and spans are read now: their latency passes behind the output.
+            const int nb = (k + 1) & 1;
+            ok = mbar_wait(&sm->unit_full[nb], ((k + 1) >> 1) & 1, abort_flag, p.status, 0x821);
+            x = sm->unit[nb];
+            if (ok && x.n > 0) span = span_of(p, x.b, x.q0 + row);
+            // ---------------- output: thread (h, row) writes its features of O / (l_0 + l_1). The unit's Q
+            // buffer is idle (its last score MMA completed before this thread's last wait on S): it carries
+            // l_h of every half and row, then the bf16 output tile.
+            uint8_t* qbuf = base + qb * kTile;
+            float* lsum = reinterpret_cast<float*>(qbuf);
+            lsum[h * BM + row] = l;
+            named_bar_sync(1, 2 * BM);   // both halves' sums are in shared memory
+            const float L = lsum[row] + lsum[BM + row];
+            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
+            const uint32_t gl = g - 1;   // the unit's last tile: its P.V completes O
+            mbar_wait(&sm->p_free[gl & 1], (gl >> 1) & 1, abort_flag, p.status, 0x822);
+            __syncwarp();
+            tc_fence_after();
+            uint32_t o[kOut];
+            if constexpr (kOut == 64) tmem_ld_x64(o_tmem, o);
+            else tmem_ld_x32(o_tmem, o);
+            named_bar_sync(1, 2 * BM);   // every thread has read the sums the staging overwrites
+#pragma unroll
+            for (int ch = 0; ch < kOut / 8; ++ch) {
+                const int col = h * kOut + 8 * ch;   // feature: slab col / 64, 16-byte chunk (col % 64) / 8
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
+                st_shared_v4(smem_u32(qbuf + (col / 64) * kHalf) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4), w[0],
+                             w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();   // O has been read: the next unit's first P.V may overwrite it
+            named_bar_sync(1, 2 * BM);
+            if (warp == 0 && lane == 0) {
+                if (!*abort_flag) {
+                    asm volatile(
+                        "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %2, %4, %5}], [%1];" ::"l"(
+                            reinterpret_cast<uint64_t>(&maps.out)),
+                        "r"(smem_u32(qbuf)), "r"(0), "r"(q0), "r"(head), "r"(b)
+                        : "memory");
+                    tma_store_commit();
+                }
+                tma_store_wait_read();   // the buffer may take the Q tile of unit k + 2
+                mbar_arrive(&sm->q_empty[qb]);
+            }
+        }
+        if (warp == 0 && lane == 0) tma_store_wait_all();
+        tc_fence_before();
+        named_bar_sync(3, kThreads);
+    }
 }
 
 // spans[b, i]: the run of equal ids around i. One CTA per sequence; each thread finds the bounds of
@@ -132,10 +685,40 @@ cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spa
     return launch_pdl(document_spans_kernel, dim3(B), dim3(kSpanThreads), 0, s, ids, L, spans);
 }
 
+template <int kD, int kMode>
+static cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, unsigned grid, cudaStream_t s) {
+    static_assert(smem_bytes<kD>() <= 232448, "shared memory budget");
+    cudaError_t e = cudaFuncSetAttribute(span_attn_kernel<kD, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(smem_bytes<kD>()));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(span_attn_kernel<kD, kMode>, dim3(grid), dim3(kThreads), smem_bytes<kD>(), s, p, maps);
+}
+
+// [B, L, H, d] as {64, L, d / 64, H, B}: a 64-column slab of 128 rows is one swizzled half tile
+static bool map_strided(CUtensorMap* m, const Strided& t, int B, int L, int H, int d) {
+    const uint64_t dims[5] = {64, (uint64_t)L, (uint64_t)d / 64, t.h != 0 ? (uint64_t)H : 1, t.b != 0 ? (uint64_t)B : 1};
+    const uint64_t str[4] = {(uint64_t)t.l * 2, 128, t.h != 0 ? (uint64_t)t.h * 2 : 128, t.b != 0 ? (uint64_t)t.b * 2 : 128};
+    const uint32_t box[5] = {64, 128, (uint32_t)d / 64, 1, 1};
+    return encode_bf16_tiled(m, t.p, 5, dims, str, box, true);
+}
+
 cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s) {
-    const dim3 grid((p.Lq + kWarps - 1) / kWarps, p.B * p.h), block(32 * kWarps);
-    return p.d == 64 ? launch_pdl(span_attn_simple_kernel<64>, grid, block, 0, s, p)
-                     : launch_pdl(span_attn_simple_kernel<128>, grid, block, 0, s, p);
+    SpanMaps maps;
+    if (!map_strided(&maps.q, p.q, p.B, p.Lq, p.h, p.d) || !map_strided(&maps.k, p.k, p.B, p.Lk, p.h_kv, p.d) ||
+        !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
+        return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
+    const int mode = p.slopes == nullptr && p.cap > 0.0f && p.cap <= kFixedCap ? kCapped
+                     : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
+                                                                             : kGeneral;
+    if (p.d == 64) {
+        if (mode == kPlain) return launch_mode<64, kPlain>(p, maps, grid, s);
+        if (mode == kCapped) return launch_mode<64, kCapped>(p, maps, grid, s);
+        return launch_mode<64, kGeneral>(p, maps, grid, s);
+    }
+    if (mode == kPlain) return launch_mode<128, kPlain>(p, maps, grid, s);
+    if (mode == kCapped) return launch_mode<128, kCapped>(p, maps, grid, s);
+    return launch_mode<128, kGeneral>(p, maps, grid, s);
 }
 
 }  // namespace mha

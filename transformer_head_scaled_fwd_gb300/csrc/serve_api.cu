@@ -292,6 +292,10 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
         if (H == 1) views[i]->h = 8;
         if (!aligned(ptrs[i], 16) || views[i]->b % 8 != 0 || views[i]->l % 8 != 0 || views[i]->h % 8 != 0)
             return fail(MHA_ERR_INVALID_ARG, "%s and its strides must be aligned to 16 bytes", names[i]);
+        if (views[i]->l == 0 || (i == 3 && (views[i]->b == 0 || views[i]->h == 0)))
+            return fail(MHA_ERR_INVALID_ARG, "%s: only the batch and head strides of an input may be 0", names[i]);
+        if (views[i]->b >= (int64_t(1) << 39) || views[i]->l >= (int64_t(1) << 39) || views[i]->h >= (int64_t(1) << 39))
+            return fail(MHA_ERR_UNSUPPORTED, "%s: strides must stay below 2^40 bytes", names[i]);
     }
     if (mask != nullptr) {
         if (mask->q_offset < 0 || mask->q_offset > 0x7fffffff - L_q)
@@ -303,8 +307,9 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
         p.prefix_lens = mask->prefix_lens;
         p.spans = mask->doc_spans;
     }
-    const int64_t planes = static_cast<int64_t>(B) * h;
-    if (planes > 65535) return fail(MHA_ERR_UNSUPPORTED, "B * h up to 65535 (got %lld)", static_cast<long long>(planes));
+    if (static_cast<int64_t>(B) * h > (int64_t(1) << 30) ||
+        static_cast<int64_t>(B) * h * ((L_q + 127) / 128) > 0x7fffffffll)
+        return fail(MHA_ERR_UNSUPPORTED, "B * h * ceil(L_q / 128) must stay below 2^31");
     p.B = B; p.Lq = L_q; p.Lk = L_k; p.h = h; p.h_kv = h_kv; p.d = d_k;
     p.status = mha::device_status();
     if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
