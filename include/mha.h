@@ -427,8 +427,8 @@ typedef struct {
  * for the query q [B, h, d_k] at position kv_lens[b] - 1 (append its key and value first). q and out
  * have strides (b, h; l is ignored). kv_lens: device int32 [B]; a length <= 0 gives zeros. scores NULL:
  * the plain scaled scores. MHA_BF16 or MHA_F32, d_k = 64 or 128, h a multiple of h_kv. What lies in a
- * page behind a sequence's end is not used, whatever it holds. MHA_BF16: pages and their strides
- * aligned to 16 bytes. Weights are rounded to bf16 for the product with bf16 values.
+ * page behind a sequence's end is not used, whatever it holds. The pages and their strides are aligned
+ * to 16 bytes. Weights are rounded to bf16 for the product with bf16 values.
  * workspace >= mha_paged_attention_workspace_size(...), 256-byte aligned, contents of no matter;
  * calls that overlap on the GPU need one each. The result does not depend on timing.
  */

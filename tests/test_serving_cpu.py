@@ -85,6 +85,7 @@ def test_paged_attention_refusals(lib):
     assert call(sc=scores_t(cap=-1.0)) == INV and call(sc=scores_t(scale=math.inf)) == INV
     assert call(cache=cache_t(slot_stride=65)) == INV          # not 16 bytes
     assert call(cache=cache_t(v_pages=4104)) == INV
+    assert call(dt=0, cache=cache_t(head_stride=66)) == INV and call(dt=0, cache=cache_t(k_pages=4100)) == INV
     assert call(ws=None) == INV and call(ws=ctypes.c_void_p(4100)) == INV and call(n=0) == INV
     assert bnd.paged_attention_workspace_size(1, 2, 9, 4, 64) == 0
     assert bnd.paged_attention_workspace_size(1, 2, 8, 4, 80) == 0

@@ -241,9 +241,10 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
     mha::Strided qv, ov;
     if ((st = view(q, q_strides, elem(dt), "q", &qv)) != MHA_OK) return st;
     if ((st = view(out, out_strides, elem(dt), "out", &ov)) != MHA_OK) return st;
-    if (dt == MHA_BF16 && (!aligned(cache->k_pages, 16) || !aligned(cache->v_pages, 16) || cache->page_stride % 8 != 0 ||
-                           cache->slot_stride % 8 != 0 || cache->head_stride % 8 != 0))
-        return fail(MHA_ERR_INVALID_ARG, "bf16 pages and their strides must be aligned to 16 bytes");
+    const int64_t chunk = 16 / static_cast<int64_t>(elem(dt));
+    if (!aligned(cache->k_pages, 16) || !aligned(cache->v_pages, 16) || cache->page_stride % chunk != 0 ||
+        cache->slot_stride % chunk != 0 || cache->head_stride % chunk != 0)
+        return fail(MHA_ERR_INVALID_ARG, "the pages and their strides must be aligned to 16 bytes");
     const size_t need = mha_paged_attention_workspace_size(dt, B, h, h_kv, d_k);
     if (workspace == nullptr || !aligned(workspace, 256))
         return fail(MHA_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
