@@ -5,8 +5,7 @@
 //
 // HBM-bound: K and V of every cached position are read once, 4 d_k bytes a position and key head in
 // bf16, for 4 d_k flop a query head. The heads that share a key head are the rows of one matrix
-// product (16 rows in bf16, mma.sync: the product takes a sixth of the load's time at 8 heads, and
-// CUDA cores could not keep up from 4 heads on), so the cache is read once for all of them.
+// product (mma.sync in bf16: CUDA cores could not keep up from 4 heads on), so the cache is read once for all of them.
 //
 // Work split: a unit is (sequence, key head, tile of query heads). All units' keys, in blocks of
 // kWarps steps, form one line that is cut into equal pieces, one CTA a piece, whatever the lengths
@@ -46,7 +45,6 @@ struct Step {
     static constexpr int kKeys = kStepBytes / kRow;
     static constexpr int kChunks = kRow / 16;
 };
-constexpr int kRowsBf16 = 16;
 constexpr int kMaxRows = 16;
 
 struct JoinDesc {
@@ -95,23 +93,29 @@ struct ScoreForm {
     }
 };
 
-// ------------------------------------------------------------ a warp's rows: bf16, matrix instructions
-template <int kD>
+// ------------------------------------------------------------ a warp's heads: bf16, matrix instructions
+// Both products are taken transposed, so that the long sides are the matrix instruction's 16 rows and the
+// query heads its 8 columns: S^T = K q^T (16 keys x d_k times d_k x 8 heads) and o^T = V^T P^T (16 features x
+// 16 keys times 16 keys x 8 heads). With the heads as the 16 rows, up to 8 heads fill half of every
+// instruction and of the accumulators. P^T turns from result to operand layout by a register transpose.
+template <int kD, int kNT>          // kNT tiles of 8 heads
 struct WarpBf16 {
     using T = __nv_bfloat16;
-    static constexpr int kRows = kRowsBf16;
+    static constexpr int kRows = 8 * kNT;
+    static constexpr int kQFloats = 0;      // shared memory for the query rows (they stay in registers)
     static constexpr int kKeys = Step<T, kD>::kKeys;
-    uint32_t q[kD / 16][4];
-    float o[kD / 8][4];
-    float m[2], l[2], slope[2];     // rows lane / 4 and lane / 4 + 8; l is this lane's share
+    static constexpr int kKT = kKeys / 16;
+    uint32_t q[kD / 16][kNT][2];
+    float o[kD / 16][kNT][4];       // features lane / 4 (+ 8), heads 2 (lane % 4) + {0, 1}
+    float m[kNT][2], l[kNT][2], slope[kNT][2];     // of those two heads; l is this lane's share
 
     static __device__ __forceinline__ int swizzle(int row) { return row & 7; }
 
-    __device__ __forceinline__ void start(const PagedAttnParams& p, int b, int head0, int rows, int lane) {
+    __device__ __forceinline__ void start(const PagedAttnParams& p, float*, int b, int head0, int rows, int lane) {
         const T* base = static_cast<const T*>(p.q) + b * p.q_b + head0 * p.q_h;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = (lane >> 2) + 8 * r;
+        for (int nt = 0; nt < kNT; ++nt) {
+            const int row = nt * 8 + (lane >> 2);      // operand column: head lane / 4
             const T* x = base + row * p.q_h + 2 * (lane & 3);
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
@@ -122,137 +126,138 @@ struct WarpBf16 {
                         v.x = x[16 * k + 8 * hf];
                         v.y = x[16 * k + 8 * hf + 1];
                     }
-                    q[k][2 * hf + r] = *reinterpret_cast<uint32_t*>(&v);
+                    q[k][nt][hf] = *reinterpret_cast<uint32_t*>(&v);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
             }
-            slope[r] = p.slopes != nullptr && row < rows ? p.slopes[head0 + row] * kLog2e : 0.0f;
-            m[r] = -CUDART_INF_F;
-            l[r] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hd = nt * 8 + 2 * (lane & 3) + e;
+                slope[nt][e] = p.slopes != nullptr && hd < rows ? p.slopes[head0 + hd] * kLog2e : 0.0f;
+                m[nt][e] = -CUDART_INF_F;
+                l[nt][e] = 0.0f;
+            }
         }
-#pragma unroll
-        for (int i = 0; i < kD / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     }
 
     // keys key0 .. key0 + kKeys - 1 in shared memory at k, v; live: bit i: key0 + i counts
     __device__ __forceinline__ void step(uint32_t k, uint32_t v, int key0, uint32_t live, int n, const ScoreForm& form,
                                          int rows, int lane) {
         constexpr int kRow = Step<T, kD>::kRow;
-        float s[kKeys / 8][4];
-        const int mi = lane >> 3, r8 = lane & 7;
+        const int r8 = lane & 7, mi = lane >> 3;
+        float s[kKT][kNT][4];
 #pragma unroll
-        for (int t = 0; t < kKeys / 8; ++t) {
+        for (int t = 0; t < kKT; ++t) {
+            const uint32_t row = k + (t * 16 + (mi & 1) * 8 + r8) * kRow;
+            const uint32_t c0 = static_cast<uint32_t>(((mi >> 1) ^ r8) << 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
-        }
+            for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-        for (int kp = 0; kp < kD / 32; ++kp) {
+                for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.0f;
 #pragma unroll
-            for (int t = 0; t < kKeys / 8; ++t) {
+            for (int kk = 0; kk < kD / 16; ++kk) {
                 uint32_t f[4];
-                ldsm4(f, k + (t * 8 + r8) * kRow + (((kp * 4 + mi) ^ r8) << 4));
-                mma16816(s[t], q[2 * kp], f[0], f[1]);
-                mma16816(s[t], q[2 * kp + 1], f[2], f[3]);
+                ldsm4(f, row + (c0 ^ (kk << 5)));
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816(s[t][nt], f, q[kk][nt][0], q[kk][nt][1]);
             }
         }
-        const bool both = rows > 8;
-        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        bool more = false;
 #pragma unroll
-        for (int t = 0; t < kKeys / 8; ++t) {
+        for (int t = 0; t < kKT; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int i = t * 8 + 2 * (lane & 3) + e;
+            for (int e = 0; e < 4; ++e) {
+                const int i = t * 16 + (lane >> 2) + 8 * (e >> 1);
                 const bool ok = (live >> i) & 1u;
                 const float away = static_cast<float>(n - 1 - key0 - i);
-                s[t][e] = ok ? form(s[t][e], slope[0], away) : -CUDART_INF_F;
-                top[0] = fmaxf(top[0], s[t][e]);
-                if (both) {
-                    s[t][2 + e] = ok ? form(s[t][2 + e], slope[1], away) : -CUDART_INF_F;
-                    top[1] = fmaxf(top[1], s[t][2 + e]);
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                    s[t][nt][e] = ok ? form(s[t][nt][e], slope[nt][e & 1], away) : -CUDART_INF_F;
+                    more |= s[t][nt][e] > m[nt][e & 1] + kGrow;
                 }
             }
-        }
-        float alpha[2] = {1.0f, 1.0f}, ref[2];
-        bool grew = false;
+        // The maximum moves only when a score passes it by kGrow (the first keys always do); until then
+        // the weights stay below 2^kGrow and nothing is rescaled.
+        if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-            top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            if (top[r] > m[r] + kGrow || m[r] == -CUDART_INF_F) {   // the first keys set the maximum
-                const float to = fmaxf(top[r], m[r]);
-                if (m[r] != -CUDART_INF_F) {
-                    alpha[r] = ex2_approx(m[r] - to);
-                    l[r] *= alpha[r];
-                    grew = true;
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = m[nt][e];
+#pragma unroll
+                    for (int t = 0; t < kKT; ++t) top = fmax3(top, s[t][nt][e], s[t][nt][e + 2]);
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float alpha = m[nt][e] == -CUDART_INF_F ? 0.0f : ex2_approx(m[nt][e] - top);
+                    m[nt][e] = top;
+                    l[nt][e] *= alpha;
+#pragma unroll
+                    for (int i = 0; i < kD / 16; ++i) {
+                        o[i][nt][e] *= alpha;
+                        o[i][nt][e + 2] *= alpha;
+                    }
                 }
-                m[r] = to;
-            }
-            ref[r] = m[r] == -CUDART_INF_F ? 0.0f : m[r];
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int i = 0; i < kD / 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e >> 1];
         }
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks) {
-            uint32_t a[4];
+        for (int t = 0; t < kKT; ++t) {
+            uint32_t pt[kNT][2];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const float* c = s[2 * ks + hf];
-                const float p0 = ex2_approx(c[0] - ref[0]), p1 = ex2_approx(c[1] - ref[0]);
-                l[0] += p0 + p1;
-                a[2 * hf] = pack_bf16x2(p0, p1);      // weights rounded to the values' type; l takes them unrounded
-                a[2 * hf + 1] = 0u;
-                if (both) {
-                    const float p2 = ex2_approx(c[2] - ref[1]), p3 = ex2_approx(c[3] - ref[1]);
-                    l[1] += p2 + p3;
-                    a[2 * hf + 1] = pack_bf16x2(p2, p3);
+            for (int nt = 0; nt < kNT; ++nt) {
+                const float r0 = m[nt][0] == -CUDART_INF_F ? 0.0f : m[nt][0], r1 = m[nt][1] == -CUDART_INF_F ? 0.0f : m[nt][1];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float p0 = ex2_approx(s[t][nt][2 * hf] - r0), p1 = ex2_approx(s[t][nt][2 * hf + 1] - r1);
+                    l[nt][0] += p0;      // the sums take the weights before they are rounded to the values' type
+                    l[nt][1] += p1;
+                    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[nt][hf]) : "r"(pack_bf16x2(p0, p1)));
                 }
             }
+            const uint32_t row = v + (t * 16 + (mi >> 1) * 8 + r8) * kRow;
+            const uint32_t c0 = static_cast<uint32_t>(((mi & 1) ^ r8) << 4);
 #pragma unroll
-            for (int np = 0; np < kD / 16; ++np) {
+            for (int i = 0; i < kD / 16; ++i) {
                 uint32_t f[4];
-                ldsm4t(f, v + (ks * 16 + (mi & 1) * 8 + r8) * kRow + (((np * 2 + (mi >> 1)) ^ r8) << 4));
-                mma16816(o[2 * np], a, f[0], f[1]);
-                mma16816(o[2 * np + 1], a, f[2], f[3]);
+                ldsm4t(f, row + (c0 ^ (i << 5)));
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) mma16816(o[i][nt], f, pt[nt][0], pt[nt][1]);
             }
         }
     }
 
-    // the row maxima and sums to shared memory
+    // the maxima and sums of the heads to shared memory
     __device__ __forceinline__ void put_stats(float* sm_m, float* sm_l, int lane) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-            if ((lane & 3) == 0) {
-                sm_m[(lane >> 2) + 8 * r] = m[r];
-                sm_l[(lane >> 2) + 8 * r] = l[r];
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (lane < 4) {
+                    sm_m[nt * 8 + 2 * lane + e] = m[nt][e];
+                    sm_l[nt * 8 + 2 * lane + e] = sum;
+                }
             }
-        }
     }
-    // o scaled by f[row] (put) or added onto what is there (add = true), rows of kD floats
+    // o scaled by f[head], written or added (add = true) to rows of kD floats
     __device__ __forceinline__ void put(float* buf, const float* f, bool add, int rows, int lane) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = (lane >> 2) + 8 * r;
-            if (row >= rows) continue;
-            const float fr = f[row];
+        for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-            for (int i = 0; i < kD / 8; ++i) {
-                float2* y = reinterpret_cast<float2*>(buf + row * kD + 8 * i + 2 * (lane & 3));
-                float2 x = make_float2(o[i][2 * r] * fr, o[i][2 * r + 1] * fr);
-                if (add) {
-                    const float2 z = *y;
-                    x.x += z.x;
-                    x.y += z.y;
-                }
-                *y = x;
+            for (int e = 0; e < 2; ++e) {
+                const int hd = nt * 8 + 2 * (lane & 3) + e;
+                if (hd >= rows) continue;
+                const float fr = f[hd];
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float* y = buf + hd * kD + 16 * i + 8 * hf + (lane >> 2);
+                        const float x = o[i][nt][e + 2 * hf] * fr;
+                        *y = add ? *y + x : x;
+                    }
             }
-        }
     }
 };
 
@@ -261,25 +266,25 @@ template <int kD, int kR>
 struct WarpF32 {
     using T = float;
     static constexpr int kRows = kR;
+    static constexpr int kQFloats = kR * kD;
     static constexpr int kKeys = Step<T, kD>::kKeys;      // 8 or 16
     static constexpr int kLanes = 32 / kKeys;             // lanes that share a key's dot product: 4 or 2
     static constexpr int kDims = kD / kLanes;             // features a lane multiplies: 32
     static constexpr int kOwn = kD / 32;                  // features of o a lane keeps
     float o[kR][kOwn];
     float m[kR], l[kR];                                   // l is this lane's share
-    const float* q;                                       // the unit's query rows, or zeros
-    int64_t q_h;
+    uint32_t q;                                           // the unit's query rows in shared memory
     const float* slopes;
-    int rows_;
 
     // two (or four) keys of a quarter-warp's 16-byte reads land in different 64-byte (32-byte) parts
     static __device__ __forceinline__ int swizzle(int row) { return kLanes == 4 ? (row & 1) << 2 : (row & 3) << 1; }
 
-    __device__ __forceinline__ void start(const PagedAttnParams& p, int b, int head0, int rows, int) {
-        q = static_cast<const float*>(p.q) + b * p.q_b + head0 * p.q_h;
-        q_h = p.q_h;
+    __device__ __forceinline__ void start(const PagedAttnParams& p, float* shared_q, int b, int head0, int rows, int) {
+        const float* x = static_cast<const float*>(p.q) + b * p.q_b + head0 * p.q_h;
+        for (int i = threadIdx.x; i < rows * kD; i += kThreads) shared_q[i] = x[(i / kD) * p.q_h + i % kD];
+        __syncthreads();      // the last unit's readers are behind the barriers of its end
+        q = smem_u32(shared_q);
         slopes = p.slopes != nullptr ? p.slopes + head0 : nullptr;
-        rows_ = rows;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
             m[r] = -CUDART_INF_F;
@@ -315,15 +320,16 @@ struct WarpF32 {
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
             if (r >= rows) break;
-            const float* x = q + r * q_h + part * 4;
             float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
             for (int i = 0; i < kDims / 4; ++i) {
-                const float* xi = x + i * kLanes * 4;      // the same few lines for every key: L1
-                d0 = fmaf(kv[i].x, xi[0], d0);
-                d1 = fmaf(kv[i].y, xi[1], d1);
-                d0 = fmaf(kv[i].z, xi[2], d0);
-                d1 = fmaf(kv[i].w, xi[3], d1);
+                float4 x;
+                asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                             : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(q + (r * kD + (i * kLanes + part) * 4) * 4));
+                d0 = fmaf(kv[i].x, x.x, d0);
+                d1 = fmaf(kv[i].y, x.y, d1);
+                d0 = fmaf(kv[i].z, x.z, d0);
+                d1 = fmaf(kv[i].w, x.w, d1);
             }
             float s = d0 + d1;
 #pragma unroll
@@ -518,6 +524,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     int page = -1, slot = 0, kvh = 0;
     bool inside = false;
     const uint32_t stage0 = smem_u32(smem) + warp * (kStages * 2 * kStepBytes);
+    const char* k_lane = static_cast<const char*>(p.cache.k) + (lane % S::kChunks) * 16;
+    const long long v_minus_k = static_cast<const char*>(p.cache.v) - static_cast<const char*>(p.cache.k);
     auto look_up = [&]() {
         inside = false;
         if (t_ahead < t1) {
@@ -536,21 +544,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     auto issue = [&](int stage) -> uint32_t {
         const bool ok = inside && page >= 0 && page < p.cache.n_pages;
         if (inside && !ok) atomicCAS(p.status, 0, 0x501);
-        const long long off =
-            ok ? page * p.cache.page_stride + slot * p.cache.slot_stride + kvh * p.cache.head_stride : 0;
+        const long long off = ok ? (page * p.cache.page_stride + slot * p.cache.slot_stride + kvh * p.cache.head_stride) *
+                                       static_cast<int>(sizeof(T)) : 0;
         const uint32_t live = __ballot_sync(0xffffffffu, ok);
         if (live != 0) {
-            const uint32_t k = stage0 + stage * (2 * kStepBytes);
+            constexpr int kRowsPer = 32 / S::kChunks > 0 ? 32 / S::kChunks : 1;   // rows an instruction of the warp covers
+            const int row0 = lane / S::kChunks, col = lane % S::kChunks;
+            const uint32_t k = stage0 + stage * (2 * kStepBytes) + row0 * S::kRow;
 #pragma unroll
             for (int i = 0; i < kStepBytes / 512; ++i) {
-                const int id = i * 32 + lane;
-                const int row = id / S::kChunks, col = id % S::kChunks;
-                const long long ro = __shfl_sync(0xffffffffu, off, row);
+                const int row = i * kRowsPer + row0;
+                const char* src = k_lane + __shfl_sync(0xffffffffu, off, row);
                 const bool on = (live >> row) & 1u;
-                const uint32_t dst = k + row * S::kRow + ((col ^ W::swizzle(row)) << 4);
-                const long long e = ro + col * (16 / static_cast<int>(sizeof(T)));
-                cp_async16(dst, static_cast<const T*>(p.cache.k) + e, on);
-                cp_async16(dst + kStepBytes, static_cast<const T*>(p.cache.v) + e, on);
+                const uint32_t dst = k + i * (kRowsPer * S::kRow) + ((col ^ W::swizzle(row)) << 4);
+                cp_async16(dst, src, on);
+                cp_async16(dst + kStepBytes, src + v_minus_k, on);
             }
         }
         cp_commit();
@@ -565,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
 
     const ScoreForm form{p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, p.cap > 0.0f};
-    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * kStepBytes);   // 4 x [rows][kD]
+    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * 2 * kStepBytes);   // 4 x [rows][kD], then the query rows (fp32)
     W w;
     bool fresh = true, first_piece = true;
     int piece_blk = at.blk, stage = 0, rows = 0, head0 = 0;
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
             rows = min(group - ht * W::kRows, W::kRows);
             head0 = kh * group + ht * W::kRows;
-            w.start(p, at.b, head0, rows, lane);
+            w.start(p, buf + 4 * W::kRows * kD, at.b, head0, rows, lane);
             piece_blk = at.blk;
             fresh = false;
         }
@@ -643,12 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     cp_wait<0>();
 }
 
-// Joins the pieces of a unit that several CTAs share: block (c, row), threads (group, feature).
+// Joins the pieces of a unit that several CTAs share: block (c, row). Thread i weighs piece i (there are
+// at most kMaxCtas), then groups of kD / 4 threads sum every kGroups-th piece, 16 bytes a thread.
+constexpr int kJoinThreads = 256;
 template <typename T, int kD>
-__global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
     constexpr int kSlot = slot_floats<kD>();
-    constexpr int kGroups = 256 / kD;
-    __shared__ float sh_m[8], sh_o[kGroups][kD], sh_l[kGroups];
+    constexpr int kCols = kD / 4;
+    constexpr int kGroups = kJoinThreads / kCols;
+    static_assert(kMaxCtas <= kJoinThreads, "one thread a piece");
+    __shared__ float sh_f[kJoinThreads], sh_x[2][kJoinThreads / 32];
+    __shared__ float4 sh_o[kGroups][kCols];
     pdl_trigger();
     pdl_wait();
     const JoinDesc d = reinterpret_cast<const JoinDesc*>(p.partial + static_cast<int64_t>(kMaxCtas) * 2 * kSlot)[blockIdx.x];
@@ -658,40 +671,52 @@ __global__ void __launch_bounds__(256) paged_join_kernel(const __grid_constant__
     const int kh = d.unit / head_tiles, ht = d.unit - kh * head_tiles;
     const int row = blockIdx.y;
     if (row >= min(group - ht * rows_tile, rows_tile)) return;
-    auto slot = [&](int c) { return p.partial + (static_cast<int64_t>(c) * 2 + (c == d.c0 ? d.first_slot : 0)) * kSlot; };
-    float M = -CUDART_INF_F;
-    for (int c = d.c0 + threadIdx.x; c <= d.c1; c += 256) M = fmaxf(M, slot(c)[row]);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int pieces = d.c1 - d.c0 + 1;
+    const float* slots = p.partial + static_cast<int64_t>(d.c0) * 2 * kSlot;   // piece i at 2 i kSlot, piece 0 at first_slot
+    const float* mine = slots + (tid == 0 ? d.first_slot : 2 * tid) * kSlot;
+    const float mi = tid < pieces ? mine[row] : -CUDART_INF_F;
+    const float li = tid < pieces ? mine[kMaxRows + row] : 0.0f;
+    float M = mi;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if ((threadIdx.x & 31) == 0) sh_m[threadIdx.x >> 5] = M;
+    if (lane == 0) sh_x[0][warp] = M;
     __syncthreads();
-    for (int i = 0; i < 8; ++i) M = fmaxf(M, sh_m[i]);
-    const int g = threadIdx.x / kD, x = threadIdx.x % kD;
-    float L = 0.0f, a = 0.0f;
-#pragma unroll 8
-    for (int c = d.c0 + g; c <= d.c1; c += kGroups) {
-        const float* s = slot(c);
-        const float mc = s[row];
-        const float f = mc == -CUDART_INF_F ? 0.0f : ex2_approx(mc - M);
-        L = fmaf(s[kMaxRows + row], f, L);
-        a = fmaf(s[2 * kMaxRows + row * kD + x], f, a);
+#pragma unroll
+    for (int i = 0; i < kJoinThreads / 32; ++i) M = fmaxf(M, sh_x[0][i]);
+    const float f = mi == -CUDART_INF_F ? 0.0f : ex2_approx(mi - M);
+    sh_f[tid] = f;
+    const float sum = warp_add(li * f);
+    if (lane == 0) sh_x[1][warp] = sum;
+    __syncthreads();
+    const int g = tid / kCols, x = tid % kCols;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = g; i < pieces; i += kGroups) {
+        const float* o = slots + (i == 0 ? d.first_slot : 2 * i) * kSlot + 2 * kMaxRows + row * kD;
+        const float4 v = reinterpret_cast<const float4*>(o)[x];
+        const float w = sh_f[i];
+        a.x = fmaf(v.x, w, a.x);
+        a.y = fmaf(v.y, w, a.y);
+        a.z = fmaf(v.z, w, a.z);
+        a.w = fmaf(v.w, w, a.w);
     }
     sh_o[g][x] = a;
-    if (x == 0) sh_l[g] = L;
     __syncthreads();
-    if (g == 0) {
-        for (int i = 1; i < kGroups; ++i) {
-            a += sh_o[i][x];
-            L += sh_l[i];
-        }
-        store_f(static_cast<T*>(p.out) + d.b * p.o_b + (kh * group + ht * rows_tile + row) * p.o_h + x,
-                L > 0.0f ? a / L : (L == 0.0f ? 0.0f : L));
+    if (tid < kD) {
+        float L = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kJoinThreads / 32; ++i) L += sh_x[1][i];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) v += reinterpret_cast<const float*>(sh_o[i])[tid];
+        store_f(static_cast<T*>(p.out) + d.b * p.o_b + (kh * group + ht * rows_tile + row) * p.o_h + tid,
+                L > 0.0f ? v / L : (L == 0.0f ? 0.0f : L));
     }
 }
 
 template <typename W, int kD>
 cudaError_t launch_rows(const PagedAttnParams& p, cudaStream_t s) {
-    constexpr int kSmem = kWarps * kStages * 2 * kStepBytes + 4 * W::kRows * kD * static_cast<int>(sizeof(float));
+    constexpr int kSmem = kWarps * kStages * 2 * kStepBytes + (4 * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
     static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int dev = 0, sms = 0;
@@ -701,13 +726,13 @@ cudaError_t launch_rows(const PagedAttnParams& p, cudaStream_t s) {
     const int ctas = std::min(sms, kMaxCtas);
     if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(ctas), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
     const int rows = std::min(p.h / p.h_kv, W::kRows);
-    return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(ctas, rows), dim3(256), 0, s, p, static_cast<int>(W::kRows));
+    return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(ctas, rows), dim3(kJoinThreads), 0, s, p, static_cast<int>(W::kRows));
 }
 
 template <int kD>
 cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
-    if (bf16) return launch_rows<WarpBf16<kD>, kD>(p, s);
     const int group = p.h / p.h_kv;
+    if (bf16) return group <= 8 ? launch_rows<WarpBf16<kD, 1>, kD>(p, s) : launch_rows<WarpBf16<kD, 2>, kD>(p, s);
     if (group == 1) return launch_rows<WarpF32<kD, 1>, kD>(p, s);
     if (group == 2) return launch_rows<WarpF32<kD, 2>, kD>(p, s);
     if (group <= 4) return launch_rows<WarpF32<kD, 4>, kD>(p, s);
