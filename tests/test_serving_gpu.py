@@ -590,6 +590,20 @@ def test_rmsnorm_strides_and_zero_rows(bnd):
     assert (y8.float() == 0).all() and (sc == 1).all()
 
 
+def test_rmsnorm_e4m3_of_tiny_values(bnd):
+    """Groups below fp32's normal range keep their digits (448 / max would overflow)."""
+    for d, group in ((256, 128), (77, 0)):
+        x = randn(125, 3, d)
+        g = torch.full((d,), 1e-38, device="cuda")
+        groups = 1 if group == 0 else d // group
+        y, sc = torch.empty(3, d, device="cuda", dtype=E4M3), torch.empty(3, groups, device="cuda")
+        bnd.mha_rmsnorm(x, g, 1e-6, y=y, scales=sc)
+        z, ref = norm_ref(x, None, g, 1e-6)
+        v = ref / (ref.view(3, groups, -1).abs().amax(dim=2) / 448).repeat_interleave(d // groups, dim=1)
+        # y itself is rounded to steps of 2^-149, 2^-23 of the largest values here; the scale too: 2^-14 of it
+        R.check(y.float(), v, 2.0 ** -4 * v.abs() + 2.0 ** -10 + 2.0 ** -12 * 448, "tiny")
+
+
 def test_rmsnorm_nan_stays_in_its_row(bnd):
     x = randn(130, 4, 1024, dtype=BF)
     x[1, 5] = float("nan")

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -315,46 +316,80 @@ MHA_PAGED_BAD_PAGE = 0x501
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDED, ROPE_RAMP = range(5)
 
 
-def _want(t, name, dtype, shape, device):
-    """t is a CUDA tensor of this dtype, shape and device (the current one, where the call is enqueued)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+# These calls are made once a layer and token, so what a call costs on the host counts: strides and masks go to
+# the library as packed bytes, the stream is read without making an object of it.
+_pack_strides = struct.Struct("4q").pack        # mha_strides_t is the first three
+_pack_mask = struct.Struct("@2i3P").pack        # mha_span_mask_t
+
+
+def _torch():
+    """torch's entry points used below, looked up once: (current device, current stream handle of a device)."""
+    global _current_device, _raw_stream, _bf16, _f32, _i32, _e4m3
+    import torch
+    torch.cuda.init()
+    _bf16, _f32, _i32, _e4m3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+_current_device = _raw_stream = _bf16 = _f32 = _i32 = _e4m3 = None
 
 
 def _here(t):
-    """t's device, which has to be the current CUDA device: work is enqueued there."""
-    import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    """Index of t's device, which has to be the current CUDA device: work is enqueued there."""
+    if not t.is_cuda:
         raise ValueError(f"tensors must be on the current CUDA device, not on {t.device}")
-    return t.device
+    if _current_device is None:
+        _torch()
+    dev = t.get_device()
+    if dev != _current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, not on {t.device}")
+    return dev
 
 
-def _strided(t, name):
-    """Pointer and strides of a [B, L, H, d] tensor whose last dimension is adjacent."""
-    b, l, h, d = t.stride()
-    if d != 1 and t.shape[3] != 1:
-        raise ValueError(f"the last dimension of {name} must be adjacent (stride {d})")
-    return t.data_ptr(), ctypes.byref(StridesT(b, l, h))
+def _stream_on(dev, stream):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _ints(t, name, shape, device):
+def _code(dtype):
+    if dtype is _bf16:
+        return MHA_BF16
+    if dtype is _f32:
+        return MHA_F32
+    raise TypeError(f"unsupported dtype {dtype}: use torch.bfloat16 or torch.float32")
+
+
+def _want(t, name, dtype, shape, dev):
+    """t is a CUDA tensor of this dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        return
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+
+
+def _strides(t, name):
+    """Packed strides of a [B, L, H, d] tensor whose last dimension is adjacent."""
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be adjacent (stride {st[3]})")
+    return _pack_strides(*st)
+
+
+def _ints(t, name, shape, dev):
     """Pointer of a contiguous int32 tensor, or None."""
-    import torch
     if t is None:
         return None
-    _want(t, name, torch.int32, shape, device)
+    _want(t, name, _i32, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _floats(t, name, n, device):
-    import torch
-    _want(t, name, torch.float32, (n,), device)
+def _floats(t, name):
+    dev = _here(t)
+    _want(t, name, _f32, (t.numel(),), dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -374,100 +409,116 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = ROPE_
 
 def make_rotary(inv_freq, interleaved: bool = False, scale: float = 1.0):
     """Rotary description: inv_freq is a CUDA fp32 tensor of rot_dim / 2 frequencies. Holds a reference to it."""
-    r = RotaryT(_floats(inv_freq, "inv_freq", inv_freq.numel(), _here(inv_freq)), 2 * inv_freq.numel(), int(interleaved),
-                scale)
+    r = RotaryT(_floats(inv_freq, "inv_freq"), 2 * inv_freq.numel(), int(interleaved), scale)
     r._tensors = inv_freq
     r._ref = ctypes.byref(r)
+    r._device = inv_freq.get_device()
     return r
 
 
 def make_paged_cache(k_pages, v_pages, block_table):
     """Cache description: k_pages and v_pages [n_pages, page_size, h_kv, d_k] with the same strides (any order of
     the dimensions in memory but the last), block_table int32 [B, max_pages]. Holds references to the three."""
-    import torch
-    device = _here(k_pages)
+    dev = _here(k_pages)
     n, size, h_kv, d = k_pages.shape
-    _dtype_code(k_pages)
-    _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape, device)
+    _code(k_pages.dtype)
+    _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev)
     if k_pages.stride() != v_pages.stride():
         raise ValueError("k_pages and v_pages must have the same strides")
-    if k_pages.stride(3) != 1:
+    if k_pages.stride(3) != 1 and d != 1:
         raise ValueError("the last dimension of the pages must be adjacent")
-    _want(block_table, "block_table", torch.int32, block_table.shape, device)
+    _want(block_table, "block_table", _i32, block_table.shape, dev)
     if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be [B, max_pages] with adjacent rows")
     c = PagedCacheT(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], n, size, block_table.data_ptr(),
                     block_table.stride(0), block_table.shape[1])
     c._tensors = (k_pages, v_pages, block_table)
     c._ref = ctypes.byref(c)
-    c._batch, c._heads, c._d, c._dtype, c._device = block_table.shape[0], h_kv, d, k_pages.dtype, device
+    c._heads = h_kv
+    c._for = (block_table.shape[0], d, k_pages.dtype, dev)
     return c
 
 
 def make_scores(scale: float = 0.0, cap: float = 0.0, slopes=None):
     """Score description: scale (0: 1 / sqrt(d_k)), tanh cap (0: none), slopes a CUDA fp32 [h] or None."""
-    s = ScoresT(scale, cap, None if slopes is None else _floats(slopes, "slopes", slopes.numel(), _here(slopes)))
+    s = ScoresT(scale, cap, None if slopes is None else _floats(slopes, "slopes"))
     s._tensors = slopes
     s._ref = ctypes.byref(s)
+    s._for = None if slopes is None else (slopes.numel(), slopes.get_device())
     return s
 
 
+class _SpanMask:
+    __slots__ = ("causal", "q_offset", "tensors")
+
+
 def make_span_mask(causal=False, q_offset=0, key_valid_lens=None, prefix_lens=None, doc_spans=None):
-    """Mask description for mha_attention. Holds references to the tensors."""
-    m = SpanMaskT(int(bool(causal)), q_offset, _ptr(key_valid_lens), _ptr(prefix_lens), _ptr(doc_spans))
-    m._tensors = (key_valid_lens, prefix_lens, doc_spans)
+    """Mask description for mha_attention. Holds references to the tensors (CUDA int32)."""
+    m = _SpanMask()
+    m.causal, m.q_offset, m.tensors = (1 if causal else 0), q_offset, (key_valid_lens, prefix_lens, doc_spans)
     return m
 
 
-def _check_scores(scores, h):
+def _scores_ref(scores, h, dev):
     if scores is None:
         return None
-    if scores._tensors is not None and scores._tensors.numel() != h:
-        raise ValueError(f"slopes has {scores._tensors.numel()} entries for {h} heads")
+    if scores._for is not None and scores._for != (h, dev):
+        raise ValueError(f"slopes has {scores._for[0]} entries on cuda:{scores._for[1]}, not {h} on cuda:{dev}")
     return scores._ref
+
+
+def _rotary_ref(rotary, dev):
+    if rotary._device != dev:
+        raise ValueError(f"inv_freq is on cuda:{rotary._device}, not on cuda:{dev}")
+    return rotary._ref
 
 
 def mha_rotary(q, *, rotary, q_out, k=None, k_out=None, positions=None, stream=None):
     """Turn q [B, T, h, d_k] into q_out and k [B, T, h_kv, d_k] into k_out (an output may be its input)."""
-    device = _here(q)
-    B, T, h, d = q.shape
-    _want(q_out, "q_out", q.dtype, q.shape, device)
+    dev = _here(q)
+    dtype, shape = q.dtype, q.shape
+    B, T, h, d = shape
+    _want(q_out, "q_out", dtype, shape, dev)
     kp = ks = kop = kos = None
     h_kv = 0
     if k is not None:
         h_kv = k.shape[2]
-        _want(k, "k", q.dtype, (B, T, h_kv, d), device)
-        _want(k_out, "k_out", q.dtype, k.shape, device)
-        kp, ks = _strided(k, "k")
-        kop, kos = _strided(k_out, "k_out")
-    _check(load().mha_rotary(_dtype_code(q), *_strided(q, "q"), *_strided(q_out, "q_out"), kp, ks, kop, kos, B, T, h,
-                             h_kv, d, _ints(positions, "positions", (B, T), device), rotary._ref, _stream(stream)))
+        _want(k, "k", dtype, (B, T, h_kv, d), dev)
+        _want(k_out, "k_out", dtype, k.shape, dev)
+        kp, ks, kop, kos = k.data_ptr(), _strides(k, "k"), k_out.data_ptr(), _strides(k_out, "k_out")
+    st = (_lib or load()).mha_rotary(
+        _code(dtype), q.data_ptr(), _strides(q, "q"), q_out.data_ptr(), _strides(q_out, "q_out"), kp, ks, kop, kos, B, T, h,
+        h_kv, d, _ints(positions, "positions", (B, T), dev), _rotary_ref(rotary, dev), _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_lens=None, rotary=None, stream=None):
     """Append k, v [B, T, h_kv, d_k] to the cache at positions start[b] + t, turning k (and q into q_out)."""
-    device = _here(k)
-    B, T, h_kv, d = k.shape
-    _want(v, "v", k.dtype, k.shape, device)
-    if (cache._batch, cache._heads, cache._d, cache._dtype, cache._device) != (B, h_kv, d, k.dtype, device):
+    dev = _here(k)
+    dtype, shape = k.dtype, k.shape
+    B, T, h_kv, d = shape
+    _want(v, "v", dtype, shape, dev)
+    if cache._for != (B, d, dtype, dev) or cache._heads != h_kv:
         raise ValueError("the cache's batch, heads, head width, dtype or device differ from k's")
     qp = qs = qop = qos = kop = kos = None
     h = 0
     if q is not None:
         h = q.shape[2]
-        _want(q, "q", k.dtype, (B, T, h, d), device)
-        _want(q_out, "q_out", k.dtype, q.shape, device)
-        qp, qs = _strided(q, "q")
-        qop, qos = _strided(q_out, "q_out")
+        _want(q, "q", dtype, (B, T, h, d), dev)
+        _want(q_out, "q_out", dtype, q.shape, dev)
+        qp, qs, qop, qos = q.data_ptr(), _strides(q, "q"), q_out.data_ptr(), _strides(q_out, "q_out")
     if k_out is not None:
-        _want(k_out, "k_out", k.dtype, k.shape, device)
-        kop, kos = _strided(k_out, "k_out")
+        _want(k_out, "k_out", dtype, shape, dev)
+        kop, kos = k_out.data_ptr(), _strides(k_out, "k_out")
     if start is None:
         raise ValueError("start must be an int32 tensor [B]")
-    _check(load().mha_paged_append(_dtype_code(k), qp, qs, qop, qos, *_strided(k, "k"), kop, kos, *_strided(v, "v"), B, T,
-                                   h, h_kv, d, _ints(start, "start", (B,), device),
-                                   _ints(new_lens, "new_lens", (B,), device), rotary._ref if rotary is not None else None,
-                                   cache._ref, _stream(stream)))
+    st = (_lib or load()).mha_paged_append(
+        _code(dtype), qp, qs, qop, qos, k.data_ptr(), _strides(k, "k"), kop, kos, v.data_ptr(), _strides(v, "v"), B, T, h,
+        h_kv, d, _ints(start, "start", (B,), dev), _ints(new_lens, "new_lens", (B,), dev),
+        None if rotary is None else _rotary_ref(rotary, dev), cache._ref, _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def paged_attention_workspace_size(dt: int, B: int, h: int, h_kv: int, d_k: int) -> int:
@@ -476,85 +527,105 @@ def paged_attention_workspace_size(dt: int, B: int, h: int, h_kv: int, d_k: int)
 
 def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, stream=None):
     """Attention of one new token a sequence, q [B, h, d_k], over the kv_lens[b] cached positions -> out."""
-    device = _here(q)
-    B, h, d = q.shape
-    _want(out, "out", q.dtype, q.shape, device)
-    if (cache._batch, cache._d, cache._dtype, cache._device) != (B, d, q.dtype, device):
+    dev = _here(q)
+    dtype, shape = q.dtype, q.shape
+    B, h, d = shape
+    _want(out, "out", dtype, shape, dev)
+    if cache._for != (B, d, dtype, dev):
         raise ValueError("the cache's batch, head width, dtype or device differ from q's")
-    if workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, not {device}")
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
     if kv_lens is None:
         raise ValueError("kv_lens must be an int32 tensor [B]")
     qb, qh, qd = q.stride()
     ob, oh, od = out.stride()
     if qd != 1 or od != 1:
         raise ValueError("the last dimension of q and out must be adjacent")
-    _check(load().mha_paged_attention(
-        _dtype_code(q), q.data_ptr(), ctypes.byref(StridesT(qb, 0, qh)), out.data_ptr(), ctypes.byref(StridesT(ob, 0, oh)),
-        B, h, cache._heads, d, _ints(kv_lens, "kv_lens", (B,), device), _check_scores(scores, h), cache._ref,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(stream)))
+    st = (_lib or load()).mha_paged_attention(
+        _code(dtype), q.data_ptr(), _pack_strides(qb, 0, qh, 1), out.data_ptr(), _pack_strides(ob, 0, oh, 1), B, h,
+        cache._heads, d, _ints(kv_lens, "kv_lens", (B,), dev), _scores_ref(scores, h, dev), cache._ref,
+        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def mha_document_spans(doc_ids, *, spans, stream=None):
     """spans int32 [B, L, 2] of the documents in doc_ids int32 [B, L] (one run each; < 0 is padding)."""
-    device = _here(doc_ids)
+    dev = _here(doc_ids)
     B, L = doc_ids.shape
-    _check(load().mha_document_spans(_ints(doc_ids, "doc_ids", (B, L), device), B, L,
-                                     _ints(spans, "spans", (B, L, 2), device), _stream(stream)))
+    st = (_lib or load()).mha_document_spans(_ints(doc_ids, "doc_ids", (B, L), dev), B, L,
+                                             _ints(spans, "spans", (B, L, 2), dev), _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def mha_attention(q, k, v, *, out, scores=None, mask=None, stream=None):
     """Attention of q [B, L_q, h, d_k] over k, v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]."""
-    device = _here(q)
-    B, Lq, h, d = q.shape
-    Lk, h_kv = k.shape[1], k.shape[2]
-    _want(k, "k", q.dtype, (B, Lk, h_kv, d), device)
-    _want(v, "v", q.dtype, k.shape, device)
-    _want(out, "out", q.dtype, q.shape, device)
+    dev = _here(q)
+    dtype, shape, k_shape = q.dtype, q.shape, k.shape
+    B, Lq, h, d = shape
+    Lk, h_kv = k_shape[1], k_shape[2]
+    _want(k, "k", dtype, (B, Lk, h_kv, d), dev)
+    _want(v, "v", dtype, k_shape, dev)
+    _want(out, "out", dtype, shape, dev)
     ref = None
     if mask is not None:
-        valid, prefix, spans = mask._tensors
-        _ints(valid, "key_valid_lens", (B,), device)
-        _ints(prefix, "prefix_lens", (B,), device)
-        _ints(spans, "doc_spans", (B, Lq, 2), device)
-        ref = ctypes.byref(mask)
-    _check(load().mha_attention(_dtype_code(q), *_strided(q, "q"), *_strided(k, "k"), *_strided(v, "v"),
-                                *_strided(out, "out"), B, Lq, Lk, h, h_kv, d, _check_scores(scores, h), ref,
-                                _stream(stream)))
+        valid, prefix, spans = mask.tensors
+        ref = _pack_mask(mask.causal, mask.q_offset, _ints(valid, "key_valid_lens", (B,), dev) or 0,
+                         _ints(prefix, "prefix_lens", (B,), dev) or 0, _ints(spans, "doc_spans", (B, Lq, 2), dev) or 0)
+    st = (_lib or load()).mha_attention(
+        _code(dtype), q.data_ptr(), _strides(q, "q"), k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"),
+        out.data_ptr(), _strides(out, "out"), B, Lq, Lk, h, h_kv, d, _scores_ref(scores, h, dev), ref,
+        _stream_on(dev, stream))
+    if st:
+        _check(st)
+
+
+def _rows(t, name, d):
+    """Row stride of a [rows, d] tensor with adjacent rows."""
+    s = t.stride()
+    if s[1] != 1 and d != 1:
+        raise ValueError(f"the rows of {name} must be adjacent")
+    return s[0]
 
 
 def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=None, stream=None):
     """y = gain * z / rms(z), z = x + residual (written to sum_out), rows of length d = x.shape[-1], x [rows, d].
     y has x's dtype, or torch.float8_e4m3fn with scales fp32 [rows, groups] (one group: the row)."""
-    import torch
-    device = _here(x)
-    rows, d = x.shape
+    dev = _here(x)
+    dtype, shape = x.dtype, x.shape
+    rows, d = shape
     group = 0
+    rp = rs = zp = zs = gp = cp = None
     if scales is None:
-        _want(y, "y", x.dtype, x.shape, device)
+        _want(y, "y", dtype, shape, dev)
     else:
-        _want(y, "y", torch.float8_e4m3fn, x.shape, device)
+        _want(y, "y", _e4m3, shape, dev)
         groups = scales.shape[1]
-        _want(scales, "scales", torch.float32, (rows, groups), device)
+        _want(scales, "scales", _f32, (rows, groups), dev)
         if not scales.is_contiguous() or groups < 1 or d % groups != 0:
             raise ValueError("scales must be contiguous [rows, groups] with groups dividing d")
-        group = 0 if groups == 1 else d // groups
-    for name, t in (("residual", residual), ("sum_out", sum_out)):
-        if t is not None:
-            _want(t, name, x.dtype, x.shape, device)
-    if sum_out is not None and residual is None:
-        raise ValueError("sum_out needs a residual")
+        if groups > 1:
+            group = d // groups
+        cp = scales.data_ptr()
+    if residual is not None:
+        _want(residual, "residual", dtype, shape, dev)
+        rp, rs = residual.data_ptr(), _rows(residual, "residual", d)
+    if sum_out is not None:
+        if residual is None:
+            raise ValueError("sum_out needs a residual")
+        _want(sum_out, "sum_out", dtype, shape, dev)
+        zp, zs = sum_out.data_ptr(), _rows(sum_out, "sum_out", d)
     if gain is not None:
-        _want(gain, "gain", x.dtype, (d,), device)
-    for name, t in (("x", x), ("y", y), ("residual", residual), ("sum_out", sum_out)):
-        if t is not None and d > 1 and t.stride(1) != 1:
-            raise ValueError(f"the rows of {name} must be adjacent")
-    if gain is not None and d > 1 and gain.stride(0) != 1:
-        raise ValueError("gain must be contiguous")
-    _check(load().mha_rmsnorm(
-        _dtype_code(x), x.data_ptr(), x.stride(0), _ptr(residual), residual.stride(0) if residual is not None else 0,
-        _ptr(sum_out), sum_out.stride(0) if sum_out is not None else 0, _ptr(gain), eps, rows, d, y.data_ptr(), y.stride(0),
-        _ptr(scales), group, _stream(stream)))
+        _want(gain, "gain", dtype, (d,), dev)
+        if not gain.is_contiguous():
+            raise ValueError("gain must be contiguous")
+        gp = gain.data_ptr()
+    st = (_lib or load()).mha_rmsnorm(
+        _code(dtype), x.data_ptr(), _rows(x, "x", d), rp, rs or 0, zp, zs or 0, gp, eps, rows, d, y.data_ptr(),
+        _rows(y, "y", d), cp, group, _stream_on(dev, stream))
+    if st:
+        _check(st)
 
 
 def mha_selftest_wait_timeout(stream=None):

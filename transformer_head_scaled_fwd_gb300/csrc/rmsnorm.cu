@@ -22,6 +22,182 @@ __device__ __forceinline__ uint8_t to_e4m3(float v) {
     return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
 }
 
+// The scale of a group whose largest value is `top`, and y / scale as two products (a division an element costs
+// more than the rest of the pass). `up` keeps 448 / top finite for groups far below fp32's normal range.
+struct Quant {
+    float scale, up, inv;
+    __device__ __forceinline__ explicit Quant(float top) {
+        up = top < 0x1p-100f ? 0x1p100f : 1.0f;
+        scale = top == 0.0f ? 1.0f : top / kE4M3Max;
+        inv = top == 0.0f ? 1.0f : kE4M3Max / (top * up);
+    }
+    __device__ __forceinline__ float operator()(float y) const { return y * up * inv; }
+};
+
+// 16-byte accesses of kVec elements; the row stays in registers between the passes.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[8]) { unpack(*reinterpret_cast<const uint4*>(p), f); }
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = __bfloat1622float2(h[i]);
+            f[2 * i] = t.x;
+            f[2 * i + 1] = t.y;
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&f)[8]) {
+        uint4 v = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+        *reinterpret_cast<uint4*>(p) = v;
+    }
+};
+template <>
+struct Vec<float> {
+    static constexpr int kN = 4;
+    static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
+        f[0] = __uint_as_float(v.x);
+        f[1] = __uint_as_float(v.y);
+        f[2] = __uint_as_float(v.z);
+        f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ void load(const float* p, float (&f)[4]) { unpack(*reinterpret_cast<const uint4*>(p), f); }
+    static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+
+// Two values to two bytes, low first, nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
+}
+template <int kN>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[kN]) {
+    if constexpr (kN == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16, e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
+    else
+        *reinterpret_cast<uint32_t*>(p) = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+}
+
+// Sum (or maximum) over the kThr threads of a row; one barrier, `part` is not used again by the kernel.
+template <int kThr, bool kMax>
+__device__ __forceinline__ float row_reduce(float v, float* part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(0xffffffffu, v, o);
+        v = kMax ? fmaxf(v, w) : v + w;
+    }
+    if constexpr (kThr > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int i = 1; i < kThr / 32; ++i) v = kMax ? fmaxf(v, part[i]) : v + part[i];
+    }
+    return v;
+}
+
+// kThr threads a row, kC chunks of 16 bytes a thread. Rows of d elements, d a multiple of kVec, everything
+// aligned to 16 bytes (y in e4m3 to kVec). kThr = 32: eight rows a CTA.
+template <typename T, int kThr, int kC, bool kQuant>
+__global__ void __launch_bounds__(kThr < 256 && kThr > 32 ? kThr : 256) rmsnorm_vec_kernel(const __grid_constant__ RmsNormParams p) {
+    using V = Vec<T>;
+    constexpr int kN = V::kN;
+    __shared__ float part[2][32];
+    const int tid = kThr == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const int64_t row = kThr == 32 ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    if (row >= p.rows) return;      // kThr = 32 only: whole warps, and no barrier follows
+    const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
+    const T* r = static_cast<const T*>(p.residual) + row * p.r_stride;
+    const T* gain = static_cast<const T*>(p.gain);
+    uint4 raw[kC], res[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int i = (c * kThr + tid) * kN;
+        raw[c] = i < p.d ? *reinterpret_cast<const uint4*>(x + i) : make_uint4(0, 0, 0, 0);
+        res[c] = p.residual != nullptr && i < p.d ? *reinterpret_cast<const uint4*>(r + i) : make_uint4(0, 0, 0, 0);
+    }
+    float z[kC][kN];
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        float a[kN], b[kN];
+        V::unpack(raw[c], a);
+        V::unpack(res[c], b);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            z[c][e] = a[e] + b[e];
+            ss = fmaf(z[c][e], z[c][e], ss);
+        }
+    }
+    if (p.sum != nullptr) {
+        T* sum = static_cast<T*>(p.sum) + row * p.s_stride;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = (c * kThr + tid) * kN;
+            if (i < p.d) V::store(sum + i, z[c]);
+        }
+    }
+    const float inv = rsqrtf(row_reduce<kThr, false>(ss, part[0]) / p.d + p.eps);
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+        const int i = (c * kThr + tid) * kN;
+        float g[kN];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) g[e] = 1.0f;
+        if (gain != nullptr && i < p.d) V::load(gain + i, g);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) z[c][e] = z[c][e] * inv * g[e];
+    }
+    if constexpr (!kQuant) {
+        T* y = static_cast<T*>(p.y) + row * p.y_stride;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = (c * kThr + tid) * kN;
+            if (i < p.d) V::store(y + i, z[c]);
+        }
+    } else {
+        uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.y_stride;
+        const bool whole = p.group == p.d;
+        float top[kC];
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            top[c] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) top[c] = fmaxf(top[c], fabsf(z[c][e]));
+        }
+        if (whole) {
+#pragma unroll
+            for (int c = 1; c < kC; ++c) top[0] = fmaxf(top[0], top[c]);
+            top[0] = row_reduce<kThr, true>(top[0], part[1]);
+            if (tid == 0) p.scales[row] = Quant(top[0]).scale;
+#pragma unroll
+            for (int c = 1; c < kC; ++c) top[c] = top[0];
+        } else {
+            // a group is p.group / kN neighbouring lanes (4 to 32) of one chunk
+#pragma unroll
+            for (int c = 0; c < kC; ++c) {
+                const int i = (c * kThr + tid) * kN;
+                for (int o = 1; o < p.group / kN; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
+                if (i < p.d && i % p.group == 0) p.scales[row * (p.d / p.group) + i / p.group] = Quant(top[c]).scale;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+            const int i = (c * kThr + tid) * kN;
+            const Quant quant(top[c]);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) z[c][e] = quant(z[c][e]);
+            if (i < p.d) store_e4m3<kN>(y + i, z[c]);
+        }
+    }
+}
+
 // CTA per row, any d and any alignment: the row is read again from cache for each pass.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rmsnorm_any_kernel(const __grid_constant__ RmsNormParams p) {
@@ -73,22 +249,49 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_any_kernel(const __grid_cons
             __syncthreads();
             for (int w = 0; w < kThreads / 32; ++w) top = fmaxf(top, part[w]);
         }
-        const float scale = top == 0.0f ? 1.0f : top / kE4M3Max;
-        if (whole ? threadIdx.x == 0 : lane == 0) p.scales[row * groups + g] = scale;
+        const Quant quant(top);
+        if (whole ? threadIdx.x == 0 : lane == 0) p.scales[row * groups + g] = quant.scale;
         for (int i = i0; i < i1; i += step) {
             const float v = y_of(i);
             if (sum) store_f(sum + i, z_of(i));
-            y[i] = to_e4m3(v / scale);
+            y[i] = to_e4m3(quant(v));
         }
     }
+}
+
+template <typename T, int kThr, int kC>
+cudaError_t launch_vec(const RmsNormParams& p, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>(kThr == 32 ? (p.rows + 7) / 8 : p.rows)), block(kThr == 32 ? 256 : kThr);
+    return p.scales != nullptr ? launch_pdl(rmsnorm_vec_kernel<T, kThr, kC, true>, grid, block, 0, s, p)
+                               : launch_pdl(rmsnorm_vec_kernel<T, kThr, kC, false>, grid, block, 0, s, p);
+}
+
+template <typename T>
+cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
+    constexpr int kN = Vec<T>::kN;
+    auto ok = [&](const void* q, int64_t stride) {
+        return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && (p.rows == 1 || stride % kN == 0);
+    };
+    const bool y_ok = p.scales != nullptr ? reinterpret_cast<uintptr_t>(p.y) % kN == 0 && (p.rows == 1 || p.y_stride % kN == 0)
+                                          : ok(p.y, p.y_stride);
+    if (p.d % kN == 0 && ok(p.x, p.x_stride) && ok(p.residual, p.residual ? p.r_stride : 0) &&
+        ok(p.sum, p.sum ? p.s_stride : 0) && ok(p.gain, 0) && y_ok) {
+        const int chunks = p.d / kN;     // of 16 bytes in a row
+        if (chunks <= 32) return launch_vec<T, 32, 1>(p, s);
+        if (chunks <= 64) return launch_vec<T, 32, 2>(p, s);
+        if (chunks <= 128) return launch_vec<T, 64, 2>(p, s);
+        if (chunks <= 256) return launch_vec<T, 128, 2>(p, s);
+        if (chunks <= 512) return launch_vec<T, 256, 2>(p, s);
+        if (chunks <= 1024) return launch_vec<T, 256, 4>(p, s);
+        if (chunks <= 2048) return launch_vec<T, 256, 8>(p, s);
+    }
+    return launch_pdl(rmsnorm_any_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(kThreads), 0, s, p);
 }
 
 }  // namespace
 
 cudaError_t launch_rmsnorm(const RmsNormParams& p, bool bf16, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(p.rows));
-    return bf16 ? launch_pdl(rmsnorm_any_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, s, p)
-                : launch_pdl(rmsnorm_any_kernel<float>, grid, dim3(kThreads), 0, s, p);
+    return bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
 }
 
 }  // namespace mha
