@@ -361,7 +361,7 @@ mha_status_t mha_rotary_frequencies(float* inv_freq, float* scale, int rot_dim, 
  * Turns queries and keys: q [B, T, h, d_k] -> q_out, and, unless k is NULL, k [B, T, h_kv, d_k] ->
  * k_out. positions: device int32 [B, T] (any value, contiguous) or NULL for 0 .. T-1. An output may
  * be its input with the same strides (in place); otherwise they must not overlap. MHA_F32 or MHA_BF16,
- * any d_k <= 1024. h_kv, the k strides and k_out are ignored if k is NULL. One launch.
+ * any d_k <= 512. h_kv, the k strides and k_out are ignored if k is NULL. One launch.
  */
 mha_status_t mha_rotary(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
                         void* q_out, const mha_strides_t* q_out_strides,

@@ -517,7 +517,8 @@ NORM = [
     # dtype, rows, d, residual, gain
     (BF, 1, 1, False, False), (BF, 3, 7, True, True), (BF, 5, 64, True, False), (BF, 33, 1024, True, True),
     (BF, 2, 1000, False, True), (BF, 9, 4096, True, True), (BF, 4, 8192, True, True), (BF, 3, 20000, True, True),
-    (BF, 3, 16384, False, True), (BF, 1, 65536, True, True), (BF, 300, 520, True, True),
+    (BF, 3, 16384, False, True), (BF, 1, 65536, True, True), (BF, 300, 520, True, True), (BF, 700, 1024, True, True), (BF, 611, 4096, False, True), (BF, 650, 2040, True, False),
+    (BF, 9, 255, True, True), (BF, 4, 2047, True, True), (BF, 3, 4095, True, True), (BF, 2, 8191, True, True),
     (F32, 1, 1, True, True), (F32, 17, 1000, True, True), (F32, 4, 2048, False, False), (F32, 3, 12292, True, True),
     (F32, 2, 4099, True, True),
 ]
@@ -545,7 +546,8 @@ def test_rmsnorm(bnd, dtype, rows, d, res, gain):
 
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,d,group", [(1, 64, 0), (5, 999, 0), (7, 1024, 128), (3, 4096, 64), (2, 160, 32),
-                                          (40, 4096, 0), (3, 8192, 128), (2, 20000, 32), (3, 16384, 0), (2, 30000, 0)])
+                                          (40, 4096, 0), (3, 8192, 128), (2, 20000, 32), (3, 16384, 0), (2, 30000, 0),
+                                          (620, 1024, 32), (615, 4096, 128), (5, 255, 0), (2, 3999, 0), (700, 64, 64)])
 def test_rmsnorm_e4m3(bnd, dtype, rows, d, group):
     """The scale to fp32 rounding; each value within half a step of e4m3 (2^-4 relative; 2^-10 below the
     smallest normal, 2^-6) of y / scale, where y / scale itself is off by the fp32 error of y and the scale."""

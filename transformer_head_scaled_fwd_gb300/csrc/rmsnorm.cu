@@ -18,29 +18,43 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kE4M3Max = 448.0f;
 
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-    return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
+// Two values to two bytes, low first, nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
 }
+__device__ __forceinline__ uint8_t to_e4m3(float v) { return static_cast<uint8_t>(e4m3x2(v, 0.0f)); }
 
-// The scale of a group whose largest value is `top`, and y / scale as two products (a division an element costs
-// more than the rest of the pass). `up` keeps 448 / top finite for groups far below fp32's normal range.
+// The scale of a group whose largest value is `top`, and y / scale as products: divisions an element, or
+// even a group, cost more than the rest of the pass (a group of 128 at d = 4096: 162 us with two divisions a
+// group, see the kernel for the products). `up` keeps the reciprocal inside fp32's normal range.
 struct Quant {
     float scale, up, inv;
     __device__ __forceinline__ explicit Quant(float top) {
-        up = top < 0x1p-100f ? 0x1p100f : 1.0f;
-        scale = top == 0.0f ? 1.0f : top / kE4M3Max;
-        inv = top == 0.0f ? 1.0f : kE4M3Max / (top * up);
+        up = top < 0x1p-100f ? 0x1p100f : top > 0x1p100f ? 0x1p-100f : 1.0f;
+        scale = top == 0.0f ? 1.0f : top * (1.0f / kE4M3Max);
+        inv = top == 0.0f ? 1.0f : kE4M3Max * rcp_approx(top * up);
     }
     __device__ __forceinline__ float operator()(float y) const { return y * up * inv; }
 };
 
-// 16-byte accesses of kVec elements; the row stays in registers between the passes.
+// Accesses of 16 bytes (Vec) or, for rows of odd length or start, of one element (One).
+template <typename T_>
+struct One {
+    using T = T_;
+    using Raw = T_;
+    static constexpr int kN = 1;
+    static __device__ __forceinline__ Raw zero() { return T(0.0f); }
+    static __device__ __forceinline__ void unpack(Raw v, float (&f)[1]) { f[0] = load_f(&v); }
+    static __device__ __forceinline__ void store(T* p, const float (&f)[1]) { store_f(p, f[0]); }
+};
 template <typename T>
 struct Vec;
 template <>
 struct Vec<__nv_bfloat16> {
+    using T = __nv_bfloat16;
+    using Raw = uint4;
     static constexpr int kN = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&f)[8]) { unpack(*reinterpret_cast<const uint4*>(p), f); }
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
     static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) {
         const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
@@ -57,32 +71,32 @@ struct Vec<__nv_bfloat16> {
 };
 template <>
 struct Vec<float> {
+    using T = float;
+    using Raw = uint4;
     static constexpr int kN = 4;
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
     static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[4]) {
         f[0] = __uint_as_float(v.x);
         f[1] = __uint_as_float(v.y);
         f[2] = __uint_as_float(v.z);
         f[3] = __uint_as_float(v.w);
     }
-    static __device__ __forceinline__ void load(const float* p, float (&f)[4]) { unpack(*reinterpret_cast<const uint4*>(p), f); }
     static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
     }
 };
 
-// Two values to two bytes, low first, nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3));
-}
 template <int kN>
 __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[kN]) {
     if constexpr (kN == 8)
         *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16, e4m3x2(f[4], f[5]) | e4m3x2(f[6], f[7]) << 16);
-    else
+    else if constexpr (kN == 4)
         *reinterpret_cast<uint32_t*>(p) = e4m3x2(f[0], f[1]) | e4m3x2(f[2], f[3]) << 16;
+    else
+        *p = to_e4m3(f[0]);
 }
 
-// Sum (or maximum) over the kThr threads of a row; one barrier, `part` is not used again by the kernel.
+// Sum (or maximum) over the kThr threads of a row; one barrier of theirs, `part` is used once.
 template <int kThr, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float* part) {
 #pragma unroll
@@ -91,8 +105,8 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
         v = kMax ? fmaxf(v, w) : v + w;
     }
     if constexpr (kThr > 32) {
-        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-        __syncthreads();
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x % kThr / 32] = v;
+        named_bar_sync(1 + threadIdx.x / kThr, kThr);
         v = part[0];
 #pragma unroll
         for (int i = 1; i < kThr / 32; ++i) v = kMax ? fmaxf(v, part[i]) : v + part[i];
@@ -100,27 +114,33 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
     return v;
 }
 
-// kThr threads a row, kC chunks of 16 bytes a thread. Rows of d elements, d a multiple of kVec, everything
-// aligned to 16 bytes (y in e4m3 to kVec). kThr = 32: eight rows a CTA.
-template <typename T, int kThr, int kC, bool kQuant>
-__global__ void __launch_bounds__(kThr < 256 && kThr > 32 ? kThr : 256) rmsnorm_vec_kernel(const __grid_constant__ RmsNormParams p) {
-    using V = Vec<T>;
+// Rows a CTA takes: as many as fill 256 threads while a row takes 64 or fewer (an SM starts a CTA in about 0.2 us:
+// 32768 rows of 501 took 39 us with a CTA each, 27 us so), else one (two rows of 128 threads end together: 32768 x
+// 4096 without residual took 84 us instead of 78 us).
+__host__ __device__ constexpr int rows_of_cta(int thr) { return thr <= 64 ? kThreads / thr : 1; }
+
+// The row stays in registers between the passes: kThr threads a row, kC accesses a thread. Groups need Vec (a group is up to 32 neighbouring lanes of one access).
+template <typename V, int kThr, int kC, bool kQuant>
+__global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(const __grid_constant__ RmsNormParams p) {
+    using T = typename V::T;
+    using Raw = typename V::Raw;
     constexpr int kN = V::kN;
-    __shared__ float part[2][32];
-    const int tid = kThr == 32 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = kThr == 32 ? static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    constexpr int kRowsCta = rows_of_cta(kThr);
+    __shared__ float part[2][kRowsCta][kThr / 32];
+    const int tid = threadIdx.x % kThr, sub = threadIdx.x / kThr;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsCta + sub;
     pdl_trigger();
     pdl_wait();
-    if (row >= p.rows) return;      // kThr = 32 only: whole warps, and no barrier follows
+    if (row >= p.rows) return;      // all threads of the row: its barriers are its own
     const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
     const T* r = static_cast<const T*>(p.residual) + row * p.r_stride;
     const T* gain = static_cast<const T*>(p.gain);
-    uint4 raw[kC], res[kC];
+    Raw raw[kC], res[kC];
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
         const int i = (c * kThr + tid) * kN;
-        raw[c] = i < p.d ? *reinterpret_cast<const uint4*>(x + i) : make_uint4(0, 0, 0, 0);
-        res[c] = p.residual != nullptr && i < p.d ? *reinterpret_cast<const uint4*>(r + i) : make_uint4(0, 0, 0, 0);
+        raw[c] = i < p.d ? *reinterpret_cast<const Raw*>(x + i) : V::zero();
+        res[c] = p.residual != nullptr && i < p.d ? *reinterpret_cast<const Raw*>(r + i) : V::zero();
     }
     float z[kC][kN];
     float ss = 0.0f;
@@ -143,14 +163,14 @@ __global__ void __launch_bounds__(kThr < 256 && kThr > 32 ? kThr : 256) rmsnorm_
             if (i < p.d) V::store(sum + i, z[c]);
         }
     }
-    const float inv = rsqrtf(row_reduce<kThr, false>(ss, part[0]) / p.d + p.eps);
+    const float inv = rsqrtf(row_reduce<kThr, false>(ss, part[0][sub]) / p.d + p.eps);
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
         const int i = (c * kThr + tid) * kN;
         float g[kN];
 #pragma unroll
         for (int e = 0; e < kN; ++e) g[e] = 1.0f;
-        if (gain != nullptr && i < p.d) V::load(gain + i, g);
+        if (gain != nullptr && i < p.d) V::unpack(*reinterpret_cast<const Raw*>(gain + i), g);
 #pragma unroll
         for (int e = 0; e < kN; ++e) z[c][e] = z[c][e] * inv * g[e];
     }
@@ -174,7 +194,7 @@ __global__ void __launch_bounds__(kThr < 256 && kThr > 32 ? kThr : 256) rmsnorm_
         if (whole) {
 #pragma unroll
             for (int c = 1; c < kC; ++c) top[0] = fmaxf(top[0], top[c]);
-            top[0] = row_reduce<kThr, true>(top[0], part[1]);
+            top[0] = row_reduce<kThr, true>(top[0], part[1][sub]);
             if (tid == 0) p.scales[row] = Quant(top[0]).scale;
 #pragma unroll
             for (int c = 1; c < kC; ++c) top[c] = top[0];
@@ -183,8 +203,11 @@ __global__ void __launch_bounds__(kThr < 256 && kThr > 32 ? kThr : 256) rmsnorm_
 #pragma unroll
             for (int c = 0; c < kC; ++c) {
                 const int i = (c * kThr + tid) * kN;
-                for (int o = 1; o < p.group / kN; o <<= 1) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
-                if (i < p.d && i % p.group == 0) p.scales[row * (p.d / p.group) + i / p.group] = Quant(top[c]).scale;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+                    if (o * kN < p.group) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
+                if (i < p.d && (i & (p.group - 1)) == 0)
+                    p.scales[row * (p.d >> p.group_log2) + (i >> p.group_log2)] = Quant(top[c]).scale;
             }
         }
 #pragma unroll
@@ -259,16 +282,19 @@ __global__ void __launch_bounds__(kThreads) rmsnorm_any_kernel(const __grid_cons
     }
 }
 
-template <typename T, int kThr, int kC>
-cudaError_t launch_vec(const RmsNormParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>(kThr == 32 ? (p.rows + 7) / 8 : p.rows)), block(kThr == 32 ? 256 : kThr);
-    return p.scales != nullptr ? launch_pdl(rmsnorm_vec_kernel<T, kThr, kC, true>, grid, block, 0, s, p)
-                               : launch_pdl(rmsnorm_vec_kernel<T, kThr, kC, false>, grid, block, 0, s, p);
+template <typename V, int kThr, int kC>
+cudaError_t launch_row(const RmsNormParams& p, cudaStream_t s) {
+    constexpr int kRowsCta = rows_of_cta(kThr);
+    const dim3 grid(static_cast<unsigned>((p.rows + kRowsCta - 1) / kRowsCta)), block(kThr * kRowsCta);
+    return p.scales != nullptr ? launch_pdl(rmsnorm_row_kernel<V, kThr, kC, true>, grid, block, 0, s, p)
+                               : launch_pdl(rmsnorm_row_kernel<V, kThr, kC, false>, grid, block, 0, s, p);
 }
 
 template <typename T>
 cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
-    constexpr int kN = Vec<T>::kN;
+    using V = Vec<T>;
+    using O = One<T>;
+    constexpr int kN = V::kN;
     auto ok = [&](const void* q, int64_t stride) {
         return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && (p.rows == 1 || stride % kN == 0);
     };
@@ -276,14 +302,25 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
                                           : ok(p.y, p.y_stride);
     if (p.d % kN == 0 && ok(p.x, p.x_stride) && ok(p.residual, p.residual ? p.r_stride : 0) &&
         ok(p.sum, p.sum ? p.s_stride : 0) && ok(p.gain, 0) && y_ok) {
-        const int chunks = p.d / kN;     // of 16 bytes in a row
-        if (chunks <= 32) return launch_vec<T, 32, 1>(p, s);
-        if (chunks <= 64) return launch_vec<T, 32, 2>(p, s);
-        if (chunks <= 128) return launch_vec<T, 64, 2>(p, s);
-        if (chunks <= 256) return launch_vec<T, 128, 2>(p, s);
-        if (chunks <= 512) return launch_vec<T, 256, 2>(p, s);
-        if (chunks <= 1024) return launch_vec<T, 256, 4>(p, s);
-        if (chunks <= 2048) return launch_vec<T, 256, 8>(p, s);
+        // Four accesses a thread keep enough bytes in flight (without a residual 78 us against 90 us with two, 32768 x
+        // 4096); when there are fewer rows than fill the SMs, twice the threads finish a row sooner (16 x 1024: 6.7
+        // against 8.2 us with the launch).
+        const bool few = p.rows <= 608;
+        const int chunks = p.d / kN;
+        if (chunks <= 32) return launch_row<V, 32, 1>(p, s);
+        if (chunks <= 64) return launch_row<V, 32, 2>(p, s);
+        if (chunks <= 128) return few ? launch_row<V, 64, 2>(p, s) : launch_row<V, 32, 4>(p, s);
+        if (chunks <= 256) return few ? launch_row<V, 128, 2>(p, s) : launch_row<V, 64, 4>(p, s);
+        if (chunks <= 512) return few ? launch_row<V, 256, 2>(p, s) : launch_row<V, 128, 4>(p, s);
+        if (chunks <= 1024) return launch_row<V, 256, 4>(p, s);
+        if (chunks <= 2048) return launch_row<V, 256, 8>(p, s);
+    } else if (p.scales == nullptr || p.group == p.d) {
+        if (p.d <= 256) return launch_row<O, 32, 8>(p, s);
+        if (p.d <= 512) return launch_row<O, 32, 16>(p, s);
+        if (p.d <= 1024) return launch_row<O, 64, 16>(p, s);
+        if (p.d <= 2048) return launch_row<O, 128, 16>(p, s);
+        if (p.d <= 4096) return launch_row<O, 256, 16>(p, s);
+        if (p.d <= 8192) return launch_row<O, 256, 32>(p, s);
     }
     return launch_pdl(rmsnorm_any_kernel<T>, dim3(static_cast<unsigned>(p.rows)), dim3(kThreads), 0, s, p);
 }

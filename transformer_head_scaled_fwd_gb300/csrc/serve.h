@@ -64,6 +64,7 @@ struct RotaryParams {
     float scale;
     int B, T, h, h_kv, d;
     int* status;
+    FastDiv by_t;            // set by the launcher
 };
 cudaError_t launch_rotary(const RotaryParams& p, bool bf16, cudaStream_t s);
 
@@ -109,7 +110,8 @@ struct RmsNormParams {
     float* scales;           // or nullptr: y in the input's type
     int64_t x_stride, r_stride, s_stride, y_stride;
     int64_t rows;
-    int d, group;            // group: elements a scale covers (d: the row)
+    int d, group;            // group: elements a scale covers (d: the row; else 2^group_log2)
+    int group_log2;
     float eps;
 };
 cudaError_t launch_rmsnorm(const RmsNormParams& p, bool bf16, cudaStream_t s);

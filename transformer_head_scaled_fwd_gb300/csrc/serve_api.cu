@@ -107,10 +107,13 @@ mha_status_t check_scores(const mha_scores_t* s, int d_k, float* scale, float* c
     return MHA_OK;
 }
 
+// heads of all tokens that one launch turns or copies (32-bit CTA numbers)
+constexpr int64_t kMostRows = int64_t(1) << 30;
+
 mha_status_t check_bt(int B, int T, int d_k) {
     if (B <= 0 || T <= 0 || d_k <= 0)
         return fail(MHA_ERR_INVALID_ARG, "sizes must be positive (B=%d T=%d d_k=%d)", B, T, d_k);
-    if (d_k > 1024) return fail(MHA_ERR_UNSUPPORTED, "d_k <= 1024 is implemented (d_k = %d)", d_k);
+    if (d_k > 512) return fail(MHA_ERR_UNSUPPORTED, "d_k <= 512 is implemented (d_k = %d)", d_k);
     if (static_cast<int64_t>(B) * T > 0x7fffffffll) return fail(MHA_ERR_UNSUPPORTED, "B * T must stay below 2^31");
     return MHA_OK;
 }
@@ -170,6 +173,8 @@ mha_status_t mha_rotary(mha_dtype_t dt, const void* q, const mha_strides_t* q_st
     if ((st = check_dtype(dt)) != MHA_OK || (st = check_bt(B, T, d_k)) != MHA_OK) return st;
     if (h <= 0 || (k != nullptr && h_kv <= 0))
         return fail(MHA_ERR_INVALID_ARG, "heads must be positive (h=%d h_kv=%d)", h, h_kv);
+    if (static_cast<int64_t>(B) * T * (static_cast<int64_t>(h) + (k != nullptr ? h_kv : 0)) > kMostRows)
+        return fail(MHA_ERR_UNSUPPORTED, "B * T * (h + h_kv) must stay below 2^30");
     if (rotary == nullptr) return fail(MHA_ERR_INVALID_ARG, "rotary must not be NULL");
     if ((st = check_rotary(rotary, d_k)) != MHA_OK) return st;
     mha::RotaryParams p{};
@@ -196,6 +201,8 @@ mha_status_t mha_paged_append(mha_dtype_t dt, const void* q, const mha_strides_t
     if ((st = check_dtype(dt)) != MHA_OK || (st = check_bt(B, T, d_k)) != MHA_OK) return st;
     if (h_kv <= 0 || (q != nullptr && h <= 0))
         return fail(MHA_ERR_INVALID_ARG, "heads must be positive (h=%d h_kv=%d)", h, h_kv);
+    if (static_cast<int64_t>(B) * T * ((q != nullptr ? static_cast<int64_t>(h) : 0) + 2 * static_cast<int64_t>(h_kv)) > kMostRows)
+        return fail(MHA_ERR_UNSUPPORTED, "B * T * (h + 2 h_kv) must stay below 2^30");
     if (start == nullptr) return fail(MHA_ERR_INVALID_ARG, "start must not be NULL");
     if (rotary != nullptr && (st = check_rotary(rotary, d_k)) != MHA_OK) return st;
     mha::RotaryParams p{};
@@ -345,6 +352,7 @@ mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const 
     p.scales = scales;
     p.x_stride = x_stride; p.r_stride = residual_stride; p.s_stride = sum_stride; p.y_stride = y_stride;
     p.rows = rows; p.d = d; p.group = group == 0 ? d : group; p.eps = eps;
+    p.group_log2 = group == 128 ? 7 : group == 64 ? 6 : 5;
     return launched(mha::launch_rmsnorm(p, dt == MHA_BF16, as_stream(stream)), "RMS norm");
 }
 
