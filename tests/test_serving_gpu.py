@@ -261,6 +261,8 @@ PAGED = [
     (BF, 64, 1, 128, 128, "slots", [129], {}),
     (BF, 33, 11, 64, 100, "slots", [201, 99, 100, 0], {}),
     (BF, 7, 7, 128, 16, "slots", [2000, 3], {}),
+    (BF, 8, 2, 64, 16, "slots", [300, 0, 256, 257, 1, 700, 512, 768, 513, 2, 900], {}),      # units of 0 to 4 blocks
+    (BF, 12, 12, 128, 32, "slots", [448, 129, 128, 127] * 20, {}),                              # more units than SMs
     (F32, 4, 4, 64, 16, "slots", [1, 0, 15, 16, 17, 100], {}),
     (F32, 8, 2, 128, 24, "heads", [333, 1, 48], dict(cap=15.0)),
     (F32, 9, 3, 64, 1, "slots", [66, 2], dict(slopes=True)),
@@ -408,6 +410,10 @@ ATT = [
     (2, 640, 640, 5, 5, 64, dict(causal=True, cap=50.0, valid=[640, 320])),
     (1, 100, 40, 2, 2, 64, dict(causal=True)),            # more queries than keys: the last rows see all
     (1, 65, 129, 16, 2, 128, dict(causal=True, q_offset=500)),     # all queries behind all keys
+    (1, 130, 700, 4, 2, 128, dict(causal=True, q_offset=570, cap=10.0, valid=[650])),
+    (2, 600, 600, 2, 1, 128, dict(docs=20, causal=True, cap=30.0)),
+    (1, 600, 600, 2, 1, 64, dict(cap=59.0)),
+    (1, 600, 600, 2, 1, 64, dict(cap=300.0, causal=True)),
 ]
 
 

@@ -27,12 +27,16 @@ constexpr int kHeadGroup = 8;
 
 // How scores become weights:
 //   kPlain   scale > 0, no cap, no bias: running maximum of the raw scores, one multiply-add each
-//   kCapped  a cap of at most kFixedCap, no bias: every score lies in [-cap, cap], so the weights are
+//   kCapped  a cap of at most kFixedCap, no bias, long rows: every score lies in [-cap, cap], so the weights are
 //            exp(s) with no maximum at all (2^+-87 at most, far inside fp32 and bf16): no maximum,
-//            no rescaling, no exchange between the two halves of a row
+//            no rescaling, no exchange between the two halves of a row (4 x 8192, 8 heads of 128: 519 us, kGeneral
+//            683 us). The largest weight is then rounded to bf16 like any other, while under a running maximum it is
+//            exactly 1: rows of a few keys would be off by 1.8e-3 where kGeneral is off by 1.3e-3, so short key ranges
+//            and document spans go there.
 //   kGeneral anything else: scores formed first, then as kPlain
 enum Mode { kPlain, kCapped, kGeneral };
 constexpr float kFixedCap = 60.0f;
+constexpr int kFixedKeys = 512;
 
 // One unit as the scheduler publishes it; n == 0 means no more work.
 struct UnitInfo {
@@ -708,7 +712,7 @@ cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s) {
         !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
         return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
-    const int mode = p.slopes == nullptr && p.cap > 0.0f && p.cap <= kFixedCap ? kCapped
+    const int mode = p.slopes == nullptr && p.spans == nullptr && p.cap > 0.0f && p.cap <= kFixedCap && p.Lk >= kFixedKeys ? kCapped
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
     if (p.d == 64) {

@@ -37,6 +37,7 @@ constexpr int kStages = 3;
 constexpr int kStepBytes = 4096;        // of keys, and of values, in one step of a warp
 constexpr int kMaxCtas = 192;           // slots of the workspace
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kWholeBlocks = 4;
 constexpr float kGrow = 8.0f;           // log2 units the maximum may grow before o and l are rescaled
 
 template <typename T, int kD>
@@ -83,12 +84,14 @@ __device__ __forceinline__ float cap_log2(float x, float top) {
     return fmaf(-2.0f * top, rcp_approx(1.0f + ex2_approx(x * (2.0f * kLog2e))), top);
 }
 
-// A score in log2 units from q.k: capped, minus the distance bias.
+// A score in log2 units from q.k: capped, minus the distance bias. fp32 takes the library's tanh: 2^-22 of a cap of
+// 50 would be an error of 2 10^-5 in a weight, which bf16 weights hide and fp32 ones do not.
 struct ScoreForm {
-    float in, top;     // capped: s = cap_log2(dot * in, top), else dot * in
+    float in, top;     // capped: s = top * tanh(dot * in), else dot * in
     bool capped;
-    __device__ __forceinline__ float operator()(float dot, float slope, float away) const {
-        const float s = capped ? cap_log2(dot * in, top) : dot * in;
+    template <bool kExact>
+    __device__ __forceinline__ float of(float dot, float slope, float away) const {
+        const float s = !capped ? dot * in : kExact ? top * tanhf(dot * in) : cap_log2(dot * in, top);
         return fmaf(-slope, away, s);
     }
 };
@@ -173,7 +176,7 @@ struct WarpBf16 {
                 const float away = static_cast<float>(n - 1 - key0 - i);
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
-                    s[t][nt][e] = ok ? form(s[t][nt][e], slope[nt][e & 1], away) : -CUDART_INF_F;
+                    s[t][nt][e] = ok ? form.of<false>(s[t][nt][e], slope[nt][e & 1], away) : -CUDART_INF_F;
                     more |= s[t][nt][e] > m[nt][e & 1] + kGrow;
                 }
             }
@@ -201,16 +204,22 @@ struct WarpBf16 {
         }
 #pragma unroll
         for (int t = 0; t < kKT; ++t) {
-            uint32_t pt[kNT][2];
+            // A weight goes into the product as two bf16 numbers, its rounding and the rest: the values' own rounding is
+            // then the only one. The second product costs no time (the loads bound the kernel); with one the result
+            // was off by 2.4e-3 where rounding the exact result to bf16 gives 1.7e-3.
+            uint32_t pt[kNT][2], rest[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
                 const float r0 = m[nt][0] == -CUDART_INF_F ? 0.0f : m[nt][0], r1 = m[nt][1] == -CUDART_INF_F ? 0.0f : m[nt][1];
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
                     const float p0 = ex2_approx(s[t][nt][2 * hf] - r0), p1 = ex2_approx(s[t][nt][2 * hf + 1] - r1);
-                    l[nt][0] += p0;      // the sums take the weights before they are rounded to the values' type
+                    l[nt][0] += p0;
                     l[nt][1] += p1;
-                    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[nt][hf]) : "r"(pack_bf16x2(p0, p1)));
+                    const uint32_t hi = pack_bf16x2(p0, p1);
+                    const uint32_t lo = pack_bf16x2(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[nt][hf]) : "r"(hi));
+                    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(rest[nt][hf]) : "r"(lo));
                 }
             }
             const uint32_t row = v + (t * 16 + (mi >> 1) * 8 + r8) * kRow;
@@ -220,7 +229,10 @@ struct WarpBf16 {
                 uint32_t f[4];
                 ldsm4t(f, row + (c0 ^ (i << 5)));
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) mma16816(o[i][nt], f, pt[nt][0], pt[nt][1]);
+                for (int nt = 0; nt < kNT; ++nt) {
+                    mma16816(o[i][nt], f, pt[nt][0], pt[nt][1]);
+                    mma16816(o[i][nt], f, rest[nt][0], rest[nt][1]);
+                }
             }
         }
     }
@@ -334,7 +346,7 @@ struct WarpF32 {
             float s = d0 + d1;
 #pragma unroll
             for (int w = 1; w < kLanes; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            s = ok ? form(s, slopes != nullptr ? slopes[r] * kLog2e : 0.0f, away) : -CUDART_INF_F;
+            s = ok ? form.of<true>(s, slopes != nullptr ? slopes[r] * kLog2e : 0.0f, away) : -CUDART_INF_F;
             float top = s;
 #pragma unroll
             for (int w = kLanes; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
@@ -399,11 +411,15 @@ struct Lens {
     __device__ __forceinline__ int blocks(int n) const { return n / block + (n % block != 0); }
 };
 
+struct Found {
+    long long before;    // blocks before sequence b
+    int b;
+};
+
 struct Shared {
     float m[kWarps][kMaxRows], l[kWarps][kMaxRows], f[kWarps][kMaxRows];
     long long scan[kWarps];
-    long long before;
-    int found_b;
+    Found found[2];
 };
 
 __device__ __forceinline__ long long warp_sum64(long long v) {
@@ -452,14 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     const int c = blockIdx.x;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     if (c >= ctas) {
-        if (threadIdx.x == 0) join[c].c1 = -1, join[c].c0 = 0;
+        if (threadIdx.x == 0 && !p.whole) join[c] = JoinDesc{0, -1, 0, 0, 0};
         return;
     }
     // CTA c takes blocks [c total / ctas, (c + 1) total / ctas); block t belongs to the last CTA that starts at or before it
-    const long long t0 = c * total / ctas, t1 = (c + 1) * total / ctas;
+    long long t0 = c * total / ctas, t1 = (c + 1) * total / ctas;
     auto owner = [&](long long t) { return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1); };
 
-    // ---- the sequence that t0 falls into
+    // ---- the sequences that t0 and t1 fall into (t1 may be the end of the line)
     long long acc = 0;   // blocks (of one unit) before sequence b0
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
@@ -479,22 +495,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             all += sh.scan[w];
         }
         const long long lo = (acc + inc - v) * units, hi = (acc + inc) * units;
-        if (t0 >= lo && t0 < hi) {
-            sh.found_b = b;
-            sh.before = lo;
-        }
+        if (t0 >= lo && t0 < hi) sh.found[0] = Found{lo, b};
+        if (t1 >= lo && t1 < hi) sh.found[1] = Found{lo, b};
         acc += all;
-        if (t0 < acc * units) break;
+        if (t1 < acc * units) break;
     }
     __syncthreads();
-    Cursor at;      // the block that is computed
-    at.b = sh.found_b;
-    at.n = lens.len(at.b);
-    at.nblk = lens.blocks(at.n);
-    const long long rem = t0 - sh.before;
-    at.unit = static_cast<int>(rem / at.nblk);
-    at.blk = static_cast<int>(rem - static_cast<long long>(at.unit) * at.nblk);
-    if (threadIdx.x == 0) {
+    auto cursor_at = [&](long long t, const Found& f) {
+        Cursor x;
+        x.b = f.b;
+        x.n = lens.len(x.b);
+        x.nblk = lens.blocks(x.n);
+        const long long rem = t - f.before;
+        x.unit = static_cast<int>(rem / x.nblk);
+        x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * x.nblk);
+        return x;
+    };
+    Cursor at = cursor_at(t0, sh.found[0]);      // the block that is computed
+    if (p.whole) {
+        // units are not split: a CTA takes those that start in its piece of the line
+        if (t1 < total) {
+            const Cursor e = cursor_at(t1, sh.found[1]);
+            if (e.blk > 0) t1 += e.nblk - e.blk;
+        }
+    } else if (threadIdx.x == 0) {
         JoinDesc d{0, -1, 0, 0, 0};
         const long long u0 = t0 - at.blk;       // first block of the unit
         if (at.blk > 0 && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
@@ -517,6 +541,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             x.nblk = lens.blocks(x.n);
         } while (x.n == 0);
     };
+
+    if (p.whole && at.blk > 0) {
+        t0 += at.nblk - at.blk;
+        at.blk = at.nblk - 1;
+        advance(at);
+    }
 
     // ---- loads: lane i looks up the page of key i of the step one step ahead of its loads
     Cursor ahead = at;
@@ -715,7 +745,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 }
 
 template <typename W, int kD>
-cudaError_t launch_rows(const PagedAttnParams& p, cudaStream_t s) {
+cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     constexpr int kSmem = kWarps * kStages * 2 * kStepBytes + (4 * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
     static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -724,6 +754,16 @@ cudaError_t launch_rows(const PagedAttnParams& p, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(sms, kMaxCtas);
+    // A sequence of kWholeBlocks blocks at most is not worth the second kernel: its CTA takes longer over the unit by
+    // less than the join costs.
+    constexpr int kBlock = Step<typename W::T, kD>::kKeys * kWarps;
+    p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= kWholeBlocks * kBlock;
+    if (p.whole) {
+        const int group = p.h / p.h_kv;
+        const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((group + W::kRows - 1) / W::kRows);
+        return launch_pdl(paged_attn_kernel<W, kD>, dim3(static_cast<unsigned>(std::min<int64_t>(units, ctas))), dim3(kThreads),
+                          kSmem, s, p);
+    }
     if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(ctas), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
     const int rows = std::min(p.h / p.h_kv, W::kRows);
     return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(ctas, rows), dim3(kJoinThreads), 0, s, p, static_cast<int>(W::kRows));

@@ -81,6 +81,7 @@ struct PagedAttnParams {
     int B, h, h_kv, d;
     float* partial;          // workspace
     int* status;
+    int whole;               // set by the launcher: no unit is split
 };
 size_t paged_attn_workspace(bool bf16, int B, int h, int h_kv, int d);
 cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t s);
