@@ -15,11 +15,15 @@ namespace {
 
 constexpr int BM = 128;          // queries of a unit
 constexpr int BN = 128;          // keys of a tile
-constexpr int kThreads = 384;
+constexpr int kParts = 4;        // softmax threads a query row: each takes 32 keys of a tile
+constexpr int kKeys = BN / kParts;
+constexpr int kSoftWarps = 4 * kParts;
+constexpr int kSoft = 32 * kSoftWarps;
+constexpr int kThreads = kSoft + 128;
 constexpr uint32_t kHalf = 128 * 128;        // one 128-row x 64-column bf16 half tile = 16 KB
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;                // + 128 b: score buffers S_0, S_1
-constexpr uint32_t kColP = 256;              // + 64 b + 32 h: weight buffers P_0, P_1 (two halves each)
+constexpr uint32_t kColP = 256;              // + 64 b + 16 h: weight buffers P_0, P_1
 constexpr uint32_t kColO = 384;              // output accumulator, d_k features
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleThreshold = 8.0f;
@@ -63,8 +67,8 @@ struct SmemSpan {
     uint64_t v_full[4], v_empty[4];
     uint64_t v_edge;                         // the tile that holds the valid length has arrived
     uint64_t s_full[2];                      // score buffer b holds S(j) (commit)
-    uint64_t s_free[2];                      // S(j) of buffer b loaded by both halves (256 arrivals)
-    uint64_t p_full[2];                      // P(j) of weight buffer b written by both halves (256 arrivals)
+    uint64_t s_free[2];                      // S(j) of buffer b loaded (one arrival a softmax warp)
+    uint64_t p_full[2];                      // P(j) of weight buffer b written (one arrival a softmax warp)
     uint64_t p_free[2];                      // P.V(j) of weight buffer b done (commit)
     uint64_t unit_full[2];                   // unit slot published by the scheduler
     uint64_t steal_full[2];                  // answer to a request for another unit
@@ -72,7 +76,7 @@ struct SmemSpan {
     UnitInfo unit[2];
     uint32_t tmem_base;
     int abort_flag;
-    float mx[2][2][BM];                      // [tile parity][half][row]: the halves' tile maxima, exchanged
+    float mx[kParts][BM];                    // the parts' tile maxima, exchanged when a row's maximum grows
 };
 template <int kD>
 constexpr size_t smem_bytes() { return Tiles<kD>::kOffBar + sizeof(SmemSpan); }
@@ -182,15 +186,15 @@ constexpr float kTanhRange2 = 0.25f;
 constexpr float kT0 = 0.999999463558197f, kT1 = -0.33326318860054016f, kT2 = 0.13190296292304993f,
                 kT3 = -0.04440222680568695f;
 
-// u[0..63] -> cap log2(e) tanh(u * a), a = scale / cap, 16 scores at a time: the polynomial where all of a
+// u -> cap log2(e) tanh(u * a), a = scale / cap, 16 scores at a time: the polynomial where all of a
 // warp's scores allow it (two instructions and a half a score, packed), else 1 - 2 / (1 + e^2x), which is
 // good to 2^-22 of 1 over the whole range.
-__device__ __forceinline__ void cap_scores(uint32_t (&u)[64], float a, float top) {
+__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], float a, float top) {
     const float2 a2 = make_float2(a, a);
     const float2 c3 = make_float2(kT3 * top, kT3 * top), c2 = make_float2(kT2 * top, kT2 * top),
                  c1 = make_float2(kT1 * top, kT1 * top), c0 = make_float2(kT0 * top, kT0 * top);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kKeys / 16; ++q) {
         float2 x[8], y[8];
         float far = 0.0f;
 #pragma unroll
@@ -219,14 +223,14 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[64], float a, float top
 }
 
 // Scores in log2 units minus slope |i - j|: away = i - (first key of u), slope in log2 units.
-__device__ __forceinline__ void bias_scores(uint32_t (&u)[64], float away, float slope) {
-    const bool below = away >= 63.0f, above = away <= 0.0f;
+__device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, float slope) {
+    const bool below = away >= kKeys - 1.0f, above = away <= 0.0f;
     if (__all_sync(0xffffffffu, below) || __all_sync(0xffffffffu, above)) {   // |away - c| is linear in c
         const float s = __all_sync(0xffffffffu, below) ? slope : -slope;
         float2 b = make_float2(-s * away, fmaf(-s, away, s));
         const float2 step = make_float2(2.0f * s, 2.0f * s);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < kKeys / 2; ++c) {
             const float2 r = fadd2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])),
                                    ffma2(step, make_float2(c, c), b));
             u[2 * c] = __float_as_uint(r.x);
@@ -234,7 +238,7 @@ __device__ __forceinline__ void bias_scores(uint32_t (&u)[64], float away, float
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < 64; ++c)
+        for (int c = 0; c < kKeys; ++c)
             u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c])));
     }
 }
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                                                                 const __grid_constant__ SpanMaps maps) {
     using G = Tiles<kD>;
     constexpr uint32_t kTile = G::kTile;
-    constexpr int kOut = kD / 2;      // output features of a softmax thread
+    constexpr int kOut = kD / kParts;      // output features of a softmax thread
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
     SmemSpan* sm = reinterpret_cast<SmemSpan*>(base + G::kOffBar);
@@ -264,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             mbar_init(&sm->unit_full[i], 1);
             mbar_init(&sm->steal_full[i], 1);
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->s_free[i], 2 * BM);
-            mbar_init(&sm->p_full[i], 2 * BM);
+            mbar_init(&sm->s_free[i], kSoftWarps);
+            mbar_init(&sm->p_full[i], kSoftWarps);
             mbar_init(&sm->p_free[i], 1);
         }
         for (int s = 0; s < 4; ++s) {
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         tma_prefetch_desc(&maps.v);
         tma_prefetch_desc(&maps.out);
     }
-    if (warp == 9) {
+    if (warp == kSoftWarps + 1) {
         tmem_alloc(&sm->tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -293,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
     volatile int* abort_flag = &sm->abort_flag;
     pdl_wait();   // the tensors and the mask parts come from earlier kernels
 
-    if (warp >= 8) {
-        regs_dec<64>();
-        if (warp == 8) {
+    if (warp >= kSoftWarps) {
+        regs_dec<56>();
+        if (warp == kSoftWarps) {
             // ------------------------------------------------ scheduler, Q and K loads
             int u = blockIdx.x;
             uint32_t gk = 0;   // K tiles issued so far
@@ -336,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 }
                 __syncwarp();
             }
-        } else if (warp == 11) {
+        } else if (warp == kSoftWarps + 3) {
             // ------------------------------------------------ V loads
             uint32_t gv = 0, edges = 0;
             for (int k = 0;; ++k) {
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     }
                 }
             }
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == kSoftWarps + 1 && lane == 0) {
             // ------------------------------------------------ score MMAs: S(j) = Q K_j^T
             constexpr uint32_t idesc_s = idesc_bf16(BM, BN, false, false);
             const uint32_t k_addr = smem_u32(base + G::kOffK);
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 for (int j = 0; j < n; ++j, ++gk) {
                     const int s = gk % G::kStagesK;
                     mbar_wait(&sm->k_full[s], (gk / G::kStagesK) & 1, abort_flag, p.status, 0x818);
-                    // buffer gk mod 2 is free once both halves have loaded score tile gk - 2
+                    // buffer gk mod 2 is free once all softmax warps have loaded score tile gk - 2
                     const int sb = gk & 1;
                     if (gk >= 2) mbar_wait(&sm->s_free[sb], ((gk >> 1) - 1) & 1, abort_flag, p.status, 0x819);
                     tc_fence_after();
@@ -403,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     tc_commit(&sm->k_empty[s]);
                 }
             }
-        } else if (warp == 10 && lane == 0) {
+        } else if (warp == kSoftWarps + 2 && lane == 0) {
             // ------------------------------------------------ P.V MMAs: O += P(j) V_j
             constexpr uint32_t idesc_o = idesc_bf16(BM, kD, false, true);
             const uint32_t v_addr = smem_u32(base + G::kOffV);
@@ -433,21 +437,21 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         tc_fence_before();
         __syncwarp();
         named_bar_sync(3, kThreads);
-        if (warp == 9) {
+        if (warp == kSoftWarps + 1) {
             __syncwarp();
             tc_fence_after();
             tmem_dealloc(tmem, kTmemCols);
         }
     } else {
-        regs_inc<216>();
-        // ------------------------------------------------ softmax: thread (h, row), keys 64 h .. 64 h + 63
+        regs_inc<104>();
+        // ------------------------------------------------ softmax: thread (h, row), keys 32 h .. 32 h + 31 of a tile
         const int h = warp >> 2;
-        const int q = warp & 3;   // lane quarter; warps q and q + 4 hold the two halves of the same rows
+        const int q = warp & 3;   // lane quarter; warps q, q + 4, ... hold the parts of the same rows
         const int row = q * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
-        const uint32_t s_tmem = tmem + lane_off + kColS + h * 64;     // + 128 b
-        const uint32_t p_tmem = tmem + lane_off + kColP + h * 32;     // + 64 b
-        const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;   // this half's output features
+        const uint32_t s_tmem = tmem + lane_off + kColS + h * kKeys;          // + 128 b
+        const uint32_t p_tmem = tmem + lane_off + kColP + h * (kKeys / 2);    // + 64 b
+        const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;           // this part's output features
         const float scale_log2 = p.scale * kLog2e;
         const float tanh_in = p.cap > 0.0f ? p.scale / p.cap : 0.0f, tanh_out = p.cap * kLog2e;
         uint32_t g = 0;   // score tiles consumed so far
@@ -458,28 +462,29 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             const int qb = k & 1;
             __syncwarp();
             // every softmax thread takes the same decision (a give-up in one thread stops all)
-            if (!named_bar_and(1, 2 * BM, ok && x.n > 0)) break;
+            if (!named_bar_and(1, kSoft, ok && x.n > 0)) break;
             const int n = x.n, q0 = x.q0, b = x.b, head = x.head;
             const int2 iv = interval_of(p, x.valid, x.seen, span, q0 + row);
             const float slope = kMode == kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
-            float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to both halves
-            float l = 0.0f;            // this half's share of the row sum
+            float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to its parts
+            float l = 0.0f;            // this part's share of the row sum
             for (int j = 0; j < n; ++j, ++g) {
                 const uint32_t sb = g & 1;
                 mbar_wait(&sm->s_full[sb], (g >> 1) & 1, abort_flag, p.status, 0x81e);
                 __syncwarp();
                 tc_fence_after();
-                uint32_t u[64];
-                tmem_ld_x64(s_tmem + sb * 128, u);
+                uint32_t u[kKeys];
+                tmem_ld_x32(s_tmem + sb * 128, u);
                 tc_fence_before();
-                mbar_arrive(&sm->s_free[sb]);
-                const int k0 = (x.j0 + j) * BN + h * 64;   // first key of this half
-                const bool edge = k0 < x.lo_max || k0 + 64 > x.hi_min;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->s_free[sb]);
+                const int k0 = (x.j0 + j) * BN + h * kKeys;   // first key of this part
+                const bool edge = k0 < x.lo_max || k0 + kKeys > x.hi_min;
                 float sc = 1.0f;
                 if constexpr (kMode == kPlain) {
                     if (edge) {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
                     } else {
                         sc = scale_log2;
                     }
@@ -490,43 +495,45 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                         cap_scores(u, tanh_in, tanh_out);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
                     }
                     if (slope != 0.0f) bias_scores(u, static_cast<float>(q0 + row + p.q_offset - k0), slope);
                 }
                 if (edge) {
                     const uint32_t first = iv.x - k0, many = max(iv.y - iv.x, 0);   // keys first .. first + many - 1 of u
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
+                    for (int c = 0; c < kKeys; ++c)
                         if (static_cast<uint32_t>(c) - first >= many) u[c] = __float_as_uint(-CUDART_INF_F);
                 }
                 float alpha = 1.0f;
                 bool grow = false;
                 float mref = 0.0f;
                 if constexpr (kMode != kCapped) {
-                    float a4[4];
+                    float a2[2];
 #pragma unroll
-                    for (int c4 = 0; c4 < 4; ++c4) {
-                        float a = fmax3(__uint_as_float(u[16 * c4]), __uint_as_float(u[16 * c4 + 1]),
-                                        __uint_as_float(u[16 * c4 + 2]));
+                    for (int c2 = 0; c2 < 2; ++c2) {
+                        float a = fmax3(__uint_as_float(u[16 * c2]), __uint_as_float(u[16 * c2 + 1]),
+                                        __uint_as_float(u[16 * c2 + 2]));
 #pragma unroll
                         for (int e = 3; e < 15; e += 2)
-                            a = fmax3(a, __uint_as_float(u[16 * c4 + e]), __uint_as_float(u[16 * c4 + e + 1]));
-                        a4[c4] = fmaxf(a, __uint_as_float(u[16 * c4 + 15]));
+                            a = fmax3(a, __uint_as_float(u[16 * c2 + e]), __uint_as_float(u[16 * c2 + e + 1]));
+                        a2[c2] = fmaxf(a, __uint_as_float(u[16 * c2 + 15]));
                     }
-                    // this half's tile max (log2 units), exchanged with the other half of the row
-                    const float mth = fmaxf(fmax3(a4[0], a4[1], a4[2]), a4[3]) * sc;
-                    sm->mx[sb][h][row] = mth;
-                    named_bar_sync(4 + q, 64);   // warps q and q + 4
-                    const float m_new = fmaxf(m, fmaxf(mth, sm->mx[sb][h ^ 1][row]));
-                    if (m == -CUDART_INF_F) {
-                        m = m_new;   // first keys of the row (-inf while it has none)
-                    } else {
-                        grow = (m_new - m) > kRescaleThreshold;
-                        if (grow) {
-                            alpha = ex2_approx(m - m_new);
+                    // The reference moves only when the tile passes it by 2^8 (or holds the row's first keys); whether any
+                    // row of these 32 does is agreed by a barrier of the four warps, and only then are the parts'
+                    // maxima exchanged.
+                    const float mth = fmaxf(a2[0], a2[1]) * sc;   // this part's tile max (log2 units)
+                    if (named_bar_or(4 + q, 32 * kParts, mth > m + kRescaleThreshold)) {
+                        sm->mx[h][row] = mth;
+                        named_bar_sync(4 + q, 32 * kParts);
+                        float top = mth;
+#pragma unroll
+                        for (int o = 1; o < kParts; ++o) top = fmaxf(top, sm->mx[(h + o) % kParts][row]);
+                        if (top > m + kRescaleThreshold) {
+                            grow = m != -CUDART_INF_F;
+                            alpha = ex2_approx(m - top);   // 0 for the first keys
                             l *= alpha;
-                            m = m_new;
+                            m = top;
                         }
                     }
                     // with no key of the row yet (m = -inf) every weight is exp2(-inf) = 0
@@ -534,22 +541,21 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 }
                 const float2 sc2 = make_float2(sc, sc);
                 const float2 nm2 = make_float2(-mref, -mref);
-                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                 make_float2(0.f, 0.f)};
-                uint32_t pk[32];
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[kKeys / 2];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) {
+                for (int c = 0; c < kKeys / 2; ++c) {
                     float2 e2 = make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
                     if constexpr (kMode == kPlain) e2 = ffma2(e2, sc2, nm2);
                     if constexpr (kMode == kGeneral) e2 = fadd2(e2, nm2);
                     e2.x = ex2_approx(e2.x);
                     e2.y = ex2_approx(e2.y);
-                    acc[c & 3] = fadd2(acc[c & 3], e2);
+                    acc[c & 1] = fadd2(acc[c & 1], e2);
                     // the weights are rounded to bf16 for the product; the sum takes them unrounded
                     pk[c] = pack_bf16x2(e2.x, e2.y);
                 }
-                const float2 s4 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
-                l += s4.x + s4.y;
+                const float2 s2 = fadd2(acc[0], acc[1]);
+                l += s2.x + s2.y;
                 // weight buffer sb is free once P.V(g - 2) has read it
                 if (g >= 2) {
                     mbar_wait(&sm->p_free[sb], ((g >> 1) - 1) & 1, abort_flag, p.status, 0x81f);
@@ -557,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     tc_fence_after();
                 }
                 if (kMode != kCapped && j > 0 && __any_sync(0xffffffffu, grow)) {
-                    // O is rescaled (this half's features) once P.V(g - 1) has completed; at j = 0 the first
+                    // O is rescaled (this part's features) once P.V(g - 1) has completed; at j = 0 the first
                     // P.V overwrites O, after the previous unit's output has been read
                     mbar_wait(&sm->p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, p.status, 0x820);
                     __syncwarp();
@@ -571,36 +577,34 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                         tmem_st_x16(o_tmem + q4 * 16, o);
                     }
                 }
-#pragma unroll
-                for (int q4 = 0; q4 < 2; ++q4)
-                    tmem_st_x16_nowait(p_tmem + sb * 64 + q4 * 16,
-                                       *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q4]));
+                tmem_st_x16_nowait(p_tmem + sb * 64, pk);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&sm->p_full[sb]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->p_full[sb]);
             }
             // The next unit's slot and spans are read now: their latency passes behind the output.
             const int nb = (k + 1) & 1;
             ok = mbar_wait(&sm->unit_full[nb], ((k + 1) >> 1) & 1, abort_flag, p.status, 0x821);
             x = sm->unit[nb];
             if (ok && x.n > 0) span = span_of(p, x.b, x.q0 + row);
-            // ---------------- output: thread (h, row) writes its features of O / (l_0 + l_1). The unit's Q
+            // ---------------- output: thread (h, row) writes its features of O / (l_0 + ... + l_3). The unit's Q
             // buffer is idle (its last score MMA completed before this thread's last wait on S): it carries
-            // l_h of every half and row, then the bf16 output tile.
+            // l_h of every part and row, then the bf16 output tile.
             uint8_t* qbuf = base + qb * kTile;
             float* lsum = reinterpret_cast<float*>(qbuf);
             lsum[h * BM + row] = l;
-            named_bar_sync(1, 2 * BM);   // both halves' sums are in shared memory
-            const float L = lsum[row] + lsum[BM + row];
+            named_bar_sync(1, kSoft);   // all parts' sums are in shared memory
+            const float L = (lsum[row] + lsum[BM + row]) + (lsum[2 * BM + row] + lsum[3 * BM + row]);
             const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
             const uint32_t gl = g - 1;   // the unit's last tile: its P.V completes O
             mbar_wait(&sm->p_free[gl & 1], (gl >> 1) & 1, abort_flag, p.status, 0x822);
             __syncwarp();
             tc_fence_after();
             uint32_t o[kOut];
-            if constexpr (kOut == 64) tmem_ld_x64(o_tmem, o);
-            else tmem_ld_x32(o_tmem, o);
-            named_bar_sync(1, 2 * BM);   // every thread has read the sums the staging overwrites
+            if constexpr (kOut == 32) tmem_ld_x32(o_tmem, o);
+            else tmem_ld_x16(o_tmem, o);
+            named_bar_sync(1, kSoft);   // every thread has read the sums the staging overwrites
 #pragma unroll
             for (int ch = 0; ch < kOut / 8; ++ch) {
                 const int col = h * kOut + 8 * ch;   // feature: slab col / 64, 16-byte chunk (col % 64) / 8
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             }
             fence_proxy_async_smem();
             tc_fence_before();   // O has been read: the next unit's first P.V may overwrite it
-            named_bar_sync(1, 2 * BM);
+            named_bar_sync(1, kSoft);
             if (warp == 0 && lane == 0) {
                 if (!*abort_flag) {
                     asm volatile(

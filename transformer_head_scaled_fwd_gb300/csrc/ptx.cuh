@@ -178,6 +178,20 @@ __device__ __forceinline__ bool named_bar_and(int id, int nthreads, bool pred) {
     return r != 0;
 }
 
+// The same with OR.
+__device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(pred)), "r"(id), "r"(nthreads)
+        : "memory");
+    return r != 0;
+}
+
 // Per-warpgroup register budget changes (all four warps of a warpgroup execute these).
 template <int N>
 __device__ __forceinline__ void regs_inc() {
