@@ -413,6 +413,9 @@ ATT = [
     (1, 130, 700, 4, 2, 128, dict(causal=True, q_offset=570, cap=10.0, valid=[650])),
     (2, 600, 600, 2, 1, 128, dict(docs=20, causal=True, cap=30.0)),
     (1, 600, 600, 2, 1, 64, dict(cap=59.0)),
+    (2, 700, 700, 3, 3, 64, dict(docs=60, pad=300)),                # whole query tiles without a key
+    (60, 300, 300, 8, 4, 64, dict(valid=[0, 300, 0, 0] * 15, causal=True)),     # many units without a key
+    (3, 128, 4000, 2, 2, 64, dict(causal=True, q_offset=100, valid=[4000, 77, 0])),
     (1, 600, 600, 2, 1, 64, dict(cap=300.0, causal=True)),
 ]
 

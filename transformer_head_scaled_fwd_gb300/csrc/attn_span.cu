@@ -1,46 +1,39 @@
-// attn_span.cu -- attention with grouped heads over strided tensors, capped and biased scores,
-// and masks that leave each query one interval of keys (document spans, prefix, causal, valid
-// length: their intersection is an interval [lo, hi)). An empty interval gives a row of zeros.
+// attn_span.cu -- attention under span masks; document spans.
+//
+// Grouped heads over strided tensors, capped and biased scores, and masks that leave each query one
+// interval of keys (document spans, prefix, causal, valid length: their intersection is an interval
+// [lo, hi)), so a tile is either inside every row's interval, and not masked at all, or needs two comparisons a
+// score. An empty interval gives a row of zeros.
+//
+//   m, l, O: running maximum (log2 units), sum and output of a row over the key tiles seen so far; a tile's weights
+//   are exp2(s - m), O and l are rescaled when m grows by more than 8 (exact: the final O / l uses the same m).
+//
+// Tensor- and issue-bound: 4 d_k flop a (query, key) pair on tcgen05, one exponential and about seven instructions a
+// score on the softmax warps. Unit of work: 128 query rows of one head. Warps: 16 softmax warps, four threads a row
+// (with two, 4 x 8192 causal took 389 us instead of 361 us: eight warps do not cover their own latencies), and four
+// that schedule and load Q and K, issue score MMAs, issue P.V MMAs, and load V. Scores and weights are double-buffered
+// in tensor memory, so the score MMAs of tile j + 1 run during the softmax of tile j, and the next unit's loads and
+// first scores run during this unit's output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
+// softmax warps rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
+// Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408 us.
 #include <algorithm>
 
-#include <math_constants.h>
-
+#include "attn_span.cuh"
 #include "launch.h"
-#include "mha_internal.h"
-#include "ptx.cuh"
-#include "serve.h"
 
 namespace mha {
 namespace {
 
 constexpr int BM = 128;          // queries of a unit
-constexpr int BN = 128;          // keys of a tile
 constexpr int kParts = 4;        // softmax threads a query row: each takes 32 keys of a tile
 constexpr int kKeys = BN / kParts;
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoft = 32 * kSoftWarps;
 constexpr int kThreads = kSoft + 128;
-constexpr uint32_t kHalf = 128 * 128;        // one 128-row x 64-column bf16 half tile = 16 KB
-constexpr uint32_t kTmemCols = 512;
+constexpr int kLongKeys = 2048;  // d_k = 64, plain scores, no spans: from here on the kernel of two query tiles a unit
 constexpr uint32_t kColS = 0;                // + 128 b: score buffers S_0, S_1
 constexpr uint32_t kColP = 256;              // + 64 b + 16 h: weight buffers P_0, P_1
 constexpr uint32_t kColO = 384;              // output accumulator, d_k features
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleThreshold = 8.0f;
-constexpr int kHeadGroup = 8;
-
-// How scores become weights:
-//   kPlain   scale > 0, no cap, no bias: running maximum of the raw scores, one multiply-add each
-//   kCapped  a cap of at most kFixedCap, no bias, long rows: every score lies in [-cap, cap], so the weights are
-//            exp(s) with no maximum at all (2^+-87 at most, far inside fp32 and bf16): no maximum,
-//            no rescaling, no exchange between the two halves of a row (4 x 8192, 8 heads of 128: 519 us, kGeneral
-//            683 us). The largest weight is then rounded to bf16 like any other, while under a running maximum it is
-//            exactly 1: rows of a few keys would be off by 1.8e-3 where kGeneral is off by 1.3e-3, so short key ranges
-//            and document spans go there.
-//   kGeneral anything else: scores formed first, then as kPlain
-enum Mode { kPlain, kCapped, kGeneral };
-constexpr float kFixedCap = 60.0f;
-constexpr int kFixedKeys = 512;
 
 // One unit as the scheduler publishes it; n == 0 means no more work.
 struct UnitInfo {
@@ -80,58 +73,6 @@ struct SmemSpan {
 };
 template <int kD>
 constexpr size_t smem_bytes() { return Tiles<kD>::kOffBar + sizeof(SmemSpan); }
-
-struct SpanMaps {
-    CUtensorMap q, k, v, out;   // {64, L, d_k / 64, heads, B}, box {64, 128, d_k / 64, 1, 1}
-};
-// Coordinates of a (head, sequence) in a map: a broadcast dimension (stride 0) has one entry there.
-__device__ __forceinline__ int at_h(const Strided& t, int head) { return t.h != 0 ? head : 0; }
-__device__ __forceinline__ int at_b(const Strided& t, int b) { return t.b != 0 ? b : 0; }
-
-__device__ __forceinline__ void tma_load_5d(const CUtensorMap* m, uint64_t* bar, void* dst, int c1, int c3, int c4) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c3), "r"(c4)
-        : "memory");
-}
-
-// Work stealing: the grid has one CTA a unit; a running CTA asks the hardware to cancel the launch of
-// one that has not started and does its unit instead (its set-up is paid once, and no counter in
-// memory is needed). After a refusal no further request is made.
-__device__ __forceinline__ void steal_request(void* answer, uint64_t* bar) {
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile(
-        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-            smem_u32(answer)),
-        "r"(smem_u32(bar))
-        : "memory");
-}
-// blockIdx.x of the cancelled CTA, or -1
-__device__ __forceinline__ int steal_answer(const void* answer) {
-    int x;
-    asm volatile(
-        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 x, y, z, w;\n\t"
-        "ld.shared.b128 r, [%1];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-        "mov.b32 x, -1;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {x, y, z, w}, r;\n\t"
-        "mov.b32 %0, x;\n\t}"
-        : "=r"(x)
-        : "r"(smem_u32(answer))
-        : "memory");
-    return x;
-}
-
-// Keys [x, y) of query i: the unit's valid length and prefix, its own span.
-__device__ __forceinline__ int2 interval_of(const SpanAttnParams& p, int valid, int seen, int2 span, int i) {
-    const int hi = p.causal ? min(valid, max(i + p.q_offset + 1, seen)) : valid;
-    return make_int2(max(span.x, 0), min(span.y, hi));
-}
-__device__ __forceinline__ int2 span_of(const SpanAttnParams& p, int b, int i) {
-    if (p.spans == nullptr || i >= p.Lq) return make_int2(0, p.Lk);
-    return reinterpret_cast<const int2*>(p.spans)[static_cast<int64_t>(b) * p.Lq + i];
-}
 
 // Unit u of the schedule (a whole warp): groups of kHeadGroup (batch, head) pairs, whose keys and values
 // stay in L2, inside a group the query tiles from the last (longest under a causal mask) to the first.
@@ -180,69 +121,6 @@ __device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int 
     return x;
 }
 
-// tanh(x) = x P(x^2) for |x| <= 1/2: minimax polynomial of degree 3 in x^2 (Remez exchange on the
-// relative error; 2^-21.8 of 1 in fp32 arithmetic).
-constexpr float kTanhRange2 = 0.25f;
-constexpr float kT0 = 0.999999463558197f, kT1 = -0.33326318860054016f, kT2 = 0.13190296292304993f,
-                kT3 = -0.04440222680568695f;
-
-// u -> cap log2(e) tanh(u * a), a = scale / cap, 16 scores at a time: the polynomial where all of a
-// warp's scores allow it (two instructions and a half a score, packed), else 1 - 2 / (1 + e^2x), which is
-// good to 2^-22 of 1 over the whole range.
-__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], float a, float top) {
-    const float2 a2 = make_float2(a, a);
-    const float2 c3 = make_float2(kT3 * top, kT3 * top), c2 = make_float2(kT2 * top, kT2 * top),
-                 c1 = make_float2(kT1 * top, kT1 * top), c0 = make_float2(kT0 * top, kT0 * top);
-#pragma unroll
-    for (int q = 0; q < kKeys / 16; ++q) {
-        float2 x[8], y[8];
-        float far = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = 16 * q + 2 * e;
-            x[e] = fmul2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), a2);
-            y[e] = fmul2(x[e], x[e]);
-            far = fmax3(far, y[e].x, y[e].y);
-        }
-        if (!__any_sync(0xffffffffu, far > kTanhRange2)) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 r = fmul2(ffma2(ffma2(ffma2(c3, y[e], c2), y[e], c1), y[e], c0), x[e]);
-                u[16 * q + 2 * e] = __float_as_uint(r.x);
-                u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float v = (e & 1) ? x[e >> 1].y : x[e >> 1].x;
-                const float r = rcp_approx(1.0f + ex2_approx(v * (2.0f * kLog2e)));
-                u[16 * q + e] = __float_as_uint(fmaf(-2.0f * top, r, top));
-            }
-        }
-    }
-}
-
-// Scores in log2 units minus slope |i - j|: away = i - (first key of u), slope in log2 units.
-__device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, float slope) {
-    const bool below = away >= kKeys - 1.0f, above = away <= 0.0f;
-    if (__all_sync(0xffffffffu, below) || __all_sync(0xffffffffu, above)) {   // |away - c| is linear in c
-        const float s = __all_sync(0xffffffffu, below) ? slope : -slope;
-        float2 b = make_float2(-s * away, fmaf(-s, away, s));
-        const float2 step = make_float2(2.0f * s, 2.0f * s);
-#pragma unroll
-        for (int c = 0; c < kKeys / 2; ++c) {
-            const float2 r = fadd2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])),
-                                   ffma2(step, make_float2(c, c), b));
-            u[2 * c] = __float_as_uint(r.x);
-            u[2 * c + 1] = __float_as_uint(r.y);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-            u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c])));
-    }
-}
-
 template <int kD, int kMode>
 __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_constant__ SpanAttnParams p,
                                                                 const __grid_constant__ SpanMaps maps) {
@@ -272,9 +150,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             mbar_init(&sm->p_full[i], kSoftWarps);
             mbar_init(&sm->p_free[i], 1);
         }
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < G::kStagesK; ++s) {
             mbar_init(&sm->k_full[s], 1);
             mbar_init(&sm->k_empty[s], 1);
+        }
+        for (int s = 0; s < G::kStagesV; ++s) {
             mbar_init(&sm->v_full[s], 1);
             mbar_init(&sm->v_empty[s], 1);
         }
@@ -453,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         const uint32_t p_tmem = tmem + lane_off + kColP + h * (kKeys / 2);    // + 64 b
         const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;           // this part's output features
         const float scale_log2 = p.scale * kLog2e;
-        const float tanh_in = p.cap > 0.0f ? p.scale / p.cap : 0.0f, tanh_out = p.cap * kLog2e;
+        const TanhForm capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
         uint32_t g = 0;   // score tiles consumed so far
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x81d);
         UnitInfo x = sm->unit[0];
@@ -489,10 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                         sc = scale_log2;
                     }
                 } else if constexpr (kMode == kCapped) {
-                    cap_scores(u, tanh_in, tanh_out);
+                    cap_scores(u, capped);
                 } else {
                     if (p.cap > 0.0f) {
-                        cap_scores(u, tanh_in, tanh_out);
+                        cap_scores(u, capped);
                     } else {
 #pragma unroll
                         for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
@@ -694,12 +574,19 @@ cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spa
 }
 
 template <int kD, int kMode>
-static cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, unsigned grid, cudaStream_t s) {
+static cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
     static_assert(smem_bytes<kD>() <= 232448, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(span_attn_kernel<kD, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem_bytes<kD>()));
     if (e != cudaSuccess) return e;
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
     return launch_pdl(span_attn_kernel<kD, kMode>, dim3(grid), dim3(kThreads), smem_bytes<kD>(), s, p, maps);
+}
+template <int kD>
+static cudaError_t launch_d(const SpanAttnParams& p, const SpanMaps& maps, int mode, cudaStream_t s) {
+    return mode == kPlain    ? launch_mode<kD, kPlain>(p, maps, s)
+           : mode == kCapped ? launch_mode<kD, kCapped>(p, maps, s)
+                             : launch_mode<kD, kGeneral>(p, maps, s);
 }
 
 // [B, L, H, d] as {64, L, d / 64, H, B}: a 64-column slab of 128 rows is one swizzled half tile
@@ -715,18 +602,12 @@ cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s) {
     if (!map_strided(&maps.q, p.q, p.B, p.Lq, p.h, p.d) || !map_strided(&maps.k, p.k, p.B, p.Lk, p.h_kv, p.d) ||
         !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
         return cudaErrorInvalidValue;
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
     const int mode = p.slopes == nullptr && p.spans == nullptr && p.cap > 0.0f && p.cap <= kFixedCap && p.Lk >= kFixedKeys ? kCapped
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
-    if (p.d == 64) {
-        if (mode == kPlain) return launch_mode<64, kPlain>(p, maps, grid, s);
-        if (mode == kCapped) return launch_mode<64, kCapped>(p, maps, grid, s);
-        return launch_mode<64, kGeneral>(p, maps, grid, s);
-    }
-    if (mode == kPlain) return launch_mode<128, kPlain>(p, maps, grid, s);
-    if (mode == kCapped) return launch_mode<128, kCapped>(p, maps, grid, s);
-    return launch_mode<128, kGeneral>(p, maps, grid, s);
+    if (p.d == 128) return launch_d<128>(p, maps, mode, s);
+    if (mode == kPlain && p.spans == nullptr && p.Lk >= kLongKeys) return launch_span_attn_d64(p, maps, s);
+    return launch_d<64>(p, maps, mode, s);
 }
 
 }  // namespace mha

@@ -1,0 +1,173 @@
+// attn_span.cuh -- what the two kernels of attention under span masks share: modes of the scores, row
+// intervals, work stealing, capped and biased scores.
+#pragma once
+
+#include <math_constants.h>
+
+#include "mha_internal.h"
+#include "ptx.cuh"
+#include "serve.h"
+
+namespace mha {
+
+struct SpanMaps {
+    CUtensorMap q, k, v, out;   // {64, L, d_k / 64, heads, B}, box {64, 128, d_k / 64, 1, 1}
+};
+namespace {
+
+constexpr int BN = 128;          // keys of a tile
+constexpr uint32_t kHalf = 128 * 128;        // one 128-row x 64-column bf16 half tile = 16 KB
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleThreshold = 8.0f;    // log2 units that a row's maximum may grow before O and l are rescaled
+constexpr int kHeadGroup = 8;                // (batch, head) pairs whose units run together
+
+// How scores become weights:
+//   kPlain   scale > 0, no cap, no bias: running maximum of the raw scores, one multiply-add each
+//   kCapped  a cap of at most kFixedCap, no bias, long rows: every score lies in [-cap, cap], so the weights are
+//            exp(s) with no maximum at all (2^+-87 at most, far inside fp32 and bf16): no maximum,
+//            no rescaling, no exchange between the threads of a row (4 x 8192, 8 heads of 128: 408 us, kGeneral
+//            524 us). The largest weight is then rounded to bf16 like any other, while under a running maximum it is
+//            exactly 1: rows of a few keys would be off by 1.8e-3 where kGeneral is off by 1.3e-3, so short key ranges
+//            and document spans go there.
+//   kGeneral anything else: scores formed first, then as kPlain
+enum Mode { kPlain, kCapped, kGeneral };
+constexpr float kFixedCap = 60.0f;
+constexpr int kFixedKeys = 512;
+
+// Coordinates of a (head, sequence) in a map: a broadcast dimension (stride 0) has one entry there.
+__device__ __forceinline__ int at_h(const Strided& t, int head) { return t.h != 0 ? head : 0; }
+__device__ __forceinline__ int at_b(const Strided& t, int b) { return t.b != 0 ? b : 0; }
+
+__device__ __forceinline__ void tma_load_5d(const CUtensorMap* m, uint64_t* bar, void* dst, int c1, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(0), "r"(c1), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// Work stealing: the grid has one CTA a unit; a running CTA asks the hardware to cancel the launch of
+// one that has not started and does its unit instead (its set-up is paid once, and no counter in
+// memory is needed). After a refusal no further request is made.
+__device__ __forceinline__ void steal_request(void* answer, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// blockIdx.x of the cancelled CTA, or -1
+__device__ __forceinline__ int steal_answer(const void* answer) {
+    int x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 x, y, z, w;\n\t"
+        "ld.shared.b128 r, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "mov.b32 x, -1;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {x, y, z, w}, r;\n\t"
+        "mov.b32 %0, x;\n\t}"
+        : "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return x;
+}
+
+// Keys [x, y) of query i: the unit's valid length and prefix, its own span.
+__device__ __forceinline__ int2 interval_of(const SpanAttnParams& p, int valid, int seen, int2 span, int i) {
+    const int hi = p.causal ? min(valid, max(i + p.q_offset + 1, seen)) : valid;
+    return make_int2(max(span.x, 0), min(span.y, hi));
+}
+__device__ __forceinline__ int2 span_of(const SpanAttnParams& p, int b, int i) {
+    if (p.spans == nullptr || i >= p.Lq) return make_int2(0, p.Lk);
+    return reinterpret_cast<const int2*>(p.spans)[static_cast<int64_t>(b) * p.Lq + i];
+}
+
+// u -> cap log2(e) tanh(u a), a = scale / cap. tanh(x) = x P(x^2) with minimax P (Remez exchange on the relative
+// error): degree 2 for |x| <= 0.3, degree 4 for |x| <= 0.7, both within 2^-21.4 of 1 in fp32 arithmetic; beyond, 1 -
+// 2 / (1 + e^2x), within 2^-22 of 1 anywhere. Powers of a are folded into the coefficients, so a score costs two and
+// a half instructions (packed) in the first range. Which range is decided for 16 scores of a warp at a time.
+struct TanhForm {
+    float a, top;
+    float near, mid;      // bounds of u^2; below 0 where powers of a would leave fp32's range
+    __device__ __forceinline__ TanhForm(float a_, float top_) : a(a_), top(top_) {
+        const bool safe = fabsf(a) >= 0x1p-13f && fabsf(a) <= 0x1p13f;
+        near = safe ? 0.09f / (a * a) : -1.0f;
+        mid = safe ? 0.49f / (a * a) : -1.0f;
+    }
+};
+
+template <int kKeys>
+__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm& f) {
+    const float t1 = f.a * f.top, a2 = f.a * f.a;
+    const float n0 = 0.9999988675117493f * t1, n1 = -0.33310022950172424f * a2 * t1, n2 = 0.12633946537971497f * a2 * a2 * t1;
+    const float2 d0 = make_float2(n0, n0), d1 = make_float2(n1, n1), d2 = make_float2(n2, n2);
+#pragma unroll
+    for (int q = 0; q < kKeys / 16; ++q) {
+        float2 y[8];
+        float far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 x = make_float2(__uint_as_float(u[16 * q + 2 * e]), __uint_as_float(u[16 * q + 2 * e + 1]));
+            y[e] = fmul2(x, x);
+            far = fmax3(far, y[e].x, y[e].y);
+        }
+        if (!__any_sync(0xffffffffu, far > f.near)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 x = make_float2(__uint_as_float(u[16 * q + 2 * e]), __uint_as_float(u[16 * q + 2 * e + 1]));
+                const float2 r = fmul2(ffma2(ffma2(d2, y[e], d1), y[e], d0), x);
+                u[16 * q + 2 * e] = __float_as_uint(r.x);
+                u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
+            }
+        } else if (!__any_sync(0xffffffffu, far > f.mid)) {
+            const float m0 = 0.9999997019767761f * t1, m1 = -0.3333021402359009f * a2 * t1, m2 = 0.13281112909317017f * a2 * a2 * t1,
+                        m3 = -0.0508362352848053f * a2 * a2 * (a2 * t1), m4 = 0.01377371046692133f * a2 * a2 * (a2 * a2 * t1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 x = make_float2(__uint_as_float(u[16 * q + 2 * e]), __uint_as_float(u[16 * q + 2 * e + 1]));
+                float2 r = ffma2(make_float2(m4, m4), y[e], make_float2(m3, m3));
+                r = ffma2(r, y[e], make_float2(m2, m2));
+                r = ffma2(r, y[e], make_float2(m1, m1));
+                r = fmul2(ffma2(r, y[e], make_float2(m0, m0)), x);
+                u[16 * q + 2 * e] = __float_as_uint(r.x);
+                u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float r = rcp_approx(1.0f + ex2_approx(__uint_as_float(u[16 * q + e]) * (f.a * 2.0f * kLog2e)));
+                u[16 * q + e] = __float_as_uint(fmaf(-2.0f * f.top, r, f.top));
+            }
+        }
+    }
+}
+
+// Scores in log2 units minus slope |i - j|: away = i - (first key of u), slope in log2 units.
+template <int kKeys>
+__device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, float slope) {
+    const bool below = away >= kKeys - 1.0f, above = away <= 0.0f;
+    if (__all_sync(0xffffffffu, below) || __all_sync(0xffffffffu, above)) {   // |away - c| is linear in c
+        const float s = __all_sync(0xffffffffu, below) ? slope : -slope;
+        float2 b = make_float2(-s * away, fmaf(-s, away, s));
+        const float2 step = make_float2(2.0f * s, 2.0f * s);
+#pragma unroll
+        for (int c = 0; c < kKeys / 2; ++c) {
+            const float2 r = fadd2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])),
+                                   ffma2(step, make_float2(c, c), b));
+            u[2 * c] = __float_as_uint(r.x);
+            u[2 * c + 1] = __float_as_uint(r.y);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+            u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c])));
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_span_attn_d64(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s);
+
+}  // namespace mha
