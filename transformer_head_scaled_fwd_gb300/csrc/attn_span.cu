@@ -13,7 +13,7 @@
 // (with two, 4 x 8192 causal took 389 us instead of 361 us: eight warps do not cover their own latencies), and four
 // that schedule and load Q and K, issue score MMAs, issue P.V MMAs, and load V. Scores and weights are double-buffered
 // in tensor memory, so the score MMAs of tile j + 1 run during the softmax of tile j, and the next unit's loads and
-// first scores run during this unit's output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
+// first scores run during this unit's last tiles and output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
 // softmax warps rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
 // Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408 us.
 #include <algorithm>
@@ -30,6 +30,10 @@ constexpr int kKeys = BN / kParts;
 constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoft = 32 * kSoftWarps;
 constexpr int kThreads = kSoft + 128;
+// Unit slots. Unit k + kSlots is published after the score MMAs of unit k + kSlots - 2, for which the softmax has begun
+// unit k + kSlots - 4 and so ended unit k + kSlots - 5, whose P.V are done: from five slots on, every role has read
+// unit k's by then.
+constexpr int kSlots = 8;
 constexpr int kLongKeys = 2048;  // d_k = 64, plain scores, no spans: from here on the kernel of two query tiles a unit
 constexpr uint32_t kColS = 0;                // + 128 b: score buffers S_0, S_1
 constexpr uint32_t kColP = 256;              // + 64 b + 16 h: weight buffers P_0, P_1
@@ -47,15 +51,16 @@ template <int kD>
 struct Tiles {
     static constexpr int kSlabs = kD / 64;
     static constexpr uint32_t kTile = kSlabs * kHalf;       // 128 x d_k bf16
-    static constexpr int kStagesK = kD == 128 ? 3 : 4;
+    static constexpr int kStagesK = kD == 128 ? 2 : 4;
     static constexpr int kStagesV = kD == 128 ? 2 : 4;
     static constexpr uint32_t kOffK = 2 * kTile;            // two Q buffers first
     static constexpr uint32_t kOffV = kOffK + kStagesK * kTile;
-    static constexpr uint32_t kOffBar = kOffV + kStagesV * kTile;
+    static constexpr uint32_t kOffO = kOffV + kStagesV * kTile;   // the output tile on its way out
+    static constexpr uint32_t kOffBar = kOffO + kTile;
 };
 
 struct SmemSpan {
-    uint64_t q_full[2], q_empty[2];          // Q buffer loaded / output stored from it
+    uint64_t q_full[2], q_empty[2];          // Q buffer loaded / read by the unit's last score MMA (commit)
     uint64_t k_full[4], k_empty[4];
     uint64_t v_full[4], v_empty[4];
     uint64_t v_edge;                         // the tile that holds the valid length has arrived
@@ -63,10 +68,10 @@ struct SmemSpan {
     uint64_t s_free[2];                      // S(j) of buffer b loaded (one arrival a softmax warp)
     uint64_t p_full[2];                      // P(j) of weight buffer b written (one arrival a softmax warp)
     uint64_t p_free[2];                      // P.V(j) of weight buffer b done (commit)
-    uint64_t unit_full[2];                   // unit slot published by the scheduler
+    uint64_t unit_full[kSlots];              // unit slot published by the scheduler
     uint64_t steal_full[2];                  // answer to a request for another unit
     alignas(16) uint32_t steal[2][4];
-    UnitInfo unit[2];
+    UnitInfo unit[kSlots];
     uint32_t tmem_base;
     int abort_flag;
     float mx[kParts][BM];                    // the parts' tile maxima, exchanged when a row's maximum grows
@@ -143,7 +148,6 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm->q_full[i], 1);
             mbar_init(&sm->q_empty[i], 1);
-            mbar_init(&sm->unit_full[i], 1);
             mbar_init(&sm->steal_full[i], 1);
             mbar_init(&sm->s_full[i], 1);
             mbar_init(&sm->s_free[i], kSoftWarps);
@@ -158,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             mbar_init(&sm->v_full[s], 1);
             mbar_init(&sm->v_empty[s], 1);
         }
+        for (int s = 0; s < kSlots; ++s) mbar_init(&sm->unit_full[s], 1);
         mbar_init(&sm->v_edge, 1);
         sm->abort_flag = 0;
         fence_barrier_init();
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             uint32_t gk = 0;   // K tiles issued so far
             for (int k = 0;; ++k) {
                 const int qb = k & 1;
-                // unit k - 2 has stored its output from this Q buffer (and every role has read its slot)
+                // the score MMAs of unit k - 2 have read this Q buffer
                 if (k >= 2) mbar_wait(&sm->q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.status, 0x810);
                 if (k >= 1) {
                     const int a = (k - 1) & 1;
@@ -196,16 +201,16 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 u = __shfl_sync(0xffffffffu, u, 0);
                 if (__any_sync(0xffffffffu, u < 0 || *abort_flag != 0)) {
                     if (lane == 0) {
-                        sm->unit[qb].n = 0;
-                        mbar_arrive(&sm->unit_full[qb]);
+                        sm->unit[k % kSlots].n = 0;
+                        mbar_arrive(&sm->unit_full[k % kSlots]);
                     }
                     break;
                 }
                 if (lane == 0) steal_request(&sm->steal[qb][0], &sm->steal_full[qb]);
                 const UnitInfo x = unit_of(p, u, lane);
                 if (lane == 0) {
-                    sm->unit[qb] = x;
-                    mbar_arrive(&sm->unit_full[qb]);
+                    sm->unit[k % kSlots] = x;
+                    mbar_arrive(&sm->unit_full[k % kSlots]);
                     const int kvh = x.head / (p.h / p.h_kv);
                     mbar_arrive_expect_tx(&sm->q_full[qb], kTile);
                     tma_load_5d(&maps.q, &sm->q_full[qb], base + qb * kTile, x.q0, at_h(p.q, x.head),
@@ -224,9 +229,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             // ------------------------------------------------ V loads
             uint32_t gv = 0, edges = 0;
             for (int k = 0;; ++k) {
-                const int qb = k & 1;
-                const bool ok = mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x813);
-                const UnitInfo x = sm->unit[qb];
+                const bool ok = mbar_wait(&sm->unit_full[k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 0x813);
+                const UnitInfo x = sm->unit[k % kSlots];
                 if (!__all_sync(0xffffffffu, ok && x.n > 0)) break;
                 const int kvh = x.head / (p.h / p.h_kv);
                 for (int j = 0; j < x.n; ++j, ++gv) {
@@ -264,8 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             uint32_t gk = 0;   // score tiles issued so far
             for (int k = 0;; ++k) {
                 const int qb = k & 1;
-                if (!mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x816)) break;
-                const int n = sm->unit[qb].n;
+                if (!mbar_wait(&sm->unit_full[k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 0x816)) break;
+                const int n = sm->unit[k % kSlots].n;
                 if (n == 0) break;
                 const uint32_t qa = smem_u32(base + qb * kTile);
                 mbar_wait(&sm->q_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x817);
@@ -286,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     tc_commit(&sm->s_full[sb]);
                     tc_commit(&sm->k_empty[s]);
                 }
+                tc_commit(&sm->q_empty[qb]);
             }
         } else if (warp == kSoftWarps + 2 && lane == 0) {
             // ------------------------------------------------ P.V MMAs: O += P(j) V_j
@@ -293,9 +298,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             const uint32_t v_addr = smem_u32(base + G::kOffV);
             uint32_t gv = 0;   // P.V steps issued so far
             for (int k = 0;; ++k) {
-                const int qb = k & 1;
-                if (!mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x81a)) break;
-                const int n = sm->unit[qb].n;
+                if (!mbar_wait(&sm->unit_full[k % kSlots], (k / kSlots) & 1, abort_flag, p.status, 0x81a)) break;
+                const int n = sm->unit[k % kSlots].n;
                 if (n == 0) break;
                 for (int j = 0; j < n; ++j, ++gv) {
                     const int s = gv % G::kStagesV;
@@ -339,7 +343,6 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         UnitInfo x = sm->unit[0];
         int2 span = ok && x.n > 0 ? span_of(p, x.b, x.q0 + row) : make_int2(0, 0);
         for (int k = 0;; ++k) {
-            const int qb = k & 1;
             __syncwarp();
             // every softmax thread takes the same decision (a give-up in one thread stops all)
             if (!named_bar_and(1, kSoft, ok && x.n > 0)) break;
@@ -464,17 +467,18 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 if (lane == 0) mbar_arrive(&sm->p_full[sb]);
             }
             // The next unit's slot and spans are read now: their latency passes behind the output.
-            const int nb = (k + 1) & 1;
-            ok = mbar_wait(&sm->unit_full[nb], ((k + 1) >> 1) & 1, abort_flag, p.status, 0x821);
-            x = sm->unit[nb];
+            const int next = k + 1;
+            ok = mbar_wait(&sm->unit_full[next % kSlots], (next / kSlots) & 1, abort_flag, p.status, 0x821);
+            x = sm->unit[next % kSlots];
             if (ok && x.n > 0) span = span_of(p, x.b, x.q0 + row);
-            // ---------------- output: thread (h, row) writes its features of O / (l_0 + ... + l_3). The unit's Q
-            // buffer is idle (its last score MMA completed before this thread's last wait on S): it carries
-            // l_h of every part and row, then the bf16 output tile.
-            uint8_t* qbuf = base + qb * kTile;
-            float* lsum = reinterpret_cast<float*>(qbuf);
+            // ---------------- output: thread (h, row) writes its features of O / (l_0 + ... + l_3). The output tile's
+            // buffer first carries l_h of every part and row; the previous unit's store has read it.
+            uint8_t* obuf = base + G::kOffO;
+            if (warp == 0 && lane == 0) tma_store_wait_read();
+            named_bar_sync(1, kSoft);
+            float* lsum = reinterpret_cast<float*>(obuf);
             lsum[h * BM + row] = l;
-            named_bar_sync(1, kSoft);   // all parts' sums are in shared memory
+            named_bar_sync(4 + q, 32 * kParts);   // the four warps of these rows
             const float L = (lsum[row] + lsum[BM + row]) + (lsum[2 * BM + row] + lsum[3 * BM + row]);
             const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
             const uint32_t gl = g - 1;   // the unit's last tile: its P.V completes O
@@ -492,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
-                st_shared_v4(smem_u32(qbuf + (col / 64) * kHalf) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4), w[0],
+                st_shared_v4(smem_u32(obuf + (col / 64) * kHalf) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4), w[0],
                              w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
@@ -503,12 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     asm volatile(
                         "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %2, %4, %5}], [%1];" ::"l"(
                             reinterpret_cast<uint64_t>(&maps.out)),
-                        "r"(smem_u32(qbuf)), "r"(0), "r"(q0), "r"(head), "r"(b)
+                        "r"(smem_u32(obuf)), "r"(0), "r"(q0), "r"(head), "r"(b)
                         : "memory");
                     tma_store_commit();
                 }
-                tma_store_wait_read();   // the buffer may take the Q tile of unit k + 2
-                mbar_arrive(&sm->q_empty[qb]);
             }
         }
         if (warp == 0 && lane == 0) tma_store_wait_all();
