@@ -110,6 +110,7 @@ def test_attention_refusals(lib):
     assert lib.mha_document_spans(None, 1, 1, P, None) == INV
     assert lib.mha_document_spans(P, 0, 1, P, None) == INV
     assert lib.mha_document_spans(P, 1, 1, ctypes.c_void_p(4100), None) == INV
+    assert lib.mha_document_spans(P, 70000, 1, P, None) == UNS
 
 
 def test_rmsnorm_refusals(lib):

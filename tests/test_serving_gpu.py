@@ -493,7 +493,8 @@ def test_attention_long_causal(bnd):
             R.check(got[:, r:r + 1], ref, tol, f"row {r}")
 
 
-@pytest.mark.parametrize("B,L,mean,pad", [(1, 1, 5, 0), (3, 1000, 30, 100), (2, 5003, 700, 0), (1, 1024, 1, 1)])
+@pytest.mark.parametrize("B,L,mean,pad", [(1, 1, 5, 0), (3, 1000, 30, 100), (2, 5003, 700, 0), (1, 1024, 1, 1), (2, 4096, 5000, 0),
+                                         (1, 2048, 1024, 1024), (3, 33, 9, 2), (1, 9000, 4000, 0)])
 def test_document_spans(bnd, B, L, mean, pad):
     ids = docs_of(90, B, L, mean, pad)
     spans = torch.full((B, L, 2), -5, dtype=torch.int32, device="cuda")

@@ -269,6 +269,7 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
 mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* spans, void* stream) {
     if (doc_ids == nullptr || spans == nullptr) return fail(MHA_ERR_INVALID_ARG, "doc_ids and spans must not be NULL");
     if (B <= 0 || L <= 0) return fail(MHA_ERR_INVALID_ARG, "sizes must be positive (B=%d L=%d)", B, L);
+    if (B > 65535 || L > 0x7ffffbff) return fail(MHA_ERR_UNSUPPORTED, "B up to 65535, L below 2^31 - 1024 (got %d, %d)", B, L);
     if (!aligned(doc_ids, 4) || !aligned(spans, 8))
         return fail(MHA_ERR_INVALID_ARG, "doc_ids must be aligned to 4 bytes and spans to 8");
     return launched(mha::launch_document_spans(doc_ids, B, L, spans, as_stream(stream)), "document spans");
