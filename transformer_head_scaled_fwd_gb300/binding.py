@@ -346,10 +346,6 @@ def _here(t):
     return dev
 
 
-def _stream_on(dev, stream):
-    return _raw_stream(dev) if stream is None else stream.cuda_stream
-
-
 def _code(dtype):
     if dtype is _bf16:
         return MHA_BF16
@@ -369,19 +365,22 @@ def _want(t, name, dtype, shape, dev):
     raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
 
 
-def _strides(t, name):
-    """Packed strides of a [B, L, H, d] tensor whose last dimension is adjacent."""
+def _view(t, name, dtype, shape, dev):
+    """(pointer, packed strides) of a [B, L, H, d] tensor of this dtype, shape and device, its last dimension adjacent."""
     st = t.stride()
-    if st[3] != 1 and t.shape[3] != 1:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _want(t, name, dtype, shape, dev)
+    if st[3] != 1 and shape[3] != 1:
         raise ValueError(f"the last dimension of {name} must be adjacent (stride {st[3]})")
-    return _pack_strides(*st)
+    return t.data_ptr(), _pack_strides(*st)
 
 
 def _ints(t, name, shape, dev):
     """Pointer of a contiguous int32 tensor, or None."""
     if t is None:
         return None
-    _want(t, name, _i32, shape, dev)
+    if t.dtype is not _i32 or t.shape != shape or t.get_device() != dev:
+        _want(t, name, _i32, shape, dev)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
@@ -478,17 +477,18 @@ def mha_rotary(q, *, rotary, q_out, k=None, k_out=None, positions=None, stream=N
     dev = _here(q)
     dtype, shape = q.dtype, q.shape
     B, T, h, d = shape
-    _want(q_out, "q_out", dtype, shape, dev)
+    qp, qs = _view(q, "q", dtype, shape, dev)
+    qop, qos = _view(q_out, "q_out", dtype, shape, dev)
     kp = ks = kop = kos = None
     h_kv = 0
     if k is not None:
         h_kv = k.shape[2]
-        _want(k, "k", dtype, (B, T, h_kv, d), dev)
-        _want(k_out, "k_out", dtype, k.shape, dev)
-        kp, ks, kop, kos = k.data_ptr(), _strides(k, "k"), k_out.data_ptr(), _strides(k_out, "k_out")
+        k_shape = (B, T, h_kv, d)
+        kp, ks = _view(k, "k", dtype, k_shape, dev)
+        kop, kos = _view(k_out, "k_out", dtype, k_shape, dev)
     st = (_lib or load()).mha_rotary(
-        _code(dtype), q.data_ptr(), _strides(q, "q"), q_out.data_ptr(), _strides(q_out, "q_out"), kp, ks, kop, kos, B, T, h,
-        h_kv, d, _ints(positions, "positions", (B, T), dev), _rotary_ref(rotary, dev), _stream_on(dev, stream))
+        _code(dtype), qp, qs, qop, qos, kp, ks, kop, kos, B, T, h, h_kv, d, _ints(positions, "positions", (B, T), dev),
+        _rotary_ref(rotary, dev), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
@@ -498,25 +498,26 @@ def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_
     dev = _here(k)
     dtype, shape = k.dtype, k.shape
     B, T, h_kv, d = shape
-    _want(v, "v", dtype, shape, dev)
     if cache._for != (B, d, dtype, dev) or cache._heads != h_kv:
         raise ValueError("the cache's batch, heads, head width, dtype or device differ from k's")
+    kp, ks = _view(k, "k", dtype, shape, dev)
+    vp, vs = _view(v, "v", dtype, shape, dev)
     qp = qs = qop = qos = kop = kos = None
     h = 0
     if q is not None:
         h = q.shape[2]
-        _want(q, "q", dtype, (B, T, h, d), dev)
-        _want(q_out, "q_out", dtype, q.shape, dev)
-        qp, qs, qop, qos = q.data_ptr(), _strides(q, "q"), q_out.data_ptr(), _strides(q_out, "q_out")
+        q_shape = (B, T, h, d)
+        qp, qs = _view(q, "q", dtype, q_shape, dev)
+        qop, qos = _view(q_out, "q_out", dtype, q_shape, dev)
     if k_out is not None:
-        _want(k_out, "k_out", dtype, shape, dev)
-        kop, kos = k_out.data_ptr(), _strides(k_out, "k_out")
+        kop, kos = _view(k_out, "k_out", dtype, shape, dev)
     if start is None:
         raise ValueError("start must be an int32 tensor [B]")
+    one = (B,)
     st = (_lib or load()).mha_paged_append(
-        _code(dtype), qp, qs, qop, qos, k.data_ptr(), _strides(k, "k"), kop, kos, v.data_ptr(), _strides(v, "v"), B, T, h,
-        h_kv, d, _ints(start, "start", (B,), dev), _ints(new_lens, "new_lens", (B,), dev),
-        None if rotary is None else _rotary_ref(rotary, dev), cache._ref, _stream_on(dev, stream))
+        _code(dtype), qp, qs, qop, qos, kp, ks, kop, kos, vp, vs, B, T, h, h_kv, d, _ints(start, "start", one, dev),
+        _ints(new_lens, "new_lens", one, dev), None if rotary is None else _rotary_ref(rotary, dev), cache._ref,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
@@ -544,7 +545,7 @@ def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, strea
     st = (_lib or load()).mha_paged_attention(
         _code(dtype), q.data_ptr(), _pack_strides(qb, 0, qh, 1), out.data_ptr(), _pack_strides(ob, 0, oh, 1), B, h,
         cache._heads, d, _ints(kv_lens, "kv_lens", (B,), dev), _scores_ref(scores, h, dev), cache._ref,
-        workspace.data_ptr(), workspace.nbytes, _stream_on(dev, stream))
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
@@ -554,7 +555,7 @@ def mha_document_spans(doc_ids, *, spans, stream=None):
     dev = _here(doc_ids)
     B, L = doc_ids.shape
     st = (_lib or load()).mha_document_spans(_ints(doc_ids, "doc_ids", (B, L), dev), B, L,
-                                             _ints(spans, "spans", (B, L, 2), dev), _stream_on(dev, stream))
+                                             _ints(spans, "spans", (B, L, 2), dev), _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
@@ -562,31 +563,34 @@ def mha_document_spans(doc_ids, *, spans, stream=None):
 def mha_attention(q, k, v, *, out, scores=None, mask=None, stream=None):
     """Attention of q [B, L_q, h, d_k] over k, v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]."""
     dev = _here(q)
-    dtype, shape, k_shape = q.dtype, q.shape, k.shape
+    dtype, shape = q.dtype, q.shape
     B, Lq, h, d = shape
-    Lk, h_kv = k_shape[1], k_shape[2]
-    _want(k, "k", dtype, (B, Lk, h_kv, d), dev)
-    _want(v, "v", dtype, k_shape, dev)
-    _want(out, "out", dtype, shape, dev)
+    Lk, h_kv = k.shape[1], k.shape[2]
+    k_shape = (B, Lk, h_kv, d)
+    qp, qs = _view(q, "q", dtype, shape, dev)
+    kp, ks = _view(k, "k", dtype, k_shape, dev)
+    vp, vs = _view(v, "v", dtype, k_shape, dev)
+    op, os_ = _view(out, "out", dtype, shape, dev)
     ref = None
     if mask is not None:
         valid, prefix, spans = mask.tensors
         ref = _pack_mask(mask.causal, mask.q_offset, _ints(valid, "key_valid_lens", (B,), dev) or 0,
                          _ints(prefix, "prefix_lens", (B,), dev) or 0, _ints(spans, "doc_spans", (B, Lq, 2), dev) or 0)
     st = (_lib or load()).mha_attention(
-        _code(dtype), q.data_ptr(), _strides(q, "q"), k.data_ptr(), _strides(k, "k"), v.data_ptr(), _strides(v, "v"),
-        out.data_ptr(), _strides(out, "out"), B, Lq, Lk, h, h_kv, d, _scores_ref(scores, h, dev), ref,
-        _stream_on(dev, stream))
+        _code(dtype), qp, qs, kp, ks, vp, vs, op, os_, B, Lq, Lk, h, h_kv, d, _scores_ref(scores, h, dev), ref,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
 
-def _rows(t, name, d):
-    """Row stride of a [rows, d] tensor with adjacent rows."""
-    s = t.stride()
-    if s[1] != 1 and d != 1:
+def _rows(t, name, dtype, shape, dev):
+    """(pointer, row stride) of a [rows, d] tensor of this dtype, shape and device with adjacent rows."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _want(t, name, dtype, shape, dev)
+    s0, s1 = t.stride()
+    if s1 != 1 and shape[1] != 1:
         raise ValueError(f"the rows of {name} must be adjacent")
-    return s[0]
+    return t.data_ptr(), s0
 
 
 def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=None, stream=None):
@@ -595,12 +599,13 @@ def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=N
     dev = _here(x)
     dtype, shape = x.dtype, x.shape
     rows, d = shape
-    group = 0
-    rp = rs = zp = zs = gp = cp = None
+    xp, xs = _rows(x, "x", dtype, shape, dev)
+    group = rs = zs = 0
+    rp = zp = gp = cp = None
     if scales is None:
-        _want(y, "y", dtype, shape, dev)
+        yp, ys = _rows(y, "y", dtype, shape, dev)
     else:
-        _want(y, "y", _e4m3, shape, dev)
+        yp, ys = _rows(y, "y", _e4m3, shape, dev)
         groups = scales.shape[1]
         _want(scales, "scales", _f32, (rows, groups), dev)
         if not scales.is_contiguous() or groups < 1 or d % groups != 0:
@@ -609,21 +614,18 @@ def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=N
             group = d // groups
         cp = scales.data_ptr()
     if residual is not None:
-        _want(residual, "residual", dtype, shape, dev)
-        rp, rs = residual.data_ptr(), _rows(residual, "residual", d)
+        rp, rs = _rows(residual, "residual", dtype, shape, dev)
     if sum_out is not None:
         if residual is None:
             raise ValueError("sum_out needs a residual")
-        _want(sum_out, "sum_out", dtype, shape, dev)
-        zp, zs = sum_out.data_ptr(), _rows(sum_out, "sum_out", d)
+        zp, zs = _rows(sum_out, "sum_out", dtype, shape, dev)
     if gain is not None:
-        _want(gain, "gain", dtype, (d,), dev)
-        if not gain.is_contiguous():
+        if gain.dtype is not dtype or gain.shape != (d,) or gain.get_device() != dev or not gain.is_contiguous():
+            _want(gain, "gain", dtype, (d,), dev)
             raise ValueError("gain must be contiguous")
         gp = gain.data_ptr()
-    st = (_lib or load()).mha_rmsnorm(
-        _code(dtype), x.data_ptr(), _rows(x, "x", d), rp, rs or 0, zp, zs or 0, gp, eps, rows, d, y.data_ptr(),
-        _rows(y, "y", d), cp, group, _stream_on(dev, stream))
+    st = (_lib or load()).mha_rmsnorm(_code(dtype), xp, xs, rp, rs, zp, zs, gp, eps, rows, d, yp, ys, cp, group,
+                                      _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 
