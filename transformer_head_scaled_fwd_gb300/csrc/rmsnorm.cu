@@ -114,10 +114,10 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
     return v;
 }
 
-// Rows a CTA takes: as many as fill 256 threads while a row takes 64 or fewer (an SM starts a CTA in about 0.2 us:
-// 32768 rows of 501 took 39 us with a CTA each, 27 us so), else one (two rows of 128 threads end together: 32768 x
-// 4096 without residual took 84 us instead of 78 us).
-__host__ __device__ constexpr int rows_of_cta(int thr) { return thr <= 64 ? kThreads / thr : 1; }
+// Rows a CTA takes: as many as fill its 256 threads, because an SM starts CTAs one after the other, each in about 0.2
+// us (32768 rows of 501: 39 us with a CTA of 64 threads each, 27 us so; 32768 x 4096 without residual, 128 threads a row:
+// 108 us with one row a CTA, 84 us with two).
+__host__ __device__ constexpr int rows_of_cta(int thr) { return kThreads / thr; }
 
 // The row stays in registers between the passes: kThr threads a row, kC accesses a thread. Groups need Vec (a group is up to 32 neighbouring lanes of one access).
 template <typename V, int kThr, int kC, bool kQuant>
@@ -302,9 +302,9 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
                                           : ok(p.y, p.y_stride);
     if (p.d % kN == 0 && ok(p.x, p.x_stride) && ok(p.residual, p.residual ? p.r_stride : 0) &&
         ok(p.sum, p.sum ? p.s_stride : 0) && ok(p.gain, 0) && y_ok) {
-        // Four accesses a thread keep enough bytes in flight (without a residual 78 us against 90 us with two, 32768 x
-        // 4096); when there are fewer rows than fill the SMs, twice the threads finish a row sooner (16 x 1024: 6.7
-        // against 8.2 us with the launch).
+        // Four accesses a thread keep enough bytes in flight (32768 x 4096 without a residual: 84 us, with two 130 us);
+        // when there are fewer rows than fill the SMs, twice the threads finish a row sooner (16 x 1024: 6.7 against
+        // 8.2 us with the launch).
         const bool few = p.rows <= 608;
         const int chunks = p.d / kN;
         if (chunks <= 32) return launch_row<V, 32, 1>(p, s);

@@ -237,12 +237,12 @@ cudaError_t launch_n(const RotaryParams& p, cudaStream_t s) {
     const int nq = p.q.p != nullptr ? p.h : 0, nk = p.k.p != nullptr ? p.h_kv : 0;
     plan.q = fast_div(static_cast<uint32_t>(std::max(nq, 1)));
     plan.k = fast_div(static_cast<uint32_t>(std::max(nk, 1)));
-    // kRows rows a thread where that leaves two CTAs an SM; the tokens of a CTA's rows (of the fewest heads) have
-    // their cos and sin in 32 KB
+    // the tokens of a CTA's rows (of the fewest heads) have their cos and sin in 32 KB
     const int fewest = nk > 0 && (nq == 0 || nk < nq) ? nk : nq;
     const size_t token_bytes = sizeof(TokenInfo) + sizeof(float2) * (p.rot / 2);
     const int64_t most = std::max<int64_t>(1, static_cast<int64_t>((32 << 10) / token_bytes) - 1) * fewest;
     const int64_t all_rows = plan.total * (nq + (p.v.p != nullptr ? 2 : 1) * nk);
+    // kRows rows a thread where that leaves two CTAs an SM (equal waves of smaller CTAs were no faster)
     const int64_t spread = (all_rows + 303) / 304;
     plan.per_cta = static_cast<int>(std::max<int64_t>(1, std::min({static_cast<int64_t>(kRows) * plan.rows, most, spread})));
     plan.tokens = (plan.per_cta + fewest - 1) / fewest + 1;
