@@ -416,6 +416,14 @@ ATT = [
     (2, 700, 700, 3, 3, 64, dict(docs=60, pad=300)),                # whole query tiles without a key
     (60, 300, 300, 8, 4, 64, dict(valid=[0, 300, 0, 0] * 15, causal=True)),     # many units without a key
     (3, 128, 4000, 2, 2, 64, dict(causal=True, q_offset=100, valid=[4000, 77, 0])),
+    # long key ranges of d_k = 64
+    (1, 1, 2000, 2, 1, 64, {}),
+    (2, 300, 1800, 4, 2, 64, dict(causal=True, q_offset=1500, slopes=True)),
+    (2, 1700, 1700, 2, 2, 64, dict(docs=300, causal=True, pad=500)),
+    (2, 1700, 1700, 2, 1, 64, dict(docs=90, cap=20.0)),
+    (1, 257, 2500, 2, 2, 64, dict(cap=100.0, slopes=True)),
+    (30, 200, 1600, 4, 4, 64, dict(causal=True, q_offset=1400, valid=[0, 1600, 0, 0, 1, 1401] * 5)),
+    (2, 1600, 1600, 2, 2, 64, dict(causal=True, prefix=[900, 0], valid=[1600, 1000])),
     (1, 600, 600, 2, 1, 64, dict(cap=300.0, causal=True)),
 ]
 
@@ -453,11 +461,11 @@ def test_attention(bnd, B, Lq, Lk, h, hk, d, opt):
     assert torch.equal(got, run_attention(bnd, q, k, v, **opt))
 
 
-@pytest.mark.parametrize("d", [64, 128])
-def test_attention_head_major_strides_and_spans(bnd, d):
+@pytest.mark.parametrize("d,L", [(64, 200), (128, 200), (64, 1650)])
+def test_attention_head_major_strides_and_spans(bnd, d, L):
     """[B, h, L, d] storage (the workspace's order), an output inside a wider tensor, arbitrary spans with
     empty and inverted rows."""
-    B, L, h, hk = 2, 200, 4, 2
+    B, h, hk = 2, 4, 2
     q = randn(70, B, h, L, d, dtype=BF).transpose(1, 2)
     k, v = randn(71, B, hk, L, d, dtype=BF).transpose(1, 2), randn(72, B, hk, L, d, dtype=BF).transpose(1, 2)
     rng = random.Random(7)

@@ -168,6 +168,6 @@ __device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, fl
 
 }  // namespace
 
-cudaError_t launch_span_attn_d64(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s);
+cudaError_t launch_span_attn_d64(const SpanAttnParams& p, const SpanMaps& maps, int mode, cudaStream_t s);
 
 }  // namespace mha

@@ -1,16 +1,23 @@
-// attn_span_d64.cu -- attention under span masks for heads of 64 (see attn_span.cu for the masks and the formulas).
+// attn_span_d64.cu -- attention under span masks for heads of 64 over long key ranges (attn_span.cu has the masks, the
+// formulas, and the kernel for everything else).
 //
-// At d_k = 64 the two products of a tile take half as long as at 128, the softmax as long as ever, so its overhead a
-// tile decides. Unit of work: two query tiles of 128 rows of one head, one thread a row (no exchange between threads at
-// all), each key and value tile loaded once for both. The two tiles are independent but for the loads: warpgroup t has
-// the rows of tile t, its scores S_t, weights P_t and output O_t in tensor memory; while one is in its softmax, the
-// tensor cores work for the other. A tile of keys is computed only for the query tiles whose rows can see it.
+// At d_k = 64 the two products of a tile take half as long as at 128, the softmax as long as ever. The warps of one
+// scheduler then stand in the same phase of the same tile: all in their exponentials (512 cycles of the special
+// function unit a tile), then none. So a unit of work is two query tiles of 128 rows of one head, two threads a row,
+// and the two tiles' warps are independent but for the loads: warpgroup pair t has the rows of tile t, its scores S_t,
+// weights P_t and output O_t in tensor memory, and one tile's exponentials pass while the other waits for its scores
+// or stores its weights. Each key and value tile is loaded once for both, and computed only for the query tiles whose
+// rows can see it.
+//
+// Measured, 4 x 8192 causal, 16 heads: 541 us, 1017 TFLOP/s (0.53 of measured bf16 peak; all keys 1072); the kernel of
+// one query tile 660 us; two query tiles with one thread a row (eight softmax warps) 581 us, all keys 987 against 1026
+// us. With a distance bias 935 (1099) us. Capped scores without a maximum gain nothing from it (795 against 721 us) and
+// stay with the other kernel.
 //
 // Tensor memory (512 columns): S_0 S_1 (fp32, 128 each), P_0 P_1 (bf16, 64 each), O_0 O_1 (fp32, 64 each).
-// Shared memory: two Q buffers of two tiles (after its last score MMA a buffer stages the unit's output), K and V
-// rings of four tiles. Warps: 0-3 / 4-7 softmax of tile 0 / 1, then scheduler and Q, K loads; score MMAs; P.V MMAs;
-// V loads. Registers: 168 a thread at launch; the third warpgroup drops to 64, the others rise to 216
-// (128 * 64 + 256 * 216 = 63488 <= 384 * 168).
+// Shared memory: two Q buffers of two tiles, K and V rings of four tiles, the two output tiles on their way out. Warps:
+// 0-7 / 8-15 softmax of tile 0 / 1, then scheduler and Q, K loads; score MMAs; P.V MMAs; V loads. Registers: 96 a
+// thread at launch; the last warpgroup drops to 56, the others rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
 #include <algorithm>
 
 #include "attn_span.cuh"
@@ -21,7 +28,11 @@ namespace {
 
 constexpr int BM = 128;                      // rows of a query tile
 constexpr int kRowsUnit = 2 * BM;
-constexpr int kThreads = 384;
+constexpr int kParts = 2;                    // softmax threads a row: each takes 64 keys of a tile
+constexpr int kKeys = BN / kParts;
+constexpr int kGroup = 128 * kParts;         // softmax threads of a query tile
+constexpr int kSoftWarps = 2 * kGroup / 32;
+constexpr int kThreads = 2 * kGroup + 128;
 constexpr int kD = 64;
 constexpr uint32_t kTile = kHalf;            // 128 x 64 bf16
 constexpr int kStages = 4;                   // of K and of V
@@ -29,7 +40,8 @@ constexpr uint32_t kColP = 256;              // + 64 t
 constexpr uint32_t kColO = 384;              // + 64 t
 constexpr uint32_t kOffK = 4 * kTile;        // two Q buffers of two tiles first
 constexpr uint32_t kOffV = kOffK + kStages * kTile;
-constexpr uint32_t kOffBar = kOffV + kStages * kTile;
+constexpr uint32_t kOffO = kOffV + kStages * kTile;   // the output tiles on their way out
+constexpr uint32_t kOffBar = kOffO + 2 * kTile;
 
 // One unit as the scheduler publishes it; b < 0 means no more work.
 struct UnitInfo {
@@ -42,19 +54,20 @@ struct UnitInfo {
 
 struct Smem64 {
     uint64_t q_full[2];                      // Q buffer loaded
-    uint64_t q_empty[2];                     // output stored from it (both tiles), and every role has read the unit's slot:
-                                             // one without keys gives three of them nothing else to do
+    uint64_t q_empty[2];                     // its unit's score MMAs done (commit), and the other four roles have read
+                                             // the unit's slot (a unit without keys gives them nothing else to do)
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_empty[kStages];
     uint64_t v_edge;                         // the tile that holds the valid length has arrived
-    uint64_t s_full[2], s_free[2];           // S_t computed (commit) / loaded (four warps)
-    uint64_t p_full[2], p_free[2];           // P_t written (four warps) / P.V done (commit)
+    uint64_t s_full[2], s_free[2];           // S_t computed (commit) / loaded (one arrival a warp)
+    uint64_t p_full[2], p_free[2];           // P_t written (one arrival a warp) / P.V done (commit)
     uint64_t unit_full[2];                   // unit slot published by the scheduler
     uint64_t steal_full[2];                  // answer to a request for another unit
     alignas(16) uint32_t steal[2][4];
     UnitInfo unit[2];
     uint32_t tmem_base;
     int abort_flag;
+    float mx[2][kParts][BM];                 // the parts' tile maxima, exchanged when a row's maximum grows
 };
 constexpr size_t kSmemBytes = kOffBar + sizeof(Smem64);
 
@@ -118,8 +131,10 @@ __device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int 
     return x;
 }
 
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid_constant__ SpanAttnParams p,
                                                                     const __grid_constant__ SpanMaps maps) {
+    constexpr int kOut = kD / kParts;            // output features of a softmax thread
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
     Smem64* sm = reinterpret_cast<Smem64*>(base + kOffBar);
@@ -139,8 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
             mbar_init(&sm->unit_full[i], 1);
             mbar_init(&sm->steal_full[i], 1);
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->s_free[i], 4);
-            mbar_init(&sm->p_full[i], 4);
+            mbar_init(&sm->s_free[i], 4 * kParts);
+            mbar_init(&sm->p_full[i], 4 * kParts);
             mbar_init(&sm->p_free[i], 1);
         }
         for (int s = 0; s < kStages; ++s) {
@@ -157,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
         tma_prefetch_desc(&maps.v);
         tma_prefetch_desc(&maps.out);
     }
-    if (warp == 9) {
+    if (warp == kSoftWarps + 1) {
         tmem_alloc(&sm->tmem_base, kTmemCols);
         tmem_relinquish();
     }
@@ -168,15 +183,15 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
     volatile int* abort_flag = &sm->abort_flag;
     pdl_wait();   // the tensors and the mask parts come from earlier kernels
 
-    if (warp >= 8) {
-        regs_dec<64>();
-        if (warp == 8) {
+    if (warp >= kSoftWarps) {
+        regs_dec<56>();
+        if (warp == kSoftWarps) {
             // ------------------------------------------------ scheduler, Q and K loads
             int u = blockIdx.x;
             uint32_t gk = 0;   // K tiles issued so far
             for (int k = 0;; ++k) {
                 const int qb = k & 1;
-                // unit k - 2 has stored its output from this Q buffer, and every role has read its slot
+                // the score MMAs of unit k - 2 have read this Q buffer, and every role its slot
                 if (k >= 2) mbar_wait(&sm->q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.status, 0x830);
                 if (k >= 1) {
                     const int a = (k - 1) & 1;
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 }
                 __syncwarp();
             }
-        } else if (warp == 11) {
+        } else if (warp == kSoftWarps + 3) {
             // ------------------------------------------------ V loads
             uint32_t gv = 0, edges = 0;
             for (int k = 0;; ++k) {
@@ -249,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                     }
                 }
             }
-        } else if (warp == 9 && lane == 0) {
+        } else if (warp == kSoftWarps + 1 && lane == 0) {
             // ------------------------------------------------ score MMAs: S_t(j) = Q_t K_j^T
             constexpr uint32_t idesc_s = idesc_bf16(BM, BN, false, false);
             const uint32_t k_addr = smem_u32(base + kOffK);
@@ -259,7 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 if (!mbar_wait(&sm->unit_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x836)) break;
                 const UnitInfo x = sm->unit[qb];
                 if (x.b < 0) break;
-                mbar_arrive(&sm->q_empty[qb]);
                 mbar_wait(&sm->q_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x837);
                 for (int j = 0; j < x.n; ++j, ++gk) {
                     const int s = gk % kStages;
@@ -280,8 +294,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                     }
                     tc_commit(&sm->k_empty[s]);
                 }
+                tc_commit(&sm->q_empty[qb]);
             }
-        } else if (warp == 10 && lane == 0) {
+        } else if (warp == kSoftWarps + 2 && lane == 0) {
             // ------------------------------------------------ P.V MMAs: O_t += P_t(j) V_j
             constexpr uint32_t idesc_o = idesc_bf16(BM, kD, false, true);
             const uint32_t v_addr = smem_u32(base + kOffV);
@@ -316,21 +331,24 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
         tc_fence_before();
         __syncwarp();
         named_bar_sync(3, kThreads);
-        if (warp == 9) {
+        if (warp == kSoftWarps + 1) {
             __syncwarp();
             tc_fence_after();
             tmem_dealloc(tmem, kTmemCols);
         }
     } else {
-        regs_inc<216>();
-        // ------------------------------------------------ softmax: warpgroup t, one thread a row of query tile t
-        const int t = warp >> 2;
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_tmem = tmem + lane_off + t * 128;
-        const uint32_t p_tmem = tmem + lane_off + kColP + t * 64;
-        const uint32_t o_tmem = tmem + lane_off + kColO + t * 64;
+        regs_inc<104>();
+        // ------------------------------------------------ softmax: thread (t, h, row), keys 64 h .. 64 h + 63 of a tile
+        const int t = warp / (kSoftWarps / 2), h = (warp >> 2) % kParts, q = warp & 3;
+        const int row = q * 32 + lane;
+        const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
+        const uint32_t s_tmem = tmem + lane_off + t * 128 + h * kKeys;
+        const uint32_t p_tmem = tmem + lane_off + kColP + t * 64 + h * (kKeys / 2);
+        const uint32_t o_tmem = tmem + lane_off + kColO + t * 64 + h * kOut;     // this part's output features
+        const int pair = 4 + t * 4 + q;                                          // barrier of the warps that share rows
+        const bool first = warp % (kSoftWarps / 2) == 0 && lane == 0;            // one thread of the group
         const float scale_log2 = p.scale * kLog2e;
+        const TanhForm capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
         uint32_t g = 0;   // score tiles of this query tile consumed so far
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x83d);
         UnitInfo x = sm->unit[0];
@@ -339,71 +357,94 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
             const int qb = k & 1;
             __syncwarp();
             // every thread of the group takes the same decision (a give-up in one thread stops all)
-            if (!named_bar_and(1 + t, BM, ok && x.b >= 0)) break;
+            if (!named_bar_and(1 + t, kGroup, ok && x.b >= 0)) break;
+            if (first) mbar_arrive(&sm->q_empty[qb]);      // all of the group have read the slot
             const int b = x.b, head = x.head, q0 = x.q0 + t * BM, j0 = x.j0;
             const int from = t ? x.from[1] : x.from[0], to = t ? x.to[1] : x.to[0];
             const int lo_max = t ? x.lo_max[1] : x.lo_max[0], hi_min = t ? x.hi_min[1] : x.hi_min[0];
             const int2 iv = interval_of(p, x.valid, x.seen, span, q0 + row);
-            float m = -CUDART_INF_F;   // the row's reference max (log2 units)
-            float l = 0.0f;
+            const float slope = kMode == kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
+            float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to its parts
+            float l = 0.0f;            // this part's share of the row sum
             for (int j = from; j < to; ++j, ++g) {
                 mbar_wait(&sm->s_full[t], g & 1, abort_flag, p.status, 0x83e);
                 __syncwarp();
                 tc_fence_after();
-                uint32_t u[128];
-                tmem_ld_x128(s_tmem, u);
+                uint32_t u[kKeys];
+                tmem_ld_x64(s_tmem, u);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->s_free[t]);
-                const int k0 = (j0 + j) * BN;
-                const bool edge = k0 < lo_max || k0 + BN > hi_min;
-                float sc = scale_log2;
-                if (edge) {
-                    sc = 1.0f;
+                const int k0 = (j0 + j) * BN + h * kKeys;   // first key of this part
+                const bool edge = k0 < lo_max || k0 + kKeys > hi_min;
+                float sc = 1.0f;
+                if constexpr (kMode == kPlain) {
+                    if (edge) {
 #pragma unroll
-                    for (int c = 0; c < BN; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                    } else {
+                        sc = scale_log2;
+                    }
+                } else {
+                    if (p.cap > 0.0f) {
+                        cap_scores(u, capped);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                    }
+                    if (slope != 0.0f) bias_scores(u, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                }
+                if (edge) {
                     const uint32_t first = iv.x - k0, many = max(iv.y - iv.x, 0);   // keys first .. first + many - 1 of u
 #pragma unroll
-                    for (int c = 0; c < BN; ++c)
+                    for (int c = 0; c < kKeys; ++c)
                         if (static_cast<uint32_t>(c) - first >= many) u[c] = __float_as_uint(-CUDART_INF_F);
                 }
                 float alpha = 1.0f;
                 bool grow = false;
                 float a4[4];
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    float a = fmax3(__uint_as_float(u[32 * c4]), __uint_as_float(u[32 * c4 + 1]),
-                                    __uint_as_float(u[32 * c4 + 2]));
+                for (int c2 = 0; c2 < 4; ++c2) {
+                    float a = fmax3(__uint_as_float(u[16 * c2]), __uint_as_float(u[16 * c2 + 1]),
+                                    __uint_as_float(u[16 * c2 + 2]));
 #pragma unroll
-                    for (int e = 3; e < 31; e += 2)
-                        a = fmax3(a, __uint_as_float(u[32 * c4 + e]), __uint_as_float(u[32 * c4 + e + 1]));
-                    a4[c4] = fmaxf(a, __uint_as_float(u[32 * c4 + 31]));
+                    for (int e = 3; e < 15; e += 2)
+                        a = fmax3(a, __uint_as_float(u[16 * c2 + e]), __uint_as_float(u[16 * c2 + e + 1]));
+                    a4[c2] = fmaxf(a, __uint_as_float(u[16 * c2 + 15]));
                 }
-                const float top = fmaxf(fmax3(a4[0], a4[1], a4[2]), a4[3]) * sc;
-                // the reference moves only when the tile passes it by 2^8 (or holds the row's first keys)
-                if (top > m + kRescaleThreshold) {
-                    grow = m != -CUDART_INF_F;
-                    alpha = ex2_approx(m - top);   // 0 for the first keys
-                    l *= alpha;
-                    m = top;
+                // The reference moves only when the tile passes it by 2^8 (or holds the row's first keys); whether any
+                // row of these 32 does is agreed by a barrier of the two warps, and only then are the parts'
+                // maxima exchanged.
+                const float mth = fmaxf(fmax3(a4[0], a4[1], a4[2]), a4[3]) * sc;   // this part's tile max (log2 units)
+                if (named_bar_or(pair, 32 * kParts, mth > m + kRescaleThreshold)) {
+                    sm->mx[t][h][row] = mth;
+                    named_bar_sync(pair, 32 * kParts);
+                    const float top = fmaxf(mth, sm->mx[t][h ^ 1][row]);
+                    if (top > m + kRescaleThreshold) {
+                        grow = m != -CUDART_INF_F;
+                        alpha = ex2_approx(m - top);   // 0 for the first keys
+                        l *= alpha;
+                        m = top;
+                    }
                 }
                 // with no key of the row yet (m = -inf) every weight is exp2(-inf) = 0
                 const float mref = (m == -CUDART_INF_F) ? 0.0f : m;
                 const float2 sc2 = make_float2(sc, sc);
                 const float2 nm2 = make_float2(-mref, -mref);
-                float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                uint32_t pk[64];
+                float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                uint32_t pk[kKeys / 2];
 #pragma unroll
-                for (int c = 0; c < 64; ++c) {
+                for (int c = 0; c < kKeys / 2; ++c) {
                     float2 e2 = make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
-                    e2 = ffma2(e2, sc2, nm2);
+                    if constexpr (kMode == kPlain) e2 = ffma2(e2, sc2, nm2);
+                    if constexpr (kMode == kGeneral) e2 = fadd2(e2, nm2);
                     e2.x = ex2_approx(e2.x);
                     e2.y = ex2_approx(e2.y);
-                    acc[c & 3] = fadd2(acc[c & 3], e2);
+                    acc[c & 1] = fadd2(acc[c & 1], e2);
                     // the weights are rounded to bf16 for the product; the sum takes them unrounded
                     pk[c] = pack_bf16x2(e2.x, e2.y);
                 }
-                const float2 s2 = fadd2(fadd2(acc[0], acc[1]), fadd2(acc[2], acc[3]));
+                const float2 s2 = fadd2(acc[0], acc[1]);
                 l += s2.x + s2.y;
                 // P_t and O_t are free once P.V(g - 1) has completed
                 if (g >= 1) {
@@ -413,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 }
                 if (j > from && __any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                    for (int q4 = 0; q4 < 4; ++q4) {
+                    for (int q4 = 0; q4 < kOut / 16; ++q4) {
                         uint32_t o[16];
                         tmem_ld_x16(o_tmem + q4 * 16, o);
 #pragma unroll
@@ -422,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                     }
                 }
 #pragma unroll
-                for (int q4 = 0; q4 < 4; ++q4)
+                for (int q4 = 0; q4 < kKeys / 32; ++q4)
                     tmem_st_x16_nowait(p_tmem + q4 * 16, *reinterpret_cast<const uint32_t(*)[16]>(&pk[16 * q4]));
                 tmem_st_wait();
                 tc_fence_before();
@@ -434,63 +475,67 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
             ok = mbar_wait(&sm->unit_full[nb], ((k + 1) >> 1) & 1, abort_flag, p.status, 0x840);
             x = sm->unit[nb];
             if (ok && x.b >= 0) span = span_of(p, x.b, x.q0 + t * BM + row);
-            // ---------------- output. The tile's Q buffer stages it: loaded (a tile without keys has read nothing of it
-            // yet) and, where it was used, read by its last score MMA.
-            uint8_t* qbuf = base + (2 * qb + t) * kTile;
-            mbar_wait(&sm->q_full[qb], (k >> 1) & 1, abort_flag, p.status, 0x841);
-            uint32_t o[64];
+            // ---------------- output: thread (h, row) writes its features of O / (l_0 + l_1). The output tile's buffer first
+            // carries l_h of both parts and every row; the previous unit's store has read it.
+            uint8_t* obuf = base + kOffO + t * kTile;
+            if (first) tma_store_wait_read();
+            named_bar_sync(1 + t, kGroup);
+            float* lsum = reinterpret_cast<float*>(obuf);
+            lsum[h * BM + row] = l;
+            named_bar_sync(pair, 32 * kParts);
+            const float L = lsum[row] + lsum[BM + row];
+            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
+            uint32_t o[kOut];
             if (to > from) {
                 mbar_wait(&sm->p_free[t], (g - 1) & 1, abort_flag, p.status, 0x842);   // the last P.V completes O
                 __syncwarp();
                 tc_fence_after();
-                tmem_ld_x64(o_tmem, o);
-                tc_fence_before();   // O has been read: the next unit's first P.V may overwrite it
-                const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // no key: a row of zeros; NaN stays
-#pragma unroll
-                for (int c = 0; c < 64; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv);
+                tmem_ld_x32(o_tmem, o);
             } else {
 #pragma unroll
-                for (int c = 0; c < 64; ++c) o[c] = 0u;
+                for (int c = 0; c < kOut; ++c) o[c] = 0u;
             }
-            const uint32_t stage = smem_u32(qbuf) + row * 128;
+            named_bar_sync(1 + t, kGroup);   // every thread has read the sums the staging overwrites
 #pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
+            for (int ch = 0; ch < kOut / 8; ++ch) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]), __uint_as_float(o[ch * 8 + 2 * e + 1]));
-                st_shared_v4(stage + ((ch ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
+                st_shared_v4(smem_u32(obuf) + row * 128 + (((h * (kOut / 8) + ch) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();
-            named_bar_sync(4 + t, BM);
-            if ((warp & 3) == 0 && lane == 0) {
-                if (!*abort_flag && q0 < p.Lq) {
-                    asm volatile(
-                        "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %2, %4, %5}], [%1];" ::"l"(
-                            reinterpret_cast<uint64_t>(&maps.out)),
-                        "r"(smem_u32(qbuf)), "r"(0), "r"(q0), "r"(head), "r"(b)
-                        : "memory");
-                    tma_store_commit();
-                }
-                tma_store_wait_read();   // the buffer may take the Q tile of unit k + 2
-                mbar_arrive(&sm->q_empty[qb]);
+            tc_fence_before();   // O has been read: the next unit's first P.V may overwrite it
+            named_bar_sync(1 + t, kGroup);
+            if (first && !*abort_flag && q0 < p.Lq) {
+                asm volatile(
+                    "cp.async.bulk.tensor.5d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %2, %4, %5}], [%1];" ::"l"(
+                        reinterpret_cast<uint64_t>(&maps.out)),
+                    "r"(smem_u32(obuf)), "r"(0), "r"(q0), "r"(head), "r"(b)
+                    : "memory");
+                tma_store_commit();
             }
         }
-        if ((warp & 3) == 0 && lane == 0) tma_store_wait_all();
+        if (first) tma_store_wait_all();
         tc_fence_before();
         named_bar_sync(3, kThreads);
     }
 }
 
-}  // namespace
-
-cudaError_t launch_span_attn_d64(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
+template <int kMode>
+cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
     static_assert(kSmemBytes <= 232448, "shared memory budget");
-    cudaError_t e = cudaFuncSetAttribute(span_attn_d64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(span_attn_d64_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(kSmemBytes));
     if (e != cudaSuccess) return e;
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + kRowsUnit - 1) / kRowsUnit));
-    return launch_pdl(span_attn_d64_kernel, dim3(grid), dim3(kThreads), kSmemBytes, s, p, maps);
+    return launch_pdl(span_attn_d64_kernel<kMode>, dim3(grid), dim3(kThreads), kSmemBytes, s, p, maps);
+}
+
+}  // namespace
+
+cudaError_t launch_span_attn_d64(const SpanAttnParams& p, const SpanMaps& maps, int mode, cudaStream_t s) {
+    return mode == kPlain ? launch_mode<kPlain>(p, maps, s) : launch_mode<kGeneral>(p, maps, s);
 }
 
 }  // namespace mha
