@@ -5,7 +5,7 @@
 #include <math_constants.h>
 
 #include "mha_internal.h"
-#include "ptx.cuh"
+#include "ptx_serve.cuh"
 #include "serve.h"
 
 namespace mha {

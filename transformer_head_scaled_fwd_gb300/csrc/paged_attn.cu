@@ -25,7 +25,7 @@
 #include "elem.cuh"
 #include "launch.h"
 #include "mha_internal.h"
-#include "ptx.cuh"
+#include "ptx_serve.cuh"
 #include "serve.h"
 
 namespace mha {
