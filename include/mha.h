@@ -399,7 +399,8 @@ typedef struct {
  *   their outputs are left as they were; rotary NULL: keys enter as they are.
  *   k_out NULL, or [B, T, h_kv, d_k]: the turned keys, for an attention over the prompt itself.
  *   q NULL, or [B, T, h, d_k] -> q_out turned the same way.
- * In-place rules as for mha_rotary. start is not changed: the caller adds the counts.
+ * In-place rules as for mha_rotary; no output overlaps another input either (k_out may be k only
+ * where v is not the same memory). start is not changed: the caller adds the counts.
  */
 mha_status_t mha_paged_append(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
                               void* q_out, const mha_strides_t* q_out_strides,
@@ -467,7 +468,8 @@ mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* s
  *   q [B, L_q, h, d_k], k and v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]
  * h a multiple of h_kv (head n reads key head n / (h / h_kv)); scores, mask NULL: plain, all keys.
  * MHA_BF16 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
- * behind key_valid_lens[b] are not used, whatever they hold. No workspace.
+ * behind key_valid_lens[b] are not used, whatever they hold; elsewhere a masked value that is not
+ * finite may reach rows that do not attend to it (0 * NaN). No workspace.
  */
 mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
                            const void* k, const mha_strides_t* k_strides,

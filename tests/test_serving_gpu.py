@@ -754,3 +754,90 @@ def test_attention_and_norm_captured(bnd):
         R.check(out, ref, tol, "captured attention")
         z, want = norm_ref(out.view(B * L, h * d), None, None, 1e-6)
         R.check(y, want, norm_tol(z, want, h * d, BF), "captured norm")
+
+
+def _step(bnd, seed, stream=None):
+    """One call of each operator on its own tensors; the outputs."""
+    B, h, hk, d, page = 2, 8, 2, 64, 16
+    table, n_pages = table_of(seed, B, 20)
+    kp, vp = pages_of(seed + 1, n_pages, page, hk, d, BF)
+    cache = bnd.make_paged_cache(kp, vp, table)
+    q, k, v = randn(seed + 3, B, 70, h, d, dtype=BF), randn(seed + 4, B, 70, hk, d, dtype=BF), randn(seed + 5, B, 70, hk, d, dtype=BF)
+    q1, k1, att, dec = torch.empty_like(q), torch.empty_like(k), torch.empty_like(q), torch.empty(B, h, d, dtype=BF, device="cuda")
+    ws = torch.empty(bnd.paged_attention_workspace_size(bnd.MHA_BF16, B, h, hk, d), dtype=torch.uint8, device="cuda")
+    y = torch.empty(B * 70, h * d, dtype=BF, device="cuda")
+    ids = docs_of(seed + 6, B, 70, 20)
+    spans = torch.empty(B, 70, 2, dtype=torch.int32, device="cuda")
+    rot, zero, held = bnd.make_rotary(freqs(d)), ints([0] * B), ints([300, 70])
+    torch.cuda.synchronize()
+
+    def call():
+        bnd.mha_paged_append(k, v, zero, cache=cache, q=q, q_out=q1, k_out=k1, rotary=rot, stream=stream)
+        bnd.mha_document_spans(ids, spans=spans, stream=stream)
+        bnd.mha_attention(q1, k1, v, out=att, mask=bnd.make_span_mask(causal=True, doc_spans=spans), stream=stream)
+        bnd.mha_rmsnorm(att.view(B * 70, h * d), None, 1e-6, y=y, stream=stream)
+        bnd.mha_paged_attention(q1[:, 69], held, cache=cache, out=dec, workspace=ws, stream=stream)
+    return call, (q1, k1, att, dec, y, kp, vp)
+
+
+def test_explicit_streams_from_two_host_threads(bnd):
+    """Two host threads, a stream each, call after call at once: the same results as one after the other."""
+    import threading
+    want = []
+    for seed in (300, 320):
+        call, outs = _step(bnd, seed)
+        call()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+    jobs, errors = [], []
+    for seed in (300, 320):
+        s = torch.cuda.Stream()
+        jobs.append(_step(bnd, seed, s) + (s,))
+
+    def work(job):
+        try:
+            for _ in range(50):
+                job[0]()
+            job[2].synchronize()
+        except Exception as e:
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for job, ref in zip(jobs, want):
+        for got, o in zip(job[1], ref):
+            assert torch.equal(got, o)
+
+
+def test_first_call_may_be_captured():
+    """A fresh process whose first calls are captured into a graph: nothing has to be set up before."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import test_serving_gpu as T
+from transformer_head_scaled_fwd_gb300 import binding as bnd
+call, outs = T._step(bnd, 340)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = [o.clone() for o in outs]
+for o in outs[:5]:
+    o.zero_()
+call()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, outs))
+assert bnd.mha_check_device_status() == 0
+print("captured first")
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr

@@ -47,6 +47,20 @@ __device__ __forceinline__ void tma_load_5d(const CUtensorMap* m, uint64_t* bar,
         : "memory");
 }
 
+// After a give-up: waits, with a limit of its own, until the copy that completes phase `parity` of `bar` has landed, so
+// that none is in flight when the CTA's shared memory is released.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+    const uint32_t a = smem_u32(bar);
+    for (uint32_t it = 0; it < (1u << 16) && !mbar_try_wait(a, parity); ++it) {
+    }
+}
+// The last tiles of a ring of kStages into which `issued` were loaded.
+template <int kStages>
+__device__ __forceinline__ void drain_ring(uint64_t* full, uint32_t issued) {
+    for (uint32_t i = 1; i <= kStages && i <= issued; ++i)
+        drain(&full[(issued - i) % kStages], ((issued - i) / kStages) & 1);
+}
+
 // Work stealing: the grid has one CTA a unit; a running CTA asks the hardware to cancel the launch of
 // one that has not started and does its unit instead (its set-up is paid once, and no counter in
 // memory is needed). After a refusal no further request is made.

@@ -188,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
         if (warp == kSoftWarps) {
             // ------------------------------------------------ scheduler, Q and K loads
             int u = blockIdx.x;
-            uint32_t gk = 0;   // K tiles issued so far
-            for (int k = 0;; ++k) {
+            uint32_t gk = 0;       // K tiles issued so far
+            int loaded = 0;        // units whose Q was
+            for (int k = 0;; ++k, ++loaded) {
                 const int qb = k & 1;
                 // the score MMAs of unit k - 2 have read this Q buffer, and every role its slot
                 if (k >= 2) mbar_wait(&sm->q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.status, 0x830);
@@ -227,6 +228,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 }
                 __syncwarp();
             }
+            if (lane == 0 && *abort_flag) {
+                drain_ring<kStages>(sm->k_full, gk);
+                drain_ring<2>(sm->q_full, loaded);
+                drain_ring<2>(sm->steal_full, loaded);
+            }
         } else if (warp == kSoftWarps + 3) {
             // ------------------------------------------------ V loads
             uint32_t gv = 0, edges = 0;
@@ -263,6 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                         if (lane == 0) mbar_arrive(&sm->v_full[s]);
                     }
                 }
+            }
+            if (lane == 0 && *abort_flag) {
+                drain_ring<kStages>(sm->v_full, gv);
+                if (edges > 0) drain(&sm->v_edge, (edges - 1) & 1);
             }
         } else if (warp == kSoftWarps + 1 && lane == 0) {
             // ------------------------------------------------ score MMAs: S_t(j) = Q_t K_j^T
