@@ -286,19 +286,20 @@ struct WarpF32 {
     float o[kR][kOwn];
     float m[kR], l[kR];                                   // l is this lane's share
     uint32_t q;                                           // the unit's query rows in shared memory
-    const float* slopes;
+    float slope[kR];
 
     // two (or four) keys of a quarter-warp's 16-byte reads land in different 64-byte (32-byte) parts
     static __device__ __forceinline__ int swizzle(int row) { return kLanes == 4 ? (row & 1) << 2 : (row & 3) << 1; }
 
     __device__ __forceinline__ void start(const PagedAttnParams& p, float* shared_q, int b, int head0, int rows, int) {
         const float* x = static_cast<const float*>(p.q) + b * p.q_b + head0 * p.q_h;
-        for (int i = threadIdx.x; i < rows * kD; i += kThreads) shared_q[i] = x[(i / kD) * p.q_h + i % kD];
+        for (int i = threadIdx.x; i < kR * kD; i += kThreads)
+            shared_q[i] = i < rows * kD ? x[(i / kD) * p.q_h + i % kD] : 0.0f;
         __syncthreads();      // the last unit's readers are behind the barriers of its end
         q = smem_u32(shared_q);
-        slopes = p.slopes != nullptr ? p.slopes + head0 : nullptr;
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
+            slope[r] = p.slopes != nullptr && r < rows ? p.slopes[head0 + r] * kLog2e : 0.0f;
             m[r] = -CUDART_INF_F;
             l[r] = 0.0f;
 #pragma unroll
@@ -306,6 +307,8 @@ struct WarpF32 {
         }
     }
 
+    // All kR rows are computed, whether the unit has them or not: their chains then run side by side (with a test a
+    // row, 16 x 8192 at 4 heads a key head took 125 us).
     __device__ __forceinline__ void step(uint32_t k, uint32_t v, int key0, uint32_t live, int n, const ScoreForm& form,
                                          int rows, int lane) {
         constexpr int kRow = Step<T, kD>::kRow;
@@ -329,9 +332,9 @@ struct WarpF32 {
         }
         const bool ok = (live >> key) & 1u;
         const float away = static_cast<float>(n - 1 - key0 - key);
+        float s[kR];
 #pragma unroll
         for (int r = 0; r < kR; ++r) {
-            if (r >= rows) break;
             float d0 = 0.0f, d1 = 0.0f;
 #pragma unroll
             for (int i = 0; i < kDims / 4; ++i) {
@@ -343,22 +346,32 @@ struct WarpF32 {
                 d0 = fmaf(kv[i].z, x.z, d0);
                 d1 = fmaf(kv[i].w, x.w, d1);
             }
-            float s = d0 + d1;
+            s[r] = d0 + d1;
+        }
+        bool more = false;
 #pragma unroll
-            for (int w = 1; w < kLanes; w <<= 1) s += __shfl_xor_sync(0xffffffffu, s, w);
-            s = ok ? form.of<true>(s, slopes != nullptr ? slopes[r] * kLog2e : 0.0f, away) : -CUDART_INF_F;
-            float top = s;
+        for (int r = 0; r < kR; ++r) {
 #pragma unroll
-            for (int w = kLanes; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-            const float to = fmaxf(top, m[r]);
-            if (to > m[r]) {      // the same in every lane
-                const float alpha = m[r] == -CUDART_INF_F ? 0.0f : ex2_approx(m[r] - to);
+            for (int w = 1; w < kLanes; w <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], w);
+            s[r] = ok ? form.of<true>(s[r], slope[r], away) : -CUDART_INF_F;
+            more |= s[r] > m[r];
+        }
+        if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+            for (int r = 0; r < kR; ++r) {
+                float top = fmaxf(s[r], m[r]);
+#pragma unroll
+                for (int w = kLanes; w < 32; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float alpha = m[r] == -CUDART_INF_F ? 0.0f : ex2_approx(m[r] - top);   // 1 where it stays
                 l[r] *= alpha;
 #pragma unroll
                 for (int e = 0; e < kOwn; ++e) o[r][e] *= alpha;
-                m[r] = to;
+                m[r] = top;
             }
-            const float w = ex2_approx(s - (m[r] == -CUDART_INF_F ? 0.0f : m[r]));
+        }
+#pragma unroll
+        for (int r = 0; r < kR; ++r) {
+            const float w = ex2_approx(s[r] - (m[r] == -CUDART_INF_F ? 0.0f : m[r]));
             if (part == 0) l[r] += w;
 #pragma unroll
             for (int j = 0; j < kKeys; ++j) {
@@ -472,7 +485,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         return;
     }
     // CTA c takes blocks [c total / ctas, (c + 1) total / ctas); block t belongs to the last CTA that starts at or before it
-    long long t0 = c * total / ctas, t1 = (c + 1) * total / ctas;
+    const bool small = total < (1 << 24);       // kMaxCtas * total fits 32 bits: divisions a quarter as long
+    auto start_of = [&](long long i) -> long long {
+        return small ? static_cast<uint32_t>(i * total) / static_cast<uint32_t>(ctas) : i * total / ctas;
+    };
+    long long t0 = start_of(c), t1 = start_of(c + 1);
     auto owner = [&](long long t) { return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1); };
 
     // ---- the sequences that t0 and t1 fall into (t1 may be the end of the line)
@@ -507,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         x.n = lens.len(x.b);
         x.nblk = lens.blocks(x.n);
         const long long rem = t - f.before;
-        x.unit = static_cast<int>(rem / x.nblk);
+        x.unit = small ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(x.nblk)) : static_cast<int>(rem / x.nblk);
         x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * x.nblk);
         return x;
     };
@@ -526,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             d.c1 = owner(u0 + at.nblk - 1);
             d.b = at.b;
             d.unit = at.unit;
-            d.first_slot = (c - 1) * total / ctas == u0 ? 0 : 1;
+            d.first_slot = start_of(c - 1) == u0 ? 0 : 1;
         }
         join[c] = d;
     }
