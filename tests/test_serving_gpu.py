@@ -598,6 +598,26 @@ def test_rmsnorm_strides_and_zero_rows(bnd):
     bnd.mha_rmsnorm(odd, g, 1e-6, y=y)
     z, ref = norm_ref(odd, None, g, 1e-6)
     R.check(y, ref, norm_tol(z, ref, d, BF), "unaligned")
+    for dt in (BF, F32):                                              # every start within a 16-byte piece, odd lengths
+        for first in range(9):
+            for n in (1, 3, 9, 700, 1023, 5001):
+                a = randn(500 + first, 3 * n + first, dtype=dt)[first:].view(3, n)
+                b = randn(510 + first, 3 * n + first, dtype=dt)[first:].view(3, n)
+                outs = [torch.full((3 * n + first + 9,), 5.0, dtype=dt, device="cuda") for _ in range(2)]
+                yy, ss = (o[first:first + 3 * n].view(3, n) for o in outs)
+                gg = randn(520, n, dtype=dt)
+                bnd.mha_rmsnorm(a, gg, 1e-6, y=yy, residual=b, sum_out=ss)
+                z, ref = norm_ref(a, b, gg, 1e-6)
+                R.check(yy, ref, norm_tol(z, ref, n, dt), f"start {first}")
+                R.check(ss, z, R.HALF[dt] * z.abs(), "sum")
+                for o in outs:
+                    assert (o[:first] == 5).all() and (o[first + 3 * n:] == 5).all()
+                y8 = torch.full((3 * n + first + 9,), 3.0, device="cuda").to(E4M3)
+                sc = torch.empty(3, 1, device="cuda")
+                bnd.mha_rmsnorm(a, gg, 1e-6, y=y8[first:first + 3 * n].view(3, n), residual=b, scales=sc)
+                v = ref / (ref.abs().amax(dim=1, keepdim=True) / 448)
+                R.check(y8.float()[first:first + 3 * n].view(3, n), v, 2.0 ** -4 * v.abs() * 1.01 + 2.0 ** -10 + 448 * n * 2.0 ** -23, "e4m3")
+                assert (y8.float()[:first] == 3).all() and (y8.float()[first + 3 * n:] == 3).all()
     one = randn(123, 1, d, dtype=BF).expand(rows, d)                  # one residual for all rows
     bnd.mha_rmsnorm(x, g, 1e-6, y=y, residual=one)
     z, ref = norm_ref(x, one, g, 1e-6)
