@@ -6,7 +6,10 @@
 // Dekker): t * f in one float is off by up to 2^-25 of its size, 0.03 rad at t = 10^6. Whole turns
 // are removed exactly before the sum is rounded, so cos and sin are good to a few 2^-24 anywhere.
 //
-// HBM-bound: every element is read once and written once (keys twice where k_out is asked for).
+// HBM-bound: every element is read once and written once (keys twice where k_out is asked for). Measured, 4 x 8192
+// tokens appended in bf16: 32 + 8 heads of 128, half of each turned, 872 MB: 134 us, 6.5 TB/s (0.96 of measured copy
+// bandwidth); 16 + 16 heads of 64: 76 us (0.91); 3 x 2501 tokens of 16 + 16 fp32 heads of 64, no cache: 22.7 us (0.80,
+// start and end included).
 #include <algorithm>
 
 #include "elem.cuh"
