@@ -378,21 +378,17 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 float sc = 1.0f;
                 if constexpr (kMode == kPlain) {
                     if (edge) {
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                        scale_scores(u, scale_log2);
                     } else {
                         sc = scale_log2;
                     }
                 } else if constexpr (kMode == kCapped) {
                     cap_scores(u, capped);
                 } else {
-                    if (p.cap > 0.0f) {
-                        cap_scores(u, capped);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
-                    }
-                    if (slope != 0.0f) bias_scores(u, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                    if (p.cap > 0.0f) cap_scores(u, capped);
+                    const float by = p.cap > 0.0f ? 1.0f : scale_log2;
+                    if (slope != 0.0f) bias_scores(u, by, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                    else if (by != 1.0f) scale_scores(u, by);
                 }
                 if (edge) {
                     const uint32_t first = iv.x - k0, many = max(iv.y - iv.x, 0);   // keys first .. first + many - 1 of u

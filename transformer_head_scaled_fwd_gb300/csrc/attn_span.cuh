@@ -158,17 +158,27 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm&
     }
 }
 
-// Scores in log2 units minus slope |i - j|: away = i - (first key of u), slope in log2 units.
 template <int kKeys>
-__device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, float slope) {
+__device__ __forceinline__ void scale_scores(uint32_t (&u)[kKeys], float scale) {
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 2) {
+        const float2 r = fmul2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), make_float2(scale, scale));
+        u[c] = __float_as_uint(r.x);
+        u[c + 1] = __float_as_uint(r.y);
+    }
+}
+
+// u * scale - slope |i - j|: away = i - (first key of u), scale and slope in log2 units.
+template <int kKeys>
+__device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float scale, float away, float slope) {
     const bool below = away >= kKeys - 1.0f, above = away <= 0.0f;
+    const float2 sc = make_float2(scale, scale);
     if (__all_sync(0xffffffffu, below) || __all_sync(0xffffffffu, above)) {   // |away - c| is linear in c
         const float s = __all_sync(0xffffffffu, below) ? slope : -slope;
-        float2 b = make_float2(-s * away, fmaf(-s, away, s));
-        const float2 step = make_float2(2.0f * s, 2.0f * s);
+        const float2 b = make_float2(-s * away, fmaf(-s, away, s)), step = make_float2(2.0f * s, 2.0f * s);
 #pragma unroll
         for (int c = 0; c < kKeys / 2; ++c) {
-            const float2 r = fadd2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])),
+            const float2 r = ffma2(make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1])), sc,
                                    ffma2(step, make_float2(c, c), b));
             u[2 * c] = __float_as_uint(r.x);
             u[2 * c + 1] = __float_as_uint(r.y);
@@ -176,7 +186,7 @@ __device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float away, fl
     } else {
 #pragma unroll
         for (int c = 0; c < kKeys; ++c)
-            u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c])));
+            u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c]) * scale));
     }
 }
 

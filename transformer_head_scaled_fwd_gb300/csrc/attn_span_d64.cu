@@ -11,8 +11,8 @@
 //
 // Measured, 4 x 8192 causal, 16 heads: 541 us, 1017 TFLOP/s (0.53 of measured bf16 peak; all keys 1072); the kernel of
 // one query tile 660 us; two query tiles with one thread a row (eight softmax warps) 581 us, all keys 987 against 1026
-// us. With a distance bias 935 (1099) us. Capped scores without a maximum gain nothing from it (795 against 721 us) and
-// stay with the other kernel.
+// us. With a distance bias 814 us (1099 in the other layout, with scale and bias as two steps). Capped scores without a
+// maximum gain nothing from it (795 against 721 us) and stay with the other kernel.
 //
 // Tensor memory (512 columns): S_0 S_1 (fp32, 128 each), P_0 P_1 (bf16, 64 each), O_0 O_1 (fp32, 64 each).
 // Shared memory: two Q buffers of two tiles, K and V rings of four tiles, the two output tiles on their way out. Warps:
@@ -390,19 +390,15 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 float sc = 1.0f;
                 if constexpr (kMode == kPlain) {
                     if (edge) {
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
+                        scale_scores(u, scale_log2);
                     } else {
                         sc = scale_log2;
                     }
                 } else {
-                    if (p.cap > 0.0f) {
-                        cap_scores(u, capped);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) * scale_log2);
-                    }
-                    if (slope != 0.0f) bias_scores(u, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                    if (p.cap > 0.0f) cap_scores(u, capped);
+                    const float by = p.cap > 0.0f ? 1.0f : scale_log2;
+                    if (slope != 0.0f) bias_scores(u, by, static_cast<float>(q0 + row + p.q_offset - k0), slope);
+                    else if (by != 1.0f) scale_scores(u, by);
                 }
                 if (edge) {
                     const uint32_t first = iv.x - k0, many = max(iv.y - iv.x, 0);   // keys first .. first + many - 1 of u
