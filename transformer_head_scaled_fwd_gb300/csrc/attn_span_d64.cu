@@ -11,7 +11,7 @@
 //
 // Measured, 4 x 8192 causal, 16 heads: 541 us, 1017 TFLOP/s (0.53 of measured bf16 peak; all keys 1072); the kernel of
 // one query tile 660 us; two query tiles with one thread a row (eight softmax warps) 581 us, all keys 987 against 1026
-// us. With a distance bias 814 us (1099 in the other layout, with scale and bias as two steps). Capped scores without a
+// us. With a distance bias 814 us (in the other layout 896). Capped scores without a
 // maximum gain nothing from it (795 against 721 us) and stay with the other kernel.
 //
 // Tensor memory (512 columns): S_0 S_1 (fp32, 128 each), P_0 P_1 (bf16, 64 each), O_0 O_1 (fp32, 64 each).
