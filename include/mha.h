@@ -467,7 +467,7 @@ mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* s
  * Attention with grouped heads over strided tensors, scores and mask as above:
  *   q [B, L_q, h, d_k], k and v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]
  * h a multiple of h_kv (head n reads key head n / (h / h_kv)); scores, mask NULL: plain, all keys.
- * MHA_BF16 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
+ * MHA_BF16 or MHA_F32 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
  * behind key_valid_lens[b] are not used, whatever they hold; elsewhere a masked value that is not
  * finite may reach rows that do not attend to it (0 * NaN). No workspace.
  */
@@ -482,13 +482,13 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
  * RMS norm of rows, with the residual's addition before it and, on request, 8-bit output:
  *   z = x + residual;  y = gain * z / sqrt(mean(z^2) + eps)
  *   x, residual, sum [rows, d] with row strides (elements), type dt; residual NULL: z = x, and sum is
- *   ignored; sum NULL: z is not written. sum may be x or residual (same stride). The norm is of the
- *   fp32 sum, not of its rounding. gain [d] type dt, or NULL (ones).
+ *   ignored; sum NULL: z is not written. sum may be x or residual, and y of type dt too if sum is not (same
+ *   stride). The norm is of the fp32 sum, not of its rounding. gain [d] type dt, or NULL (ones).
  *   scales NULL: y has type dt. Otherwise y is e4m3 (1 byte an element, finite form): each group of
  *   `group` elements of a row (0: the whole row; else 32, 64 or 128, dividing d) has
  *   scale = max |y| / 448 (1 where that is 0), y8 = y / scale rounded to nearest even, and scales
  *   [rows, groups], fp32, contiguous, receives it. NaN stays NaN.
- *   d >= 1, any; rows >= 0.
+ *   1 <= d <= 2^30; rows >= 0.
  */
 mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const void* residual,
                          int64_t residual_stride, void* sum, int64_t sum_stride, const void* gain, float eps,

@@ -96,7 +96,8 @@ def test_attention_refusals(lib):
     def call(dt=1, q=P, k=P, v=P, out=P, B_=2, Lq=8, Lk=8, h=8, hk=4, d=64, sc=None, qs=None, mask=None):
         return lib.mha_attention(dt, q, qs or st(), k, st(), v, st(), out, st(), B_, Lq, Lk, h, hk, d, sc,
                                  ctypes.byref(mask) if mask is not None else None, None)
-    assert call(dt=0) == UNS
+    assert call(dt=3) == INV and call(dt=0, qs=st(l=66)) == INV and call(dt=0, q=ctypes.c_void_p(4100)) == INV
+    assert call(Lk=0x7fffff01) == UNS and call(Lq=0x7fffff01) == UNS
     assert call(d=32) == UNS and call(h=6) == INV and call(Lk=0) == INV
     assert call(q=None) == INV and call(out=None) == INV
     assert call(qs=st(l=65)) == INV and call(q=ctypes.c_void_p(4104)) == INV
@@ -117,7 +118,7 @@ def test_rmsnorm_refusals(lib):
     def call(dt=1, x=P, r=P, s=P, y=P, rows=4, d=256, eps=1e-6, scales=None, group=0, ys=256, ss=256, xs=256):
         return lib.mha_rmsnorm(dt, x, xs, r, 256, s, ss, None, eps, rows, d, y, ys, scales, group, None)
     assert call(dt=3) == INV
-    assert call(rows=-1) == INV and call(d=0) == INV and call(rows=1 << 31) == UNS
+    assert call(rows=-1) == INV and call(d=0) == INV and call(rows=1 << 31) == UNS and call(d=(1 << 30) + 1) == UNS
     assert call(eps=-1.0) == INV and call(eps=math.nan) == INV
     assert call(x=None) == INV and call(y=None) == INV
     assert call(x=ctypes.c_void_p(4097)) == INV

@@ -461,6 +461,44 @@ def test_attention(bnd, B, Lq, Lk, h, hk, d, opt):
     assert torch.equal(got, run_attention(bnd, q, k, v, **opt))
 
 
+@pytest.mark.parametrize("B,Lq,Lk,h,hk,d,opt", ATT)
+def test_attention_fp32(bnd, B, Lq, Lk, h, hk, d, opt):
+    opt = dict(opt)
+    pad = opt.pop("pad", 0)
+    if opt.get("slopes"):
+        opt["slopes"] = slopes_of(h)
+    if opt.get("docs"):
+        opt["docs"] = docs_of(64, B, Lk, opt["docs"], pad)
+    q, kv = randn(65, B, Lq, h, d) * 1.5, randn(66, B, Lk, 2 * hk, d)
+    k, v = kv[:, :, :hk], kv[:, :, hk:]
+    if opt.get("valid"):
+        for b, n in enumerate(opt["valid"]):
+            k[b, n:], v[b, n:] = float("nan"), float("inf")
+    got = run_attention(bnd, q, k, v, **opt)
+    ref, tol = attention_ref(q, k, v, **opt)
+    R.check(got, ref, tol, "attention, fp32")
+    assert torch.equal(got, run_attention(bnd, q, k, v, **opt))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_fp32_strides_and_spans(bnd, d):
+    """Head-major storage, a shared query (stride 0), a key at a 16-byte start inside wider rows, an output inside a wider
+    tensor, arbitrary spans."""
+    B, L, h, hk = 2, 150, 4, 2
+    q = randn(67, B, L, 1, d).expand(B, L, h, d)
+    k = randn(68, B, L, hk, d + 8)[..., 4:d + 4]
+    v = randn(69, 1, hk, L, d).transpose(1, 2).expand(B, L, hk, d)
+    rng = random.Random(9)
+    spans = ints([[[rng.randint(-20, L), rng.randint(-20, L + 20)] for _ in range(L)] for _ in range(B)])
+    wide = torch.full((B, L, h + 3, d), 7.0, device="cuda")
+    got = run_attention(bnd, q, k, v, out=wide[:, :, 1:h + 1], spans=spans, scale=0.3)
+    ref, tol = attention_ref(q, k, v, spans=spans, scale=0.3)
+    R.check(got, ref, tol, "spans")
+    assert (wide[:, :, 0] == 7).all() and (wide[:, :, h + 1:] == 7).all()
+    empty = spans[..., 0].clamp(min=0) >= spans[..., 1].clamp(max=L)
+    assert empty.any() and (got[empty] == 0).all()
+
+
 @pytest.mark.parametrize("d,L", [(64, 200), (128, 200), (64, 1650)])
 def test_attention_head_major_strides_and_spans(bnd, d, L):
     """[B, h, L, d] storage (the workspace's order), an output inside a wider tensor, arbitrary spans with
@@ -560,6 +598,9 @@ def test_rmsnorm(bnd, dtype, rows, d, res, gain):
         assert torch.equal(y2, y) and torch.equal(s3, s)
         bnd.mha_rmsnorm(x, g, 1e-5, y=y2, residual=r)                        # no sum wanted
         assert torch.equal(y2, y)
+    y3 = x.clone()
+    bnd.mha_rmsnorm(y3, g, 1e-5, y=y3, residual=r)                           # y over x
+    assert torch.equal(y3, y)
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -659,16 +700,17 @@ def test_rmsnorm_nan_stays_in_its_row(bnd):
 
 
 # ------------------------------------------------------------------------------------------ together
-@pytest.mark.parametrize("h,hk,d,sc", [(4, 2, 64, dict(cap=30.0)), (4, 1, 128, dict(slopes=True))])
-def test_prompt_and_steps_together(bnd, h, hk, d, sc):
+@pytest.mark.parametrize("dtype,h,hk,d,sc", [(BF, 4, 2, 64, dict(cap=30.0)), (BF, 4, 1, 128, dict(slopes=True)),
+                                             (F32, 4, 2, 64, dict(slopes=True)), (F32, 4, 1, 128, dict(cap=30.0))])
+def test_prompt_and_steps_together(bnd, dtype, h, hk, d, sc):
     """Norm, projection, rotary and append, attention over the prompt, then single tokens over the cache: every
     step's output equals the row that attention over the whole sequence gives, in 64 bits from the same
     projected tensors."""
     B, L, T0, width, page = 3, 150, 121, 256, 16
     lens = [121, 64, 1]
     sc = {n: slopes_of(h) if n == "slopes" else x for n, x in sc.items()}
-    x, gain = randn(140, B, L, width, dtype=BF), (randn(141, width) * 0.2 + 1).to(BF)
-    w = randn(142, (h + 2 * hk) * d, width, dtype=BF) * width ** -0.5
+    x, gain = randn(140, B, L, width, dtype=dtype), (randn(141, width) * 0.2 + 1).to(dtype)
+    w = randn(142, (h + 2 * hk) * d, width, dtype=dtype) * width ** -0.5
     normed = torch.empty_like(x)
     bnd.mha_rmsnorm(x.view(B * L, width), gain, 1e-6, y=normed.view(B * L, width))
     qkv = (normed @ w.T).view(B, L, h + 2 * hk, d)
@@ -679,11 +721,11 @@ def test_prompt_and_steps_together(bnd, h, hk, d, sc):
     qr, kr = torch.empty_like(q), torch.empty_like(k)
     bnd.mha_rotary(q, k=k, q_out=qr, k_out=kr, rotary=rot)
     table, n_pages = table_of(143, B, -(-L // page))
-    kp, vp = pages_of(144, n_pages, page, hk, d, BF)
+    kp, vp = pages_of(144, n_pages, page, hk, d, dtype)
     kp.fill_(float("nan")), vp.fill_(float("nan"))
     cache = bnd.make_paged_cache(kp, vp, table)
     scores = bnd.make_scores(**sc)
-    q0, k0 = torch.empty(B, T0, h, d, dtype=BF, device="cuda"), torch.empty(B, T0, hk, d, dtype=BF, device="cuda")
+    q0, k0 = torch.empty(B, T0, h, d, dtype=dtype, device="cuda"), torch.empty(B, T0, hk, d, dtype=dtype, device="cuda")
     held = ints([0] * B)
     bnd.mha_paged_append(k[:, :T0], v[:, :T0], held, cache=cache, q=q[:, :T0], q_out=q0, k_out=k0, new_lens=ints(lens), rotary=rot)
     held += ints(lens)
@@ -694,8 +736,8 @@ def test_prompt_and_steps_together(bnd, h, hk, d, sc):
     ref, tol = attention_ref(qr, kr, v, causal=True, **sc)
     for b, n in enumerate(lens):
         R.check(out[b, :n], ref[b, :n], tol[b, :n], "prompt")
-    ws = torch.empty(bnd.paged_attention_workspace_size(bnd.MHA_BF16, B, h, hk, d), dtype=torch.uint8, device="cuda")
-    q1, o1 = torch.empty(B, 1, h, d, dtype=BF, device="cuda"), torch.empty(B, h, d, dtype=BF, device="cuda")
+    ws = torch.empty(bnd.paged_attention_workspace_size(bnd.MHA_BF16 if dtype == BF else bnd.MHA_F32, B, h, hk, d), dtype=torch.uint8, device="cuda")
+    q1, o1 = torch.empty(B, 1, h, d, dtype=dtype, device="cuda"), torch.empty(B, h, d, dtype=dtype, device="cuda")
     for step in range(20):
         at = [n + step for n in lens]
         pick = lambda t: torch.stack([t[b, at[b]:at[b] + 1] for b in range(B)])

@@ -98,7 +98,8 @@ struct SpanAttnParams {
     int B, Lq, Lk, h, h_kv, d;
     int* status;
 };
-cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s);
+cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s);        // bf16
+cudaError_t launch_span_attn_f32(const SpanAttnParams& p, cudaStream_t s);
 cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spans, cudaStream_t s);
 
 // ------------------------------------------------------------ RMS norm

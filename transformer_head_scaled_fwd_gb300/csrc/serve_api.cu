@@ -280,9 +280,11 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
                            const mha_strides_t* out_strides, int B, int L_q, int L_k, int h, int h_kv, int d_k,
                            const mha_scores_t* scores, const mha_span_mask_t* mask, void* stream) {
     mha_status_t st;
-    if (dt != MHA_BF16) return fail(MHA_ERR_UNSUPPORTED, "attention under span masks is implemented for bf16 only");
+    if ((st = check_dtype(dt)) != MHA_OK) return st;
     if (B <= 0 || L_q <= 0 || L_k <= 0)
         return fail(MHA_ERR_INVALID_ARG, "sizes must be positive (B=%d L_q=%d L_k=%d)", B, L_q, L_k);
+    if (L_q > 0x7fffff00 || L_k > 0x7fffff00)
+        return fail(MHA_ERR_UNSUPPORTED, "L_q and L_k must stay below 2^31 - 255 (got %d, %d)", L_q, L_k);
     if ((st = check_heads(h, h_kv)) != MHA_OK) return st;
     if (d_k != 64 && d_k != 128)
         return fail(MHA_ERR_UNSUPPORTED, "attention under span masks is implemented for d_k = 64 and 128 (d_k = %d)", d_k);
@@ -292,14 +294,15 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
     const mha_strides_t* strides[4] = {q_strides, k_strides, v_strides, out_strides};
     mha::Strided* views[4] = {&p.q, &p.k, &p.v, &p.out};
     const char* names[4] = {"q", "k", "v", "out"};
+    const int64_t chunk = 16 / static_cast<int64_t>(elem(dt));
     for (int i = 0; i < 4; ++i) {
         const int L = i == 0 || i == 3 ? L_q : L_k, H = i == 0 || i == 3 ? h : h_kv;
-        if ((st = view(ptrs[i], strides[i], 2, names[i], views[i])) != MHA_OK) return st;
+        if ((st = view(ptrs[i], strides[i], elem(dt), names[i], views[i])) != MHA_OK) return st;
         // a dimension of one element has no stride to speak of
-        if (B == 1) views[i]->b = 8;
-        if (L == 1) views[i]->l = 8;
-        if (H == 1) views[i]->h = 8;
-        if (!aligned(ptrs[i], 16) || views[i]->b % 8 != 0 || views[i]->l % 8 != 0 || views[i]->h % 8 != 0)
+        if (B == 1) views[i]->b = chunk;
+        if (L == 1) views[i]->l = chunk;
+        if (H == 1) views[i]->h = chunk;
+        if (!aligned(ptrs[i], 16) || views[i]->b % chunk != 0 || views[i]->l % chunk != 0 || views[i]->h % chunk != 0)
             return fail(MHA_ERR_INVALID_ARG, "%s and its strides must be aligned to 16 bytes", names[i]);
         if (views[i]->l == 0 || (i == 3 && (views[i]->b == 0 || views[i]->h == 0)))
             return fail(MHA_ERR_INVALID_ARG, "%s: only the batch and head strides of an input may be 0", names[i]);
@@ -317,12 +320,13 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
         p.spans = mask->doc_spans;
     }
     if (static_cast<int64_t>(B) * h > (int64_t(1) << 30) ||
-        static_cast<int64_t>(B) * h * ((L_q + 127) / 128) > 0x7fffffffll)
-        return fail(MHA_ERR_UNSUPPORTED, "B * h * ceil(L_q / 128) must stay below 2^31");
+        static_cast<int64_t>(B) * h * ((L_q + 63) / 64) > 0x7fffffffll)
+        return fail(MHA_ERR_UNSUPPORTED, "B * h * ceil(L_q / 64) must stay below 2^31");
     p.B = B; p.Lq = L_q; p.Lk = L_k; p.h = h; p.h_kv = h_kv; p.d = d_k;
     p.status = mha::device_status();
     if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
-    return launched(mha::launch_span_attn(p, as_stream(stream)), "attention");
+    return launched(dt == MHA_BF16 ? mha::launch_span_attn(p, as_stream(stream)) : mha::launch_span_attn_f32(p, as_stream(stream)),
+                    "attention");
 }
 
 mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
@@ -332,7 +336,8 @@ mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const 
     if ((st = check_dtype(dt)) != MHA_OK) return st;
     if (rows < 0 || d <= 0) return fail(MHA_ERR_INVALID_ARG, "rows must be >= 0 and d positive (rows=%lld d=%d)",
                                         static_cast<long long>(rows), d);
-    if (rows > 0x7fffffffll) return fail(MHA_ERR_UNSUPPORTED, "rows must stay below 2^31");
+    if (rows > 0x7fffffffll || d > (1 << 30))
+        return fail(MHA_ERR_UNSUPPORTED, "rows must stay below 2^31 and d up to 2^30 (got d=%d)", d);
     if (!(eps >= 0.0f) || !std::isfinite(eps)) return fail(MHA_ERR_INVALID_ARG, "eps must be finite and >= 0");
     if (scales != nullptr && group != 0 && group != 32 && group != 64 && group != 128)
         return fail(MHA_ERR_INVALID_ARG, "group must be 0, 32, 64 or 128 (got %d)", group);
