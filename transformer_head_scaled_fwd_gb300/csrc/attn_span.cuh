@@ -29,7 +29,8 @@ constexpr int kHeadGroup = 8;                // (batch, head) pairs whose units 
 //            no rescaling, no exchange between the threads of a row (4 x 8192, 8 heads of 128: 408 us, kGeneral
 //            524 us). The largest weight is then rounded to bf16 like any other, while under a running maximum it is
 //            exactly 1: rows of a few keys would be off by 1.8e-3 where kGeneral is off by 1.3e-3, so short key ranges
-//            and document spans go there.
+//            and document spans go there. Sums of n weighted values stay in fp32's range for |v| up to 2^40 / n at the
+//            largest cap (all scores at +cap), and from 2^-39 (all at -cap).
 //   kGeneral anything else: scores formed first, then as kPlain
 enum Mode { kPlain, kCapped, kGeneral };
 constexpr float kFixedCap = 60.0f;
