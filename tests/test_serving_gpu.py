@@ -517,6 +517,16 @@ def test_attention_head_major_strides_and_spans(bnd, d, L):
     assert empty.any() and (got[empty] == 0).all()
 
 
+@pytest.mark.parametrize("d,L,cap", [(64, 700, 50.0), (128, 700, 20.0), (128, 130, 50.0), (64, 1600, 0.0)])
+def test_attention_rows_of_one_key_are_its_value(bnd, d, L, cap):
+    """One weight divided by itself is 1 whatever it was rounded to, so the only rounding is of a bf16 value to bf16."""
+    q, k, v = (randn(73 + i, 2, L, n, d, dtype=BF) for i, n in enumerate((4, 2, 2)))
+    got = run_attention(bnd, q * 2, k, v, causal=True, cap=cap)
+    assert torch.equal(got[:, 0], v[:, 0].repeat_interleave(2, dim=1))
+    last = run_attention(bnd, q[:, :1] * 2, k, v, causal=True, cap=cap, q_offset=L, valid=[1, 1])
+    assert torch.equal(last[:, 0], v[:, 0].repeat_interleave(2, dim=1))
+
+
 def test_attention_broadcast_inputs(bnd):
     """Keys and values shared by all sequences, a query shared by all heads (strides of 0)."""
     B, L, h, hk, d = 3, 140, 4, 2, 64
