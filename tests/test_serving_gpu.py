@@ -1,6 +1,7 @@
 """Serving operators on the GPU against plain 64-bit forms (tests/serving_ref.py)."""
 import math
 import random
+import struct
 
 import pytest
 
@@ -913,3 +914,115 @@ print("captured first")
 """ % (os.path.dirname(here), here)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------------------------------ the binding's two ways
+def one_of_each(bnd, dtype=BF):
+    """A dict of calls with their outputs: {name: (call(**changes), [outputs])}."""
+    B, T, h, hk, d, page, N = 2, 5, 4, 2, 64, 8, 6
+    qkv = randn(170, B, T, h + 2 * hk, d, dtype=dtype)
+    q, k, v = qkv[:, :, :h], qkv[:, :, h:h + hk], qkv[:, :, h + hk:]
+    rot = bnd.make_rotary(freqs(32), interleaved=True, scale=1.1)
+    kp, vp = (torch.zeros(N, page, hk, d, dtype=dtype, device="cuda") for _ in range(2))
+    cache = bnd.make_paged_cache(kp, vp, ints([[3, 1], [0, 5]]))
+    dt = bnd.MHA_BF16 if dtype == BF else bnd.MHA_F32
+    ws = torch.empty(bnd.paged_attention_workspace_size(dt, B, h, hk, d), dtype=torch.uint8, device="cuda")
+    scores = bnd.make_scores(cap=20.0, slopes=slopes_of(h))
+    ids, spans = ints([[0, 0, 1, 1, -1], [4, 4, 4, 4, 4]]), torch.zeros(B, T, 2, dtype=torch.int32, device="cuda")
+    q_out, k_out = torch.zeros(B, T, h, d, dtype=dtype, device="cuda"), torch.zeros(B, T, hk, d, dtype=dtype, device="cuda")
+    a_out, d_out = torch.zeros_like(q_out), torch.zeros(B, h, d, dtype=dtype, device="cuda")
+    x, r, gain = randn(171, 3, 256, dtype=dtype), randn(172, 3, 256, dtype=dtype), randn(173, 256, dtype=dtype)
+    z, y8, sc = torch.zeros_like(x), torch.zeros(3, 256, device="cuda", dtype=E4M3), torch.zeros(3, 2, device="cuda")
+    mask = bnd.make_span_mask(causal=True, q_offset=1, key_valid_lens=ints([5, 3]), prefix_lens=ints([2, 0]), doc_spans=spans)
+    mk = lambda f, kw: lambda **ch: f(**{**kw, **ch})
+    return {
+        "rotary": (mk(bnd.mha_rotary, dict(q=q, k=k, q_out=q_out, k_out=k_out, rotary=rot, positions=ints([[9, 8, 7, 6, 5]] * 2))),
+                   [q_out, k_out]),
+        "append": (mk(bnd.mha_paged_append, dict(k=k, v=v, start=ints([0, 6]), cache=cache, q=q, q_out=q_out, k_out=k_out,
+                                                 new_lens=ints([5, 2]), rotary=rot)), [q_out, k_out, kp, vp]),
+        "decode": (mk(bnd.mha_paged_attention, dict(q=q[:, 0], kv_lens=ints([5, 8]), cache=cache, out=d_out, workspace=ws,
+                                                    scores=scores)), [d_out]),
+        "spans": (mk(bnd.mha_document_spans, dict(doc_ids=ids, spans=spans)), [spans]),
+        "attention": (mk(bnd.mha_attention, dict(q=q, k=k, v=v, out=a_out, scores=scores, mask=mask)), [a_out]),
+        "rmsnorm": (mk(bnd.mha_rmsnorm, dict(x=x, gain=gain, eps=1e-5, y=y8, residual=r, sum_out=z, scales=sc)), [y8, z, sc]),
+    }
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_native_and_ctypes_calls_are_the_same(bnd, monkeypatch, dtype):
+    """Every call once through the native front and once through ctypes: the same bits, on the current stream and on a
+    given one, with optional arguments and without."""
+    calls = one_of_each(bnd, dtype)
+    calls["rotary"][0]()
+    assert bnd._front is not None, "the native front is not built"
+    optional = {"rotary": [{}, dict(k=None, k_out=None), dict(positions=None)],
+                "append": [{}, dict(q=None, q_out=None), dict(k_out=None), dict(new_lens=None), dict(rotary=None)],
+                "decode": [{}, dict(scores=None)], "spans": [{}],
+                "attention": [{}, dict(scores=None), dict(mask=None), dict(mask=bnd.make_span_mask()), dict(mask=bnd.make_span_mask(causal=True))],
+                "rmsnorm": [{}, dict(gain=None), dict(sum_out=None), dict(sum_out=None, residual=None)]}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for name, (call, outs) in calls.items():
+        for change in optional[name]:
+            got = []
+            for front in (bnd._front, None):
+                with monkeypatch.context() as m:
+                    m.setattr(bnd, "_front", front)
+                    for o in outs:
+                        o.view(torch.uint8).zero_()
+                    torch.cuda.synchronize()
+                    with torch.cuda.stream(side) if front is None else torch.cuda.stream(torch.cuda.default_stream()):
+                        call(**change, stream=side if front is not None else None)
+                    torch.cuda.synchronize()
+                    got.append([o.view(torch.uint8).clone() for o in outs])
+            assert all(torch.equal(a, b) for a, b in zip(*got)), (name, change)
+            assert any(a.any() for a in got[0]), (name, change)
+    calls["spans"][0](), calls["attention"][0](), torch.cuda.synchronize()
+
+
+def test_native_calls_leave_faults_to_python(bnd):
+    """What is not in order: the native front declines without doing anything, and the error names the argument."""
+    calls = one_of_each(bnd)
+    calls["spans"][0]()
+    half = lambda *s: torch.zeros(*s, device="cuda", dtype=torch.float16)
+    fp = lambda *s: torch.zeros(*s, device="cuda")
+    bf = lambda *s: torch.zeros(*s, device="cuda", dtype=BF)
+    cpu = torch.zeros(2, 5, 4, 64, dtype=BF)
+    other = bnd.make_paged_cache(bf(6, 8, 4, 64), bf(6, 8, 4, 64), ints([[3, 1], [0, 5]]))
+    bad = {
+        "rotary": [dict(q=half(2, 5, 4, 64)), dict(q_out=bf(2, 5, 4, 32)), dict(k_out=fp(2, 5, 2, 64)), dict(q=cpu), dict(rotary=None),
+                   dict(positions=ints([1, 2])), dict(positions=torch.zeros(2, 5, dtype=torch.int64, device="cuda")), dict(k_out=None),
+                   dict(q=bf(2, 5, 64, 4).transpose(2, 3)), dict(q=3)],
+        "append": [dict(cache=other), dict(v=bf(2, 4, 2, 64)), dict(start=None), dict(start=ints([1])), dict(new_lens=fp(2)),
+                   dict(q_out=None), dict(k=cpu), dict(cache=None)],
+        "decode": [dict(out=fp(2, 4, 64)), dict(kv_lens=None), dict(workspace=bf(1)), dict(scores=bnd.make_scores(slopes=slopes_of(8))),
+                   dict(q=bf(3, 4, 64)), dict(q=bf(2, 3, 64), out=bf(2, 3, 64))],
+        "spans": [dict(spans=ints([[1]])), dict(doc_ids=fp(2, 5))],
+        "attention": [dict(v=bf(2, 4, 2, 64)), dict(q=half(2, 5, 4, 64)), dict(out=bf(2, 5, 4, 128)), dict(mask=bnd.make_span_mask(q_offset=-1)),
+                      dict(mask=bnd.make_span_mask(key_valid_lens=ints([1]))), dict(mask=bnd.make_span_mask(q_offset=1 << 40)),
+                      dict(k=bf(2, 5, 3, 64), v=bf(2, 5, 3, 64))],
+        "rmsnorm": [dict(y=bf(3, 256)), dict(scales=fp(3, 3)), dict(scales=fp(3, 128)), dict(residual=None), dict(gain=bf(255)), dict(eps=-1.0),
+                    dict(x=bf(256, 3).t()), dict(x=bf(768))],
+    }
+    for name, changes in bad.items():
+        call, outs = calls[name]
+        for o in outs:
+            o.view(torch.uint8).fill_(7)
+        for change in changes:
+            with pytest.raises((ValueError, TypeError, AttributeError, bnd.MHAError, struct.error)):
+                call(**change)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert (o.view(torch.uint8) == 7).all(), name
+
+
+def test_native_call_of_a_changed_description(bnd):
+    """A description's fields may be changed between calls: both ways read them at the call."""
+    q = randn(175, 1, 3, 2, 64)
+    out, want = torch.empty_like(q), torch.empty_like(q)
+    rot = bnd.make_rotary(freqs(64))
+    bnd.mha_rotary(q, q_out=want, rotary=bnd.make_rotary(freqs(64), scale=2.0))
+    bnd.mha_rotary(q, q_out=out, rotary=rot)
+    rot.scale = 2.0
+    bnd.mha_rotary(q, q_out=out, rotary=rot)
+    assert torch.equal(out, want)

@@ -16,6 +16,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import warnings
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -316,22 +317,33 @@ MHA_PAGED_BAD_PAGE = 0x501
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDED, ROPE_RAMP = range(5)
 
 
-# These calls are made once a layer and token, so what a call costs on the host counts: strides and masks go to
-# the library as packed bytes, the stream is read without making an object of it.
+# These calls are made once a layer and token, so what a call costs on the host counts. Each goes to its namesake in
+# _front (csrc/front.cpp), which checks and makes the call in native code; where that finds anything out of order, or is
+# not built, the Python below checks again, names the fault, or makes the call through ctypes.
 _pack_strides = struct.Struct("4q").pack        # mha_strides_t is the first three
 _pack_mask = struct.Struct("@2i3P").pack        # mha_span_mask_t
 
 
 def _torch():
     """torch's entry points used below, looked up once: (current device, current stream handle of a device)."""
-    global _current_device, _raw_stream, _bf16, _f32, _i32, _e4m3
+    global _current_device, _raw_stream, _bf16, _f32, _i32, _e4m3, _front
     import torch
     torch.cuda.init()
+    try:
+        from . import _front as front
+        if torch.__version__.split("+")[0] == front.torch_version.split("+")[0]:
+            front.set_library(*(ctypes.cast(getattr(load(), n), ctypes.c_void_p).value for n in _FRONT))
+            _front = front
+    except ImportError:
+        pass
+    if _front is None:
+        warnings.warn("_front.so is not built for this torch: serving calls cost more on the host")
     _bf16, _f32, _i32, _e4m3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-_current_device = _raw_stream = _bf16 = _f32 = _i32 = _e4m3 = None
+_current_device = _raw_stream = _bf16 = _f32 = _i32 = _e4m3 = _front = None
+_FRONT = ("mha_rotary", "mha_paged_append", "mha_paged_attention", "mha_document_spans", "mha_attention", "mha_rmsnorm")
 
 
 def _here(t):
@@ -412,6 +424,7 @@ def make_rotary(inv_freq, interleaved: bool = False, scale: float = 1.0):
     r._tensors = inv_freq
     r._ref = ctypes.byref(r)
     r._device = inv_freq.get_device()
+    r._native = struct.pack("Pq", ctypes.addressof(r), r._device)
     return r
 
 
@@ -435,6 +448,7 @@ def make_paged_cache(k_pages, v_pages, block_table):
     c._ref = ctypes.byref(c)
     c._heads = h_kv
     c._for = (block_table.shape[0], d, k_pages.dtype, dev)
+    c._native = struct.pack("P5q", ctypes.addressof(c), block_table.shape[0], d, _code(k_pages.dtype), dev, h_kv)
     return c
 
 
@@ -444,6 +458,7 @@ def make_scores(scale: float = 0.0, cap: float = 0.0, slopes=None):
     s._tensors = slopes
     s._ref = ctypes.byref(s)
     s._for = None if slopes is None else (slopes.numel(), slopes.get_device())
+    s._native = struct.pack("P2q", ctypes.addressof(s), *(s._for or (-1, -1)))
     return s
 
 
@@ -474,6 +489,8 @@ def _rotary_ref(rotary, dev):
 
 def mha_rotary(q, *, rotary, q_out, k=None, k_out=None, positions=None, stream=None):
     """Turn q [B, T, h, d_k] into q_out and k [B, T, h_kv, d_k] into k_out (an output may be its input)."""
+    if _front is not None and _front.rotary(q, rotary, q_out, k, k_out, positions, stream):
+        return
     dev = _here(q)
     dtype, shape = q.dtype, q.shape
     B, T, h, d = shape
@@ -495,6 +512,8 @@ def mha_rotary(q, *, rotary, q_out, k=None, k_out=None, positions=None, stream=N
 
 def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_lens=None, rotary=None, stream=None):
     """Append k, v [B, T, h_kv, d_k] to the cache at positions start[b] + t, turning k (and q into q_out)."""
+    if _front is not None and _front.paged_append(k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream):
+        return
     dev = _here(k)
     dtype, shape = k.dtype, k.shape
     B, T, h_kv, d = shape
@@ -528,6 +547,8 @@ def paged_attention_workspace_size(dt: int, B: int, h: int, h_kv: int, d_k: int)
 
 def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, stream=None):
     """Attention of one new token a sequence, q [B, h, d_k], over the kv_lens[b] cached positions -> out."""
+    if _front is not None and _front.paged_attention(q, kv_lens, cache, out, workspace, scores, stream):
+        return
     dev = _here(q)
     dtype, shape = q.dtype, q.shape
     B, h, d = shape
@@ -552,6 +573,8 @@ def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, strea
 
 def mha_document_spans(doc_ids, *, spans, stream=None):
     """spans int32 [B, L, 2] of the documents in doc_ids int32 [B, L] (one run each; < 0 is padding)."""
+    if _front is not None and _front.document_spans(doc_ids, spans, stream):
+        return
     dev = _here(doc_ids)
     B, L = doc_ids.shape
     st = (_lib or load()).mha_document_spans(_ints(doc_ids, "doc_ids", (B, L), dev), B, L,
@@ -562,6 +585,8 @@ def mha_document_spans(doc_ids, *, spans, stream=None):
 
 def mha_attention(q, k, v, *, out, scores=None, mask=None, stream=None):
     """Attention of q [B, L_q, h, d_k] over k, v [B, L_k, h_kv, d_k] -> out [B, L_q, h, d_k]."""
+    if _front is not None and _front.attention(q, k, v, out, scores, mask, stream):
+        return
     dev = _here(q)
     dtype, shape = q.dtype, q.shape
     B, Lq, h, d = shape
@@ -596,6 +621,8 @@ def _rows(t, name, dtype, shape, dev):
 def mha_rmsnorm(x, gain, eps: float, *, y, residual=None, sum_out=None, scales=None, stream=None):
     """y = gain * z / rms(z), z = x + residual (written to sum_out), rows of length d = x.shape[-1], x [rows, d].
     y has x's dtype, or torch.float8_e4m3fn with scales fp32 [rows, groups] (one group: the row)."""
+    if _front is not None and _front.rmsnorm(x, gain, eps, y, residual, sum_out, scales, stream):
+        return
     dev = _here(x)
     dtype, shape = x.dtype, x.shape
     rows, d = shape

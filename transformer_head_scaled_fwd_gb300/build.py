@@ -10,15 +10,22 @@ the library.
 MHA_DEVICE_CHECKS defined, so the kernels check their block and tile indices at
 entry and record a status code (mha_check_device_status) instead of touching
 memory when one falls outside the problem.
+
+``build()`` also compiles ``csrc/front.cpp`` (the host compiler, torch's headers)
+into ``_front.so``, through which the Python binding makes the serving calls.
+Without torch's or Python's headers it is left out, and the binding uses ctypes.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +33,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmha.so")
 LIB_DEBUG = os.path.join(PKG, "libmha_debug.so")
+FRONT = os.path.join(PKG, "_front.so")
+FRONT_SRC = os.path.join(CSRC, "front.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -52,8 +61,50 @@ def needs_build(lib: str = LIB) -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def build_front(force: bool = False):
+    """Compile _front.so for this interpreter and the installed torch; None where their headers are missing."""
+    spec = importlib.util.find_spec("torch")
+    torch = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
+    python = sysconfig.get_paths()["include"]
+    gxx = shutil.which("g++")
+    if (torch is None or gxx is None or not os.path.exists(os.path.join(python, "Python.h"))
+            or not os.path.exists(os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h"))):
+        print("_front.so is not built: g++ or the headers of Python or torch are missing", file=sys.stderr)
+        return None
+    stamp = os.path.join(BUILD, "front.stamp")
+    made_for = f"{sys.version}\n{importlib.metadata.version('torch')}\n{torch}\n"
+    deps = [FRONT_SRC, os.path.join(ROOT, "include", "mha.h"), __file__]
+    if not force and os.path.exists(FRONT) and os.path.exists(stamp) and open(stamp).read() == made_for \
+            and all(os.path.getmtime(p) <= os.path.getmtime(FRONT) for p in deps):
+        return FRONT
+    os.makedirs(BUILD, exist_ok=True)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    include = [python, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"), cuda]
+    libs = os.path.join(torch, "lib")
+    tmp = FRONT + f".tmp{os.getpid()}"
+    r = subprocess.run([gxx, "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{p}" for p in include), FRONT_SRC, "-o", tmp,
+                        f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}"],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on front.cpp:\n{r.stderr}")
+    os.replace(tmp, FRONT)
+    with open(stamp, "w") as f:
+        f.write(made_for)
+    return FRONT
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
+    if not debug:
+        with cf.ThreadPoolExecutor(max_workers=1) as ex:   # beside nvcc
+            front = ex.submit(build_front, force)
+            lib = _build_library(lib, force, verbose, extra_flags, debug)
+            front.result()
+        return lib
+    return _build_library(lib, force, verbose, extra_flags, debug)
+
+
+def _build_library(lib, force, verbose, extra_flags, debug) -> str:
     if not force and not needs_build(lib):
         return lib
     out_dir = BUILD + ("_debug" if debug else "")
