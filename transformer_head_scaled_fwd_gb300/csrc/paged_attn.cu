@@ -468,107 +468,132 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     pdl_trigger();
     pdl_wait();
 
-    // ---- total number of blocks, and the sequences that have none. Up to 32 sequences are summed by every warp for
-    // itself, without a barrier before the first loads.
-    const bool few = p.B <= 32;
-    long long total = 0, inc = 0, v = 0;     // few: blocks (of one unit) up to and of sequence `lane`
-    if (few) {
-        if (lane < p.B) {
-            v = lens.blocks(lens.len(lane));
-            if (p.kv_lens[lane] > room) atomicCAS(p.status, 0, 0x501);
-        }
-        inc = warp_scan64(v, lane);
-        total = __shfl_sync(0xffffffffu, inc, 31);
-    } else {
-        for (int b = threadIdx.x; b < p.B; b += kThreads) {
-            if (p.kv_lens[b] > room) atomicCAS(p.status, 0, 0x501);
-            v += lens.blocks(lens.len(b));
-        }
-        v = warp_sum64(v);
-        if (lane == 0) sh.scan[warp] = v;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) total += sh.scan[w];
-    }
-    total *= units;
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (lens.len(b) > 0) continue;
-        for (int i = threadIdx.x; i < p.h * kD; i += kThreads)
-            store_f(static_cast<T*>(p.out) + b * p.o_b + (i / kD) * p.o_h + i % kD, 0.0f);
-    }
     const int c = blockIdx.x;
-    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    if (c >= ctas) {
-        if (threadIdx.x == 0 && !p.whole) join[c] = JoinDesc{0, -1, 0, 0, 0};
-        return;
-    }
-    // CTA c takes blocks [c total / ctas, (c + 1) total / ctas); block t belongs to the last CTA that starts at or before it
-    const bool small = total < (1 << 24);       // kMaxCtas * total fits 32 bits: divisions a quarter as long
-    auto start_of = [&](long long i) -> long long {
-        return small ? static_cast<uint32_t>(i * total) / static_cast<uint32_t>(ctas) : i * total / ctas;
-    };
-    long long t0 = start_of(c), t1 = start_of(c + 1);
-    auto owner = [&](long long t) { return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1); };
-
-    // ---- the sequences that t0 and t1 fall into (t1 may be the end of the line)
-    Found found[2] = {};
-    if (few) {
-        const long long lo = (inc - v) * units, hi = inc * units;
-        const int b0 = __ffs(__ballot_sync(0xffffffffu, t0 >= lo && t0 < hi)) - 1;
-        const int b1 = max(__ffs(__ballot_sync(0xffffffffu, t1 >= lo && t1 < hi)) - 1, 0);
-        found[0] = Found{__shfl_sync(0xffffffffu, lo, b0), b0};
-        found[1] = Found{__shfl_sync(0xffffffffu, lo, b1), b1};
+    Cursor at;               // the block that is computed
+    long long t0, t1;        // the CTA's blocks of the line
+    int early = -1;          // page of the warp's first key `lane`
+    if (p.direct) {
+        // a CTA a unit: the first pages are looked up beside the length
+        at.b = c / units;
+        at.unit = c - at.b * units;
+        at.blk = 0;
+        const int key = warp * kKeys + lane, held = p.kv_lens[at.b];
+        if (lane < kKeys && key < room) early = p.cache.table[at.b * p.cache.table_stride + p.cache.page.div(key)];
+        at.n = static_cast<int>(min(static_cast<int64_t>(max(held, 0)), room));
+        at.nblk = lens.blocks(at.n);
+        t0 = 0;
+        t1 = at.nblk;
+        if (held > room && threadIdx.x == 0) atomicCAS(p.status, 0, 0x501);
+        if (at.n == 0) {
+            const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
+            const int many = min(group - ht * W::kRows, W::kRows), first = kh * group + ht * W::kRows;
+            for (int i = threadIdx.x; i < many * kD; i += kThreads)
+                store_f(static_cast<T*>(p.out) + at.b * p.o_b + (first + i / kD) * p.o_h + i % kD, 0.0f);
+            return;
+        }
     } else {
-        long long acc = 0;   // blocks (of one unit) before sequence b0
-        for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-            const int b = b0 + threadIdx.x;
-            v = b < p.B ? lens.blocks(lens.len(b)) : 0;
-            inc = warp_scan64(v, lane);
-            __syncthreads();
-            if (lane == 31) sh.scan[warp] = inc;
-            __syncthreads();
-            long long all = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                if (w < warp) inc += sh.scan[w];
-                all += sh.scan[w];
+        // ---- total number of blocks, and the sequences that have none. Up to 32 sequences are summed by every warp for
+        // itself, without a barrier before the first loads.
+        const bool few = p.B <= 32;
+        long long total = 0, inc = 0, v = 0;     // few: blocks (of one unit) up to and of sequence `lane`
+        if (few) {
+            if (lane < p.B) {
+                v = lens.blocks(lens.len(lane));
+                if (p.kv_lens[lane] > room) atomicCAS(p.status, 0, 0x501);
             }
-            const long long lo = (acc + inc - v) * units, hi = (acc + inc) * units;
-            if (t0 >= lo && t0 < hi) sh.found[0] = Found{lo, b};
-            if (t1 >= lo && t1 < hi) sh.found[1] = Found{lo, b};
-            acc += all;
-            if (t1 < acc * units) break;
+            inc = warp_scan64(v, lane);
+            total = __shfl_sync(0xffffffffu, inc, 31);
+        } else {
+            for (int b = threadIdx.x; b < p.B; b += kThreads) {
+                if (p.kv_lens[b] > room) atomicCAS(p.status, 0, 0x501);
+                v += lens.blocks(lens.len(b));
+            }
+            v = warp_sum64(v);
+            if (lane == 0) sh.scan[warp] = v;
+            __syncthreads();
+            for (int w = 0; w < kWarps; ++w) total += sh.scan[w];
         }
-        __syncthreads();
-        found[0] = sh.found[0];
-        found[1] = sh.found[1];
-    }
-    auto cursor_at = [&](long long t, const Found& f) {
-        Cursor x;
-        x.b = f.b;
-        x.n = lens.len(x.b);
-        x.nblk = lens.blocks(x.n);
-        const long long rem = t - f.before;
-        x.unit = small ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(x.nblk)) : static_cast<int>(rem / x.nblk);
-        x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * x.nblk);
-        return x;
-    };
-    Cursor at = cursor_at(t0, found[0]);      // the block that is computed
-    if (p.whole) {
-        // units are not split: a CTA takes those that start in its piece of the line
-        if (t1 < total) {
-            const Cursor e = cursor_at(t1, found[1]);
-            if (e.blk > 0) t1 += e.nblk - e.blk;
+        total *= units;
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            if (lens.len(b) > 0) continue;
+            for (int i = threadIdx.x; i < p.h * kD; i += kThreads)
+                store_f(static_cast<T*>(p.out) + b * p.o_b + (i / kD) * p.o_h + i % kD, 0.0f);
         }
-    } else if (threadIdx.x == 0) {
-        JoinDesc d{0, -1, 0, 0, 0};
-        const long long u0 = t0 - at.blk;       // first block of the unit
-        if (at.blk > 0 && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
-            d.c0 = c - 1;
-            d.c1 = owner(u0 + at.nblk - 1);
-            d.b = at.b;
-            d.unit = at.unit;
-            d.first_slot = start_of(c - 1) == u0 ? 0 : 1;
+        const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+        if (c >= ctas) {
+            if (threadIdx.x == 0 && !p.whole) join[c] = JoinDesc{0, -1, 0, 0, 0};
+            return;
         }
-        join[c] = d;
+        // CTA c takes blocks [c total / ctas, (c + 1) total / ctas); block t belongs to the last CTA that starts at or before it
+        const bool small = total < (1 << 24);       // kMaxCtas * total fits 32 bits: divisions a quarter as long
+        auto start_of = [&](long long i) -> long long {
+            return small ? static_cast<uint32_t>(i * total) / static_cast<uint32_t>(ctas) : i * total / ctas;
+        };
+        t0 = start_of(c);
+        t1 = start_of(c + 1);
+        auto owner = [&](long long t) { return static_cast<int>(((t + 1) * ctas + total - 1) / total - 1); };
+
+        // ---- the sequences that t0 and t1 fall into (t1 may be the end of the line)
+        Found found[2] = {};
+        if (few) {
+            const long long lo = (inc - v) * units, hi = inc * units;
+            const int b0 = __ffs(__ballot_sync(0xffffffffu, t0 >= lo && t0 < hi)) - 1;
+            const int b1 = max(__ffs(__ballot_sync(0xffffffffu, t1 >= lo && t1 < hi)) - 1, 0);
+            found[0] = Found{__shfl_sync(0xffffffffu, lo, b0), b0};
+            found[1] = Found{__shfl_sync(0xffffffffu, lo, b1), b1};
+        } else {
+            long long acc = 0;   // blocks (of one unit) before sequence b0
+            for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+                const int b = b0 + threadIdx.x;
+                v = b < p.B ? lens.blocks(lens.len(b)) : 0;
+                inc = warp_scan64(v, lane);
+                __syncthreads();
+                if (lane == 31) sh.scan[warp] = inc;
+                __syncthreads();
+                long long all = 0;
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w < warp) inc += sh.scan[w];
+                    all += sh.scan[w];
+                }
+                const long long lo = (acc + inc - v) * units, hi = (acc + inc) * units;
+                if (t0 >= lo && t0 < hi) sh.found[0] = Found{lo, b};
+                if (t1 >= lo && t1 < hi) sh.found[1] = Found{lo, b};
+                acc += all;
+                if (t1 < acc * units) break;
+            }
+            __syncthreads();
+            found[0] = sh.found[0];
+            found[1] = sh.found[1];
+        }
+        auto cursor_at = [&](long long t, const Found& f) {
+            Cursor x;
+            x.b = f.b;
+            x.n = lens.len(x.b);
+            x.nblk = lens.blocks(x.n);
+            const long long rem = t - f.before;
+            x.unit = small ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(x.nblk)) : static_cast<int>(rem / x.nblk);
+            x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * x.nblk);
+            return x;
+        };
+        at = cursor_at(t0, found[0]);
+        if (p.whole) {
+            // units are not split: a CTA takes those that start in its piece of the line
+            if (t1 < total) {
+                const Cursor e = cursor_at(t1, found[1]);
+                if (e.blk > 0) t1 += e.nblk - e.blk;
+            }
+        } else if (threadIdx.x == 0) {
+            JoinDesc d{0, -1, 0, 0, 0};
+            const long long u0 = t0 - at.blk;       // first block of the unit
+            if (at.blk > 0 && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
+                d.c0 = c - 1;
+                d.c1 = owner(u0 + at.nblk - 1);
+                d.b = at.b;
+                d.unit = at.unit;
+                d.first_slot = start_of(c - 1) == u0 ? 0 : 1;
+            }
+            join[c] = d;
+        }
     }
     auto advance = [&](Cursor& x) {
         if (++x.blk < x.nblk) return;
@@ -582,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         } while (x.n == 0);
     };
 
-    if (p.whole && at.blk > 0) {
+    if (p.whole && at.blk > 0) {      // never where a CTA has a unit of its own
         t0 += at.nblk - at.blk;
         at.blk = at.nblk - 1;
         advance(at);
@@ -596,7 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     const uint32_t stage0 = smem_u32(smem) + warp * (kStages * 2 * kStepBytes);
     const char* k_lane = static_cast<const char*>(p.cache.k) + (lane % S::kChunks) * 16;
     const long long v_minus_k = static_cast<const char*>(p.cache.v) - static_cast<const char*>(p.cache.k);
-    auto look_up = [&]() {
+    auto look_up = [&](bool first = false) {
         inside = false;
         if (t_ahead < t1) {
             const int key = (ahead.blk * kWarps + warp) * kKeys + lane;
@@ -604,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (lane < kKeys && key < ahead.n) {
                 const int i = p.cache.page.div(key);
                 slot = key - i * static_cast<int>(p.cache.page.d);
-                page = p.cache.table[ahead.b * p.cache.table_stride + i];
+                page = first && p.direct ? early : p.cache.table[ahead.b * p.cache.table_stride + i];
                 inside = true;
             }
             advance(ahead);
@@ -635,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         return live;
     };
     uint32_t live[kStages];
-    look_up();
+    look_up(true);
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) {
         live[s] = issue(s);
@@ -800,6 +825,7 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     constexpr int kBlock = Step<typename W::T, kD>::kKeys * kWarps;
     p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= kWholeBlocks * kBlock;
     const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + W::kRows - 1) / W::kRows);
+    p.direct = p.whole && units <= ctas;
     if (p.whole) {
         return launch_pdl(paged_attn_kernel<W, kD>, dim3(static_cast<unsigned>(std::min<int64_t>(units, ctas))), dim3(kThreads),
                           kSmem, s, p);

@@ -82,6 +82,7 @@ struct PagedAttnParams {
     float* partial;          // workspace
     int* status;
     int whole;               // set by the launcher: no unit is split
+    int direct;              // ... and each has a CTA of its own
 };
 size_t paged_attn_workspace(bool bf16, int B, int h, int h_kv, int d);
 cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t s);
