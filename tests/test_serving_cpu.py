@@ -197,3 +197,24 @@ def test_frequencies_refusals(lib):
         with pytest.raises(bnd.MHAError) as e:
             bnd.rotary_frequencies(*args)
         assert e.value.status == INV
+
+
+def test_native_front_declines_what_is_no_call():
+    """The native front on CPU tensors and other objects: False, and nothing done; bad addresses are refused."""
+    torch = pytest.importorskip("torch")
+    from transformer_head_scaled_fwd_gb300 import build as B
+    if B.build_front() is None:
+        pytest.skip("the headers of Python or torch are missing")
+    from transformer_head_scaled_fwd_gb300 import _front as front
+    x = torch.zeros(2, 3, 4, 64)
+    for name, n in (("rotary", 7), ("paged_append", 10), ("paged_attention", 7), ("document_spans", 3), ("attention", 7),
+                    ("rmsnorm", 8)):
+        f = getattr(front, name)
+        assert f() is False and f(*[None] * n) is False and f(*[x] * n) is False and f(*[1.5] * n) is False
+        assert f(*[x] * (n + 1)) is False
+    with pytest.raises(TypeError):
+        front.set_library(1)
+    with pytest.raises(ValueError):
+        front.set_library(0, 0, 0, 0, 0, 0)
+    with pytest.raises(TypeError):
+        front.set_library(*["x"] * 6)
