@@ -20,9 +20,9 @@
 // no weight: what lies there is never touched.
 //
 // Measured (bf16): 16 sequences of 8192, 16 heads of 64, 537 MB: 88-92 us, 5.8-6.1 TB/s; 48 ragged ones up to 15000, 32 / 8
-// heads of 128, 1.5 GB: 245 us, 6.2 TB/s (0.91 of measured copy bandwidth); one of 131071, 16 / 2 heads: 32 us, of which
+// heads of 128, 1.5 GB: 245 us, 6.2 TB/s (0.91 of measured copy bandwidth); one of 131071, 16 / 2 heads: 30.5 us, of which
 // 20 us are its traffic: the two launches, the look-ups (length, page, key: three dependent loads) and the join are the
-// rest, 12 us at any length, and 7.2 TB/s is what each further key costs.
+// rest, 11 us at any length, and 7.2 TB/s is what each further key costs.
 #include <algorithm>
 
 #include <math_constants.h>
@@ -749,6 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 // Joins the pieces of a unit that several CTAs share: block (c, row). Thread i weighs piece i (there are
 // at most kMaxCtas), then groups of kD / 4 threads sum every kGroups-th piece, 16 bytes a thread.
 constexpr int kJoinThreads = 256;
+constexpr int kEarly = 8;        // loads of a thread that do not wait for the weights (one of 131071: 31.8 -> 30.5 us, of 16000: 12.9 -> 12.1)
 template <typename T, int kD>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
     constexpr int kSlot = slot_floats<kD>();
@@ -770,6 +771,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const int pieces = d.c1 - d.c0 + 1;
     const float* slots = p.partial + static_cast<int64_t>(d.c0) * 2 * kSlot;   // piece i at 2 i kSlot, piece 0 at first_slot
     const float* mine = slots + (tid == 0 ? d.first_slot : 2 * tid) * kSlot;
+    const int g = tid / kCols, x = tid % kCols;
+    auto at = [&](int i) {
+        return reinterpret_cast<const float4*>(slots + (i == 0 ? d.first_slot : 2 * i) * kSlot + 2 * kMaxRows + row * kD)[x];
+    };
+    float4 early[kEarly];      // on their way while the weights are found
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+        if (g + i * kGroups < pieces) early[i] = at(g + i * kGroups);
     const float mi = tid < pieces ? mine[row] : -CUDART_INF_F;
     const float li = tid < pieces ? mine[kMaxRows + row] : 0.0f;
     float M = mi;
@@ -784,18 +793,19 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const float sum = warp_add(li * f);
     if (lane == 0) sh_x[1][warp] = sum;
     __syncthreads();
-    const int g = tid / kCols, x = tid % kCols;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = g; i < pieces; i += kGroups) {
-        const float* o = slots + (i == 0 ? d.first_slot : 2 * i) * kSlot + 2 * kMaxRows + row * kD;
-        const float4 v = reinterpret_cast<const float4*>(o)[x];
+    auto add = [&](int i, const float4& v) {
         const float w = sh_f[i];
         a.x = fmaf(v.x, w, a.x);
         a.y = fmaf(v.y, w, a.y);
         a.z = fmaf(v.z, w, a.z);
         a.w = fmaf(v.w, w, a.w);
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kEarly; ++i)
+        if (g + i * kGroups < pieces) add(g + i * kGroups, early[i]);
+#pragma unroll 4
+    for (int i = g + kEarly * kGroups; i < pieces; i += kGroups) add(i, at(i));
     sh_o[g][x] = a;
     __syncthreads();
     if (tid < kD) {
