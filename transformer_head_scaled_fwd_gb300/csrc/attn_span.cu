@@ -15,7 +15,8 @@
 // in tensor memory, so the score MMAs of tile j + 1 run during the softmax of tile j, and the next unit's loads and
 // first scores run during this unit's last tiles and output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
 // softmax warps rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
-// Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408 us.
+// Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408-418 us, with a
+// distance bias 471 us.
 #include <algorithm>
 
 #include "attn_span.cuh"
