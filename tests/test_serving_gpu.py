@@ -426,6 +426,15 @@ ATT = [
     (30, 200, 1600, 4, 4, 64, dict(causal=True, q_offset=1400, valid=[0, 1600, 0, 0, 1, 1401] * 5)),
     (2, 1600, 1600, 2, 2, 64, dict(causal=True, prefix=[900, 0], valid=[1600, 1000])),
     (1, 600, 600, 2, 1, 64, dict(cap=300.0, causal=True)),
+    # few queries, long keys: several CTAs share a query tile
+    (1, 1, 8192, 4, 1, 128, dict(causal=True, q_offset=8191)),
+    (2, 3, 4100, 2, 2, 64, dict(causal=True, q_offset=4097, slopes=True)),
+    (1, 130, 5000, 3, 1, 128, dict(causal=True, q_offset=4870, cap=30.0)),
+    (3, 40, 3000, 2, 1, 64, dict(valid=[0, 100, 3000], cap=50.0)),       # pieces, and whole units, without a key
+    (2, 129, 2100, 4, 2, 128, dict(causal=True, q_offset=60, valid=[2100, 70], prefix=[0, 1500])),
+    (1, 1100, 1100, 2, 1, 64, dict(docs=300, causal=True, pad=200)),
+    (1, 2048, 2048, 1, 1, 128, dict(causal=True, slopes=True, cap=100.0)),
+    (20, 17, 1030, 2, 1, 128, dict(causal=True, q_offset=900, valid=[0, 1, 128, 129, 512, 513, 900, 917, 918, 1030] * 2)),
 ]
 
 
@@ -914,6 +923,62 @@ print("captured first")
 """ % (os.path.dirname(here), here)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+def _few_queries(bnd, seed, d):
+    q, k, v = randn(seed, 2, 3, 4, d, dtype=BF), randn(seed + 1, 2, 2500, 2, d, dtype=BF), randn(seed + 2, 2, 2500, 2, d, dtype=BF)
+    out = torch.zeros_like(q)
+    mask = bnd.make_span_mask(causal=True, q_offset=2400, key_valid_lens=ints([2500, 900]))
+    return lambda stream=None: bnd.mha_attention(q, k, v, out=out, mask=mask, stream=stream), out
+
+
+def test_shared_units_captured_first():
+    """A fresh process that captures attention of few queries over long keys as its first call."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import test_serving_gpu as T
+from transformer_head_scaled_fwd_gb300 import binding as bnd
+call, out = T._few_queries(bnd, 360, 128)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+    call()
+g.replay()
+torch.cuda.synchronize()
+got = out.clone()
+out.zero_()
+call()
+torch.cuda.synchronize()
+assert got.any() and torch.equal(got, out)
+assert bnd.mha_check_device_status() == 0
+print("captured first")
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+def test_shared_units_on_two_streams(bnd):
+    """Two streams of calls whose clusters want the same SMs: the results of one after the other."""
+    jobs = [_few_queries(bnd, 370 + 10 * i, d) + (torch.cuda.Stream(),) for i, d in enumerate((64, 128))]
+    want = []
+    for call, out, s in jobs:
+        call()
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(100):
+        for call, out, s in jobs:
+            call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(j[1], w) for j, w in zip(jobs, want))
 
 
 # ------------------------------------------------------------------------------------------ the binding's two ways

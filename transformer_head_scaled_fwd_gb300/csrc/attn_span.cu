@@ -18,9 +18,11 @@
 // Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408-418 us, with a
 // distance bias 471 us.
 #include <algorithm>
+#include <atomic>
 
 #include "attn_span.cuh"
 #include "launch.h"
+#include "ptx_pair.cuh"
 
 namespace mha {
 namespace {
@@ -87,14 +89,15 @@ struct SmemSpan {
     UnitInfo unit[kSlots];
     uint32_t tmem_base;
     int abort_flag;
-    float mx[kParts][BM];                    // the parts' tile maxima, exchanged when a row's maximum grows
+    float mx[kParts][BM];                    // the parts' tile maxima, exchanged when a row's maximum grows; kSplit, at the end:
+                                             // maximum [0] and sum [1] of this CTA's part
 };
 template <int kD>
 constexpr size_t smem_bytes() { return Tiles<kD>::kOffBar + sizeof(SmemSpan); }
 
-// Unit u of the schedule (a whole warp): groups of kHeadGroup (batch, head) pairs, whose keys and values
+// Place of unit u of the schedule: groups of kHeadGroup (batch, head) pairs, whose keys and values
 // stay in L2, inside a group the query tiles from the last (longest under a causal mask) to the first.
-__device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int lane) {
+__device__ __forceinline__ UnitInfo place_of(const SpanAttnParams& p, int u) {
     const int planes = p.B * p.h;
     const int tiles = (p.Lq + BM - 1) / BM;
     const int grp = u / (kHeadGroup * tiles);
@@ -106,6 +109,12 @@ __device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int 
     x.b = plane / p.h;
     x.head = plane - x.b * p.h;
     x.q0 = qt * BM;
+    return x;
+}
+
+// Unit u (a whole warp).
+__device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int lane) {
+    UnitInfo x = place_of(p, u);
     x.valid = p.valid_lens != nullptr ? min(max(p.valid_lens[x.b], 0), p.Lk) : p.Lk;
     x.seen = p.prefix_lens != nullptr ? p.prefix_lens[x.b] : 0;
     int lo_min = p.Lk, lo_max = 0, hi_min = p.Lk, hi_max = 0;
@@ -139,7 +148,55 @@ __device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int 
     return x;
 }
 
-template <int kD, int kMode>
+// The parts of a unit that kPieces CTAs share, each in its CTA's shared memory: maxima and sums of the rows from m_at on,
+// outputs [row][part_pitch] from o_at on. A CTA joins BM / kPieces rows, a thread four features of up to eight parts'
+// rows, all of whose loads are in flight together (one row after the other: 15.4 against 14.4 us
+// at 128 x 2048 keys by two, d_k = 128).
+__host__ __device__ constexpr int part_pitch(int d) { return d + 4; }
+template <int kD, int kPieces>
+__device__ __forceinline__ void join_parts(const SpanAttnParams& p, const UnitInfo& at, int piece, uint32_t m_at, uint32_t o_at) {
+    constexpr int kRows = BM / kPieces, kCols = kD / 4, kStep = kSoft / kCols;      // rows of one pass
+    constexpr int kItems = kRows > kStep ? kRows / kStep : 1;
+    const int c = threadIdx.x % kCols * 4, r0 = threadIdx.x / kCols;
+    float ms[kItems][kPieces], ls[kItems][kPieces];
+    float4 os[kItems][kPieces];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int r = piece * kRows + min(r0 + i * kStep, kRows - 1);
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) {
+            ms[i][s] = ld_cluster(mapa_shared(m_at + r * 4, s));
+            ls[i][s] = ld_cluster(mapa_shared(m_at + (BM + r) * 4, s));
+            os[i][s] = ld_cluster4(mapa_shared(o_at + (r * part_pitch(kD) + c) * 4, s));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int r = piece * kRows + r0 + i * kStep;
+        if (r0 + i * kStep >= kRows || at.q0 + r >= p.Lq) continue;
+        float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) M = fmaxf(M, ms[i][s]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) {
+            if (ms[i][s] == -CUDART_INF_F) continue;   // no key: its output may hold anything
+            const float f = ex2_approx(ms[i][s] - M);
+            L = fmaf(f, ls[i][s], L);
+            a.x = fmaf(f, os[i][s].x, a.x);
+            a.y = fmaf(f, os[i][s].y, a.y);
+            a.z = fmaf(f, os[i][s].z, a.z);
+            a.w = fmaf(f, os[i][s].w, a.w);
+        }
+        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key at all: zeros; NaN stays
+        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out.p) + at.b * p.out.b + (at.q0 + r) * p.out.l + at.head * p.out.h + c;
+        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    }
+}
+
+// kSplit: the CTAs of a cluster share a unit, each with its piece of the key tiles; they join their parts through one
+// another's shared memory.
+template <int kD, int kMode, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_constant__ SpanAttnParams p,
                                                                 const __grid_constant__ SpanMaps maps) {
     using G = Tiles<kD>;
@@ -148,9 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* base = smem_raw;
     SmemSpan* sm = reinterpret_cast<SmemSpan*>(base + G::kOffBar);
+    const int pieces = kSplit ? p.pieces : 1, piece = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
     pdl_trigger();
     if ((smem_u32(base) & 1023u) != 0) {
-        // the 128-byte-swizzled tiles need 1024-byte alignment: refuse rather than compute garbage
+        // the 128-byte-swizzled tiles need 1024-byte alignment: refuse rather than compute garbage (all CTAs of a
+        // cluster alike)
         pdl_wait();
         if (threadIdx.x == 0) atomicCAS(p.status, 0, 0x802);
         return;
@@ -199,14 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         regs_dec<56>();
         if (warp == kSoftWarps) {
             // ------------------------------------------------ scheduler, Q and K loads
-            int u = blockIdx.x;
+            int u = blockIdx.x / pieces;
             uint32_t gk = 0;       // K tiles issued so far
             int loaded = 0;        // units whose Q was
             for (int k = 0;; ++k, ++loaded) {
                 const int qb = k & 1;
                 // the score MMAs of unit k - 2 have read this Q buffer
                 if (k >= 2) mbar_wait(&sm->q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.status, 0x810);
-                if (k >= 1) {
+                if (kSplit && k >= 1) {
+                    u = -1;
+                } else if (k >= 1) {
                     const int a = (k - 1) & 1;
                     const bool ok = mbar_wait(&sm->steal_full[a], ((k - 1) >> 1) & 1, abort_flag, p.status, 0x811);
                     u = ok ? steal_answer(&sm->steal[a][0]) : -1;
@@ -220,8 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     }
                     break;
                 }
-                if (lane == 0) steal_request(&sm->steal[qb][0], &sm->steal_full[qb]);
-                const UnitInfo x = unit_of(p, u, lane);
+                if (!kSplit && lane == 0) steal_request(&sm->steal[qb][0], &sm->steal_full[qb]);
+                UnitInfo x = unit_of(p, u, lane);
+                if constexpr (kSplit) {
+                    const int first = static_cast<int>(static_cast<int64_t>(x.n) * piece / pieces);
+                    x.n = static_cast<int>(static_cast<int64_t>(x.n) * (piece + 1) / pieces) - first;
+                    x.j0 += first;
+                    if (x.n == 0) {   // fewer tiles than pieces
+                        if (lane == 0) {
+                            sm->unit[0].n = 0;
+                            mbar_arrive(&sm->unit_full[0]);
+                        }
+                        break;
+                    }
+                }
                 if (lane == 0) {
                     sm->unit[k % kSlots] = x;
                     mbar_arrive(&sm->unit_full[k % kSlots]);
@@ -243,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             if (lane == 0 && *abort_flag) {
                 drain_ring<G::kStagesK>(sm->k_full, gk);
                 drain_ring<2>(sm->q_full, loaded);
-                drain_ring<2>(sm->steal_full, loaded);
+                if (!kSplit) drain_ring<2>(sm->steal_full, loaded);
             }
         } else if (warp == kSoftWarps + 3) {
             // ------------------------------------------------ V loads
@@ -351,6 +424,11 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             tc_fence_after();
             tmem_dealloc(tmem, kTmemCols);
         }
+        if constexpr (kSplit) {   // the softmax warps' two
+            __syncwarp();
+            cluster_sync_all();
+            cluster_sync_all();
+        }
     } else {
         regs_inc<104>();
         // ------------------------------------------------ softmax: thread (h, row), keys 32 h .. 32 h + 31 of a tile
@@ -367,6 +445,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x81d);
         UnitInfo x = sm->unit[0];
         int2 span = ok && x.n > 0 ? span_of(p, x.b, x.q0 + row) : make_int2(0, 0);
+        // kSplit: this CTA's part, [row][kPitch], in place of the key and value tiles
+        constexpr int kPitch = part_pitch(kD);
+        float* const part = reinterpret_cast<float*>(base + G::kOffK);
+        static_assert(BM * kPitch * 4 <= static_cast<int>(G::kOffO - G::kOffK), "a part fits the tiles");
+        if (kSplit && h == 0) {
+            sm->mx[0][row] = -CUDART_INF_F;
+            sm->mx[1][row] = 0.0f;
+        }
         for (int k = 0;; ++k) {
             __syncwarp();
             // every softmax thread takes the same decision (a give-up in one thread stops all)
@@ -516,6 +602,17 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             uint32_t o[kOut];
             if constexpr (kOut == 32) tmem_ld_x32(o_tmem, o);
             else tmem_ld_x16(o_tmem, o);
+            if constexpr (kSplit) {
+                // the only unit of this CTA: every copy and product that used the tiles has completed
+#pragma unroll
+                for (int c = 0; c < kOut; c += 4)
+                    *reinterpret_cast<uint4*>(part + row * kPitch + h * kOut + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                if (h == 0) {
+                    sm->mx[0][row] = kMode == kCapped ? 0.0f : m;
+                    sm->mx[1][row] = L;
+                }
+                continue;
+            }
             named_bar_sync(1, kSoft);   // every thread has read the sums the staging overwrites
 #pragma unroll
             for (int ch = 0; ch < kOut / 8; ++ch) {
@@ -544,6 +641,18 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         if (warp == 0 && lane == 0) tma_store_wait_all();
         tc_fence_before();
         named_bar_sync(3, kThreads);
+        if constexpr (kSplit) {
+            // ------------------------------------------------ join: a CTA takes BM / pieces rows of all parts
+            __syncwarp();
+            cluster_sync_all();
+            const UnitInfo at = place_of(p, blockIdx.x / pieces);
+            const uint32_t m_at = smem_u32(&sm->mx[0][0]), o_at = smem_u32(part);
+            if (pieces == 2) join_parts<kD, 2>(p, at, piece, m_at, o_at);
+            else if (pieces == 4) join_parts<kD, 4>(p, at, piece, m_at, o_at);
+            else join_parts<kD, 8>(p, at, piece, m_at, o_at);
+            __syncwarp();
+            cluster_sync_all();   // the others have read this CTA's part
+        }
     }
 }
 
@@ -600,15 +709,83 @@ cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spa
     return launch_pdl(document_spans_kernel, dim3((L + kSpanThreads - 1) / kSpanThreads, B), dim3(kSpanThreads), 0, s, ids, L, spans);
 }
 
+// launch_pdl with clusters of `size` CTAs.
+template <typename... Params, typename... Args>
+static cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int size, size_t smem, cudaStream_t s,
+                                      Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
+static int64_t units_of(const SpanAttnParams& p) { return static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM); }
+
+template <int kD, int kMode, bool kSplit>
+static cudaError_t launch_as(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
+    static_assert(smem_bytes<kD>() <= 232448, "shared memory budget");
+    auto kernel = span_attn_kernel<kD, kMode, kSplit>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<kD>()));
+    if (e != cudaSuccess) return e;
+    const dim3 grid(static_cast<unsigned>(units_of(p) * p.pieces));
+    return kSplit ? launch_pdl_cluster(kernel, grid, dim3(kThreads), p.pieces, smem_bytes<kD>(), s, p, maps)
+                  : launch_pdl(kernel, grid, dim3(kThreads), smem_bytes<kD>(), s, p, maps);
+}
 template <int kD, int kMode>
 static cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
-    static_assert(smem_bytes<kD>() <= 232448, "shared memory budget");
-    cudaError_t e = cudaFuncSetAttribute(span_attn_kernel<kD, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem_bytes<kD>()));
-    if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
-    return launch_pdl(span_attn_kernel<kD, kMode>, dim3(grid), dim3(kThreads), smem_bytes<kD>(), s, p, maps);
+    return p.pieces > 1 ? launch_as<kD, kMode, true>(p, maps, s) : launch_as<kD, kMode, false>(p, maps, s);
 }
+// Clusters of `size` CTAs that the current device runs at once (an SM holds one CTA of any instance); asked once a
+// device, for it is a property of the device.
+static int clusters_at_once(int size) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][4];      // by log2(size); 0: not asked, else 1 + the answer
+    const int lg = size == 8 ? 3 : size == 4 ? 2 : 1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+    if (const int k = known[dev][lg].load(std::memory_order_relaxed)) return k - 1;
+    auto kernel = span_attn_kernel<128, kGeneral, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<128>();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<128>())) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+        return 0;
+    known[dev][lg].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+// CTAs that share a unit: with few units (few queries over long keys) most SMs would stand idle and a unit would go
+// through its keys alone. As many as let all units run at once, from a number of keys on that pays for the two cluster
+// barriers and the join (2 to 3 us). 128 queries, 8 heads of 64 (128), us alone and shared: 2048 keys 17.2 (16.3), by two 12.7
+// (14.2), four 10.5 (12.3), eight 9.9 (11.5); one query, 4096 keys, by eight 28.9 -> 9.4 (26.7 -> 10.3). Where the clusters do
+// not run at once they cost twice that: 16 units by eight 17.8 (20.9).
+static int pieces_of(const SpanAttnParams& p) {
+    const int64_t reach = p.causal && p.prefix_lens == nullptr ? std::min<int64_t>(p.Lk, static_cast<int64_t>(p.q_offset) + p.Lq) : p.Lk;
+    const int64_t units = units_of(p);
+    if (reach < 768 || units > 256) return 1;
+    if (units <= clusters_at_once(8)) return 8;                       // one query, 768 keys: 7.3 against 8.1 us
+    if (reach >= 1024 && units <= clusters_at_once(4)) return 4;      // 30 units, 1024 keys: 9.7 against 10.2 (d_k = 128: 11.4, 11.0)
+    if (reach >= 1536 && units <= clusters_at_once(2)) return 2;      // 60 units, 1536 keys: 12.3 against 14.8 (14.3, 14.4)
+    return 1;
+}
+
 template <int kD>
 static cudaError_t launch_d(const SpanAttnParams& p, const SpanMaps& maps, int mode, cudaStream_t s) {
     return mode == kPlain    ? launch_mode<kD, kPlain>(p, maps, s)
@@ -624,7 +801,9 @@ static bool map_strided(CUtensorMap* m, const Strided& t, int B, int L, int H, i
     return encode_bf16_tiled(m, t.p, 5, dims, str, box, true);
 }
 
-cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s) {
+cudaError_t launch_span_attn(const SpanAttnParams& given, cudaStream_t s) {
+    SpanAttnParams p = given;
+    p.pieces = pieces_of(p);
     SpanMaps maps;
     if (!map_strided(&maps.q, p.q, p.B, p.Lq, p.h, p.d) || !map_strided(&maps.k, p.k, p.B, p.Lk, p.h_kv, p.d) ||
         !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
@@ -633,7 +812,7 @@ cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s) {
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
     if (p.d == 128) return launch_d<128>(p, maps, mode, s);
-    if (mode != kCapped && p.Lk >= kLongKeys) return launch_span_attn_d64(p, maps, mode, s);
+    if (mode != kCapped && p.Lk >= kLongKeys && p.pieces == 1) return launch_span_attn_d64(p, maps, mode, s);
     return launch_d<64>(p, maps, mode, s);
 }
 

@@ -98,6 +98,7 @@ struct SpanAttnParams {
     int causal, q_offset;
     int B, Lq, Lk, h, h_kv, d;
     int* status;
+    int pieces;              // set by the launcher: CTAs that share a unit
 };
 cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s);        // bf16
 cudaError_t launch_span_attn_f32(const SpanAttnParams& p, cudaStream_t s);
