@@ -426,6 +426,12 @@ ATT = [
     (30, 200, 1600, 4, 4, 64, dict(causal=True, q_offset=1400, valid=[0, 1600, 0, 0, 1, 1401] * 5)),
     (2, 1600, 1600, 2, 2, 64, dict(causal=True, prefix=[900, 0], valid=[1600, 1000])),
     (1, 600, 600, 2, 1, 64, dict(cap=300.0, causal=True)),
+    # ... with more tiles of 128 queries than SMs
+    (3, 300, 1800, 18, 6, 64, dict(causal=True, q_offset=1500, slopes=True)),
+    (2, 1700, 1700, 6, 2, 64, dict(docs=300, causal=True, pad=500)),
+    (2, 1700, 1700, 6, 3, 64, dict(docs=90, cap=20.0)),
+    (4, 257, 1537, 13, 1, 64, dict(cap=100.0, slopes=True, valid=[1537, 0, 700, 1536])),
+    (2, 1600, 1600, 6, 6, 64, dict(causal=True, prefix=[900, 0], valid=[1600, 1000])),
     # few queries, long keys: several CTAs share a query tile
     (1, 1, 8192, 4, 1, 128, dict(causal=True, q_offset=8191)),
     (2, 3, 4100, 2, 2, 64, dict(causal=True, q_offset=4097, slopes=True)),
@@ -509,11 +515,11 @@ def test_attention_fp32_strides_and_spans(bnd, d):
     assert empty.any() and (got[empty] == 0).all()
 
 
-@pytest.mark.parametrize("d,L", [(64, 200), (128, 200), (64, 1650)])
-def test_attention_head_major_strides_and_spans(bnd, d, L):
+@pytest.mark.parametrize("d,L,h", [(64, 200, 4), (128, 200, 4), (64, 1650, 4), (64, 1650, 6)])
+def test_attention_head_major_strides_and_spans(bnd, d, L, h):
     """[B, h, L, d] storage (the workspace's order), an output inside a wider tensor, arbitrary spans with
     empty and inverted rows."""
-    B, h, hk = 2, 4, 2
+    B, hk = 2, 2
     q = randn(70, B, h, L, d, dtype=BF).transpose(1, 2)
     k, v = randn(71, B, hk, L, d, dtype=BF).transpose(1, 2), randn(72, B, hk, L, d, dtype=BF).transpose(1, 2)
     rng = random.Random(7)
@@ -527,7 +533,7 @@ def test_attention_head_major_strides_and_spans(bnd, d, L):
     assert empty.any() and (got[empty] == 0).all()
 
 
-@pytest.mark.parametrize("d,L,cap", [(64, 700, 50.0), (128, 700, 20.0), (128, 130, 50.0), (64, 1600, 0.0)])
+@pytest.mark.parametrize("d,L,cap", [(64, 700, 50.0), (128, 700, 20.0), (128, 130, 50.0), (64, 1600, 0.0), (64, 2500, 0.0)])
 def test_attention_rows_of_one_key_are_its_value(bnd, d, L, cap):
     """One weight divided by itself is 1 whatever it was rounded to, so the only rounding is of a bf16 value to bf16."""
     q, k, v = (randn(73 + i, 2, L, n, d, dtype=BF) for i, n in enumerate((4, 2, 2)))

@@ -38,7 +38,8 @@ constexpr int kThreads = kSoft + 128;
 // unit k's by then.
 constexpr int kSlots = 8;
 // d_k = 64: from here on the kernel of two query tiles a unit (4 x L causal, 16 heads: L = 1024 31.2 against 28.7 us,
-// 1536 44.0 against 45.1 us, 4096 169 against 190 us).
+// 1536 44.0 against 45.1 us, 4096 169 against 190 us), where there are more units of one tile than SMs (1024 queries over
+// 4096 keys: 24 heads 42.5 against 48.4 us, 19 heads, all of whose units run at once, 41.6 against 27.7 us).
 constexpr int kLongKeys = 1536;
 constexpr uint32_t kColS = 0;                // + 128 b: score buffers S_0, S_1
 constexpr uint32_t kColP = 256;              // + 64 b + 16 h: weight buffers P_0, P_1
@@ -812,7 +813,11 @@ cudaError_t launch_span_attn(const SpanAttnParams& given, cudaStream_t s) {
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
     if (p.d == 128) return launch_d<128>(p, maps, mode, s);
-    if (mode != kCapped && p.Lk >= kLongKeys && p.pieces == 1) return launch_span_attn_d64(p, maps, mode, s);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (mode != kCapped && p.Lk >= kLongKeys && p.Lq > BM && units_of(p) > sms) return launch_span_attn_d64(p, maps, mode, s);
     return launch_d<64>(p, maps, mode, s);
 }
 
