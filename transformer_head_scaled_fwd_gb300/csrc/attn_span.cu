@@ -15,14 +15,12 @@
 // in tensor memory, so the score MMAs of tile j + 1 run during the softmax of tile j, and the next unit's loads and
 // first scores run during this unit's last tiles and output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
 // softmax warps rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
+// Few units (few queries over long keys): the CTAs of a cluster share one, see pieces_of.
 // Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408-418 us, with a
 // distance bias 471 us.
 #include <algorithm>
-#include <atomic>
 
 #include "attn_span.cuh"
-#include "launch.h"
-#include "ptx_pair.cuh"
 
 namespace mha {
 namespace {
@@ -147,52 +145,6 @@ __device__ __forceinline__ UnitInfo unit_of(const SpanAttnParams& p, int u, int 
     x.lo_max = lo_max;
     x.hi_min = hi_min;
     return x;
-}
-
-// The parts of a unit that kPieces CTAs share, each in its CTA's shared memory: maxima and sums of the rows from m_at on,
-// outputs [row][part_pitch] from o_at on. A CTA joins BM / kPieces rows, a thread four features of up to eight parts'
-// rows, all of whose loads are in flight together (one row after the other: 15.4 against 14.4 us
-// at 128 x 2048 keys by two, d_k = 128).
-__host__ __device__ constexpr int part_pitch(int d) { return d + 4; }
-template <int kD, int kPieces>
-__device__ __forceinline__ void join_parts(const SpanAttnParams& p, const UnitInfo& at, int piece, uint32_t m_at, uint32_t o_at) {
-    constexpr int kRows = BM / kPieces, kCols = kD / 4, kStep = kSoft / kCols;      // rows of one pass
-    constexpr int kItems = kRows > kStep ? kRows / kStep : 1;
-    const int c = threadIdx.x % kCols * 4, r0 = threadIdx.x / kCols;
-    float ms[kItems][kPieces], ls[kItems][kPieces];
-    float4 os[kItems][kPieces];
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int r = piece * kRows + min(r0 + i * kStep, kRows - 1);
-#pragma unroll
-        for (int s = 0; s < kPieces; ++s) {
-            ms[i][s] = ld_cluster(mapa_shared(m_at + r * 4, s));
-            ls[i][s] = ld_cluster(mapa_shared(m_at + (BM + r) * 4, s));
-            os[i][s] = ld_cluster4(mapa_shared(o_at + (r * part_pitch(kD) + c) * 4, s));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < kItems; ++i) {
-        const int r = piece * kRows + r0 + i * kStep;
-        if (r0 + i * kStep >= kRows || at.q0 + r >= p.Lq) continue;
-        float M = -CUDART_INF_F, L = 0.0f;
-#pragma unroll
-        for (int s = 0; s < kPieces; ++s) M = fmaxf(M, ms[i][s]);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int s = 0; s < kPieces; ++s) {
-            if (ms[i][s] == -CUDART_INF_F) continue;   // no key: its output may hold anything
-            const float f = ex2_approx(ms[i][s] - M);
-            L = fmaf(f, ls[i][s], L);
-            a.x = fmaf(f, os[i][s].x, a.x);
-            a.y = fmaf(f, os[i][s].y, a.y);
-            a.z = fmaf(f, os[i][s].z, a.z);
-            a.w = fmaf(f, os[i][s].w, a.w);
-        }
-        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key at all: zeros; NaN stays
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out.p) + at.b * p.out.b + (at.q0 + r) * p.out.l + at.head * p.out.h + c;
-        *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    }
 }
 
 // kSplit: the CTAs of a cluster share a unit, each with its piece of the key tiles; they join their parts through one
@@ -648,9 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             cluster_sync_all();
             const UnitInfo at = place_of(p, blockIdx.x / pieces);
             const uint32_t m_at = smem_u32(&sm->mx[0][0]), o_at = smem_u32(part);
-            if (pieces == 2) join_parts<kD, 2>(p, at, piece, m_at, o_at);
-            else if (pieces == 4) join_parts<kD, 4>(p, at, piece, m_at, o_at);
-            else join_parts<kD, 8>(p, at, piece, m_at, o_at);
+            join_parts<__nv_bfloat16, kD, BM, kSoft>(p, at.b, at.head, at.q0, pieces, piece, m_at, o_at);
             __syncwarp();
             cluster_sync_all();   // the others have read this CTA's part
         }
@@ -710,25 +660,6 @@ cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spa
     return launch_pdl(document_spans_kernel, dim3((L + kSpanThreads - 1) / kSpanThreads, B), dim3(kSpanThreads), 0, s, ids, L, spans);
 }
 
-// launch_pdl with clusters of `size` CTAs.
-template <typename... Params, typename... Args>
-static cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int size, size_t smem, cudaStream_t s,
-                                      Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-}
-
 static int64_t units_of(const SpanAttnParams& p) { return static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM); }
 
 template <int kD, int kMode, bool kSplit>
@@ -745,31 +676,12 @@ template <int kD, int kMode>
 static cudaError_t launch_mode(const SpanAttnParams& p, const SpanMaps& maps, cudaStream_t s) {
     return p.pieces > 1 ? launch_as<kD, kMode, true>(p, maps, s) : launch_as<kD, kMode, false>(p, maps, s);
 }
-// Clusters of `size` CTAs that the current device runs at once (an SM holds one CTA of any instance); asked once a
-// device, for it is a property of the device.
 static int clusters_at_once(int size) {
-    constexpr int kDevices = 64;
-    static std::atomic<int> known[kDevices][4];      // by log2(size); 0: not asked, else 1 + the answer
-    const int lg = size == 8 ? 3 : size == 4 ? 2 : 1;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
-    if (const int k = known[dev][lg].load(std::memory_order_relaxed)) return k - 1;
+    static ClusterRoom room;      // an SM holds one CTA of any instance
     auto kernel = span_attn_kernel<128, kGeneral, true>;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(size);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<128>();
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_bytes<128>())) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
-        return 0;
-    known[dev][lg].store(n + 1, std::memory_order_relaxed);
-    return n;
+    constexpr size_t kBytes = smem_bytes<128>();
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kBytes)) != cudaSuccess) return 0;
+    return room.at_once(kernel, kThreads, kBytes, size);
 }
 
 // CTAs that share a unit: with few units (few queries over long keys) most SMs would stand idle and a unit would go

@@ -4,7 +4,11 @@
 
 #include <math_constants.h>
 
+#include <atomic>
+
+#include "launch.h"
 #include "mha_internal.h"
+#include "ptx_pair.cuh"
 #include "ptx_serve.cuh"
 #include "serve.h"
 
@@ -201,6 +205,111 @@ __device__ __forceinline__ void bias_scores(uint32_t (&u)[kKeys], float scale, f
             u[c] = __float_as_uint(fmaf(-slope, fabsf(away - static_cast<float>(c)), __uint_as_float(u[c]) * scale));
     }
 }
+
+// A unit that the CTAs of a cluster share: each has its piece of the key tiles, and leaves its part in its shared memory:
+// maxima of kUnit rows from m_at on, their sums behind them, outputs [row][part_pitch] from o_at on. A CTA joins kUnit /
+// kPieces rows, a thread four features of a row of all parts at a time; all its loads are in flight together (one row after
+// the other: 15.4 against 14.4 us at 128 x 2048 keys by two, d_k = 128, bf16).
+__host__ __device__ constexpr int part_pitch(int d) { return d + 4; }
+__device__ __forceinline__ void store4(__nv_bfloat16* y, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+}
+__device__ __forceinline__ void store4(float* y, float a, float b, float c, float d) {
+    *reinterpret_cast<float4*>(y) = make_float4(a, b, c, d);
+}
+template <typename T, int kD, int kUnit, int kThr, int kPieces>
+__device__ __forceinline__ void join_by(const SpanAttnParams& p, int b, int head, int q0, int piece, uint32_t m_at, uint32_t o_at) {
+    constexpr int kRows = kUnit / kPieces, kCols = kD / 4, kStep = kThr / kCols;      // rows of one pass
+    constexpr int kItems = kRows > kStep ? kRows / kStep : 1;
+    const int c = threadIdx.x % kCols * 4, r0 = threadIdx.x / kCols;
+    float ms[kItems][kPieces], ls[kItems][kPieces];
+    float4 os[kItems][kPieces];
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int r = piece * kRows + min(r0 + i * kStep, kRows - 1);
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) {
+            ms[i][s] = ld_cluster(mapa_shared(m_at + r * 4, s));
+            ls[i][s] = ld_cluster(mapa_shared(m_at + (kUnit + r) * 4, s));
+            os[i][s] = ld_cluster4(mapa_shared(o_at + (r * part_pitch(kD) + c) * 4, s));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+        const int r = piece * kRows + r0 + i * kStep;
+        if (r0 + i * kStep >= kRows || q0 + r >= p.Lq) continue;
+        float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) M = fmaxf(M, ms[i][s]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kPieces; ++s) {
+            if (ms[i][s] == -CUDART_INF_F) continue;   // no key: its output may hold anything
+            const float f = ex2_approx(ms[i][s] - M);
+            L = fmaf(f, ls[i][s], L);
+            a.x = fmaf(f, os[i][s].x, a.x);
+            a.y = fmaf(f, os[i][s].y, a.y);
+            a.z = fmaf(f, os[i][s].z, a.z);
+            a.w = fmaf(f, os[i][s].w, a.w);
+        }
+        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key at all: zeros; NaN stays
+        store4(static_cast<T*>(p.out.p) + b * p.out.b + (q0 + r) * p.out.l + head * p.out.h + c, a.x * inv, a.y * inv, a.z * inv,
+               a.w * inv);
+    }
+}
+template <typename T, int kD, int kUnit, int kThr>
+__device__ __forceinline__ void join_parts(const SpanAttnParams& p, int b, int head, int q0, int pieces, int piece, uint32_t m_at,
+                                           uint32_t o_at) {
+    if (pieces == 2) join_by<T, kD, kUnit, kThr, 2>(p, b, head, q0, piece, m_at, o_at);
+    else if (pieces == 4) join_by<T, kD, kUnit, kThr, 4>(p, b, head, q0, piece, m_at, o_at);
+    else join_by<T, kD, kUnit, kThr, 8>(p, b, head, q0, piece, m_at, o_at);
+}
+
+// launch_pdl with clusters of `size` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int size, size_t smem, cudaStream_t s,
+                                      Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
+}
+
+// Clusters of a kernel, allowed `smem` bytes by the caller, that the current device runs at once; asked once a device and
+// size, for it is a property of the device.
+struct ClusterRoom {
+    static constexpr int kDevices = 64;
+    std::atomic<int> known[kDevices][4] = {};      // by log2(size); 0: not asked, else 1 + the answer
+    template <typename Kernel>
+    int at_once(Kernel kernel, int threads, size_t smem, int size) {
+        const int lg = size == 8 ? 3 : size == 4 ? 2 : 1;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+        if (const int k = known[dev][lg].load(std::memory_order_relaxed)) return k - 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+        known[dev][lg].store(n + 1, std::memory_order_relaxed);
+        return n;
+    }
+};
 
 }  // namespace
 

@@ -13,8 +13,9 @@
 // heads of 128: 1364 us; single ones in the product 1448 us, in both 1562 us).
 // Measured, 2 x 4096, 8 heads of 128: all keys 2792 us, 49 TFLOP/s (0.66 of 128 multiply-adds a clock and SM); causal
 // 1364 us; of 64: 1628 and 782 us.
+#include <algorithm>
+
 #include "attn_span.cuh"
-#include "launch.h"
 
 namespace mha {
 namespace {
@@ -47,18 +48,19 @@ __device__ __forceinline__ void load_tile(float* dst, const float* src, int64_t 
     }
 }
 
-template <int kD>
+template <int kD, bool kSplit>
 __global__ void __launch_bounds__(kThreads, Geo<kD>::kCtas) span_attn_f32_kernel(const __grid_constant__ SpanAttnParams p) {
     constexpr int kTile = Geo<kD>::kTile, kV4 = kD / 64;      // float4 of the output a row and thread
     extern __shared__ __align__(16) float sm[];
     float *qs = sm, *ks = sm + kTile, *vs = sm + 2 * kTile, *ps = sm + 3 * kTile;
     int2* ivs = reinterpret_cast<int2*>(ps + BM * BK);
+    const int pieces = kSplit ? p.pieces : 1, piece = kSplit ? static_cast<int>(cluster_ctarank()) : 0;
     pdl_trigger();
     pdl_wait();   // the tensors and the mask parts come from earlier kernels
 
     // units with the last queries first: the longest under a causal mask
     const int planes = p.B * p.h, tiles = (p.Lq + BM - 1) / BM;
-    const int back = blockIdx.x / planes, plane = blockIdx.x - back * planes;
+    const int unit = blockIdx.x / pieces, back = unit / planes, plane = unit - back * planes;
     const int q0 = (tiles - 1 - back) * BM, b = plane / p.h, head = plane - b * p.h, kvh = head / (p.h / p.h_kv);
     const int lane = threadIdx.x & 31;
     const int valid = p.valid_lens != nullptr ? min(max(p.valid_lens[b], 0), p.Lk) : p.Lk;
@@ -84,7 +86,12 @@ __global__ void __launch_bounds__(kThreads, Geo<kD>::kCtas) span_attn_f32_kernel
     hi_min = __reduce_min_sync(0xffffffffu, hi_min);
     lo_min = __reduce_min_sync(0xffffffffu, lo_min);
     hi_max = __reduce_max_sync(0xffffffffu, hi_max);
-    const int j0 = lo_min / BK, j1 = hi_max > lo_min ? (hi_max + BK - 1) / BK : j0;
+    int j0 = lo_min / BK, j1 = hi_max > lo_min ? (hi_max + BK - 1) / BK : j0;
+    if constexpr (kSplit) {
+        const int64_t n = j1 - j0;
+        j1 = j0 + static_cast<int>(n * (piece + 1) / pieces);
+        j0 += static_cast<int>(n * piece / pieces);
+    }
 
     const float* q = static_cast<const float*>(p.q.p) + b * p.q.b + head * p.q.h;
     const float* k = static_cast<const float*>(p.k.p) + b * p.k.b + kvh * p.k.h;
@@ -217,13 +224,37 @@ __global__ void __launch_bounds__(kThreads, Geo<kD>::kCtas) span_attn_f32_kernel
                 }
         }
     }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+    if constexpr (kSplit) {
+        // the part in place of the key and value tiles, its statistics in place of the weights
+        float* const part = ks;
+        static_assert(BM * part_pitch(kD) <= 2 * kTile, "a part fits the tiles");
+        __syncthreads();   // the last values and weights have been read
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int row = rg * kRows + i;
+            if (kg == 0) {
+                ps[row] = m[i];
+                ps[BM + row] = l[i];
+            }
+#pragma unroll
+            for (int e = 0; e < kV4; ++e) *reinterpret_cast<float4*>(part + row * part_pitch(kD) + e * 64 + kg * 4) = o[i][e];
+        }
+        __syncwarp();
+        cluster_sync_all();
+        join_parts<float, kD, BM, kThreads>(p, b, head, q0, pieces, piece, smem_u32(ps), smem_u32(part));
+        __syncwarp();
+        cluster_sync_all();   // the others have read this CTA's part
+        return;
+    }
     float* out = static_cast<float*>(p.out.p) + b * p.out.b + head * p.out.h;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int row = q0 + rg * kRows + i;
-        float L = l[i];
-#pragma unroll
-        for (int d = 1; d < kLanes; d <<= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+        const float L = l[i];
         const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
         if (row >= p.Lq) continue;
 #pragma unroll
@@ -234,13 +265,37 @@ __global__ void __launch_bounds__(kThreads, Geo<kD>::kCtas) span_attn_f32_kernel
 }
 
 template <int kD>
-cudaError_t launch_d(const SpanAttnParams& p, cudaStream_t s) {
+cudaError_t launch_d(SpanAttnParams p, cudaStream_t s) {
     constexpr int kBytes = Geo<kD>::kBytes;
     static_assert(Geo<kD>::kCtas * (kBytes + 1024) <= 228 * 1024, "shared memory budget");
-    cudaError_t e = cudaFuncSetAttribute(span_attn_f32_kernel<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    const int64_t units = static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM);
+    // As in bf16: as many CTAs a unit as let all units run at once; a tile takes longer here, so fewer keys pay for it. Where
+    // clusters of eight fit with a CTA an SM they ask for more shared memory than half an SM has, because side by side
+    // they take twice as long (one query over 4096 keys, 8 heads of 64 (128), us by one CTA 344 (499), side by side 77
+    // (111), an SM each 43 (70)); more units share SMs (200 queries over 2000 keys, 20 heads: 350 -> 94 (413 -> 219)).
+    constexpr int kAlone = 120 * 1024;
+    static_assert(kBytes <= kAlone, "room for the tiles");
+    auto kernel = span_attn_f32_kernel<kD, true>;
+    static ClusterRoom alone, shared;
+    const int64_t reach = p.causal && p.prefix_lens == nullptr ? std::min<int64_t>(p.Lk, static_cast<int64_t>(p.q_offset) + p.Lq) : p.Lk;
+    int bytes = kAlone;
+    p.pieces = 1;
+    if (reach >= 256 && units <= 1024) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
+        if (e != cudaSuccess) return e;
+        if (units <= alone.at_once(kernel, kThreads, kAlone, 8)) {
+            p.pieces = 8;
+        } else {
+            bytes = kBytes;
+            for (int size = 8; size > 1 && p.pieces == 1; size /= 2)
+                if (units <= shared.at_once(kernel, kThreads, kBytes, size)) p.pieces = size;
+        }
+    }
+    if (p.pieces > 1)
+        return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(units * p.pieces)), dim3(kThreads), p.pieces, bytes, s, p);
+    cudaError_t e = cudaFuncSetAttribute(span_attn_f32_kernel<kD, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.h * ((p.Lq + BM - 1) / BM));
-    return launch_pdl(span_attn_f32_kernel<kD>, dim3(grid), dim3(kThreads), kBytes, s, p);
+    return launch_pdl(span_attn_f32_kernel<kD, false>, dim3(static_cast<unsigned>(units)), dim3(kThreads), kBytes, s, p);
 }
 
 }  // namespace
