@@ -63,6 +63,9 @@ ROTARY = [
     (F32, 1, 7, 1, 3, 128, 96, False, 123456789),
     (F32, 1, 7, 2, 1, 5, 2, True, 9),
     (F32, 1, 3, 2, 1, 256, 256, False, 0),
+    # halves of odd length beside wide heads
+    (BF, 2, 37, 5, 2, 64, 14, False, 9), (BF, 2, 19, 6, 2, 128, 126, False, 500), (BF, 1, 301, 3, 1, 512, 510, False, 3),
+    (F32, 1, 21, 3, 3, 64, 10, False, 4), (F32, 3, 50, 2, 1, 256, 250, False, 100000), (BF, 1, 9, 4, 1, 16, 2, False, 7),
 ]
 
 
@@ -94,6 +97,19 @@ def test_rotary_in_place_default_and_negative_positions(bnd):
     bnd.mha_rotary(x, q_out=z, positions=pos, rotary=bnd.make_rotary(f))
     ref = R.rotate(x, pos, f)
     R.check(z, ref, R.rotate_tol(x, ref, f, False, BF), "negative positions")
+
+
+@pytest.mark.parametrize("dtype,d,rot", [(BF, 64, 22), (BF, 128, 126), (F32, 64, 6)])
+def test_rotary_in_place_with_odd_halves(bnd, dtype, d, rot):
+    x = randn(3, 3, 200, 6, d, dtype=dtype)
+    y, z = x.clone(), torch.empty_like(x)
+    r = bnd.make_rotary(freqs(rot))
+    bnd.mha_rotary(y, q_out=y, rotary=r)
+    bnd.mha_rotary(x, q_out=z, rotary=r)
+    assert torch.equal(y, z) and not torch.equal(x, z)
+    narrow = torch.empty(3, 200, 6, d + 1, device="cuda", dtype=dtype)[..., 1:]      # the same bits an element an access
+    bnd.mha_rotary(x, q_out=narrow, rotary=r)
+    assert torch.equal(narrow, z)
 
 
 def test_rotary_unaligned_views(bnd):
@@ -137,6 +153,8 @@ APPEND = [
     (BF, 33, 2, 2, 128, 128, True, 64, "heads", [60, 64, 1], None),
     (F32, 21, 3, 1, 64, 64, False, 8, "slots", [5, 0, 90], [21, 1, 20]),
     (F32, 5, 2, 2, 20, 6, True, 7, "slots", [5, 0, 9], [5, -2, 9]),      # lengths beyond T and below 0
+    (BF, 33, 5, 2, 64, 22, False, 8, "heads", [0, 23, 50], [33, 0, 17]),
+    (F32, 33, 5, 2, 64, 62, False, 8, "slots", [0, 23, 50], [33, 0, 17]),
 ]
 
 

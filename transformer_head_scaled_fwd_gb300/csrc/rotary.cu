@@ -74,17 +74,23 @@ struct TokenInfo {
     int64_t slot;       // elements, or -1
 };
 
+// kStaged: the half layout where no wide chunk's partner is a chunk (rot / 2 odd, say). A thread moves one chunk of a row,
+// and the pairs turn in shared memory, one a thread at a time (6 x 585 tokens of 40 + 5 bf16 heads of 64, 14 features turned:
+// 27.6 us with an element an access, 16.6 us so; 4 x 8192 of 32 + 8 heads of 128, 126 turned: 447 and 224 us). Chunks of four
+// bf16 elements that pair up are as fast as that or faster.
 struct RowPlan {
     FastDiv q, k;           // heads
+    FastDiv half;           // kStaged: rot / 2
     int items, turn;        // of a row; of those, the ones that turn
     int rows;               // rows of the CTA at a time: threads / items
     int per_cta;            // rows of a CTA: up to kRows * rows
     int tokens;             // most tokens that such rows touch
+    int stage_at;           // kStaged: offset of the rows in shared memory
     int ctas_q, ctas_k;     // then the values'
     int64_t total;          // B * T
 };
 
-template <typename T, int kN>
+template <typename T, int kN, bool kStaged>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p, const RowPlan plan) {
     using C = Chunk<T, kN>;
     using Raw = decltype(C::raw);
@@ -92,6 +98,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int half = p.rot / 2;
     TokenInfo* info = reinterpret_cast<TokenInfo*>(smem);
     float2* turns = reinterpret_cast<float2*>(info + plan.tokens);     // [tokens][half]
+    T* stage = reinterpret_cast<T*>(smem + plan.stage_at);              // kStaged: [rows][d]
     pdl_trigger();
     pdl_wait();
     const int job = static_cast<int>(blockIdx.x) < plan.ctas_q ? 0 : static_cast<int>(blockIdx.x) < plan.ctas_q + plan.ctas_k ? 1 : 2;
@@ -120,7 +127,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const int r = threadIdx.x / plan.items, c = threadIdx.x - r * plan.items;
     int c0, c1;     // the item's elements
     bool turns_here = job != 2 && c < plan.turn;
-    if (job == 2) {
+    if (kStaged) {
+        c0 = c * kN;
+        c1 = p.d;
+    } else if (job == 2) {
         c0 = c * 2 * kN;
         c1 = c0 + kN;
     } else if (c >= plan.turn) {
@@ -147,6 +157,11 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         x0[n].raw = *reinterpret_cast<const Raw*>(src + c0);
         if (two) x1[n].raw = *reinterpret_cast<const Raw*>(src + c1);
     }
+    if constexpr (kStaged) {
+#pragma unroll
+        for (int n = 0; n < kRows; ++n)
+            if (tok[n] >= 0 && turns_here) *reinterpret_cast<Raw*>(stage + (n * plan.rows + r) * p.d + c0) = x0[n].raw;
+    }
     if (job != 2) {
         for (int i = threadIdx.x; i < here * half; i += kThreads) {
             const int tk = i / half;
@@ -170,13 +185,27 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         }
     }
     __syncthreads();
+    if (kStaged && job != 2) {
+        for (int i = threadIdx.x; i < rows * half; i += kThreads) {
+            const int row = plan.half.div(i), e = i - row * half, tk = heads.div(skip + row);
+            if (info[tk].t < 0) continue;
+            T* x = stage + row * p.d + e;
+            const float2 a = turns[tk * half + e];
+            const float u = load_f(x), v = load_f(x + half);
+            store_f(x, fmaf(u, a.x, -(v * a.y)));
+            store_f(x + half, fmaf(v, a.x, u * a.y));
+        }
+        __syncthreads();
+    }
 #pragma unroll
     for (int n = 0; n < kRows; ++n) {
         if (tok[n] < 0) continue;
         const TokenInfo& x = info[tok[n]];
         if (turns_here) {
             const float2* cs = turns + tok[n] * half;
-            if (kN > 1 && p.interleaved) {
+            if constexpr (kStaged) {
+                x0[n].raw = *reinterpret_cast<const Raw*>(stage + (n * plan.rows + r) * p.d + c0);
+            } else if (kN > 1 && p.interleaved) {
 #pragma unroll
                 for (int j = 0; j < 2 * kN; j += 2) {
                     C& y = j < kN ? x0[n] : x1[n];
@@ -212,21 +241,21 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     }
 }
 
-// Whether every chunk of kN elements is aligned and every pair of chunks turns together.
+// Whether every chunk of n elements is aligned and, unless they go through shared memory, every pair of chunks turns together.
 template <typename T>
-bool chunks_fit(const RotaryParams& p, int n) {
+bool chunks_fit(const RotaryParams& p, int n, bool staged = false) {
     const size_t bytes = n * sizeof(T);
     auto tensor = [&](const Strided& x) {
         return x.p == nullptr || (reinterpret_cast<uintptr_t>(x.p) % bytes == 0 && x.b % n == 0 && x.l % n == 0 && x.h % n == 0);
     };
-    return p.d % n == 0 && (p.interleaved || (p.rot % n == 0 && p.rot / 2 % n == 0)) && tensor(p.q) && tensor(p.q_out) &&
+    return p.d % n == 0 && (staged || p.interleaved || (p.rot % n == 0 && p.rot / 2 % n == 0)) && tensor(p.q) && tensor(p.q_out) &&
            tensor(p.k) && tensor(p.k_out) && tensor(p.v) &&
            (p.cache.k == nullptr ||
             (reinterpret_cast<uintptr_t>(p.cache.k) % bytes == 0 && reinterpret_cast<uintptr_t>(p.cache.v) % bytes == 0 &&
              p.cache.page_stride % n == 0 && p.cache.slot_stride % n == 0 && p.cache.head_stride % n == 0));
 }
 
-template <typename T, int kN>
+template <typename T, int kN, bool kStaged = false>
 cudaError_t launch_n(const RotaryParams& p, cudaStream_t s) {
     constexpr int kPair = 2 * kN;
     RowPlan plan;
@@ -235,6 +264,11 @@ cudaError_t launch_n(const RotaryParams& p, cudaStream_t s) {
     const bool inside = p.interleaved && kN > 1;
     plan.turn = inside ? (p.d + kPair - 1) / kPair : (p.rot + kPair - 1) / kPair;
     plan.items = plan.turn + (inside ? 0 : (p.d - p.rot + kPair - 1) / kPair);
+    if (kStaged) {
+        plan.half = fast_div(static_cast<uint32_t>(p.rot / 2));
+        plan.turn = (p.rot + kN - 1) / kN;
+        plan.items = p.d / kN;
+    }
     plan.rows = kThreads / plan.items;
     plan.total = static_cast<int64_t>(p.B) * p.T;
     const int nq = p.q.p != nullptr ? p.h : 0, nk = p.k.p != nullptr ? p.h_kv : 0;
@@ -253,16 +287,20 @@ cudaError_t launch_n(const RotaryParams& p, cudaStream_t s) {
     plan.ctas_q = ctas(nq);
     plan.ctas_k = ctas(nk);
     const int64_t grid = static_cast<int64_t>(plan.ctas_q) + plan.ctas_k + (p.v.p != nullptr ? ctas(nk) : 0);
-    return launch_pdl(rotary_kernel<T, kN>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), plan.tokens * token_bytes, s, p,
-                      plan);
+    // tokens' part: at most 32 KB; the rows: kRows * kThreads chunks of 16 bytes at most
+    plan.stage_at = static_cast<int>((plan.tokens * token_bytes + 15) / 16 * 16);
+    const size_t smem = plan.stage_at + (kStaged ? kRows * plan.rows * p.d * sizeof(T) : 0);
+    return launch_pdl(rotary_kernel<T, kN, kStaged>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p, plan);
 }
 
 template <typename T>
 cudaError_t launch_t(RotaryParams p, cudaStream_t s) {
     p.by_t = fast_div(static_cast<uint32_t>(p.T));
-    if constexpr (sizeof(T) == 2)
-        if (chunks_fit<T>(p, 8)) return launch_n<T, 8>(p, s);
-    if (chunks_fit<T>(p, 4)) return launch_n<T, 4>(p, s);
+    constexpr int kWide = 16 / sizeof(T);
+    if (chunks_fit<T>(p, kWide)) return launch_n<T, kWide>(p, s);
+    if constexpr (kWide == 8)
+        if (chunks_fit<T>(p, 4)) return launch_n<T, 4>(p, s);
+    if (!p.interleaved && p.rot > 0 && chunks_fit<T>(p, kWide, true)) return launch_n<T, kWide, true>(p, s);
     if (chunks_fit<T>(p, 2)) return launch_n<T, 2>(p, s);
     return launch_n<T, 1>(p, s);
 }
