@@ -16,8 +16,8 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
-import warnings
 import threading
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmha.so")
