@@ -621,6 +621,9 @@ NORM = [
     (BF, 9, 255, True, True), (BF, 4, 2047, True, True), (BF, 3, 4095, True, True), (BF, 2, 8191, True, True),
     (F32, 1, 1, True, True), (F32, 17, 1000, True, True), (F32, 4, 2048, False, False), (F32, 3, 12292, True, True),
     (F32, 2, 4099, True, True),
+    # several rows a warp
+    (BF, 131, 64, True, True), (BF, 67, 128, False, True), (BF, 35, 24, True, True), (BF, 1000, 96, True, False), (F32, 77, 32, True, True),
+    (F32, 41, 64, False, True), (F32, 1, 16, True, True), (BF, 77, 33, True, True), (F32, 45, 63, True, True), (BF, 9, 123, False, True),
 ]
 
 
@@ -650,7 +653,8 @@ def test_rmsnorm(bnd, dtype, rows, d, res, gain):
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("rows,d,group", [(1, 64, 0), (5, 999, 0), (7, 1024, 128), (3, 4096, 64), (2, 160, 32),
                                           (40, 4096, 0), (3, 8192, 128), (2, 20000, 32), (3, 16384, 0), (2, 30000, 0),
-                                          (620, 1024, 32), (615, 4096, 128), (5, 255, 0), (2, 3999, 0), (700, 64, 64)])
+                                          (620, 1024, 32), (615, 4096, 128), (5, 255, 0), (2, 3999, 0), (700, 64, 64),
+                                          (77, 64, 32), (41, 128, 32), (99, 128, 64), (33, 128, 0), (19, 96, 32), (50, 48, 0), (77, 123, 0)])
 def test_rmsnorm_e4m3(bnd, dtype, rows, d, group):
     """The scale to fp32 rounding; each value within half a step of e4m3 (2^-4 relative; 2^-10 below the
     smallest normal, 2^-6) of y / scale, where y / scale itself is off by the fp32 error of y and the scale."""

@@ -98,11 +98,11 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[kN]) {
         *p = to_e4m3(f[0]);
 }
 
-// Sum (or maximum) over the kThr threads of a row; one barrier of theirs, `part` is used once.
+// Sum (or maximum) over the kThr threads of a row; for more than a warp one barrier of theirs, `part` is used once.
 template <int kThr, bool kMax>
 __device__ __forceinline__ float row_reduce(float v, float* part) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = (kThr < 32 ? kThr : 32) / 2; o > 0; o >>= 1) {
         const float w = __shfl_xor_sync(0xffffffffu, v, o);
         v = kMax ? fmaxf(v, w) : v + w;
     }
@@ -121,19 +121,22 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
 // 108 us with one row a CTA, 84 us with two).
 __host__ __device__ constexpr int rows_of_cta(int thr) { return kThreads / thr; }
 
-// The row stays in registers between the passes: kThr threads a row, kC accesses a thread. Groups need Vec (a group is up to 32 neighbouring lanes of one access).
+// The row stays in registers between the passes: kThr threads a row, kC accesses a thread. Groups need Vec (a group is up to 32 neighbouring lanes of one access;
+// rows of fewer lanes hold no wider group than that, or are one group).
 template <typename V, int kThr, int kC, bool kQuant>
 __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(const __grid_constant__ RmsNormParams p) {
     using T = typename V::T;
     using Raw = typename V::Raw;
     constexpr int kN = V::kN;
     constexpr int kRowsCta = rows_of_cta(kThr);
-    __shared__ float part[2][kRowsCta][kThr / 32];
+    __shared__ float part[2][kRowsCta][kThr < 32 ? 1 : kThr / 32];
     const int tid = threadIdx.x % kThr, sub = threadIdx.x / kThr;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRowsCta + sub;
+    const int64_t mine = static_cast<int64_t>(blockIdx.x) * kRowsCta + sub;
+    const bool live = mine < p.rows;
+    const int64_t row = kThr < 32 ? min(mine, p.rows - 1) : mine;
     pdl_trigger();
     pdl_wait();
-    if (row >= p.rows) return;      // all threads of the row: its barriers are its own
+    if (kThr >= 32 && !live) return;      // all threads of the row: its barriers are its own
     const T* x = static_cast<const T*>(p.x) + row * p.x_stride;
     const T* r = static_cast<const T*>(p.residual) + row * p.r_stride;
     const T* gain = static_cast<const T*>(p.gain);
@@ -162,7 +165,7 @@ __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(co
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int i = (c * kThr + tid) * kN;
-            if (i < p.d) V::store(sum + i, z[c]);
+            if (live && i < p.d) V::store(sum + i, z[c]);
         }
     }
     const float inv = rsqrtf(row_reduce<kThr, false>(ss, part[0][sub]) / p.d + p.eps);
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(co
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
             const int i = (c * kThr + tid) * kN;
-            if (i < p.d) V::store(y + i, z[c]);
+            if (live && i < p.d) V::store(y + i, z[c]);
         }
     } else {
         uint8_t* y = static_cast<uint8_t*>(p.y) + row * p.y_stride;
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(co
 #pragma unroll
             for (int c = 1; c < kC; ++c) top[0] = fmaxf(top[0], top[c]);
             top[0] = row_reduce<kThr, true>(top[0], part[1][sub]);
-            if (tid == 0) p.scales[row] = Quant(top[0]).scale;
+            if (live && tid == 0) p.scales[row] = Quant(top[0]).scale;
 #pragma unroll
             for (int c = 1; c < kC; ++c) top[c] = top[0];
         } else {
@@ -208,7 +211,7 @@ __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(co
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1)
                     if (o * kN < p.group) top[c] = fmaxf(top[c], __shfl_xor_sync(0xffffffffu, top[c], o));
-                if (i < p.d && (i & (p.group - 1)) == 0)
+                if (live && i < p.d && (i & (p.group - 1)) == 0)
                     p.scales[row * (p.d >> p.group_log2) + (i >> p.group_log2)] = Quant(top[c]).scale;
             }
         }
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThr* rows_of_cta(kThr)) rmsnorm_row_kernel(co
             const Quant quant(top[c]);
 #pragma unroll
             for (int e = 0; e < kN; ++e) z[c][e] = quant(z[c][e]);
-            if (i < p.d) store_e4m3<kN>(y + i, z[c]);
+            if (live && i < p.d) store_e4m3<kN>(y + i, z[c]);
         }
     }
 }
@@ -309,6 +312,10 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
         // 8.2 us with the launch).
         const bool few = p.rows <= 608;
         const int chunks = p.d / kN;
+        // Narrow rows (a norm of each head) share a warp, whose instructions then serve several (1310720 x 128: 232 us with a
+        // warp a row, 126 us with 16 lanes and one access each, 103 us with 8 and two; x 64: 229, 64 and 53 us).
+        if (chunks <= 8) return launch_row<V, 4, 2>(p, s);
+        if (chunks <= 16) return launch_row<V, 8, 2>(p, s);
         if (chunks <= 32) return launch_row<V, 32, 1>(p, s);
         if (chunks <= 64) return launch_row<V, 32, 2>(p, s);
         if (chunks <= 128) return few ? launch_row<V, 64, 2>(p, s) : launch_row<V, 32, 4>(p, s);
@@ -317,6 +324,8 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
         if (chunks <= 1024) return launch_row<V, 256, 4>(p, s);
         if (chunks <= 2048) return launch_row<V, 256, 8>(p, s);
     } else if (p.scales == nullptr || p.group == p.d) {
+        if (p.d <= 64) return launch_row<O, 16, 4>(p, s);
+        if (p.d <= 128) return launch_row<O, 32, 4>(p, s);
         if (p.d <= 256) return launch_row<O, 32, 8>(p, s);
         if (p.d <= 512) return launch_row<O, 32, 16>(p, s);
         if (p.d <= 1024) return launch_row<O, 64, 16>(p, s);
