@@ -654,7 +654,8 @@ def test_rmsnorm(bnd, dtype, rows, d, res, gain):
 @pytest.mark.parametrize("rows,d,group", [(1, 64, 0), (5, 999, 0), (7, 1024, 128), (3, 4096, 64), (2, 160, 32),
                                           (40, 4096, 0), (3, 8192, 128), (2, 20000, 32), (3, 16384, 0), (2, 30000, 0),
                                           (620, 1024, 32), (615, 4096, 128), (5, 255, 0), (2, 3999, 0), (700, 64, 64),
-                                          (77, 64, 32), (41, 128, 32), (99, 128, 64), (33, 128, 0), (19, 96, 32), (50, 48, 0), (77, 123, 0)])
+                                          (77, 64, 32), (41, 128, 32), (99, 128, 64), (33, 128, 0), (19, 96, 32), (50, 48, 0), (77, 123, 0),
+                                          (23, 256, 128), (23, 256, 64), (50, 192, 64), (13, 512, 128), (21, 384, 128)])
 def test_rmsnorm_e4m3(bnd, dtype, rows, d, group):
     """The scale to fp32 rounding; each value within half a step of e4m3 (2^-4 relative; 2^-10 below the
     smallest normal, 2^-6) of y / scale, where y / scale itself is off by the fp32 error of y and the scale."""

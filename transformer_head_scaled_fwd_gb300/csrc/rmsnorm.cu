@@ -313,10 +313,11 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
         const bool few = p.rows <= 608;
         const int chunks = p.d / kN;
         // Narrow rows (a norm of each head) share a warp, whose instructions then serve several (1310720 x 128: 232 us with a
-        // warp a row, 126 us with 16 lanes and one access each, 103 us with 8 and two; x 64: 229, 64 and 53 us).
+        // warp a row, 126 us with 16 lanes and one access each, 103 us with 8 and two; x 64: 229, 64 and 53 us; 524288 x 256: 100 us with
+        // 32 lanes, 82 us with 16). 64 chunks keep 32 lanes: a group of 128 fp32 elements has as many.
         if (chunks <= 8) return launch_row<V, 4, 2>(p, s);
         if (chunks <= 16) return launch_row<V, 8, 2>(p, s);
-        if (chunks <= 32) return launch_row<V, 32, 1>(p, s);
+        if (chunks <= 32) return launch_row<V, 16, 2>(p, s);
         if (chunks <= 64) return launch_row<V, 32, 2>(p, s);
         if (chunks <= 128) return few ? launch_row<V, 64, 2>(p, s) : launch_row<V, 32, 4>(p, s);
         if (chunks <= 256) return few ? launch_row<V, 128, 2>(p, s) : launch_row<V, 64, 4>(p, s);
