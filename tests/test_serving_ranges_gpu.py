@@ -1,0 +1,111 @@
+"""Serving operators at the ends of their ranges (caps, values, empty and NaN rows, rounding of codes) and where a step
+lost or doubled would show, against plain 64-bit forms."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import serving_ref as R  # noqa: E402
+import test_serving_gpu as S  # noqa: E402
+from test_serving_gpu import BF, E4M3, F32, bnd, clean_status, ints, randn  # noqa: E402, F401
+
+pytestmark = pytest.mark.gpu
+
+
+def attend_fine(q, k, v, allowed, distance, *, scale, cap=0.0, slope=0.0):
+    """One head in fp64 with a bound of |kernel - o| from the error of each key's own score: d products summed in fp32
+    (d 2^-24 of sum |q k|), four roundings, and with a cap 2^-19 of min(cap, sum |q k|): tanh by its polynomials is within
+    2^-19.7 of its value, its three fp32 roundings within 2^-22.4; beyond |x| = 0.7 an error of 2^-22 of the cap is below
+    2^-21 of the score. A weight is then off by a relative d_j = e^(2 error_j) - 1, and o by sum p_j (d_j + sum p d) |v_j|;
+    exp2 2^-20, weights to bf16 half a step, n sums in fp32 as in serving_ref.attend_tol."""
+    dtype, (n, d) = v.dtype, v.shape
+    q, k, v = q.double(), k.double(), v.double()
+    s = (q @ k.T) * scale
+    size = (q.abs() @ k.abs().T) * abs(scale)
+    err = (d + 4) * 2.0 ** -24 * size + 4 * 2.0 ** -24 * abs(slope) * distance
+    if cap:
+        s = cap * torch.tanh(s / cap)
+        err = err.clamp(max=2 * cap) + 2.0 ** -19 * size.clamp(max=cap)
+    s = torch.where(allowed, s - slope * distance, -math.inf)
+    p = torch.softmax(s, dim=1)
+    dj = torch.expm1(2 * torch.where(allowed, err, 0.0).clamp(max=300))
+    dj = torch.where(p > 0, dj, 0.0)
+    o = p @ v
+    rel = (p * dj) @ v.abs() + (p * dj).sum(dim=1, keepdim=True) * (p @ v.abs())
+    tol = rel + (2.0 ** -20 + (R.HALF[dtype] if dtype == BF else 0.0) + 2 * (n + 16) * 2.0 ** -24) * (p @ v.abs())
+    return o, tol + R.HALF[dtype] * o.abs() + 2.0 ** -120
+
+
+def paged_fine(q, kp, vp, table, lens, hk, **sc):
+    B, h, d = q.shape
+    ref, tol = torch.zeros(B, h, d, dtype=torch.float64, device="cuda"), torch.zeros(B, h, d, dtype=torch.float64, device="cuda")
+    slopes, sc = sc.get("slopes"), dict(scale=sc.get("scale", d ** -0.5), cap=sc.get("cap", 0.0))
+    for b, n in enumerate(lens):
+        rows = table[b, : -(-n // kp.shape[1])].long()
+        ok, away = torch.ones(1, n, dtype=torch.bool, device="cuda"), (n - 1 - torch.arange(n, device="cuda"))[None].double()
+        for i in range(h):
+            k, v = (x[rows, :, i // (h // hk)].flatten(0, 1)[:n] for x in (kp, vp))
+            ref[b, i], tol[b, i] = (x[0] for x in attend_fine(q[b, i:i + 1], k, v, ok, away, slope=0.0 if slopes is None else
+                                                               slopes[i].item(), **sc))
+    return ref, tol
+
+
+def attention_fine(q, k, v, *, causal=False, q_offset=0, docs=None, slopes=None, **sc):
+    B, Lq, h, d = q.shape
+    Lk, hk = k.shape[1], k.shape[2]
+    ref, tol = torch.zeros(q.shape, dtype=torch.float64, device="cuda"), torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    sc = dict(scale=sc.get("scale", d ** -0.5), cap=sc.get("cap", 0.0))
+    i, j = torch.arange(Lq, device="cuda")[:, None] + q_offset, torch.arange(Lk, device="cuda")[None]
+    for b in range(B):
+        ok = j <= i if causal else torch.ones(Lq, Lk, dtype=torch.bool, device="cuda")
+        if docs is not None:
+            ok = ok & (docs[b][:, None] == docs[b][None])
+        for n in range(h):
+            ref[b, :, n], tol[b, :, n] = attend_fine(q[b, :, n], k[b, :, n // (h // hk)], v[b, :, n // (h // hk)], ok,
+                                                     (i - j).abs().double(), slope=0.0 if slopes is None else slopes[n].item(), **sc)
+    return ref, tol
+
+
+# ------------------------------------------------------------------------------------------ caps
+CAPS = [1e-3, 2.0, 70.0, 1e3, 1e4, 1e6, 1e30]
+
+
+def far_keys(q, k, every, score, scale):
+    """Every `every`-th key along -q of each head's first query, so that its score with that query is `score`."""
+    B, Lk, hk, d = k.shape
+    g = q.shape[2] // hk
+    for b in range(B):
+        for n in range(hk):
+            x = q[b, 0, n * g].double()
+            k[b, 3::every, n] = (x * (score / (scale * (x @ x)))).to(k.dtype)
+
+
+@pytest.mark.parametrize("dtype,h,hk,d", [(BF, 4, 2, 64), (BF, 12, 1, 128), (F32, 4, 1, 128)])
+@pytest.mark.parametrize("cap", CAPS)
+def test_paged_attention_caps_of_every_size(bnd, dtype, h, hk, d, cap):
+    """cap tanh(s / cap) keeps a score's own digits however large or small the cap is; far above the scores it changes
+    nothing."""
+    lens = [300, 17, 2500]
+    table, n_pages = S.table_of(1, 3, -(-2500 // 16))
+    kp, vp = S.pages_of(2, n_pages, 16, hk, d, dtype)
+    for gain in (2.0, 20.0):
+        q = randn(4, 3, h, d, dtype=dtype) * gain
+        got = S.run_paged(bnd, q, kp, vp, table, lens, hk, cap=cap)
+        ref, tol = paged_fine(q, kp, vp, table, lens, hk, cap=cap)
+        R.check(got, ref, tol, f"cap {cap}, scores up to about {4 * gain}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap", [1e3, 1e6])
+def test_paged_attention_far_scores_beside_near_ones(bnd, dtype, cap):
+    h, hk, d, n = 2, 2, 64, 700
+    table, n_pages = S.table_of(3, 1, -(-n // 32))
+    kp, vp = S.pages_of(4, n_pages, 32, hk, d, dtype)
+    q = randn(6, 1, h, d, dtype=dtype)
+    k = kp[table[0].long()].flatten(0, 1)[None].contiguous()
+    far_keys(q[:, None], k, 16, -0.9 * cap, d ** -0.5)
+    kp[table[0].long()] = k[0].view(-1, 32, hk, d)
+    got = S.run_paged(bnd, q, kp, vp, table, [n], hk, cap=cap)
+    ref, tol = paged_fine(q, kp, vp, table, [n], hk, cap=cap)
+    R.check(got, ref, tol, "near scores")

@@ -77,19 +77,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// cap log2(e) tanh(x): 1 - 2 / (1 + e^2x), good to 2^-22 of the cap
-__device__ __forceinline__ float cap_log2(float x, float top) {
-    return fmaf(-2.0f * top, rcp_approx(1.0f + ex2_approx(x * (2.0f * kLog2e))), top);
-}
-
-// A score in log2 units from q.k: capped, minus the distance bias. fp32 takes the library's tanh: 2^-22 of a cap of
-// 50 would be an error of 2 10^-5 in a weight, which bf16 weights hide and fp32 ones do not.
+// A score in log2 units from q.k: capped, minus the distance bias. fp32 takes the library's tanh: 2^-21 of a
+// score of 50 would be an error of 2 10^-5 in a weight, which bf16 values hide and fp32 ones do not.
 struct ScoreForm {
     float in, top;     // capped: s = top * tanh(dot * in), else dot * in
     bool capped;
     template <bool kExact>
     __device__ __forceinline__ float of(float dot, float slope, float away) const {
-        const float s = !capped ? dot * in : kExact ? top * tanhf(dot * in) : cap_log2(dot * in, top);
+        const float s = !capped ? dot * in : kExact ? top * tanhf(dot * in) : capped_score(dot * in, top);
         return fmaf(-slope, away, s);
     }
 };

@@ -37,6 +37,20 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return y;
 }
 
+// top * tanh(x), to about 2^-21 of itself for any x: up to |x| = 0.7 x P(x^2) with a minimax P of degree 4 (Remez
+// exchange on the relative error: 2^-21.6, coefficients below), beyond it top - 2 top / (1 + e^2x), off by 2^-22 of top.
+// The second form alone would be off by that much for small x too: with a cap far above the scores by more than a
+// score's own digits (a cap of 10^6: weights off by 15 %).
+constexpr float kTanh0 = 0.9999997019767761f, kTanh1 = -0.3333021402359009f, kTanh2 = 0.13281112909317017f,
+                kTanh3 = -0.0508362352848053f, kTanh4 = 0.01377371046692133f;
+constexpr float kTanhNear = 0.7f;
+__device__ __forceinline__ float capped_score(float x, float top) {
+    const float y = x * x;
+    const float p = fmaf(fmaf(fmaf(fmaf(kTanh4, y, kTanh3), y, kTanh2), y, kTanh1), y, kTanh0);
+    const float e = fmaf(-2.0f * top, rcp_approx(1.0f + ex2_approx(x * 2.8853900817779268f)), top);   // 2 log2(e)
+    return fabsf(x) <= kTanhNear ? top * (x * p) : e;
+}
+
 // 16 bytes to shared memory; not live: zeros, nothing is read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
