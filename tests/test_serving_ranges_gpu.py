@@ -109,3 +109,41 @@ def test_paged_attention_far_scores_beside_near_ones(bnd, dtype, cap):
     got = S.run_paged(bnd, q, kp, vp, table, [n], hk, cap=cap)
     ref, tol = paged_fine(q, kp, vp, table, [n], hk, cap=cap)
     R.check(got, ref, tol, "near scores")
+
+
+SPANS = [
+    # B, Lq, Lk, h, h_kv, d, options
+    (1, 130, 130, 2, 1, 128, dict(causal=True)),
+    (2, 300, 700, 4, 2, 64, dict(causal=True, q_offset=400)),
+    (1, 600, 600, 2, 2, 64, dict(docs=150)),
+    (1, 257, 513, 2, 1, 128, dict(slopes=True)),
+    (1, 3, 4096, 2, 1, 128, dict()),                              # several CTAs share a query tile
+    (2, 1600, 1600, 6, 6, 64, dict(causal=True, slopes=True)),    # two query tiles a unit
+]
+
+
+@pytest.mark.parametrize("B,Lq,Lk,h,hk,d,opt", SPANS)
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_caps_of_every_size(bnd, dtype, cap, B, Lq, Lk, h, hk, d, opt):
+    opt = dict(opt, cap=cap)
+    if opt.get("slopes"):
+        opt["slopes"] = S.slopes_of(h)
+    if opt.get("docs"):
+        opt["docs"] = S.docs_of(7, B, Lk, opt["docs"])
+    q, k, v = randn(8, B, Lq, h, d, dtype=dtype) * 4.0, randn(9, B, Lk, hk, d, dtype=dtype), randn(10, B, Lk, hk, d, dtype=dtype)
+    got = S.run_attention(bnd, q, k, v, **opt)
+    ref, tol = attention_fine(q, k, v, **opt)
+    R.check(got, ref, tol, f"cap {cap}")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Lq,Lk,h,d", [(1, 200, 2, 64), (1, 900, 2, 128), (2, 4096, 1, 64)])
+@pytest.mark.parametrize("cap", [1e3, 1e6])
+def test_attention_far_scores_beside_near_ones(bnd, dtype, Lq, Lk, h, d, cap):
+    q, k, v = randn(11, 1, Lq, h, d, dtype=dtype), randn(12, 1, Lk, h, d, dtype=dtype), randn(13, 1, Lk, h, d, dtype=dtype)
+    q[:, 1:] = q[:, :1]
+    far_keys(q, k, 16, -0.9 * cap, d ** -0.5)
+    got = S.run_attention(bnd, q, k, v, cap=cap)
+    ref, tol = attention_fine(q, k, v, cap=cap)
+    R.check(got, ref, tol, "near scores")

@@ -57,7 +57,7 @@ struct UnitInfo {
 // unit the order changes nothing (819 against 814 us), and the other modes keep the plain count, which costs less.
 template <int kMode>
 __device__ __forceinline__ int tile_of(const SpanAttnParams& p, int j, int n) {
-    if constexpr (kMode != kGeneral) return j;
+    if constexpr (kMode == kPlain || kMode == kCapped) return j;
     return p.slopes != nullptr && p.causal ? n - 1 - j : j;
 }
 
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         const uint32_t p_tmem = tmem + lane_off + kColP + h * (kKeys / 2);    // + 64 b
         const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;           // this part's output features
         const float scale_log2 = p.scale * kLog2e;
-        const TanhForm capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
+        const TanhForm<kMode == kSingle> capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
         uint32_t g = 0;   // score tiles consumed so far
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x81d);
         UnitInfo x = sm->unit[0];
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             if (!named_bar_and(1, kSoft, ok && x.n > 0)) break;
             const int n = x.n, q0 = x.q0, b = x.b, head = x.head;
             const int2 iv = interval_of(p, x.valid, x.seen, span, q0 + row);
-            const float slope = kMode == kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
+            const float slope = kMode >= kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
             float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to its parts
             float l = 0.0f;            // this part's share of the row sum
             for (int j = 0; j < n; ++j, ++g) {
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 } else if constexpr (kMode == kCapped) {
                     cap_scores(u, capped);
                 } else {
-                    if (p.cap > 0.0f) cap_scores(u, capped);
+                    if (kMode == kSingle || p.cap > 0.0f) cap_scores(u, capped);
                     const float by = p.cap > 0.0f ? 1.0f : scale_log2;
                     if (slope != 0.0f) bias_scores(u, by, static_cast<float>(q0 + row + p.q_offset - k0), slope);
                     else if (by != 1.0f) scale_scores(u, by);
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 for (int c = 0; c < kKeys / 2; ++c) {
                     float2 e2 = make_float2(__uint_as_float(u[2 * c]), __uint_as_float(u[2 * c + 1]));
                     if constexpr (kMode == kPlain) e2 = ffma2(e2, sc2, nm2);
-                    if constexpr (kMode == kGeneral) e2 = fadd2(e2, nm2);
+                    if constexpr (kMode >= kGeneral) e2 = fadd2(e2, nm2);
                     e2.x = ex2_approx(e2.x);
                     e2.y = ex2_approx(e2.y);
                     acc[c & 1] = fadd2(acc[c & 1], e2);
@@ -703,6 +703,7 @@ template <int kD>
 static cudaError_t launch_d(const SpanAttnParams& p, const SpanMaps& maps, int mode, cudaStream_t s) {
     return mode == kPlain    ? launch_mode<kD, kPlain>(p, maps, s)
            : mode == kCapped ? launch_mode<kD, kCapped>(p, maps, s)
+           : mode == kSingle ? launch_mode<kD, kSingle>(p, maps, s)
                              : launch_mode<kD, kGeneral>(p, maps, s);
 }
 
@@ -721,7 +722,8 @@ cudaError_t launch_span_attn(const SpanAttnParams& given, cudaStream_t s) {
     if (!map_strided(&maps.q, p.q, p.B, p.Lq, p.h, p.d) || !map_strided(&maps.k, p.k, p.B, p.Lk, p.h_kv, p.d) ||
         !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
         return cudaErrorInvalidValue;
-    const int mode = p.slopes == nullptr && p.spans == nullptr && p.cap > 0.0f && p.cap <= kFixedCap && p.Lk >= kFixedKeys ? kCapped
+    const int mode = p.cap > 0.0f && !tanh_folds(p.scale / p.cap) ? kSingle
+                     : p.slopes == nullptr && p.spans == nullptr && p.cap > 0.0f && p.cap <= kFixedCap && p.Lk >= kFixedKeys ? kCapped
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
     if (p.d == 128) return launch_d<128>(p, maps, mode, s);
@@ -729,7 +731,7 @@ cudaError_t launch_span_attn(const SpanAttnParams& given, cudaStream_t s) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    if (mode != kCapped && p.Lk >= kLongKeys && p.Lq > BM && units_of(p) > sms) return launch_span_attn_d64(p, maps, mode, s);
+    if (mode != kCapped && mode != kSingle && p.Lk >= kLongKeys && p.Lq > BM && units_of(p) > sms) return launch_span_attn_d64(p, maps, mode, s);
     return launch_d<64>(p, maps, mode, s);
 }
 

@@ -37,7 +37,9 @@ constexpr int kHeadGroup = 8;                // (batch, head) pairs whose units 
 //            of the output's norm, without it 2.3e-3; rounding the exact output alone 1.6e-3). Sums of n weighted values stay in fp32's range for |v| up to 2^40 / n at the
 //            largest cap (all scores at +cap), and from 2^-39 (all at -cap).
 //   kGeneral anything else: scores formed first, then as kPlain
-enum Mode { kPlain, kCapped, kGeneral };
+//   kSingle  as kGeneral, scale / cap outside the range of TanhForm: far scores one by one (an instance of its own: in the
+//            others the branch alone cost 2 to 10 %)
+enum Mode { kPlain, kCapped, kGeneral, kSingle };
 constexpr float kFixedCap = 60.0f;
 constexpr int kFixedKeys = 512;
 
@@ -104,22 +106,38 @@ __device__ __forceinline__ int2 span_of(const SpanAttnParams& p, int b, int i) {
     return reinterpret_cast<const int2*>(p.spans)[static_cast<int64_t>(b) * p.Lq + i];
 }
 
+template <int kKeys>
+__device__ __forceinline__ void scale_scores(uint32_t (&u)[kKeys], float scale) {
+#pragma unroll
+    for (int c = 0; c < kKeys; c += 2) {
+        const float2 r = fmul2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), make_float2(scale, scale));
+        u[c] = __float_as_uint(r.x);
+        u[c + 1] = __float_as_uint(r.y);
+    }
+}
+
 // u -> cap log2(e) tanh(u a), a = scale / cap. tanh(x) = x P(x^2) with minimax P (Remez exchange on the relative
-// error): degree 2 for |x| <= 0.3, degree 4 for |x| <= 0.7, both within 2^-21.4 of 1 in fp32 arithmetic; beyond, 1 -
-// 2 / (1 + e^2x), within 2^-22 of 1 anywhere. Powers of a are folded into the coefficients, so a score costs two and
-// a half instructions (packed) in the first range. Which range is decided for 16 scores of a warp at a time.
+// error): degree 2 for |x| <= 0.3, within 2^-19.7 of tanh, degree 4 for |x| <= 0.7, within 2^-21.2 in fp32 arithmetic; beyond,
+// 1 - 2 / (1 + e^2x), within 2^-22 of 1 anywhere. Powers of a are folded into the coefficients, so a score costs two and
+// a half instructions (packed) in the first range. Which range is decided for 16 scores of a warp at a time, so that near
+// scores beside far ones are off by 2^-22 of the cap: 3 10^-4 of a weight at a = 2^-13 (a cap of 724 or 1024), which bf16
+// weights hide. kSingle has the other caps, where that would be more than a score's own digits, or powers of a would leave
+// fp32's range: it multiplies by a first, and takes far scores one by one (4 x 8192 causal, 8 heads of 128, a cap of 10^4: 567
+// us, all scores one by one 866 us).
+template <bool kSingle_>
 struct TanhForm {
-    float a, top;
-    float near, mid;      // bounds of u^2; below 0 where powers of a would leave fp32's range
-    __device__ __forceinline__ TanhForm(float a_, float top_) : a(a_), top(top_) {
-        const bool safe = fabsf(a) >= 0x1p-13f && fabsf(a) <= 0x1p13f;
-        near = safe ? 0.09f / (a * a) : -1.0f;
-        mid = safe ? 0.49f / (a * a) : -1.0f;
+    float pre, a, top;    // x = (u pre) a, one of the two is 1
+    float near, mid;      // bounds of (u pre)^2
+    __device__ __forceinline__ TanhForm(float a_, float top_) : pre(kSingle_ ? a_ : 1.0f), a(kSingle_ ? 1.0f : a_), top(top_) {
+        near = 0.09f / (a * a);
+        mid = 0.49f / (a * a);
     }
 };
+inline bool tanh_folds(float a) { return fabsf(a) >= 0x1p-13f && fabsf(a) <= 0x1p13f; }
 
-template <int kKeys>
-__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm& f) {
+template <bool kSingle_, int kKeys>
+__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm<kSingle_>& f) {
+    if constexpr (kSingle_) scale_scores(u, f.pre);
     const float t1 = f.a * f.top, a2 = f.a * f.a;
     const float n0 = 0.9999988675117493f * t1, n1 = -0.33310022950172424f * a2 * t1, n2 = 0.12633946537971497f * a2 * a2 * t1;
     const float2 d0 = make_float2(n0, n0), d1 = make_float2(n1, n1), d2 = make_float2(n2, n2);
@@ -142,8 +160,8 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm&
                 u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
             }
         } else if (!__any_sync(0xffffffffu, far > f.mid)) {
-            const float m0 = 0.9999997019767761f * t1, m1 = -0.3333021402359009f * a2 * t1, m2 = 0.13281112909317017f * a2 * a2 * t1,
-                        m3 = -0.0508362352848053f * a2 * a2 * (a2 * t1), m4 = 0.01377371046692133f * a2 * a2 * (a2 * a2 * t1);
+            const float m0 = kTanh0 * t1, m1 = kTanh1 * a2 * t1, m2 = kTanh2 * a2 * a2 * t1, m3 = kTanh3 * a2 * a2 * (a2 * t1),
+                        m4 = kTanh4 * a2 * a2 * (a2 * a2 * t1);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float2 x = make_float2(__uint_as_float(u[16 * q + 2 * e]), __uint_as_float(u[16 * q + 2 * e + 1]));
@@ -157,20 +175,14 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm&
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
+                if constexpr (kSingle_) {
+                    u[16 * q + e] = __float_as_uint(capped_score(__uint_as_float(u[16 * q + e]), f.top));
+                    continue;
+                }
                 const float r = rcp_approx(1.0f + ex2_approx(__uint_as_float(u[16 * q + e]) * (f.a * 2.0f * kLog2e)));
                 u[16 * q + e] = __float_as_uint(fmaf(-2.0f * f.top, r, f.top));
             }
         }
-    }
-}
-
-template <int kKeys>
-__device__ __forceinline__ void scale_scores(uint32_t (&u)[kKeys], float scale) {
-#pragma unroll
-    for (int c = 0; c < kKeys; c += 2) {
-        const float2 r = fmul2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), make_float2(scale, scale));
-        u[c] = __float_as_uint(r.x);
-        u[c + 1] = __float_as_uint(r.y);
     }
 }
 

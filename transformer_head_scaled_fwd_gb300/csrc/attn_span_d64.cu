@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
         const int pair = 4 + t * 4 + q;                                          // barrier of the warps that share rows
         const bool first = warp % (kSoftWarps / 2) == 0 && lane == 0;            // one thread of the group
         const float scale_log2 = p.scale * kLog2e;
-        const TanhForm capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
+        const TanhForm<false> capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
         uint32_t g = 0;   // score tiles of this query tile consumed so far
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x83d);
         UnitInfo x = sm->unit[0];
