@@ -418,7 +418,7 @@ mha_status_t mha_paged_append(mha_dtype_t dt, const void* q, const mha_strides_t
  */
 typedef struct {
     float scale;             /* 0: 1 / sqrt(d_k) */
-    float cap;               /* 0: no cap */
+    float cap;               /* 0: no cap; scale / cap finite. Taken as 2^-100 or 2^100 beyond them */
     const float* slopes;     /* device fp32 [h] or NULL */
 } mha_scores_t;
 

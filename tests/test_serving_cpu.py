@@ -114,6 +114,14 @@ def test_attention_refusals(lib):
     assert lib.mha_document_spans(P, 70000, 1, P, None) == UNS
 
 
+def test_scale_over_cap_must_be_finite(lib):
+    sc = scores_t(scale=1e30, cap=1e-30)
+    assert lib.mha_attention(1, P, st(), P, st(), P, st(), P, st(), 2, 8, 8, 8, 4, 64, sc, None, None) == INV
+    assert b"scale / cap" in lib.mha_last_error()
+    assert lib.mha_paged_attention(1, P, st(), P, st(), 2, 8, 4, 64, P, sc, cache_t(), P, 1 << 30, None) == INV
+    assert b"scale / cap" in lib.mha_last_error()
+
+
 def test_rmsnorm_refusals(lib):
     def call(dt=1, x=P, r=P, s=P, y=P, rows=4, d=256, eps=1e-6, scales=None, group=0, ys=256, ss=256, xs=256):
         return lib.mha_rmsnorm(dt, x, xs, r, 256, s, ss, None, eps, rows, d, y, ys, scales, group, None)

@@ -147,3 +147,23 @@ def test_attention_far_scores_beside_near_ones(bnd, dtype, Lq, Lk, h, d, cap):
     got = S.run_attention(bnd, q, k, v, cap=cap)
     ref, tol = attention_fine(q, k, v, cap=cap)
     R.check(got, ref, tol, "near scores")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap,scale", [(3.4e38, None), (1e35, 1e-10), (1e-44, None), (1e-30, 1e3)])
+def test_caps_at_the_ends_of_fp32(bnd, dtype, cap, scale):
+    """Caps whose product with log2 e, or whose quotient with the scale, leaves fp32's range: no cap, or no score at all."""
+    h, hk, d, n = 4, 2, 64, 200
+    sc = dict(cap=cap) if scale is None else dict(cap=cap, scale=scale)
+    table, n_pages = S.table_of(50, 1, -(-n // 16))
+    kp, vp = S.pages_of(51, n_pages, 16, hk, d, dtype)
+    q = randn(53, 1, h, d, dtype=dtype)
+    q[0, 0] = 0.0
+    got = S.run_paged(bnd, q, kp, vp, table, [n], hk, **sc)
+    ref, tol = paged_fine(q, kp, vp, table, [n], hk, **sc)
+    R.check(got, ref, tol, "paged")
+    rows = table[0].long()
+    k, v = (x[rows].flatten(0, 1)[None, :n].contiguous() for x in (kp, vp))
+    got = S.run_attention(bnd, q[:, None].contiguous(), k, v, **sc)
+    ref, tol = attention_fine(q[:, None], k, v, **sc)
+    R.check(got, ref, tol, "attention")

@@ -102,7 +102,15 @@ mha_status_t check_scores(const mha_scores_t* s, int d_k, float* scale, float* c
     if (!std::isfinite(s->scale) || !std::isfinite(s->cap) || s->cap < 0.0f)
         return fail(MHA_ERR_INVALID_ARG, "scale must be finite and cap finite and >= 0 (got %g, %g)", s->scale, s->cap);
     if (s->scale != 0.0f) *scale = s->scale;
-    *cap = s->cap;
+    if (s->cap > 0.0f) {
+        // The kernels form scale / cap and cap log2(e), so the cap is kept where both are normal numbers. Under a smaller one
+        // scores are within 2^-100 of 0; a larger one changes scores below 2^85 (products below 2^95) by less than 2^-30 of
+        // themselves.
+        const float most = std::fmin(0x1p100f, std::fabs(*scale) < 0x1p-10f ? std::fabs(*scale) * 0x1p110f : 0x1p100f);
+        *cap = std::fmax(std::fmin(s->cap, most), 0x1p-100f);
+        if (!std::isfinite(*scale / *cap))
+            return fail(MHA_ERR_INVALID_ARG, "scale / cap must be finite (got %g / %g)", *scale, s->cap);
+    }
     *slopes = s->slopes;
     return MHA_OK;
 }
