@@ -469,8 +469,7 @@ mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* s
  * h a multiple of h_kv (head n reads key head n / (h / h_kv)); scores, mask NULL: plain, all keys.
  * MHA_BF16 or MHA_F32 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
  * behind key_valid_lens[b] are not used, whatever they hold; elsewhere a masked value that is not
- * finite may reach rows that do not attend to it (0 * NaN). With a cap, values are expected in 2^-39 .. 2^40 /
- * L_k (their weights are not taken relative to the row's largest score). No workspace.
+ * finite may reach rows that do not attend to it (0 * NaN). No workspace.
  */
 mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
                            const void* k, const mha_strides_t* k_strides,

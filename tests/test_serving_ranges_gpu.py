@@ -167,3 +167,36 @@ def test_caps_at_the_ends_of_fp32(bnd, dtype, cap, scale):
     got = S.run_attention(bnd, q[:, None].contiguous(), k, v, **sc)
     ref, tol = attention_fine(q[:, None], k, v, **sc)
     R.check(got, ref, tol, "attention")
+
+
+# ------------------------------------------------------------------------------------------ values
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,Lq,Lk,h,d,opt", [(1, 200, 600, 2, 128, {}), (1, 600, 600, 2, 64, dict(causal=True)),
+                                             (1, 2, 4096, 2, 128, {}), (1, 512, 512, 1, 128, dict(valid=[300]))])
+@pytest.mark.parametrize("cap,sign", [(59.0, 1), (59.0, -1), (30.0, -1)])
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -100])
+def test_capped_attention_of_large_and_tiny_values(bnd, dtype, B, Lq, Lk, h, d, opt, cap, sign, size):
+    """All scores at one end of the cap: weights are equal whatever the values' size is. The fp32 sum of 4096 weighted values
+    of 2^100 stays below 2^127, and a product of 2^-100 with a weight of 1 above fp32's smallest normal number."""
+    q = torch.ones(B, Lq, h, d, device="cuda", dtype=dtype) * 40.0
+    k = torch.ones(B, Lk, h, d, device="cuda", dtype=dtype) * sign * 40.0
+    v = (randn(14, B, Lk, h, d).abs() + 0.5).to(dtype)
+    got = S.run_attention(bnd, q, k, v * size, cap=cap, **opt)
+    # equal scores, in fp32 too: the reference of scores of 0, and only the values' part of its bound
+    ref, tol = S.attention_ref(torch.zeros_like(q), k, v, **opt)
+    R.check(got.double() / size, ref, tol, "values")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [40, 4000])
+@pytest.mark.parametrize("size", [2.0 ** 100, 2.0 ** -100])
+def test_capped_paged_attention_of_large_and_tiny_values(bnd, dtype, n, size):
+    h, hk, d = 4, 2, 64
+    table, n_pages = S.table_of(15, 1, -(-n // 16))
+    kp, vp = S.pages_of(16, n_pages, 16, hk, d, dtype)
+    kp.fill_(-40.0)
+    vp = (vp.float().abs() + 0.5).to(dtype)
+    q = torch.ones(1, h, d, device="cuda", dtype=dtype) * 40.0
+    got = S.run_paged(bnd, q, kp, vp * size, table, [n], hk, cap=59.0)
+    ref, tol = S.paged_ref(torch.zeros_like(q), kp, vp, table, [n], hk)
+    R.check(got.double() / size, ref, tol, "values")

@@ -16,9 +16,10 @@
 // first scores run during this unit's last tiles and output. Registers: 96 a thread at launch; the last warpgroup drops to 56 and the
 // softmax warps rise to 104 (128 * 56 + 512 * 104 = 60416 <= 640 * 96).
 // Few units (few queries over long keys): the CTAs of a cluster share one, see pieces_of.
-// Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 408-418 us, with a
+// Measured, 4 x 8192 causal, 8 heads: 361 us, 1522 TFLOP/s (0.79 of measured bf16 peak; all keys 0.84), capped 476 us, with a
 // distance bias 471 us.
 #include <algorithm>
+#include <cfloat>
 
 #include "attn_span.cuh"
 
@@ -393,6 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
         const uint32_t p_tmem = tmem + lane_off + kColP + h * (kKeys / 2);    // + 64 b
         const uint32_t o_tmem = tmem + lane_off + kColO + h * kOut;           // this part's output features
         const float scale_log2 = p.scale * kLog2e;
+        const float inv_scale = 1.0f / fabsf(scale_log2);
         const TanhForm<kMode == kSingle> capped(p.cap > 0.0f ? p.scale / p.cap : 1.0f, p.cap * kLog2e);
         uint32_t g = 0;   // score tiles consumed so far
         bool ok = mbar_wait(&sm->unit_full[0], 0, abort_flag, p.status, 0x81d);
@@ -414,6 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             const int2 iv = interval_of(p, x.valid, x.seen, span, q0 + row);
             const float slope = kMode >= kGeneral && p.slopes != nullptr ? p.slopes[head] * kLog2e : 0.0f;
             float m = -CUDART_INF_F;   // the row's reference max (log2 units), common to its parts
+            float mref = 0.0f;         // m, or 0 while it is -inf
+            float far = -1.0f;         // kCapped: (u before the cap)^2 up to which no score passes the reference by 2^8
             float l = 0.0f;            // this part's share of the row sum
             for (int j = 0; j < n; ++j, ++g) {
                 const uint32_t sb = g & 1;
@@ -428,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 const int k0 = (x.j0 + tile_of<kMode>(p, j, n)) * BN + h * kKeys;   // first key of this part
                 const bool edge = k0 < x.lo_max || k0 + kKeys > x.hi_min;
                 float sc = 1.0f;
+                float farthest = 0.0f;
                 if constexpr (kMode == kPlain) {
                     if (edge) {
                         scale_scores(u, scale_log2);
@@ -435,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                         sc = scale_log2;
                     }
                 } else if constexpr (kMode == kCapped) {
-                    cap_scores(u, capped);
+                    farthest = cap_scores(u, capped, mref);
                 } else {
-                    if (kMode == kSingle || p.cap > 0.0f) cap_scores(u, capped);
+                    if (kMode == kSingle || p.cap > 0.0f) cap_scores(u, capped, 0.0f);
                     const float by = p.cap > 0.0f ? 1.0f : scale_log2;
                     if (slope != 0.0f) bias_scores(u, by, static_cast<float>(q0 + row + p.q_offset - k0), slope);
                     else if (by != 1.0f) scale_scores(u, by);
@@ -450,8 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 }
                 float alpha = 1.0f;
                 bool grow = false;
-                float mref = 0.0f;
-                if constexpr (kMode != kCapped) {
+                auto tile_max = [&] {
                     float a2[2];
 #pragma unroll
                     for (int c2 = 0; c2 < 2; ++c2) {
@@ -462,16 +466,40 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                             a = fmax3(a, __uint_as_float(u[16 * c2 + e]), __uint_as_float(u[16 * c2 + e + 1]));
                         a2[c2] = fmaxf(a, __uint_as_float(u[16 * c2 + 15]));
                     }
-                    // The reference moves only when the tile passes it by 2^8 (or holds the row's first keys); whether any
-                    // row of these 32 does is agreed by a barrier of the four warps, and only then are the parts'
-                    // maxima exchanged.
-                    const float mth = fmaxf(a2[0], a2[1]) * sc;   // this part's tile max (log2 units)
-                    if (named_bar_or(4 + q, 32 * kParts, mth > m + kRescaleThreshold)) {
-                        sm->mx[h][row] = mth;
-                        named_bar_sync(4 + q, 32 * kParts);
-                        float top = mth;
+                    return fmaxf(a2[0], a2[1]) * sc;   // log2 units
+                };
+                // The largest of the parts' values
+                auto exchange = [&](float mine) {
+                    sm->mx[h][row] = mine;
+                    named_bar_sync(4 + q, 32 * kParts);
 #pragma unroll
-                        for (int o = 1; o < kParts; ++o) top = fmaxf(top, sm->mx[(h + o) % kParts][row]);
+                    for (int o = 1; o < kParts; ++o) mine = fmaxf(mine, sm->mx[(h + o) % kParts][row]);
+                    return mine;
+                };
+                // The reference moves only when the tile passes it by 2^8 (or holds the row's first keys); whether any
+                // row of these 32 does is agreed by a barrier of the four warps, and only then are the parts'
+                // maxima exchanged.
+                if constexpr (kMode == kCapped) {
+                    // u is relative to the reference. No score passes it by 2^8 where all |u| before the cap are below
+                    // `far`, so only otherwise is the maximum itself formed.
+                    if (named_bar_or(4 + q, 32 * kParts, farthest > far)) {
+                        const float top = exchange(tile_max());
+                        if (top > (m == -CUDART_INF_F ? -CUDART_INF_F : kRescaleThreshold)) {
+                            grow = m != -CUDART_INF_F;
+                            alpha = grow ? ex2_approx(-top) : 0.0f;
+                            l *= alpha;
+                            mref += top;
+                            m = mref;
+                            const float reach = fmaxf(m + kRescaleThreshold, 0.0f) * inv_scale;
+                            far = m + kRescaleThreshold < 0.0f ? -1.0f : m + kRescaleThreshold > capped.top ? CUDART_INF_F : fminf(reach * reach, FLT_MAX);
+#pragma unroll
+                            for (int c = 0; c < kKeys; ++c) u[c] = __float_as_uint(__uint_as_float(u[c]) - top);
+                        }
+                    }
+                } else {
+                    const float mth = tile_max();   // of this part
+                    if (named_bar_or(4 + q, 32 * kParts, mth > m + kRescaleThreshold)) {
+                        const float top = exchange(mth);
                         if (top > m + kRescaleThreshold) {
                             grow = m != -CUDART_INF_F;
                             alpha = ex2_approx(m - top);   // 0 for the first keys
@@ -498,14 +526,14 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                     pk[c] = pack_bf16x2(e2.x, e2.y);
                 }
                 const float2 s2 = fadd2(acc[0], acc[1]);
-                if (kMode != kCapped) l += s2.x + s2.y;
+                l += s2.x + s2.y;
                 // weight buffer sb is free once P.V(g - 2) has read it
                 if (g >= 2) {
                     mbar_wait(&sm->p_free[sb], ((g >> 1) - 1) & 1, abort_flag, p.status, 0x81f);
                     __syncwarp();
                     tc_fence_after();
                 }
-                if (kMode != kCapped && j > 0 && __any_sync(0xffffffffu, grow)) {
+                if (j > 0 && __any_sync(0xffffffffu, grow)) {
                     // O is rescaled (this part's features) once P.V(g - 1) has completed; at j = 0 the first
                     // P.V overwrites O, after the previous unit's output has been read
                     mbar_wait(&sm->p_free[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag, p.status, 0x820);
@@ -525,13 +553,6 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->p_full[sb]);
-                if constexpr (kMode == kCapped) {
-                    // No weight is exactly 1 here. Where a row may have few keys the sum takes the rounded weights, so
-                    // that their errors divide out (a single key: its value, exactly). Done this late it costs nothing
-                    // (418 us; before the weights are stored 430 us).
-                    const float2 w2 = edge ? sum_bf16(pk) : s2;
-                    l += w2.x + w2.y;
-                }
             }
             // The next unit's slot and spans are read now: their latency passes behind the output.
             const int next = k + 1;
@@ -561,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 for (int c = 0; c < kOut; c += 4)
                     *reinterpret_cast<uint4*>(part + row * kPitch + h * kOut + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                 if (h == 0) {
-                    sm->mx[0][row] = kMode == kCapped ? 0.0f : m;
+                    sm->mx[0][row] = m;
                     sm->mx[1][row] = L;
                 }
                 continue;
@@ -723,7 +744,7 @@ cudaError_t launch_span_attn(const SpanAttnParams& given, cudaStream_t s) {
         !map_strided(&maps.v, p.v, p.B, p.Lk, p.h_kv, p.d) || !map_strided(&maps.out, p.out, p.B, p.Lq, p.h, p.d))
         return cudaErrorInvalidValue;
     const int mode = p.cap > 0.0f && !tanh_folds(p.scale / p.cap) ? kSingle
-                     : p.slopes == nullptr && p.spans == nullptr && p.cap > 0.0f && p.cap <= kFixedCap && p.Lk >= kFixedKeys ? kCapped
+                     : p.slopes == nullptr && p.cap > 0.0f ? kCapped
                      : p.slopes == nullptr && p.cap == 0.0f && p.scale > 0.0f ? kPlain
                                                                              : kGeneral;
     if (p.d == 128) return launch_d<128>(p, maps, mode, s);

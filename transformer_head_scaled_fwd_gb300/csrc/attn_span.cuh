@@ -28,20 +28,15 @@ constexpr int kHeadGroup = 8;                // (batch, head) pairs whose units 
 
 // How scores become weights:
 //   kPlain   scale > 0, no cap, no bias: running maximum of the raw scores, one multiply-add each
-//   kCapped  a cap of at most kFixedCap, no bias, long rows: every score lies in [-cap, cap], so the weights are
-//            exp(s) with no maximum at all (2^+-87 at most, far inside fp32 and bf16): no maximum,
-//            no rescaling, no exchange between the threads of a row (4 x 8192, 8 heads of 128: 408 us, kGeneral
-//            524 us). The largest weight is then rounded to bf16 like any other, while under a running maximum it is
-//            exactly 1: rows of a few keys would be off by 1.8e-3 where kGeneral is off by 1.3e-3. So short key ranges
-//            and document spans go there, and the first rows under a causal mask sum rounded weights (4 x 8192: 2.2e-3
-//            of the output's norm, without it 2.3e-3; rounding the exact output alone 1.6e-3). Sums of n weighted values stay in fp32's range for |v| up to 2^40 / n at the
-//            largest cap (all scores at +cap), and from 2^-39 (all at -cap).
+//   kCapped  a cap, no bias: scores formed first, relative to the running maximum already. Most tiles cannot raise it, which
+//            their largest |q.k| tells, and then their own maximum is not formed (4 x 8192 causal, 8 heads of 128, a cap
+//            of 50: 476 us, with the maximum of every tile 501 us). A reference of 0 for all rows, which a small cap allows,
+//            would save the agreement too (414 us), but under it a row's weights lie anywhere in e^+-cap, and large or tiny values
+//            leave fp32's range in the sums
 //   kGeneral anything else: scores formed first, then as kPlain
 //   kSingle  as kGeneral, scale / cap outside the range of TanhForm: far scores one by one (an instance of its own: in the
 //            others the branch alone cost 2 to 10 %)
 enum Mode { kPlain, kCapped, kGeneral, kSingle };
-constexpr float kFixedCap = 60.0f;
-constexpr int kFixedKeys = 512;
 
 // Coordinates of a (head, sequence) in a map: a broadcast dimension (stride 0) has one entry there.
 __device__ __forceinline__ int at_h(const Strided& t, int head) { return t.h != 0 ? head : 0; }
@@ -124,23 +119,26 @@ __device__ __forceinline__ void scale_scores(uint32_t (&u)[kKeys], float scale) 
 // weights hide. kSingle has the other caps, where that would be more than a score's own digits, or powers of a would leave
 // fp32's range: it multiplies by a first, and takes far scores one by one (4 x 8192 causal, 8 heads of 128, a cap of 10^4: 567
 // us, all scores one by one 866 us).
-template <bool kSingle_>
+template <bool kAlone>
 struct TanhForm {
     float pre, a, top;    // x = (u pre) a, one of the two is 1
     float near, mid;      // bounds of (u pre)^2
-    __device__ __forceinline__ TanhForm(float a_, float top_) : pre(kSingle_ ? a_ : 1.0f), a(kSingle_ ? 1.0f : a_), top(top_) {
+    __device__ __forceinline__ TanhForm(float a_, float top_) : pre(kAlone ? a_ : 1.0f), a(kAlone ? 1.0f : a_), top(top_) {
         near = 0.09f / (a * a);
         mid = 0.49f / (a * a);
     }
 };
 inline bool tanh_folds(float a) { return fabsf(a) >= 0x1p-13f && fabsf(a) <= 0x1p13f; }
 
-template <bool kSingle_, int kKeys>
-__device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm<kSingle_>& f) {
-    if constexpr (kSingle_) scale_scores(u, f.pre);
+// u becomes the score minus ref; the result is the largest (u pre)^2.
+template <bool kAlone, int kKeys>
+__device__ __forceinline__ float cap_scores(uint32_t (&u)[kKeys], const TanhForm<kAlone>& f, float ref) {
+    if constexpr (kAlone) scale_scores(u, f.pre);
     const float t1 = f.a * f.top, a2 = f.a * f.a;
     const float n0 = 0.9999988675117493f * t1, n1 = -0.33310022950172424f * a2 * t1, n2 = 0.12633946537971497f * a2 * a2 * t1;
-    const float2 d0 = make_float2(n0, n0), d1 = make_float2(n1, n1), d2 = make_float2(n2, n2);
+    const float2 d0 = make_float2(n0, n0), d1 = make_float2(n1, n1), d2 = make_float2(n2, n2), by = make_float2(-ref, -ref);
+    const float end = f.top - ref;
+    float farthest = 0.0f;
 #pragma unroll
     for (int q = 0; q < kKeys / 16; ++q) {
         float2 y[8];
@@ -151,11 +149,12 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm<
             y[e] = fmul2(x, x);
             far = fmax3(far, y[e].x, y[e].y);
         }
+        farthest = fmaxf(farthest, far);
         if (!__any_sync(0xffffffffu, far > f.near)) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float2 x = make_float2(__uint_as_float(u[16 * q + 2 * e]), __uint_as_float(u[16 * q + 2 * e + 1]));
-                const float2 r = fmul2(ffma2(ffma2(d2, y[e], d1), y[e], d0), x);
+                const float2 r = ffma2(ffma2(ffma2(d2, y[e], d1), y[e], d0), x, by);
                 u[16 * q + 2 * e] = __float_as_uint(r.x);
                 u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
             }
@@ -168,32 +167,23 @@ __device__ __forceinline__ void cap_scores(uint32_t (&u)[kKeys], const TanhForm<
                 float2 r = ffma2(make_float2(m4, m4), y[e], make_float2(m3, m3));
                 r = ffma2(r, y[e], make_float2(m2, m2));
                 r = ffma2(r, y[e], make_float2(m1, m1));
-                r = fmul2(ffma2(r, y[e], make_float2(m0, m0)), x);
+                r = ffma2(ffma2(r, y[e], make_float2(m0, m0)), x, by);
                 u[16 * q + 2 * e] = __float_as_uint(r.x);
                 u[16 * q + 2 * e + 1] = __float_as_uint(r.y);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                if constexpr (kSingle_) {
-                    u[16 * q + e] = __float_as_uint(capped_score(__uint_as_float(u[16 * q + e]), f.top));
+                if constexpr (kAlone) {
+                    u[16 * q + e] = __float_as_uint(capped_score(__uint_as_float(u[16 * q + e]), f.top) - ref);
                     continue;
                 }
                 const float r = rcp_approx(1.0f + ex2_approx(__uint_as_float(u[16 * q + e]) * (f.a * 2.0f * kLog2e)));
-                u[16 * q + e] = __float_as_uint(fmaf(-2.0f * f.top, r, f.top));
+                u[16 * q + e] = __float_as_uint(fmaf(-2.0f * f.top, r, end));
             }
         }
     }
-}
-
-// Sum of pairs of bf16, low and high halves apart.
-template <int kN>
-__device__ __forceinline__ float2 sum_bf16(const uint32_t (&pk)[kN]) {
-    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-    for (int c = 0; c < kN; ++c)
-        s[c & 1] = fadd2(s[c & 1], make_float2(__uint_as_float(pk[c] << 16), __uint_as_float(pk[c] & 0xffff0000u)));
-    return fadd2(s[0], s[1]);
+    return farthest;
 }
 
 // u * scale - slope |i - j|: away = i - (first key of u), scale and slope in log2 units.

@@ -11,8 +11,9 @@
 //
 // Measured, 4 x 8192 causal, 16 heads: 541 us, 1017 TFLOP/s (0.53 of measured bf16 peak; all keys 1072); the kernel of
 // one query tile 660 us; two query tiles with one thread a row (eight softmax warps) 581 us, all keys 987 against 1026
-// us. With a distance bias 814 us (in the other layout 896). Capped scores without a
-// maximum gain nothing from it (795 against 721 us) and stay with the other kernel.
+// us. With a distance bias 814 us (in the other layout 896). Capped scores
+// without a bias stay with the other kernel (documents of 1024 190 us there, 207 us with an instance here; 4 x 8192 causal 916
+// and 870 us).
 //
 // Tensor memory (512 columns): S_0 S_1 (fp32, 128 each), P_0 P_1 (bf16, 64 each), O_0 O_1 (fp32, 64 each).
 // Shared memory: two Q buffers of two tiles, K and V rings of four tiles, the two output tiles on their way out. Warps:
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                         sc = scale_log2;
                     }
                 } else {
-                    if (p.cap > 0.0f) cap_scores(u, capped);
+                    if (p.cap > 0.0f) cap_scores(u, capped, 0.0f);
                     const float by = p.cap > 0.0f ? 1.0f : scale_log2;
                     if (slope != 0.0f) bias_scores(u, by, static_cast<float>(q0 + row + p.q_offset - k0), slope);
                     else if (by != 1.0f) scale_scores(u, by);
