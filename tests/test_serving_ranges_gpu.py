@@ -200,3 +200,33 @@ def test_capped_paged_attention_of_large_and_tiny_values(bnd, dtype, n, size):
     got = S.run_paged(bnd, q, kp, vp * size, table, [n], hk, cap=59.0)
     ref, tol = S.paged_ref(torch.zeros_like(q), kp, vp, table, [n], hk)
     R.check(got.double() / size, ref, tol, "values")
+
+
+# ------------------------------------------------------------------------------------------ rows without a key, NaN rows
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sc", [{}, dict(cap=30.0), dict(slopes=True)])
+@pytest.mark.parametrize("B,L,h,d", [(2, 200, 2, 64), (2, 200, 2, 128), (1, 700, 1, 128), (3, 1700, 6, 64)])
+def test_rows_without_a_key_are_zeros_whatever_the_values(bnd, dtype, bad, sc, B, L, h, d):
+    """Padding in front of the documents, between and behind them, with values that are not finite: its own rows are zeros."""
+    sc = dict(sc, slopes=S.slopes_of(h)) if sc.get("slopes") else sc
+    ids = torch.arange(L, device="cuda").div(90, rounding_mode="floor").int().expand(B, L).clone()
+    ids[:, :70], ids[:, 100:103], ids[:, L - 5:] = -1, -1, -1
+    pad = ids < 0
+    q, k, v = (randn(17 + i, B, L, h, d, dtype=dtype) for i in range(3))
+    v[pad] = bad
+    got = S.run_attention(bnd, q, k, v, docs=ids, **sc)
+    assert torch.equal(got[pad], torch.zeros_like(got[pad]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sc", [{}, dict(cap=30.0), dict(slopes=True)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_shared_units_rows_without_a_key(bnd, dtype, sc, d):
+    B, Lq, Lk, h = 1, 4, 4096, 2
+    sc = dict(sc, slopes=S.slopes_of(h)) if sc.get("slopes") else sc
+    q, k, v = randn(20, B, Lq, h, d, dtype=dtype), randn(21, B, Lk, h, d, dtype=dtype), randn(22, B, Lk, h, d, dtype=dtype)
+    v[:, ::97] = float("nan")
+    spans = ints([[[0, 0], [0, Lk], [500, 500], [3000, 2000]]])
+    got = S.run_attention(bnd, q, k, v, spans=spans, **sc)
+    assert torch.equal(got[:, [0, 2, 3]], torch.zeros_like(got[:, [0, 2, 3]]))

@@ -568,7 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
             lsum[h * BM + row] = l;
             named_bar_sync(4 + q, 32 * kParts);   // the four warps of these rows
             const float L = (lsum[row] + lsum[BM + row]) + (lsum[2 * BM + row] + lsum[3 * BM + row]);
-            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
+            const bool none = L == 0.0f;              // no key: a row of zeros, O may hold 0 * NaN from the tile's other rows' keys
+            const float inv = L > 0.0f ? 1.0f / L : L;   // NaN stays
             const uint32_t gl = g - 1;   // the unit's last tile: its P.V completes O
             mbar_wait(&sm->p_free[gl & 1], (gl >> 1) & 1, abort_flag, p.status, 0x822);
             __syncwarp();
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_kernel(const __grid_con
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
+                    w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
                 st_shared_v4(smem_u32(obuf + (col / 64) * kHalf) + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4), w[0],
                              w[1], w[2], w[3]);
             }

@@ -491,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
             lsum[h * BM + row] = l;
             named_bar_sync(pair, 32 * kParts);
             const float L = lsum[row] + lsum[BM + row];
-            const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
+            const bool none = L == 0.0f;              // no key: a row of zeros, O may hold 0 * NaN from the tile's other rows' keys
+            const float inv = L > 0.0f ? 1.0f / L : L;   // NaN stays
             uint32_t o[kOut];
             if (to > from) {
                 mbar_wait(&sm->p_free[t], (g - 1) & 1, abort_flag, p.status, 0x842);   // the last P.V completes O
@@ -508,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) span_attn_d64_kernel(const __grid
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
+                    w[e] = none ? 0u : pack_bf16x2(__uint_as_float(o[ch * 8 + 2 * e]) * inv, __uint_as_float(o[ch * 8 + 2 * e + 1]) * inv);
                 st_shared_v4(smem_u32(obuf) + row * 128 + (((h * (kOut / 8) + ch) ^ (row & 7)) << 4), w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_smem();

@@ -255,12 +255,14 @@ __global__ void __launch_bounds__(kThreads, Geo<kD>::kCtas) span_attn_f32_kernel
     for (int i = 0; i < kRows; ++i) {
         const int row = q0 + rg * kRows + i;
         const float L = l[i];
-        const float inv = L > 0.0f ? 1.0f / L : (L == 0.0f ? 0.0f : L);   // no key: a row of zeros; NaN stays
+        const bool none = L == 0.0f;              // no key: a row of zeros, o may hold 0 * NaN from the tile's other rows' keys
+        const float inv = L > 0.0f ? 1.0f / L : L;   // NaN stays
         if (row >= p.Lq) continue;
 #pragma unroll
         for (int e = 0; e < kV4; ++e)
             *reinterpret_cast<float4*>(out + row * p.out.l + e * 64 + kg * 4) =
-                make_float4(o[i][e].x * inv, o[i][e].y * inv, o[i][e].z * inv, o[i][e].w * inv);
+                none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                     : make_float4(o[i][e].x * inv, o[i][e].y * inv, o[i][e].z * inv, o[i][e].w * inv);
     }
 }
 
