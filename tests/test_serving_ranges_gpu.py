@@ -230,3 +230,30 @@ def test_shared_units_rows_without_a_key(bnd, dtype, sc, d):
     spans = ints([[[0, 0], [0, Lk], [500, 500], [3000, 2000]]])
     got = S.run_attention(bnd, q, k, v, spans=spans, **sc)
     assert torch.equal(got[:, [0, 2, 3]], torch.zeros_like(got[:, [0, 2, 3]]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sc", [{}, dict(cap=30.0), dict(slopes=True)])
+@pytest.mark.parametrize("Lq,Lk,h,d", [(4, 100, 2, 64), (4, 4096, 2, 64), (4, 4096, 2, 128), (130, 2048, 2, 128)])
+def test_nan_queries_give_nan_rows(bnd, dtype, sc, Lq, Lk, h, d):
+    """A query that is NaN has NaN scores with all keys: so is its row, alone, however many CTAs share its keys."""
+    sc = dict(sc, slopes=S.slopes_of(h)) if sc.get("slopes") else sc
+    q, k, v = randn(23, 1, Lq, h, d, dtype=dtype), randn(24, 1, Lk, h, d, dtype=dtype), randn(25, 1, Lk, h, d, dtype=dtype)
+    q[0, 2, 1, 5] = float("nan")
+    got = S.run_attention(bnd, q, k, v, **sc)
+    assert torch.isnan(got[0, 2, 1]).all()
+    keep = torch.ones(Lq, h, dtype=torch.bool, device="cuda")
+    keep[2, 1] = False
+    assert torch.isfinite(got[0][keep]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [40, 5000])
+def test_nan_queries_give_nan_rows_over_the_paged_cache(bnd, dtype, n):
+    h, hk, d = 4, 2, 64
+    table, n_pages = S.table_of(26, 1, -(-n // 16))
+    kp, vp = S.pages_of(27, n_pages, 16, hk, d, dtype)
+    q = randn(29, 1, h, d, dtype=dtype)
+    q[0, 1, 7] = float("nan")
+    got = S.run_paged(bnd, q, kp, vp, table, [n], hk)
+    assert torch.isnan(got[0, 1]).all() and torch.isfinite(got[0, [0, 2, 3]]).all()

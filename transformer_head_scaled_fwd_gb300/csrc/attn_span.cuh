@@ -246,7 +246,10 @@ __device__ __forceinline__ void join_by(const SpanAttnParams& p, int b, int head
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < kPieces; ++s) {
-            if (ms[i][s] == -CUDART_INF_F) continue;   // no key: its output may hold anything
+            if (ms[i][s] == -CUDART_INF_F) {   // no key: its output may hold anything; its sum is 0, or NaN if all scores are
+                L += ls[i][s];
+                continue;
+            }
             const float f = ex2_approx(ms[i][s] - M);
             L = fmaf(f, ls[i][s], L);
             a.x = fmaf(f, os[i][s].x, a.x);
