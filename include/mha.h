@@ -347,7 +347,8 @@ typedef struct {
  *                    factor above original_length / low, a blend linear in original_length / w between
  *   MHA_ROPE_RAMP    by index: kept up to the pair that turns `high` times over original_length,
  *                    divided by factor from the one that turns `low` times, linear in the index
- *                    between; *scale = 0.1 ln(factor) + 1
+ *                    between (indices rounded outwards, limited to 0 .. rot_dim - 1);
+ *                    *scale = 0.1 ln(factor) + 1
  * *scale is 1 for the others. low < high; both ignored by the first three.
  */
 typedef enum {

@@ -198,6 +198,22 @@ def test_frequencies_banded_and_ramp(lib):
         assert abs(got - ref) <= 2.0 ** -22 * ref
 
 
+@pytest.mark.parametrize("r,base,factor,length,low,high", [
+    (64, 10000.0, 8.0, 131072.0, 1.0, 32.0), (64, 10000.0, 4.0, 65536.0, 1.0, 32.0), (128, 10000.0, 4.0, 131072.0, 1.0, 32.0),
+    (64, 10000.0, 4.0, 1e9, 1.0, 32.0), (64, 10000.0, 4.0, 1e12, 1.0, 32.0), (32, 500000.0, 16.0, 8192.0, 1.0, 32.0),
+    (64, 10000.0, 2.0, 20.0, 1.0, 4.0)])
+def test_ramp_ends_where_the_slowest_pair_still_turns(lib, r, base, factor, length, low, high):
+    """The pairs that turn `high` and `low` times over the length, rounded outwards and limited to 0 .. r - 1: beyond the table
+    (which ends at r / 2 - 1) where its slowest pair turns more often than `low` times."""
+    f, s = bnd.rotary_frequencies(r, base, bnd.ROPE_RAMP, factor, length, low, high)
+    at = lambda n: r * math.log(length / (n * 2 * math.pi)) / (2 * math.log(base))
+    i0, i1 = max(math.floor(at(high)), 0), min(math.ceil(at(low)), r - 1)
+    for i, (got, want) in enumerate(zip(f.tolist(), _plain(r, base))):
+        t = min(max((i - i0) / max(i1 - i0, 1e-3), 0.0), 1.0)
+        ref = (1 - t) * want + t * want / factor
+        assert abs(got - ref) <= 2.0 ** -22 * ref
+
+
 def test_frequencies_refusals(lib):
     for args in ((63,), (0,), (64, 1.0), (64, math.nan), (64, 1e4, 7), (64, 1e4, bnd.ROPE_LINEAR, 0.5),
                  (2, 1e4, bnd.ROPE_BASE, 2.0), (64, 1e4, bnd.ROPE_BANDED, 2.0, 0.0),

@@ -148,12 +148,13 @@ mha_status_t mha_rotary_frequencies(float* inv_freq, float* scale, int rot_dim, 
     const double two_pi = 6.283185307179586476925;
     const int half = rot_dim / 2;
     if (scaling == MHA_ROPE_BASE) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
-    // MHA_ROPE_RAMP: index of the pair that turns n times over original_length
+    // MHA_ROPE_RAMP: index of the pair that turns n times over original_length. The table ends at half - 1, the ramp may end
+    // beyond it.
     auto pair_of = [&](double n) {
         return rot_dim * std::log(original_length / (n * two_pi)) / (2.0 * std::log(base));
     };
     const double first = banded ? std::fmax(std::floor(pair_of(high)), 0.0) : 0.0;
-    const double last = banded ? std::fmin(std::ceil(pair_of(low)), half - 1.0) : 0.0;
+    const double last = banded ? std::fmin(std::ceil(pair_of(low)), rot_dim - 1.0) : 0.0;
     for (int i = 0; i < half; ++i) {
         double f = std::pow(base, -2.0 * i / rot_dim);
         if (scaling == MHA_ROPE_LINEAR) {
