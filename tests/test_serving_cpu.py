@@ -2,6 +2,9 @@
 the binding, and the frequency tables of scaled rotary positions against their definitions."""
 import ctypes
 import math
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -112,6 +115,33 @@ def test_attention_refusals(lib):
     assert lib.mha_document_spans(P, 0, 1, P, None) == INV
     assert lib.mha_document_spans(P, 1, 1, ctypes.c_void_p(4100), None) == INV
     assert lib.mha_document_spans(P, 70000, 1, P, None) == UNS
+
+
+def test_prefix_lens_reach_no_kernel_unless_causal(tmp_path):
+    """The kernels' parameters from a mask, as mha_attention fills them: prefix_lens is read only if causal, so a pointer that
+    is left there otherwise is not passed on."""
+    if shutil.which("g++") is None:
+        pytest.skip("no g++")
+    src, exe = tmp_path / "mask.cpp", tmp_path / "mask"
+    src.write_text('''
+#include "mha.h"
+#include "serve.h"
+int main() {
+    static const int32_t lens[2] = {1, 2};
+    for (int causal = 0; causal < 2; ++causal) {
+        mha_span_mask_t m{causal, 7, lens, lens + 1, lens};
+        mha::SpanAttnParams p{};
+        mha::set_mask(m, &p);
+        if (p.causal != causal || p.q_offset != 7 || p.valid_lens != lens || p.spans != lens) return 1;
+        if (p.prefix_lens != (causal ? lens + 1 : nullptr)) return 2;
+    }
+    return 0;
+}
+''')
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(B.ROOT, "include"), "-I", B.CSRC, "-I", cuda, str(src), "-o", str(exe)],
+                   check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
 
 
 def test_scale_over_cap_must_be_finite(lib):

@@ -9,6 +9,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "../../include/mha.h"
+
 namespace mha {
 
 // From mha_api.cu: the device status word of the current device (nullptr on failure), and a
@@ -100,6 +102,13 @@ struct SpanAttnParams {
     int* status;
     int pieces;              // set by the launcher: CTAs that share a unit
 };
+inline void set_mask(const mha_span_mask_t& m, SpanAttnParams* p) {
+    p->causal = m.causal != 0;
+    p->q_offset = m.q_offset;
+    p->valid_lens = m.key_valid_lens;
+    p->prefix_lens = m.causal != 0 ? m.prefix_lens : nullptr;   // not read otherwise
+    p->spans = m.doc_spans;
+}
 cudaError_t launch_span_attn(const SpanAttnParams& p, cudaStream_t s);        // bf16
 cudaError_t launch_span_attn_f32(const SpanAttnParams& p, cudaStream_t s);
 cudaError_t launch_document_spans(const int32_t* ids, int B, int L, int32_t* spans, cudaStream_t s);

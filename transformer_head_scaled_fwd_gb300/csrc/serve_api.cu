@@ -322,11 +322,7 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
         if (mask->q_offset < 0 || mask->q_offset > 0x7fffffff - L_q)
             return fail(MHA_ERR_INVALID_ARG, "q_offset must be >= 0 and q_offset + L_q below 2^31 (got %d)", mask->q_offset);
         if (!aligned(mask->doc_spans, 8)) return fail(MHA_ERR_INVALID_ARG, "doc_spans must be aligned to 8 bytes");
-        p.causal = mask->causal != 0;
-        p.q_offset = mask->q_offset;
-        p.valid_lens = mask->key_valid_lens;
-        p.prefix_lens = mask->prefix_lens;
-        p.spans = mask->doc_spans;
+        mha::set_mask(*mask, &p);
     }
     if (static_cast<int64_t>(B) * h > (int64_t(1) << 30) ||
         static_cast<int64_t>(B) * h * ((L_q + 63) / 64) > 0x7fffffffll)
