@@ -272,3 +272,21 @@ def test_native_front_declines_what_is_no_call():
         front.set_library(0, 0, 0, 0, 0, 0)
     with pytest.raises(TypeError):
         front.set_library(*["x"] * 6)
+
+
+def test_a_front_that_does_not_compile_is_left_out(tmp_path, monkeypatch, capsys):
+    """_front.so is optional: where g++ fails on it (a torch without CUDA, say) there is a message, no exception, and no
+    module of an earlier build."""
+    torch = pytest.importorskip("torch")
+    if B.build_front() is None:
+        pytest.skip("the headers of Python or torch are missing")
+    bad = tmp_path / "front.cpp"
+    bad.write_text("#include <c10/no_such_header.h>\n")
+    for name, path in (("FRONT_SRC", bad), ("FRONT", tmp_path / "_front.so"), ("BUILD", tmp_path / "_build")):
+        monkeypatch.setattr(B, name, str(path))
+    (tmp_path / "_front.so").write_bytes(b"of an earlier build")
+    assert B.build_front() is None
+    assert "no_such_header" in capsys.readouterr().err
+    assert not (tmp_path / "_front.so").exists()
+    lib = B.LIB
+    assert B.build() == lib and os.path.exists(lib)

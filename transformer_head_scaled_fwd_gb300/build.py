@@ -13,7 +13,8 @@ memory when one falls outside the problem.
 
 ``build()`` also compiles ``csrc/front.cpp`` (the host compiler, torch's headers)
 into ``_front.so``, through which the Python binding makes the serving calls.
-Without torch's or Python's headers it is left out, and the binding uses ctypes.
+Where it does not compile (no headers of torch or Python, a torch without CUDA) it is left
+out with a message, and the binding uses ctypes.
 """
 from __future__ import annotations
 
@@ -62,7 +63,7 @@ def needs_build(lib: str = LIB) -> bool:
 
 
 def build_front(force: bool = False):
-    """Compile _front.so for this interpreter and the installed torch; None where their headers are missing."""
+    """Compile _front.so for this interpreter and the installed torch; None where that cannot be done."""
     spec = importlib.util.find_spec("torch")
     torch = os.path.dirname(spec.origin) if spec is not None and spec.origin else None
     python = sysconfig.get_paths()["include"]
@@ -86,7 +87,10 @@ def build_front(force: bool = False):
                         f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-Wl,-rpath,{libs}"],
                        capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on front.cpp:\n{r.stderr}")
+        if os.path.exists(FRONT):   # of other sources, or another torch
+            os.remove(FRONT)
+        print(f"_front.so is not built: g++ failed on {os.path.basename(FRONT_SRC)}:\n{r.stderr}", file=sys.stderr)
+        return None
     os.replace(tmp, FRONT)
     with open(stamp, "w") as f:
         f.write(made_for)
