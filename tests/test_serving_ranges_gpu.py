@@ -111,6 +111,26 @@ def test_paged_attention_far_scores_beside_near_ones(bnd, dtype, cap):
     R.check(got, ref, tol, "near scores")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap,scale", [(3.4e38, None), (1e35, 1e-10), (1e-44, None), (1e-30, 1e3)])
+def test_caps_at_the_ends_of_fp32(bnd, dtype, cap, scale):
+    """Caps whose product with log2 e, or whose quotient with the scale, leaves fp32's range: no cap, or no score at all."""
+    h, hk, d, n = 4, 2, 64, 200
+    sc = dict(cap=cap) if scale is None else dict(cap=cap, scale=scale)
+    table, n_pages = S.table_of(50, 1, -(-n // 16))
+    kp, vp = S.pages_of(51, n_pages, 16, hk, d, dtype)
+    q = randn(53, 1, h, d, dtype=dtype)
+    q[0, 0] = 0.0
+    got = S.run_paged(bnd, q, kp, vp, table, [n], hk, **sc)
+    ref, tol = paged_fine(q, kp, vp, table, [n], hk, **sc)
+    R.check(got, ref, tol, "paged")
+    rows = table[0].long()
+    k, v = (x[rows].flatten(0, 1)[None, :n].contiguous() for x in (kp, vp))
+    got = S.run_attention(bnd, q[:, None].contiguous(), k, v, **sc)
+    ref, tol = attention_fine(q[:, None], k, v, **sc)
+    R.check(got, ref, tol, "attention")
+
+
 SPANS = [
     # B, Lq, Lk, h, h_kv, d, options
     (1, 130, 130, 2, 1, 128, dict(causal=True)),
@@ -147,26 +167,6 @@ def test_attention_far_scores_beside_near_ones(bnd, dtype, Lq, Lk, h, d, cap):
     got = S.run_attention(bnd, q, k, v, cap=cap)
     ref, tol = attention_fine(q, k, v, cap=cap)
     R.check(got, ref, tol, "near scores")
-
-
-@pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("cap,scale", [(3.4e38, None), (1e35, 1e-10), (1e-44, None), (1e-30, 1e3)])
-def test_caps_at_the_ends_of_fp32(bnd, dtype, cap, scale):
-    """Caps whose product with log2 e, or whose quotient with the scale, leaves fp32's range: no cap, or no score at all."""
-    h, hk, d, n = 4, 2, 64, 200
-    sc = dict(cap=cap) if scale is None else dict(cap=cap, scale=scale)
-    table, n_pages = S.table_of(50, 1, -(-n // 16))
-    kp, vp = S.pages_of(51, n_pages, 16, hk, d, dtype)
-    q = randn(53, 1, h, d, dtype=dtype)
-    q[0, 0] = 0.0
-    got = S.run_paged(bnd, q, kp, vp, table, [n], hk, **sc)
-    ref, tol = paged_fine(q, kp, vp, table, [n], hk, **sc)
-    R.check(got, ref, tol, "paged")
-    rows = table[0].long()
-    k, v = (x[rows].flatten(0, 1)[None, :n].contiguous() for x in (kp, vp))
-    got = S.run_attention(bnd, q[:, None].contiguous(), k, v, **sc)
-    ref, tol = attention_fine(q[:, None], k, v, **sc)
-    R.check(got, ref, tol, "attention")
 
 
 # ------------------------------------------------------------------------------------------ values
@@ -257,3 +257,53 @@ def test_nan_queries_give_nan_rows_over_the_paged_cache(bnd, dtype, n):
     q[0, 1, 7] = float("nan")
     got = S.run_paged(bnd, q, kp, vp, table, [n], hk)
     assert torch.isnan(got[0, 1]).all() and torch.isfinite(got[0, [0, 2, 3]]).all()
+
+
+# ------------------------------------------------------------------------------------------ e4m3 codes
+def check_codes(y, y8, sc):
+    """The codes are fp32 y over the stored scale by IEEE fp32 divisions; the scale is the largest value over 448, to within
+    a product's two roundings."""
+    rows, d = y.shape
+    groups = sc.shape[1]
+    top = y.double().abs().view(rows, groups, -1).amax(dim=2)
+    assert ((sc.double() - top / 448).abs() <= 2.0 ** -23 * top / 448).all()
+    want = (y / sc.repeat_interleave(d // groups, dim=1)).to(E4M3)
+    diff = y8.view(torch.uint8) != want.view(torch.uint8)
+    assert not diff.any(), f"{int(diff.sum())} codes of {diff.numel()}"
+
+
+@pytest.mark.parametrize("rows,d,group", [(3, 256, 128), (2000, 512, 64), (700, 4096, 0), (700, 4096, 128), (64, 1001, 0), (5, 40000, 32)])
+def test_rmsnorm_codes_are_the_quotients(bnd, rows, d, group):
+    """Against the row in fp32 by the same call."""
+    x, g = randn(30, rows, d), randn(31, d) + 1.5
+    y, y8 = torch.empty(rows, d, device="cuda"), torch.empty(rows, d, device="cuda", dtype=E4M3)
+    groups = 1 if group == 0 else d // group
+    sc = torch.empty(rows, groups, device="cuda")
+    bnd.mha_rmsnorm(x, g, 1e-6, y=y)
+    bnd.mha_rmsnorm(x, g, 1e-6, y=y8, scales=sc)
+    check_codes(y, y8, sc)
+
+
+@pytest.mark.parametrize("top", [448.0, 1344.0, 448.0 / 3, 2.0 ** -120, 2.0 ** 120])
+def test_rmsnorm_codes_at_ties(bnd, top):
+    """Quotients half way between two codes, or next to it where top / 448 is not a power of two."""
+    d = 128
+    mids = torch.tensor([17, 19, 21, 23, 25, 27, 29, 31, 34, 38, 8.5, 9.5, 1.0625, 1.1875, 0.53125, 432, 400, 208] * 7 + [448.0, 448.0], device="cuda")
+    g = (mids * (top / 448)).float()
+    x = torch.ones(2, d, device="cuda")
+    x[1] = -1
+    y, y8, sc = torch.empty(2, d, device="cuda"), torch.empty(2, d, device="cuda", dtype=E4M3), torch.empty(2, 1, device="cuda")
+    bnd.mha_rmsnorm(x, g, 0.0, y=y)
+    bnd.mha_rmsnorm(x, g, 0.0, y=y8, scales=sc)
+    assert torch.equal(y[0], g) and torch.equal(y[1], -g)
+    check_codes(y, y8, sc)
+
+
+def test_rmsnorm_scale_that_would_be_zero(bnd):
+    """A largest value whose 448th part is below fp32's smallest number: a scale of 1, as for a row of zeros."""
+    x = torch.ones(2, 64, device="cuda")
+    g = torch.full((64,), 2.0 ** -145, device="cuda")
+    g[::2] = 0.0
+    y8, sc = torch.empty(2, 64, device="cuda", dtype=E4M3), torch.empty(2, 1, device="cuda")
+    bnd.mha_rmsnorm(x, g, 0.0, y=y8, scales=sc)
+    assert (sc == 1).all() and (y8.float() == 0).all()
