@@ -489,8 +489,8 @@ mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q
  *   `group` elements of a row (0: the whole row; else 32, 64 or 128, dividing d) has
  *   scale = max |y| / 448 (1 where that is 0) to within 2^-23, y8 = y / scale rounded to nearest even, and scales
  *   [rows, groups], fp32, contiguous, receives it. NaN stays NaN.
- *   1 <= d <= 2^30; rows >= 0. The squares are summed in fp32: |z| below 2^63 / sqrt(d), and rows of values all below 2^-62
- *   count as eps alone.
+ *   1 <= d <= 2^30; rows >= 0. The squares are summed in fp32: their sum has to stay below 2^128, and values below
+ *   2^-63 lose digits in it.
  */
 mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const void* residual,
                          int64_t residual_stride, void* sum, int64_t sum_stride, const void* gain, float eps,

@@ -307,3 +307,105 @@ def test_rmsnorm_scale_that_would_be_zero(bnd):
     y8, sc = torch.empty(2, 64, device="cuda", dtype=E4M3), torch.empty(2, 1, device="cuda")
     bnd.mha_rmsnorm(x, g, 0.0, y=y8, scales=sc)
     assert (sc == 1).all() and (y8.float() == 0).all()
+
+
+# ------------------------------------------------------------------------------------------ nothing lost, nothing doubled
+def norm_error(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+# Rounding normally distributed values to bf16: an error uniform over each value's step, sqrt(E step^2 / 12 / E x^2) = 1.66e-3
+# of the norm wherever the distribution's width lies between two powers of two. Weights rounded to bf16 add as much again,
+# independently: 2.35e-3. A twentieth on top for the spread of samples. fp32: products over d_k = 128 of scores up to 4 put
+# weights off by 128 * 2^-24 * 4 * 2 = 6e-5 at most.
+NORM = {("paged", BF): 1.75e-3, ("span", BF): 2.45e-3, ("paged", F32): 6e-5, ("span", F32): 6e-5}
+
+
+@pytest.mark.parametrize("dtype,B,h,hk,d,n,sc", [
+    (BF, 1, 16, 2, 128, 70001, {}), (BF, 2, 4, 4, 64, 30000, {}), (BF, 16, 8, 8, 64, 1000, dict(cap=30.0)),
+    (BF, 64, 16, 4, 64, 200, {}), (BF, 3, 20, 1, 128, 5000, dict(slopes=True)),
+    (F32, 1, 4, 1, 64, 40001, {}), (F32, 8, 8, 2, 128, 700, dict(cap=30.0))])
+def test_paged_attention_error_of_the_norm(bnd, dtype, B, h, hk, d, n, sc):
+    sc = dict(sc, slopes=S.slopes_of(h)) if sc.get("slopes") else sc
+    lens = [n - 7 * b for b in range(B)]
+    table, n_pages = S.table_of(32, B, -(-n // 64))
+    kp, vp = S.pages_of(33, n_pages, 64, hk, d, dtype)
+    q = randn(35, B, h, d, dtype=dtype)
+    got = S.run_paged(bnd, q, kp, vp, table, lens, hk, **sc)
+    ref, _ = S.paged_ref(q, kp, vp, table, lens, hk, **sc)
+    assert norm_error(got, ref) <= NORM["paged", dtype]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,Lq,Lk,h,hk,d,opt", [
+    (1, 600, 600, 2, 1, 128, dict(causal=True)), (1, 600, 600, 2, 2, 64, dict(causal=True, cap=50.0)),
+    (1, 1100, 1100, 2, 2, 128, dict(causal=True, cap=20.0)), (2, 700, 700, 2, 1, 128, dict(docs=60)),
+    (1, 700, 700, 2, 1, 64, dict(causal=True, slopes=True)),
+    (2, 1600, 1600, 6, 6, 64, dict(causal=True)), (2, 1600, 1600, 6, 6, 64, dict(docs=90, cap=20.0)),
+    (1, 16, 8192, 4, 1, 128, dict(causal=True, q_offset=8176)), (2, 16, 4100, 4, 2, 64, dict(causal=True, q_offset=4084, cap=30.0))])
+def test_attention_error_of_the_norm(bnd, dtype, B, Lq, Lk, h, hk, d, opt):
+    opt = dict(opt)
+    if opt.get("slopes"):
+        opt["slopes"] = S.slopes_of(h)
+    if opt.get("docs"):
+        opt["docs"] = S.docs_of(36, B, Lk, opt["docs"])
+    q, k, v = randn(37, B, Lq, h, d, dtype=dtype), randn(38, B, Lk, hk, d, dtype=dtype), randn(39, B, Lk, hk, d, dtype=dtype)
+    got = S.run_attention(bnd, q, k, v, **opt)
+    ref, _ = S.attention_ref(q, k, v, **opt)
+    assert norm_error(got, ref) <= NORM["span", dtype]
+
+
+def borders(n, *steps):
+    """Positions around the multiples of each step in 0 .. n - 1, the first and the last ones among them."""
+    at = {0, 1, n - 1, n - 2}
+    for s in steps:
+        for m in range(0, n + 1, s):
+            at |= {m - 1, m, m + 1}
+    return sorted(x for x in at if 0 <= x < n)
+
+
+@pytest.mark.parametrize("dtype,h,hk,d,lens,page", [
+    (BF, 4, 2, 64, [70001], 64), (BF, 16, 2, 128, [30000, 5], 128), (BF, 2, 2, 64, [1000] * 3, 16),
+    (F32, 4, 1, 64, [20001], 64), (F32, 2, 2, 128, [513, 8000, 64], 24)])
+def test_paged_attention_takes_every_key_once(bnd, dtype, h, hk, d, lens, page):
+    """Equal scores, values that are zero but at keys around the borders of steps, blocks, pages and pieces, each with a
+    feature of its own: that feature of the output is 1 / n, and 0 or 2 / n if the key is left out or taken twice. Half
+    a step of the output's type, and fp32 sums of up to 70001 ones."""
+    B, per = len(lens), -(-max(lens) // page)
+    table, n_pages = S.table_of(40, B, per)
+    kp, vp = S.pages_of(41, n_pages, page, hk, d, dtype)
+    q = torch.zeros(B, h, d, device="cuda", dtype=dtype)
+    step = max(lens) // 152 + 1                      # pieces of the line end about here, whatever the device
+    todo = [borders(n, 64, step) if n < 3000 else borders(n, 128 * 16, step) for n in lens]
+    for first in range(0, max(len(t) for t in todo), d):
+        vp.zero_()
+        want = torch.zeros(B, h, d, dtype=torch.float64, device="cuda")
+        for b, n in enumerate(lens):
+            keys = todo[b][first:first + d]
+            at = torch.tensor(keys, device="cuda", dtype=torch.long)
+            if len(keys):
+                f = torch.arange(len(keys), device="cuda")
+                vp[table[b].long()[at // page], at % page, :, f] = 1.0
+                want[b, :, :len(keys)] = 1.0 / n
+        got = S.run_paged(bnd, q, kp, vp, table, lens, hk)
+        R.check(got, want, want * (R.HALF[dtype] + 2.0 ** -8 * (dtype == F32) + 2.0 ** -10) + 0.0, "every key once")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B,Lq,Lk,h,d,causal,cap", [
+    (1, 130, 130, 2, 64, True, 0.0), (1, 3, 8192, 2, 128, False, 0.0), (1, 129, 3000, 2, 64, True, 20.0),
+    (1, 300, 1000, 1, 128, True, 0.0), (2, 1600, 1600, 6, 64, True, 0.0), (1, 1, 5000, 4, 64, False, 0.0)])
+def test_attention_takes_every_key_once(bnd, dtype, B, Lq, Lk, h, d, causal, cap):
+    q, k = torch.zeros(B, Lq, h, d, device="cuda", dtype=dtype), randn(43, B, Lk, h, d, dtype=dtype)
+    off = Lk - Lq
+    seen = (torch.arange(Lq, device="cuda") + off + 1 if causal else torch.full((Lq,), Lk, device="cuda")).double()
+    todo = borders(Lk, 64, Lk // 8 + 1)
+    for first in range(0, len(todo), d):
+        at = torch.tensor(todo[first:first + d], device="cuda")
+        f = torch.arange(len(at), device="cuda")
+        v = torch.zeros(B, Lk, h, d, device="cuda", dtype=dtype)
+        v[:, at, :, f] = 1.0
+        want = torch.zeros(B, Lq, h, d, dtype=torch.float64, device="cuda")
+        want[:, :, :, :len(at)] = torch.where(at[None] < seen[:, None], 1.0 / seen[:, None], 0.0)[:, None]
+        got = S.run_attention(bnd, q, k, v, causal=causal, q_offset=off if causal else 0, cap=cap)
+        R.check(got, want, want * (R.HALF[dtype] + 2.0 ** -8 * (dtype == F32) + 2.0 ** -10) + 0.0, "every key once")
