@@ -165,6 +165,13 @@ def test_rmsnorm_refusals(lib):
     assert call(rows=0) == bnd.MHA_OK          # nothing to do, nothing enqueued
 
 
+def test_rmsnorm_ignores_the_sum_without_a_residual(lib):
+    """Its address and stride are not looked at: what is refused is the overlap of y's rows, which comes later."""
+    odd = ctypes.c_void_p(4097)
+    args = (1, P, 256, None, -5, odd, -7, None, 1e-6, 4, 256, P, 255, None, 0, None)
+    assert lib.mha_rmsnorm(*args) == INV and b"must not overlap" in lib.mha_last_error()
+
+
 def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     q = torch.zeros(1, 2, 4, 64)
     for f in (lambda: bnd.mha_rotary(q, rotary=None, q_out=q), lambda: bnd.mha_attention(q, q, q, out=q),

@@ -350,16 +350,20 @@ mha_status_t mha_rmsnorm(mha_dtype_t dt, const void* x, int64_t x_stride, const 
         return fail(MHA_ERR_INVALID_ARG, "group must divide d (group=%d, d=%d)", group, d);
     if (rows == 0) return MHA_OK;
     if (x == nullptr || y == nullptr) return fail(MHA_ERR_INVALID_ARG, "x and y must not be NULL");
+    if (residual == nullptr) {
+        residual_stride = sum_stride = 0;
+        sum = nullptr;
+    }
     const size_t es = elem(dt);
     if (!aligned(x, es) || !aligned(residual, es) || !aligned(sum, es) || !aligned(gain, es) ||
         !aligned(y, scales ? 1 : es) || !aligned(scales, 4))
         return fail(MHA_ERR_INVALID_ARG, "a tensor is not aligned to its element type");
     if (x_stride < 0 || residual_stride < 0 || sum_stride < 0 || y_stride < 0)
         return fail(MHA_ERR_INVALID_ARG, "row strides must be >= 0");
-    if (rows > 1 && (y_stride < d || (residual != nullptr && sum != nullptr && sum_stride < d)))
+    if (rows > 1 && (y_stride < d || (sum != nullptr && sum_stride < d)))
         return fail(MHA_ERR_INVALID_ARG, "rows of y and sum must not overlap (strides below d=%d)", d);
     mha::RmsNormParams p{};
-    p.x = x; p.residual = residual; p.sum = residual != nullptr ? sum : nullptr; p.gain = gain; p.y = y;
+    p.x = x; p.residual = residual; p.sum = sum; p.gain = gain; p.y = y;
     p.scales = scales;
     p.x_stride = x_stride; p.r_stride = residual_stride; p.s_stride = sum_stride; p.y_stride = y_stride;
     p.rows = rows; p.d = d; p.group = group == 0 ? d : group; p.eps = eps;
