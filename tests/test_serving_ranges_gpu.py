@@ -169,6 +169,30 @@ def test_attention_far_scores_beside_near_ones(bnd, dtype, Lq, Lk, h, d, cap):
     R.check(got, ref, tol, "near scores")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sc", [dict(cap=59.0), dict(cap=59.0, scale=-0.11), dict(cap=300.0), dict(cap=5000.0), {}, dict(cap=59.0, slopes=True)])
+@pytest.mark.parametrize("B,Lq,Lk,h,d,opt", [(1, 200, 1500, 2, 128, {}), (1, 1300, 1300, 2, 64, dict(causal=True)),
+                                             (1, 4, 5000, 2, 64, {}), (2, 900, 900, 1, 128, dict(docs=200))])
+@pytest.mark.parametrize("way", ["rising", "falling", "deep"])
+def test_scores_that_move_the_maximum_all_along(bnd, dtype, sc, B, Lq, Lk, h, d, opt, way):
+    """Scores that grow (fall) steadily over the keys, by about 130 in all before the cap, or lie at about -100 throughout: the reference
+    of every row moves tile after tile, or starts far below zero."""
+    sc, opt = dict(sc), dict(opt)
+    if sc.get("slopes"):
+        sc["slopes"] = S.slopes_of(h)
+    if opt.get("docs"):
+        opt["docs"] = S.docs_of(60, B, Lk, opt["docs"])
+    scale = sc.get("scale", d ** -0.5)
+    q, k, v = randn(61, B, Lq, h, d), randn(62, B, Lk, h, d) * 0.3, randn(63, B, Lk, h, d, dtype=dtype)
+    q[..., 0] = 8.0                                          # one feature carries the slow part of the scores
+    t = torch.arange(Lk, device="cuda") / Lk
+    k[..., 0] = ((dict(rising=130 * t - 65, falling=65 - 130 * t, deep=-100 + 5 * t)[way]) / (8.0 * scale))[None, :, None]
+    q, k = q.to(dtype), k.to(dtype)
+    got = S.run_attention(bnd, q, k, v, **sc, **opt)
+    ref, tol = attention_fine(q, k, v, **sc, **opt)
+    R.check(got, ref, tol, way)
+
+
 # ------------------------------------------------------------------------------------------ values
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("B,Lq,Lk,h,d,opt", [(1, 200, 600, 2, 128, {}), (1, 600, 600, 2, 64, dict(causal=True)),
