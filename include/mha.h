@@ -326,9 +326,9 @@ typedef struct {
  * features (i, i + rot_dim / 2) in the half layout, (2 i, 2 i + 1) interleaved. A token at
  * position t turns pair i by the angle t * inv_freq[i]:
  *   (x_0, x_1) -> scale * (x_0 cos - x_1 sin, x_1 cos + x_0 sin)
- * Features rot_dim .. d_k - 1 pass unchanged. The angle is formed to about 2^-45 of its size and
- * reduced before it is rounded, so far positions keep fp32 accuracy; products are in fp32,
- * rounded once to the type of the tensor.
+ * Features rot_dim .. d_k - 1 pass unchanged. The angle is formed to about 2^-46 of its size and
+ * reduced before it is rounded, so positions up to 2^24 keep fp32 accuracy (beyond, the error of cos and sin grows
+ * with the position: 2^-17.5 at 2^29); products are in fp32, rounded once to the type of the tensor.
  */
 typedef struct {
     const float* inv_freq;   /* device fp32 [rot_dim / 2] */
@@ -430,7 +430,7 @@ typedef struct {
  * have strides (b, h; l is ignored). kv_lens: device int32 [B]; a length <= 0 gives zeros. scores NULL:
  * the plain scaled scores. MHA_BF16 or MHA_F32, d_k = 64 or 128, h a multiple of h_kv. What lies in a
  * page behind a sequence's end is not used, whatever it holds. The pages and their strides are aligned
- * to 16 bytes. Weights are rounded to bf16 for the product with bf16 values.
+ * to 16 bytes. Weights enter the product with bf16 values as two bf16 terms: the result is within its own rounding.
  * workspace >= mha_paged_attention_workspace_size(...), 256-byte aligned, contents of no matter;
  * calls that overlap on the GPU need one each. The result does not depend on timing.
  */
@@ -470,7 +470,8 @@ mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* s
  * h a multiple of h_kv (head n reads key head n / (h / h_kv)); scores, mask NULL: plain, all keys.
  * MHA_BF16 or MHA_F32 with d_k = 64 or 128; pointers and strides aligned to 16 bytes. Keys and values at and
  * behind key_valid_lens[b] are not used, whatever they hold; elsewhere a masked value that is not
- * finite may reach rows that do not attend to it (0 * NaN). No workspace.
+ * finite may reach rows that do not attend to it (0 * NaN), but no row without a key. Weights are rounded to bf16
+ * for the product with bf16 values. The l stride of q, k and v is not 0 (unless the length is 1). No workspace.
  */
 mha_status_t mha_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
                            const void* k, const mha_strides_t* k_strides,

@@ -5,7 +5,8 @@
 //
 // HBM-bound: K and V of every cached position are read once, 4 d_k bytes a position and key head in
 // bf16, for 4 d_k flop a query head. The heads that share a key head are the rows of one matrix
-// product (mma.sync in bf16: CUDA cores could not keep up from 4 heads on), so the cache is read once for all of them.
+// product (mma.sync in bf16: CUDA cores could not keep up from 4 heads on), so the cache is read once for up to 16 of them (8
+// in fp32); further ones are another unit, which reads it again.
 //
 // Work split: a unit is (sequence, key head, tile of query heads). All units' keys, in blocks of
 // kWarps steps, form one line that is cut into equal pieces, one CTA a piece, whatever the lengths
@@ -19,8 +20,8 @@
 // shared memory. Keys behind the end of a sequence, and pages outside the pool, arrive as zeros and get
 // no weight: what lies there is never touched.
 //
-// Measured (bf16): 16 sequences of 8192, 16 heads of 64, 537 MB: 88-92 us, 5.8-6.1 TB/s; 48 ragged ones up to 15000, 32 / 8
-// heads of 128, 1.5 GB: 245 us, 6.2 TB/s (0.91 of measured copy bandwidth); one of 131071, 16 / 2 heads: 30.5 us, of which
+// Measured (bf16): 16 sequences of 8192, 16 heads of 64, 537 MB: 89-97 us by box, 5.5-6.0 TB/s (0.81-0.89 of measured copy
+// bandwidth); 48 ragged ones up to 15000, 32 / 8 heads of 128, capped, 1.5 GB: 237 us, 6.4 TB/s (0.94); one of 131071, 16 / 2 heads: 30.5 us, of which
 // 20 us are its traffic: the two launches, the look-ups (length, page, key: three dependent loads) and the join are the
 // rest, 11 us at any length, and 7.2 TB/s is what each further key costs.
 #include <algorithm>
@@ -826,7 +827,8 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     const int ctas = std::min(sms, kMaxCtas);
     // Sequences of kWholeBlocks blocks at most are not worth the second kernel: a CTA takes longer over a unit by less
     // than the join costs (64 x 300, 32 / 8 heads of 128: 31 against 34 us; one of 500, 16 / 4 heads of 64: 10.8
-    // against 13.0 us with the launches).
+    // against 13.0 us with the launches). The lengths are on the device, so the host goes by what the table has room for:
+    // the same sequences behind a wider table take the two launches.
     constexpr int kBlock = Step<typename W::T, kD>::kKeys * kWarps;
     p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= kWholeBlocks * kBlock;
     const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + W::kRows - 1) / W::kRows);

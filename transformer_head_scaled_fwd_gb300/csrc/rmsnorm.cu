@@ -333,7 +333,7 @@ cudaError_t launch_t(const RmsNormParams& p, cudaStream_t s) {
     if (p.d % kN == 0 && ok(p.x, p.x_stride) && ok(p.residual, p.residual ? p.r_stride : 0) &&
         ok(p.sum, p.sum ? p.s_stride : 0) && ok(p.gain, 0) && y_ok) {
         // Four accesses a thread keep enough bytes in flight (32768 x 4096 without a residual: 84 us, with two 130 us);
-        // when there are fewer rows than fill the SMs, twice the threads finish a row sooner (16 x 1024: 6.7 against
+        // when there are fewer rows than four for each of 152 SMs, twice the threads finish a row sooner (16 x 1024: 6.7 against
         // 8.2 us with the launch).
         const bool few = p.rows <= 608;
         const int chunks = p.d / kN;
