@@ -270,25 +270,6 @@ __device__ __forceinline__ void join_parts(const SpanAttnParams& p, int b, int h
     else join_by<T, kD, kUnit, kThr, 8>(p, b, head, q0, piece, m_at, o_at);
 }
 
-// launch_pdl with clusters of `size` CTAs.
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int size, size_t smem, cudaStream_t s,
-                                      Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
-}
-
 // Clusters of a kernel, allowed `smem` bytes by the caller, that the current device runs at once; asked once a device and
 // size, for it is a property of the device.
 struct ClusterRoom {

@@ -83,6 +83,10 @@ struct PagedAttnParams {
     int B, h, h_kv, d;
     float* partial;          // workspace
     int* status;
+    const float* k_scales;   // a cache in 8 bits: [n_pages, page_scales]; page_scales = blocks of a page * h_kv
+    const float* v_scales;
+    FastDiv scale_block;     // tokens a scale covers
+    int64_t page_scales;
     int whole;               // set by the launcher: no unit is split
     int direct;              // ... and each has a CTA of its own
 };
