@@ -307,7 +307,7 @@ mha_status_t mha_ffn_forward(mha_dtype_t dt, const void* x,
 
 /*
  * ======================================================================================
- * Serving operators: rotary positions, a paged key/value cache, attention over it, attention
+ * Serving operators: rotary positions, a paged key/value cache (also in 8 bits) and its block table, attention over it, attention
  * with capped and biased scores under span masks, RMS norm with 8-bit output.
  *
  * Tensors here need not be contiguous: a [B, L, heads, d_k] tensor is a pointer and the three
@@ -439,6 +439,75 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
                                  void* out, const mha_strides_t* out_strides,
                                  int B, int h, int h_kv, int d_k, const int32_t* kv_lens,
                                  const mha_scores_t* scores, const mha_paged_cache_t* cache,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The block table of a paged cache as sequences grow, shrink and end, on the device: sequence b goes from held[b] to want[b]
+ * positions (device int32 [B]; below 0: 0), so from ceil(held / page_size) to ceil(want / page_size) pages.
+ *   free_pages  device int32 [n_pages], a stack: entries 0 .. *free_count - 1 are the free pages; the two are updated.
+ *   Sequences that shrink (want 0: end) give their last pages back: entry by entry pushed so that the first sequence's first
+ *   page ends on top, and -1 in the table. Then those that grow take pages from the top in the order of the sequences, the first
+ *   one's first, and find them in the table. Pages given back in a call serve in the same call.
+ *   Served is a sequence that needs no page, or whose pages and those of all sequences before it are there; one that
+ *   is not, or that wants more than max_pages pages, stays as it is.
+ *   lens      device int32 [B]: positions after the call: want[b], or held[b] where it is not served.
+ *   new_lens  device int32 [B] or NULL: max(lens - held, 0), for the append (with start = held).
+ *   slots     device int64 [B, T] or NULL: of new token t of sequence b, page * page_size + slot in the page, -1 where there is
+ *             none (t >= new_lens[b]). T is ignored without it.
+ * A call with held and want exchanged takes a step back, the stack included. Entries of the table that a call does not name, and
+ * of the stack above the pages given back, are left as they were. A page number outside [0, n_pages) moves as it is, gives no slot
+ * and records MHA_PAGED_BAD_PAGE, and so does a stack that pages given back would overflow (the ones beyond n_pages are
+ * dropped). lens and new_lens are neither held nor want. Calls that share a table or a stack are ordered by the caller.
+ */
+mha_status_t mha_paged_resize(const int32_t* held, const int32_t* want, int B, int page_size,
+                              int32_t* block_table, int64_t table_stride, int max_pages,
+                              int32_t* free_pages, int n_pages, int32_t* free_count,
+                              int32_t* lens, int32_t* new_lens, int T, int64_t* slots, void* stream);
+
+/*
+ * A paged cache in 8 bits: pages as above, strides in codes (bytes), d_k = 64 or 128; each block of `block` neighbouring
+ * slots of a page and each key head has a scale for keys and one for values, and a code c stands for c * scale.
+ */
+typedef enum { MHA_CODE_E4M3 = 0, MHA_CODE_INT8 = 1 } mha_code_t;   /* e4m3: finite form, NaN; int8: two's complement */
+typedef struct {
+    mha_paged_cache_t pages;   /* pages and strides aligned to 16 bytes */
+    mha_code_t code;
+    int block;                 /* tokens that a scale covers: divides page_size; up to 256 for the append */
+    float* k_scales;           /* device fp32 [n_pages, page_size / block, h_kv], contiguous */
+    float* v_scales;
+} mha_coded_cache_t;
+
+/*
+ * mha_paged_append into such a cache. The scale of a block is the smallest power of two s, at least 2^-120, with
+ * max |x| <= top * s over the turned keys (the values) of its tokens, top = 448 (e4m3) or 127 (int8), x in fp32; codes are
+ * x / s rounded to nearest even. A token at a block's first slot begins the block: what its scale and slots held is forgotten.
+ * Tokens that enter a block behind others keep the block's scale if theirs is not larger; else the block gets theirs, and the codes
+ * in front of them are rounded again (c * old / new). A scale of other origin is kept as it is while it is the larger one.
+ * A NaN or an infinity makes its block's scale NaN, and with it whatever attends to the block.
+ *   q, k, v, q_out, k_out: pointers and strides aligned to 16 bytes; k_out gets the turned keys in type dt. Otherwise all
+ * is as for mha_paged_append: start, new_lens, rotary, in-place rules, bad pages. Blocks are written by one sequence each. One launch.
+ */
+mha_status_t mha_coded_append(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                              void* q_out, const mha_strides_t* q_out_strides,
+                              const void* k, const mha_strides_t* k_strides,
+                              void* k_out, const mha_strides_t* k_out_strides,
+                              const void* v, const mha_strides_t* v_strides,
+                              int B, int T, int h, int h_kv, int d_k, const int32_t* start,
+                              const int32_t* new_lens, const mha_rotary_t* rotary,
+                              const mha_coded_cache_t* cache, void* stream);
+
+/*
+ * mha_paged_attention over such a cache: the attention over the values c * scale, for q and out of type dt. Scales are
+ * 0 or between 2^-120 and 2^120, of any mantissa. q enters as it is (bf16: to 2^-29 of its row's largest element; fp32:
+ * 2^-39); weights are rounded to 2^-12 of themselves for a bf16 result, to 2^-22 for an fp32 one, products and sums are fp32.
+ * What lies behind a sequence's end is not used; a block's scale is, for the block's other slots.
+ * workspace >= mha_coded_attention_workspace_size(...); kv_lens, scores, bad pages, order: as for mha_paged_attention.
+ */
+size_t mha_coded_attention_workspace_size(mha_dtype_t dt, int B, int h, int h_kv, int d_k);
+mha_status_t mha_coded_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides,
+                                 void* out, const mha_strides_t* out_strides,
+                                 int B, int h, int h_kv, int d_k, const int32_t* kv_lens,
+                                 const mha_scores_t* scores, const mha_coded_cache_t* cache,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*

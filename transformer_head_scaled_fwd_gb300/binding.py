@@ -9,7 +9,8 @@ Function names match the C entry points: ``mha_forward``,
 ``mha_forward_host``, ``mha_workspace_size``, ``mha_host_staging_size``,
 ``mha_check_device_status``; the serving operators ``mha_rotary``,
 ``mha_paged_append``, ``mha_paged_attention``, ``mha_attention``,
-``mha_document_spans``, ``mha_rmsnorm`` and the ``make_*`` descriptions they take.
+``mha_document_spans``, ``mha_rmsnorm``, ``mha_paged_resize``, ``mha_coded_append``,
+``mha_coded_attention`` and the ``make_*`` descriptions they take.
 """
 from __future__ import annotations
 
@@ -33,7 +34,8 @@ EXPORTS = ("mha_workspace_size", "mha_forward", "mha_qkv_projection", "mha_atten
            "mha_decode_workspace_size", "mha_kv_cache_prefill", "mha_decode_step",
            "mha_selftest_wait_timeout", "mha_rotary_frequencies", "mha_rotary", "mha_paged_append",
            "mha_paged_attention_workspace_size", "mha_paged_attention", "mha_document_spans",
-           "mha_attention", "mha_rmsnorm")
+           "mha_attention", "mha_rmsnorm", "mha_paged_resize", "mha_coded_append",
+           "mha_coded_attention_workspace_size", "mha_coded_attention")
 MHA_SELFTEST_WAIT_CODE = 0x7f1
 
 
@@ -62,6 +64,11 @@ class PagedCacheT(ctypes.Structure):
                 ("slot_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
                 ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
                 ("max_pages", ctypes.c_int)]
+
+
+class CodedCacheT(ctypes.Structure):
+    _fields_ = [("pages", PagedCacheT), ("code", ctypes.c_int), ("block", ctypes.c_int), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
 
 
 class ScoresT(ctypes.Structure):
@@ -145,6 +152,14 @@ def load(path: str | None = None):
         lib.mha_attention.argtypes = [i] + [vp] * 8 + [i] * 6 + [vp] * 3
         lib.mha_rmsnorm.restype = i
         lib.mha_rmsnorm.argtypes = [i, vp, i64, vp, i64, vp, i64, vp, f, i64, i, vp, i64, vp, i, vp]
+        lib.mha_paged_resize.restype = i
+        lib.mha_paged_resize.argtypes = [vp, vp, i, i, vp, i64, i, vp, i, vp, vp, vp, i, vp, vp]
+        lib.mha_coded_append.restype = i
+        lib.mha_coded_append.argtypes = [i] + [vp] * 10 + [i] * 5 + [vp] * 5
+        lib.mha_coded_attention_workspace_size.restype = sz
+        lib.mha_coded_attention_workspace_size.argtypes = [i] * 5
+        lib.mha_coded_attention.restype = i
+        lib.mha_coded_attention.argtypes = [i] + [vp] * 4 + [i] * 4 + [vp] * 4 + [sz, vp]
         _lib = lib
         return lib
 
@@ -314,6 +329,7 @@ def mha_ffn_forward(x, w_1, b_1, w_2, b_2, *, out, workspace, stream=None):
 
 # ------------------------------------------------------------------ serving operators
 MHA_PAGED_BAD_PAGE = 0x501
+MHA_CODE_E4M3, MHA_CODE_INT8 = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDED, ROPE_RAMP = range(5)
 
 
@@ -326,7 +342,7 @@ _pack_mask = struct.Struct("@2i3P").pack        # mha_span_mask_t
 
 def _torch():
     """torch's entry points used below, looked up once: (current device, current stream handle of a device)."""
-    global _current_device, _raw_stream, _bf16, _f32, _i32, _e4m3, _front
+    global _current_device, _raw_stream, _bf16, _f32, _i32, _i64, _e4m3, _i8, _front
     import torch
     torch.cuda.init()
     try:
@@ -338,12 +354,14 @@ def _torch():
         pass
     if _front is None:
         warnings.warn("_front.so is not built for this torch: serving calls cost more on the host")
-    _bf16, _f32, _i32, _e4m3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+    _bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+    _e4m3, _i8 = torch.float8_e4m3fn, torch.int8
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
-_current_device = _raw_stream = _bf16 = _f32 = _i32 = _e4m3 = _front = None
-_FRONT = ("mha_rotary", "mha_paged_append", "mha_paged_attention", "mha_document_spans", "mha_attention", "mha_rmsnorm")
+_current_device = _raw_stream = _bf16 = _f32 = _i32 = _i64 = _e4m3 = _i8 = _front = None
+_FRONT = ("mha_rotary", "mha_paged_append", "mha_paged_attention", "mha_document_spans", "mha_attention", "mha_rmsnorm",
+          "mha_paged_resize", "mha_coded_append", "mha_coded_attention")
 
 
 def _here(t):
@@ -452,6 +470,43 @@ def make_paged_cache(k_pages, v_pages, block_table):
     return c
 
 
+_CODED = 2       # in place of a dtype code, in what the native front reads
+
+
+def make_coded_cache(k_pages, v_pages, k_scales, v_scales, block_table):
+    """Description of a cache in 8 bits: pages as for make_paged_cache, torch.float8_e4m3fn or torch.int8; the scales fp32
+    [n_pages, blocks of a page, h_kv], contiguous. Holds references to the five."""
+    dev = _here(k_pages)
+    n, size, h_kv, d = k_pages.shape
+    if k_pages.dtype is not _e4m3 and k_pages.dtype is not _i8:
+        raise TypeError(f"unsupported dtype {k_pages.dtype} of coded pages: use torch.float8_e4m3fn or torch.int8")
+    _want(v_pages, "v_pages", k_pages.dtype, k_pages.shape, dev)
+    if k_pages.stride() != v_pages.stride():
+        raise ValueError("k_pages and v_pages must have the same strides")
+    if k_pages.stride(3) != 1 and d != 1:
+        raise ValueError("the last dimension of the pages must be adjacent")
+    _want(block_table, "block_table", _i32, block_table.shape, dev)
+    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be [B, max_pages] with adjacent rows")
+    blocks = k_scales.shape[1]
+    if blocks < 1 or size % blocks != 0:
+        raise ValueError(f"k_scales has {blocks} blocks a page, which do not divide its {size} slots")
+    for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        _want(t, name, _f32, (n, blocks, h_kv), dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    pages = PagedCacheT(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], n, size, block_table.data_ptr(),
+                        block_table.stride(0), block_table.shape[1])
+    c = CodedCacheT(pages, MHA_CODE_INT8 if k_pages.dtype is _i8 else MHA_CODE_E4M3, size // blocks, k_scales.data_ptr(),
+                    v_scales.data_ptr())
+    c._tensors = (k_pages, v_pages, k_scales, v_scales, block_table)
+    c._ref = ctypes.byref(c)
+    c._heads = h_kv
+    c._for = (block_table.shape[0], d, "coded", dev)
+    c._native = struct.pack("P5q", ctypes.addressof(c), block_table.shape[0], d, _CODED, dev, h_kv)
+    return c
+
+
 def make_scores(scale: float = 0.0, cap: float = 0.0, slopes=None):
     """Score description: scale (0: 1 / sqrt(d_k)), tanh cap (0: none), slopes a CUDA fp32 [h] or None."""
     s = ScoresT(scale, cap, None if slopes is None else _floats(slopes, "slopes"))
@@ -514,10 +569,21 @@ def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_
     """Append k, v [B, T, h_kv, d_k] to the cache at positions start[b] + t, turning k (and q into q_out)."""
     if _front is not None and _front.paged_append(k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream):
         return
+    _append((_lib or load()).mha_paged_append, k.dtype, k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream)
+
+
+def mha_coded_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_lens=None, rotary=None, stream=None):
+    """mha_paged_append into a cache in 8 bits (make_coded_cache)."""
+    if _front is not None and _front.coded_append(k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream):
+        return
+    _append((_lib or load()).mha_coded_append, "coded", k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream)
+
+
+def _append(entry, kind, k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream):
     dev = _here(k)
     dtype, shape = k.dtype, k.shape
     B, T, h_kv, d = shape
-    if cache._for != (B, d, dtype, dev) or cache._heads != h_kv:
+    if cache._for != (B, d, kind, dev) or cache._heads != h_kv:
         raise ValueError("the cache's batch, heads, head width, dtype or device differ from k's")
     kp, ks = _view(k, "k", dtype, shape, dev)
     vp, vs = _view(v, "v", dtype, shape, dev)
@@ -533,7 +599,7 @@ def mha_paged_append(k, v, start, *, cache, q=None, q_out=None, k_out=None, new_
     if start is None:
         raise ValueError("start must be an int32 tensor [B]")
     one = (B,)
-    st = (_lib or load()).mha_paged_append(
+    st = entry(
         _code(dtype), qp, qs, qop, qos, kp, ks, kop, kos, vp, vs, B, T, h, h_kv, d, _ints(start, "start", one, dev),
         _ints(new_lens, "new_lens", one, dev), None if rotary is None else _rotary_ref(rotary, dev), cache._ref,
         _raw_stream(dev) if stream is None else stream.cuda_stream)
@@ -549,11 +615,26 @@ def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, strea
     """Attention of one new token a sequence, q [B, h, d_k], over the kv_lens[b] cached positions -> out."""
     if _front is not None and _front.paged_attention(q, kv_lens, cache, out, workspace, scores, stream):
         return
+    _decode((_lib or load()).mha_paged_attention, q.dtype, q, kv_lens, cache, out, workspace, scores, stream)
+
+
+def coded_attention_workspace_size(dt: int, B: int, h: int, h_kv: int, d_k: int) -> int:
+    return int(load().mha_coded_attention_workspace_size(dt, B, h, h_kv, d_k))
+
+
+def mha_coded_attention(q, kv_lens, *, cache, out, workspace, scores=None, stream=None):
+    """mha_paged_attention over a cache in 8 bits (make_coded_cache)."""
+    if _front is not None and _front.coded_attention(q, kv_lens, cache, out, workspace, scores, stream):
+        return
+    _decode((_lib or load()).mha_coded_attention, "coded", q, kv_lens, cache, out, workspace, scores, stream)
+
+
+def _decode(entry, kind, q, kv_lens, cache, out, workspace, scores, stream):
     dev = _here(q)
     dtype, shape = q.dtype, q.shape
     B, h, d = shape
     _want(out, "out", dtype, shape, dev)
-    if cache._for != (B, d, dtype, dev):
+    if cache._for != (B, d, kind, dev):
         raise ValueError("the cache's batch, head width, dtype or device differ from q's")
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on cuda:{dev}")
@@ -563,10 +644,43 @@ def mha_paged_attention(q, kv_lens, *, cache, out, workspace, scores=None, strea
     ob, oh, od = out.stride()
     if qd != 1 or od != 1:
         raise ValueError("the last dimension of q and out must be adjacent")
-    st = (_lib or load()).mha_paged_attention(
+    st = entry(
         _code(dtype), q.data_ptr(), _pack_strides(qb, 0, qh, 1), out.data_ptr(), _pack_strides(ob, 0, oh, 1), B, h,
         cache._heads, d, _ints(kv_lens, "kv_lens", (B,), dev), _scores_ref(scores, h, dev), cache._ref,
         workspace.data_ptr(), workspace.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        _check(st)
+
+
+def mha_paged_resize(held, want, *, block_table, page_size: int, free_pages, free_count, lens, new_lens=None, slots=None,
+                     stream=None):
+    """Take the sequences from held to want positions (int32 [B]): pages move between block_table int32 [B, max_pages] and
+    the stack free_pages int32 [n_pages], of which free_count int32 [1] are free. lens and new_lens int32 [B] get the positions
+    reached and how many are new, slots int64 [B, T] the new tokens' slots."""
+    if _front is not None and _front.paged_resize(held, want, block_table, page_size, free_pages, free_count, lens, new_lens, slots,
+                                                  stream):
+        return
+    dev = _here(held)
+    B, = held.shape
+    one = (B,)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = block_table.shape[1]
+    _want(block_table, "block_table", _i32, (B, max_pages), dev)
+    if max_pages > 1 and block_table.stride(1) != 1:
+        raise ValueError("the rows of block_table must be adjacent")
+    sp, T = None, 0
+    if slots is not None:
+        T = slots.shape[1]
+        _want(slots, "slots", _i64, (B, T), dev)
+        if not slots.is_contiguous():
+            raise ValueError("slots must be contiguous")
+        sp = slots.data_ptr()
+    st = (_lib or load()).mha_paged_resize(
+        _ints(held, "held", one, dev), _ints(want, "want", one, dev), B, page_size, block_table.data_ptr(), block_table.stride(0),
+        max_pages, _ints(free_pages, "free_pages", (free_pages.numel(),), dev), free_pages.numel(),
+        _ints(free_count, "free_count", (1,), dev), _ints(lens, "lens", one, dev), _ints(new_lens, "new_lens", one, dev), T, sp,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
     if st:
         _check(st)
 

@@ -1,0 +1,321 @@
+// coded_attn.cu -- attention of one new token a sequence over a paged cache in 8 bits (e4m3 or int8 codes, a scale for each
+// block of tokens and key head).
+//
+//   s_j = cap tanh(scale ks_j q.ck_j / cap) - slope (n - 1 - j),  o = sum_j softmax_j(s) vs_j cv_j,  j < n
+// with codes c and the scales ks, vs of their blocks; one pass with a running maximum m and sum l. n = 0 gives zeros.
+//
+// HBM-bound: 2 d_k bytes a position and key head, half of a bf16 cache, so the same loads feed twice the keys and the
+// instructions a key count twice as much. Codes become fp16 in registers, which is exact (e4m3 is a subset of fp16, int8 is
+// below 2^8), and the products are fp16 matrix instructions on them. A query row is scaled by a power of two to below 2^15 and
+// enters as one fp16 number an element (bf16: exact down to 2^-29 of the row's largest) or as three (fp32).
+//
+// Scales: ks multiplies a score after its product. vs belongs to a weight, p_j vs_j, whose size is not bounded by that of
+// p_j, and fp16 has no range to spare: the weights have a running maximum of their own, over s_j + log2 of vs_j's power of two,
+// so that the largest lies in 2^6 .. 2^15 whatever the scales are. They are rounded to fp16 (2^-12, against 2^-9 of a bf16
+// result), for an fp32 result taken as two fp16 terms (2^-22). p_j itself is summed in fp32.
+//
+// Work split, loads and join: paged_line.cuh; a step is 32 keys.
+#include "paged_line.cuh"
+
+namespace mha {
+namespace {
+
+constexpr float kBase = 6.0f;       // log2 of the least the largest weight is taken to
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
+    float2 f;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(x));
+    return f;
+}
+
+// Four codes to fp16: bytes 0, 1 and 2, 3 (kCross: 0, 2 and 1, 3).
+template <bool kInt8, bool kCross>
+__device__ __forceinline__ void codes_f16(uint32_t x, uint32_t& a, uint32_t& b) {
+    if constexpr (kInt8) {
+        // the byte c + 128 under the exponent of 1024 is 1024 + 128 + c
+        const uint32_t u = x ^ 0x80808080u;
+        a = __byte_perm(u, 0x64646464u, kCross ? 0x4240 : 0x4140);
+        b = __byte_perm(u, 0x64646464u, kCross ? 0x4341 : 0x4342);
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(a) : "r"(0x64806480u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(b) : "r"(0x64806480u));
+    } else {
+        const uint32_t u = kCross ? __byte_perm(x, 0u, 0x3120) : x;
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(u));
+    }
+}
+
+// Exponent of a scale, at least -110: that of the weights' maximum stays within fp32's range of the scores'.
+__device__ __forceinline__ float exponent_of(float s) {
+    return static_cast<float>(max(static_cast<int>((__float_as_uint(s) >> 23) & 0xffu) - 127, -110));
+}
+
+// As in paged_attn.cu, both products are taken transposed: S^T = K q^T (16 keys x d_k times d_k x 8 heads) and
+// o^T = V^T P^T (16 features x 16 keys times 16 keys x 8 heads). An operand's 16-bit elements are made from bytes that lie
+// side by side, so the feature that a row or column of a product stands for is not its number: for K, the k of lane t of
+// four are features 4 t .. 4 t + 3 (q is loaded to match); for V, loaded transposed in units of two bytes, rows g and
+// g + 8 are features 2 g and 2 g + 1.
+template <typename T_, int kD, int kNT, bool kInt8>
+struct WarpCoded {
+    using T = T_;
+    using Step = StepOf<kD, 1, 32, kD == 128 ? 3 : 6, true>;
+    static constexpr int kRows = 8 * kNT;
+    static constexpr int kBufs = kNT * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
+    static constexpr int kQFloats = 0;
+    static constexpr int kKT = Step::kKeys / 16;
+    static constexpr bool kWide = sizeof(T) == 4;
+    static constexpr int kQT = kWide ? 3 : 1;       // fp16 terms of q
+    static constexpr int kPT = kWide ? 2 : 1;       // and of a weight
+    uint32_t q[kQT][kD / 16][kNT][2];
+    float o[kD / 16][kNT][4];       // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
+    // of those two heads: maximum of the scores, and of score + scale's exponent; 2^(m - mo + kBase); this lane's share of the
+    // sum; the bias' slope; what takes a product back to q's size
+    float m[kNT][2], mo[kNT][2], u[kNT][2], l[kNT][2], slope[kNT][2], back[kNT][2];
+
+    static __device__ __forceinline__ int swizzle(int row) { return kD == 128 ? row & 7 : (row >> 1) & 3; }
+
+    __device__ __forceinline__ void start(const PagedAttnParams& p, float*, int b, int head0, int rows, int lane) {
+        const T* base = static_cast<const T*>(p.q) + b * p.q_b + head0 * p.q_h;
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt) {
+            const int row = nt * 8 + (lane >> 2);      // operand column: head lane / 4
+            const T* x = base + row * p.q_h + 4 * (lane & 3);
+            float f[kD / 16][4];
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    f[k][e] = row < rows ? load_f(x + 16 * k + e) : 0.0f;
+                    top = fmaxf(top, fabsf(f[k][e]));
+                }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int x0 = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            // not finite, or nothing but zeros (and NaN): as it is
+            const int shift = x0 == 128 || top == 0.0f ? 0 : 14 - max(x0, -100);
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float r0 = f[k][2 * hf] * up, r1 = f[k][2 * hf + 1] * up;
+#pragma unroll
+                    for (int t = 0; t < kQT; ++t) {
+                        q[t][k][nt][hf] = pack_f16x2(r0, r1);
+                        const float2 got = unpack_f16x2(q[t][k][nt][hf]);
+                        r0 -= got.x;
+                        r1 -= got.y;
+                    }
+                }
+#pragma unroll
+            for (int k = 0; k < kD / 16; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int col = 2 * (lane & 3) + e, hd = nt * 8 + col;
+                const int of_head = __shfl_sync(0xffffffffu, shift, 4 * col);
+                back[nt][e] = __uint_as_float(static_cast<uint32_t>(127 - of_head) << 23);
+                slope[nt][e] = p.slopes != nullptr && hd < rows ? p.slopes[head0 + hd] * kLog2e : 0.0f;
+                m[nt][e] = mo[nt][e] = -CUDART_INF_F;
+                u[nt][e] = l[nt][e] = 0.0f;
+            }
+        }
+    }
+
+    // keys key0 .. key0 + 31 in shared memory at k, v, their scales behind v; live: bit i: key0 + i counts
+    __device__ __forceinline__ void step(uint32_t k, uint32_t v, int key0, uint32_t live, int n, const ScoreForm& form,
+                                         int rows, int lane) {
+        constexpr int kRow = Step::kRow;
+        const int r8 = lane & 7, mi = lane >> 3, g = lane >> 2;
+        const uint32_t row = (mi & 1) * 8 + r8;
+        const uint32_t c0 = static_cast<uint32_t>(((mi >> 1) ^ swizzle(r8)) << 4);
+        float ks[kKT][2], vs[kKT][2];
+#pragma unroll
+        for (int t = 0; t < kKT; ++t)
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t a = v + Step::kBytes + 4 * (t * 16 + 8 * hf + g);
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[t][hf]) : "r"(a));
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[t][hf]) : "r"(a + 4 * Step::kKeys));
+            }
+        float s[kKT][kNT][4];
+#pragma unroll
+        for (int t = 0; t < kKT; ++t) {
+            const uint32_t at = k + (t * 16 + row) * kRow;
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < kD / 32; ++kk) {
+                uint32_t f[4];
+                ldsm4(f, at + (c0 ^ (kk << 5)));
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {       // the two chunks of 16 features
+                    uint32_t a[4];
+                    codes_f16<kInt8, false>(f[2 * hf], a[0], a[2]);
+                    codes_f16<kInt8, false>(f[2 * hf + 1], a[1], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                        for (int x = kQT - 1; x >= 0; --x) mma_f16(s[t][nt], a, q[x][2 * kk + hf][nt][0], q[x][2 * kk + hf][nt][1]);
+                }
+            }
+        }
+        bool more = false;
+#pragma unroll
+        for (int t = 0; t < kKT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = t * 16 + g + 8 * (e >> 1);
+                const bool ok = (live >> i) & 1u;
+                const float away = static_cast<float>(n - 1 - key0 - i);
+                const float ev = exponent_of(vs[t][e >> 1]);
+#pragma unroll
+                for (int nt = 0; nt < kNT; ++nt) {
+                    const float dot = s[t][nt][e] * (ks[t][e >> 1] * back[nt][e & 1]);
+                    s[t][nt][e] = ok ? form.of<kWide>(dot, slope[nt][e & 1], away) : -CUDART_INF_F;
+                    more |= s[t][nt][e] > m[nt][e & 1] + kGrow || s[t][nt][e] + ev > mo[nt][e & 1] + kGrow;
+                }
+            }
+        // The maxima move only when one is passed by kGrow (the first keys always do that): a weight stays below
+        // 2^(kGrow + 1 + kBase) = 2^15, and nothing is rescaled in between.
+        if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float top = m[nt][e], most = mo[nt][e];
+#pragma unroll
+                    for (int t = 0; t < kKT; ++t) {
+                        top = fmax3(top, s[t][nt][e], s[t][nt][e + 2]);
+                        most = fmax3(most, s[t][nt][e] + exponent_of(vs[t][0]), s[t][nt][e + 2] + exponent_of(vs[t][1]));
+                    }
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, x));
+                    }
+                    const bool first = m[nt][e] == -CUDART_INF_F;
+                    l[nt][e] *= first ? 0.0f : ex2_approx(m[nt][e] - top);
+                    const float alpha = first ? 0.0f : ex2_approx(mo[nt][e] - most);
+                    m[nt][e] = top;
+                    mo[nt][e] = most;
+                    u[nt][e] = top == -CUDART_INF_F ? 0.0f : ex2_approx(top - most + kBase);
+#pragma unroll
+                    for (int i = 0; i < kD / 16; ++i) {
+                        o[i][nt][e] *= alpha;
+                        o[i][nt][e + 2] *= alpha;
+                    }
+                }
+        }
+#pragma unroll
+        for (int t = 0; t < kKT; ++t) {
+            uint32_t pt[kPT][kNT][2];
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const float r0 = m[nt][0] == -CUDART_INF_F ? 0.0f : m[nt][0], r1 = m[nt][1] == -CUDART_INF_F ? 0.0f : m[nt][1];
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const float p0 = ex2_approx(s[t][nt][2 * hf] - r0), p1 = ex2_approx(s[t][nt][2 * hf + 1] - r1);
+                    l[nt][0] += p0;
+                    l[nt][1] += p1;
+                    float w0 = p0 * u[nt][0] * vs[t][hf], w1 = p1 * u[nt][1] * vs[t][hf];
+#pragma unroll
+                    for (int x = 0; x < kPT; ++x) {
+                        uint32_t h = pack_f16x2(w0, w1);
+                        if (x + 1 < kPT) {
+                            const float2 got = unpack_f16x2(h);
+                            w0 -= got.x;
+                            w1 -= got.y;
+                        }
+                        asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[x][nt][hf]) : "r"(h));
+                    }
+                }
+            }
+            const uint32_t at = v + (t * 16 + row) * kRow;
+#pragma unroll
+            for (int i = 0; i < kD / 32; ++i) {
+                uint32_t f[4];
+                ldsm4t(f, at + (c0 ^ (i << 5)));
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    uint32_t a[4];
+                    codes_f16<kInt8, true>(f[2 * hf], a[0], a[1]);
+                    codes_f16<kInt8, true>(f[2 * hf + 1], a[2], a[3]);
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                        for (int x = kPT - 1; x >= 0; --x) mma_f16(o[2 * i + hf][nt], a, pt[x][nt][0], pt[x][nt][1]);
+                }
+            }
+        }
+    }
+
+    // the maxima and sums of the heads to shared memory
+    __device__ __forceinline__ void put_stats(float* sm_m, float* sm_l, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float sum = l[nt][e];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                if (lane < 4) {
+                    sm_m[nt * 8 + 2 * lane + e] = m[nt][e];
+                    sm_l[nt * 8 + 2 * lane + e] = sum;
+                }
+            }
+    }
+    // o, taken back to the scores' maximum and scaled by f[head], written or added (add = true) to rows of kD floats
+    __device__ __forceinline__ void put(float* buf, const float* f, bool add, int rows, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int hd = nt * 8 + 2 * (lane & 3) + e;
+                if (hd >= rows) continue;
+                const float fr = f[hd], up = m[nt][e] == -CUDART_INF_F ? 0.0f : ex2_approx(mo[nt][e] - m[nt][e] - kBase);
+#pragma unroll
+                for (int i = 0; i < kD / 16; ++i)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        float* y = buf + hd * kD + 16 * i + 2 * (lane >> 2) + hf;
+                        const float x = o[i][nt][e + 2 * hf] * up * fr;
+                        *y = add ? *y + x : x;
+                    }
+            }
+    }
+};
+
+template <int kD, bool kInt8>
+cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
+    if (!bf16) return launch_rows<WarpCoded<float, kD, 1, kInt8>, kD>(p, s);
+    if (p.h / p.h_kv <= 8) return launch_rows<WarpCoded<__nv_bfloat16, kD, 1, kInt8>, kD>(p, s);
+    return launch_rows<WarpCoded<__nv_bfloat16, kD, 2, kInt8>, kD>(p, s);
+}
+
+}  // namespace
+
+size_t coded_attn_workspace(int d) { return line_workspace(d); }
+
+cudaError_t launch_coded_attn(const PagedAttnParams& p, bool bf16, bool int8, cudaStream_t s) {
+    if (p.d == 64) return int8 ? launch_d<64, true>(p, bf16, s) : launch_d<64, false>(p, bf16, s);
+    return int8 ? launch_d<128, true>(p, bf16, s) : launch_d<128, false>(p, bf16, s);
+}
+
+}  // namespace mha

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <cstring>
+#include <type_traits>
 
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -26,6 +27,9 @@ struct Library {
     decltype(&mha_document_spans) document_spans;
     decltype(&mha_attention) attention;
     decltype(&mha_rmsnorm) rmsnorm;
+    decltype(&mha_paged_resize) paged_resize;
+    decltype(&mha_coded_append) coded_append;
+    decltype(&mha_coded_attention) coded_attention;
 } lib;
 
 PyObject *s_native, *s_cuda_stream, *s_causal, *s_q_offset, *s_tensors;
@@ -117,10 +121,12 @@ struct RotaryNote {
     const mha_rotary_t* at;
     int64_t dev;
 };
+template <typename Cache>
 struct CacheNote {
-    const mha_paged_cache_t* at;
-    int64_t B, d, dtype, dev, heads;
+    const Cache* at;
+    int64_t B, d, dtype, dev, heads;     // dtype kCoded: a cache in 8 bits
 };
+constexpr int64_t kCoded = 2;
 struct ScoresNote {
     const mha_scores_t* at;
     int64_t h, dev;     // of the slopes; h = -1: none
@@ -135,6 +141,19 @@ const mha_scores_t* scores_of(const Call& c, PyObject* o, int64_t h) {
     const auto x = native<ScoresNote>(o);
     need(x.h < 0 || (x.h == h && x.dev == c.dev));
     return x.at;
+}
+
+template <typename Cache>
+int64_t kind_of(mha_dtype_t dt) {
+    return std::is_same_v<Cache, mha_coded_cache_t> ? kCoded : static_cast<int64_t>(dt);
+}
+
+int int_value(PyObject* o) {
+    need(PyLong_Check(o));
+    int over = 0;
+    const long n = PyLong_AsLongAndOverflow(o, &over);
+    need(over == 0 && n >= INT32_MIN && n <= INT32_MAX);
+    return static_cast<int>(n);
 }
 
 // Runs `call` without the interpreter's lock (a launch may wait for room in its stream's queue).
@@ -186,14 +205,16 @@ bool rotary(PyObject* const* a) {
 }
 
 // k, v, start, cache, q, q_out, k_out, new_lens, rotary, stream
-bool paged_append(PyObject* const* a) {
+template <typename Cache, typename Entry>
+bool append_by(Entry entry, PyObject* const* a) {
+    need(entry != nullptr);
     Call c;
     const at::Tensor& k = c.first(a[0]);
     need(k.dim() == 4);
     const int B = size_of(k, 0), T = size_of(k, 1), h_kv = size_of(k, 2), d = size_of(k, 3);
     const mha_dtype_t dt = c.code();
-    const auto cache = native<CacheNote>(a[3]);
-    need(cache.B == B && cache.d == d && cache.dtype == dt && cache.dev == c.dev && cache.heads == h_kv);
+    const auto cache = native<CacheNote<Cache>>(a[3]);
+    need(cache.B == B && cache.d == d && cache.dtype == kind_of<Cache>(dt) && cache.dev == c.dev && cache.heads == h_kv);
     const View kv = view(k, B, T, h_kv, d), vv = view(c.of(a[1], c.type), B, T, h_kv, d);
     View qv, qo, ko;
     int h = 0;
@@ -209,21 +230,25 @@ bool paged_append(PyObject* const* a) {
     const mha_rotary_t* r = a[8] != Py_None ? rotary_of(c, a[8]) : nullptr;
     void* s = c.stream(a[9]);
     return unlocked([&] {
-        return lib.paged_append(dt, qv.p, qv.strides(), qo.p, qo.strides(), kv.p, kv.strides(), ko.p, ko.strides(), vv.p,
-                                vv.strides(), B, T, h, h_kv, d, start, new_lens, r, cache.at, s);
+        return entry(dt, qv.p, qv.strides(), qo.p, qo.strides(), kv.p, kv.strides(), ko.p, ko.strides(), vv.p, vv.strides(), B, T,
+                     h, h_kv, d, start, new_lens, r, cache.at, s);
     });
 }
+bool paged_append(PyObject* const* a) { return append_by<mha_paged_cache_t>(lib.paged_append, a); }
+bool coded_append(PyObject* const* a) { return append_by<mha_coded_cache_t>(lib.coded_append, a); }
 
 // q, kv_lens, cache, out, workspace, scores, stream
-bool paged_attention(PyObject* const* a) {
+template <typename Cache, typename Entry>
+bool decode_by(Entry entry, PyObject* const* a) {
+    need(entry != nullptr);
     Call c;
     const at::Tensor& q = c.first(a[0]);
     const at::Tensor& out = c.of(a[3], c.type);
     need(q.dim() == 3 && out.sizes() == q.sizes() && q.stride(2) == 1 && out.stride(2) == 1);
     const int B = size_of(q, 0), h = size_of(q, 1), d = size_of(q, 2);
     const mha_dtype_t dt = c.code();
-    const auto cache = native<CacheNote>(a[2]);
-    need(cache.B == B && cache.d == d && cache.dtype == dt && cache.dev == c.dev);
+    const auto cache = native<CacheNote<Cache>>(a[2]);
+    need(cache.B == B && cache.d == d && cache.dtype == kind_of<Cache>(dt) && cache.dev == c.dev);
     const at::Tensor& ws = Call::plain(a[4]);
     need(ws.get_device() == c.dev && ws.is_contiguous());
     const int32_t* lens = ints(c, a[1], {B});
@@ -232,8 +257,41 @@ bool paged_attention(PyObject* const* a) {
     void *qp = q.mutable_data_ptr(), *op = out.mutable_data_ptr(), *wp = ws.mutable_data_ptr(), *s = c.stream(a[6]);
     const size_t bytes = ws.nbytes();
     return unlocked([&] {
-        return lib.paged_attention(dt, qp, &qs, op, &os, B, h, static_cast<int>(cache.heads), d, lens, scores, cache.at, wp, bytes,
-                                   s);
+        return entry(dt, qp, &qs, op, &os, B, h, static_cast<int>(cache.heads), d, lens, scores, cache.at, wp, bytes, s);
+    });
+}
+bool paged_attention(PyObject* const* a) { return decode_by<mha_paged_cache_t>(lib.paged_attention, a); }
+bool coded_attention(PyObject* const* a) { return decode_by<mha_coded_cache_t>(lib.coded_attention, a); }
+
+// held, want, block_table, page_size, free_pages, free_count, lens, new_lens, slots, stream
+bool paged_resize(PyObject* const* a) {
+    need(lib.paged_resize != nullptr);
+    Call c;
+    const at::Tensor& held = c.first(a[0]);
+    need(held.dim() == 1 && a[1] != Py_None && a[5] != Py_None && a[6] != Py_None);
+    const int B = size_of(held, 0);
+    const int32_t *from = ints(c, a[0], {B}), *want = ints(c, a[1], {B});
+    const at::Tensor& table = c.of(a[2], at::ScalarType::Int);
+    need(table.dim() == 2 && table.size(0) == B && (table.stride(1) == 1 || table.size(1) <= 1));
+    const int max_pages = size_of(table, 1);
+    const at::Tensor& pool = c.of(a[4], at::ScalarType::Int);
+    need(pool.dim() == 1 && pool.is_contiguous());
+    const int n_pages = size_of(pool, 0);
+    int32_t *count = ints(c, a[5], {1}), *lens = ints(c, a[6], {B}), *new_lens = ints(c, a[7], {B});
+    int T = 0;
+    int64_t* slots = nullptr;
+    if (a[8] != Py_None) {
+        const at::Tensor& t = c.of(a[8], at::ScalarType::Long);
+        need(t.dim() == 2 && t.size(0) == B && t.is_contiguous());
+        T = size_of(t, 1);
+        slots = static_cast<int64_t*>(t.mutable_data_ptr());
+    }
+    int32_t *rows = static_cast<int32_t*>(table.mutable_data_ptr()), *stack = static_cast<int32_t*>(pool.mutable_data_ptr());
+    const int64_t stride = table.stride(0);
+    const int page_size = int_value(a[3]);
+    void* s = c.stream(a[9]);
+    return unlocked([&] {
+        return lib.paged_resize(from, want, B, page_size, rows, stride, max_pages, stack, n_pages, count, lens, new_lens, T, slots, s);
     });
 }
 
@@ -259,11 +317,7 @@ struct Held {
 };
 int int_of(PyObject* owner, PyObject* name) {
     const Held v(PyObject_GetAttr(owner, name));
-    need(PyLong_Check(v.o));
-    int over = 0;
-    const long n = PyLong_AsLongAndOverflow(v.o, &over);
-    need(over == 0 && n >= INT32_MIN && n <= INT32_MAX);
-    return static_cast<int>(n);
+    return int_value(v.o);
 }
 
 // q, k, v, out, scores, mask, stream
@@ -353,14 +407,15 @@ bool rmsnorm(PyObject* const* a) {
     });
 }
 
-// The addresses of the six functions, in the order of Library.
+// The addresses of the functions, in the order of Library: all of them, or the first six (the others then decline).
 PyObject* set_library(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    void* at[6];
-    if (n != 6) {
-        PyErr_SetString(PyExc_TypeError, "six addresses");
+    constexpr int kAll = sizeof(Library) / sizeof(void*);
+    void* at[kAll] = {};
+    if (n != 6 && n != kAll) {
+        PyErr_Format(PyExc_TypeError, "six addresses, or %d", kAll);
         return nullptr;
     }
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < n; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         if (at[i] == nullptr) {
             if (PyErr_Occurred() == nullptr) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -381,6 +436,9 @@ PyMethodDef methods[] = {
     MHA_ENTRY(document_spans, 3),
     MHA_ENTRY(attention, 7),
     MHA_ENTRY(rmsnorm, 8),
+    MHA_ENTRY(paged_resize, 10),
+    MHA_ENTRY(coded_append, 10),
+    MHA_ENTRY(coded_attention, 7),
     {"set_library", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&set_library)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

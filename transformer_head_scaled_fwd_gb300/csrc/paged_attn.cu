@@ -33,7 +33,7 @@ template <int kD, int kNT>          // kNT tiles of 8 heads
 struct WarpBf16 {
     using T = __nv_bfloat16;
     using Step = Halves<T, kD>;
-    static constexpr int kRows = 8 * kNT;
+    static constexpr int kRows = 8 * kNT, kBufs = 4;
     static constexpr int kQFloats = 0;      // shared memory for the query rows (they stay in registers)
     static constexpr int kKeys = Step::kKeys;
     static constexpr int kKT = kKeys / 16;
@@ -207,7 +207,7 @@ template <int kD, int kR>
 struct WarpF32 {
     using T = float;
     using Step = Halves<T, kD>;
-    static constexpr int kRows = kR;
+    static constexpr int kRows = kR, kBufs = 4;
     static constexpr int kQFloats = kR * kD;
     static constexpr int kKeys = Step::kKeys;      // 8 or 16
     static constexpr int kLanes = 32 / kKeys;             // lanes that share a key's dot product: 4 or 2
@@ -348,8 +348,7 @@ cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(bool, int, int, int, int d) {
-    const size_t slot = (2 * kMaxRows + kMaxRows * static_cast<size_t>(d)) * sizeof(float);
-    return (kMaxCtas * 2 * slot + kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+    return line_workspace(d);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t s) {

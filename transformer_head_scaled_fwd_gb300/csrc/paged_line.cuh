@@ -59,6 +59,11 @@ struct JoinDesc {
 template <int kD>
 __host__ __device__ constexpr int slot_floats() { return 2 * kMaxRows + kMaxRows * kD; }
 
+inline size_t line_workspace(int d) {
+    const size_t slot = (2 * kMaxRows + kMaxRows * static_cast<size_t>(d)) * sizeof(float);
+    return (kMaxCtas * 2 * slot + kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -357,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     }
 
     const ScoreForm form{p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, p.cap > 0.0f};
-    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * S::kStage);   // 4 x [rows][kD], then the query rows (fp32)
+    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * S::kStage);   // kBufs x [rows][kD], then the query rows (fp32)
     W w;
     bool fresh = true, first_piece = true;
     int piece_blk = at.blk, stage = 0, rows = 0, head0 = 0;
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
             rows = min(group - ht * W::kRows, W::kRows);
             head0 = kh * group + ht * W::kRows;
-            w.start(p, buf + 4 * W::kRows * kD, at.b, head0, rows, lane);
+            w.start(p, buf + W::kBufs * W::kRows * kD, at.b, head0, rows, lane);
             piece_blk = at.blk;
             fresh = false;
         }
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
         const bool unit_done = at.blk + 1 == at.nblk;
         if (unit_done || t + 1 == t1) {
-            // ---- join the warps: scaled sums of warps 4-7 in four buffers, warps 0-3 add theirs, all sum the four
+            // ---- join the warps: the last kBufs put their scaled sums in buffers, the others add theirs, all sum the buffers
             w.put_stats(sh.m[warp], sh.l[warp], lane);
             __syncthreads();
             if (lane < W::kRows) {
@@ -396,18 +401,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 sh.f[warp][lane] = mw == -CUDART_INF_F ? 0.0f : ex2_approx(mw - M);
             }
             __syncwarp();
-            float* own = buf + (warp & 3) * (W::kRows * kD);
-            if (warp >= 4) w.put(own, sh.f[warp], false, rows, lane);
-            __syncthreads();
-            if (warp < 4) w.put(own, sh.f[warp], true, rows, lane);
-            __syncthreads();
+            float* own = buf + warp % W::kBufs * (W::kRows * kD);
+#pragma unroll
+            for (int r = kWarps / W::kBufs - 1; r >= 0; --r) {
+                if (warp / W::kBufs == r) w.put(own, sh.f[warp], r != kWarps / W::kBufs - 1, rows, lane);
+                __syncthreads();
+            }
             const bool whole = unit_done && piece_blk == 0;
             float* slot_m = p.partial + (static_cast<int64_t>(c) * 2 + (first_piece ? 0 : 1)) * kSlot;
             for (int i = threadIdx.x; i < rows * kD; i += kThreads) {
                 const int row = i / kD;
                 float a = 0.0f;
 #pragma unroll
-                for (int s = 0; s < 4; ++s) a += buf[s * (W::kRows * kD) + i];
+                for (int s = 0; s < W::kBufs; ++s) a += buf[s * (W::kRows * kD) + i];
                 if (whole) {
                     float L = 0.0f;
                     for (int s = 0; s < kWarps; ++s) L += sh.l[s][row] * sh.f[s][row];
@@ -510,7 +516,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 template <typename W, int kD>
 cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
-    constexpr int kSmem = kWarps * W::Step::kStages * W::Step::kStage + (4 * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
+    constexpr int kSmem = kWarps * W::Step::kStages * W::Step::kStage + (W::kBufs * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
     static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int dev = 0, sms = 0;

@@ -1,11 +1,7 @@
 // rotary.cu -- rotary positions of queries and keys, and the append of new keys and values to
 // a paged cache on the same pass.
 //
-// Pair (x_0, x_1) of a token at position t turns by t * inv_freq[i]. The angle is formed in half
-// turns as an unevaluated sum of two floats (error-free product by fused multiply-add, after
-// Dekker): t * f in one float is off by up to 2^-25 of its size, 0.03 rad at t = 10^6. Whole turns
-// are removed exactly before the sum is rounded, so cos and sin are good to 2^-22 up to positions of 2^24; beyond,
-// the low part's own roundings (2^-46 of the angle) show: 2^-21 at 2^26, 2^-17.5 at 2^29.
+// Angles: turn.cuh.
 //
 // HBM-bound: every element is read once and written once (keys twice where k_out is asked for). Measured, 4 x 8192
 // tokens appended in bf16: 32 + 8 heads of 128, half of each turned, 872 MB: 134 us, 6.5 TB/s (0.96 of measured copy
@@ -18,29 +14,12 @@
 #include "mha_internal.h"
 #include "ptx_serve.cuh"
 #include "serve.h"
+#include "turn.cuh"
 
 namespace mha {
 namespace {
 
 constexpr int kThreads = 256;
-
-// (cos, sin) of pos * f
-__device__ __forceinline__ float2 turn_of(int pos, float f) {
-    constexpr float kInvPi = 0.318309873342514038f;        // 1 / pi rounded to fp32 ...
-    constexpr float kInvPiLow = 1.28412766334e-8f;         // ... and the rest
-    const float ph = f * kInvPi;
-    const float pl = fmaf(f, kInvPiLow, fmaf(f, kInvPi, -ph));
-    const float th = static_cast<float>(pos);
-    const float tl = static_cast<float>(static_cast<long long>(pos) - static_cast<long long>(th));
-    const float ah = th * ph;
-    float al = fmaf(th, ph, -ah);
-    al = fmaf(th, pl, al);
-    al = fmaf(tl, ph, al);
-    const float r = (ah - 2.0f * rintf(0.5f * ah)) + al;   // the difference is exact
-    float2 cs;
-    sincospif(r, &cs.y, &cs.x);
-    return cs;
-}
 
 // kN elements of a head in one access of kN * sizeof(T) bytes.
 template <int kBytes>

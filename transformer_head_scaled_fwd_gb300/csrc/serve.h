@@ -93,6 +93,46 @@ struct PagedAttnParams {
 size_t paged_attn_workspace(bool bf16, int B, int h, int h_kv, int d);
 cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t s);
 
+// ------------------------------------------------------------ a cache in 8 bits
+size_t coded_attn_workspace(int d);
+cudaError_t launch_coded_attn(const PagedAttnParams& p, bool bf16, bool int8, cudaStream_t s);
+
+struct CodedAppendParams {
+    Strided q, q_out, k, k_out, v;    // q.p, k_out.p may be nullptr
+    PagedView cache;                  // strides in bytes
+    float* k_scales;                  // [n_pages, page_scales]
+    float* v_scales;
+    int64_t page_scales;              // blocks of a page * h_kv
+    FastDiv block;                    // tokens a scale covers
+    const int32_t* start;             // [B]
+    const int32_t* new_lens;          // [B] or nullptr
+    const float* inv_freq;            // [rot / 2]
+    int rot, interleaved;             // rot 0: nothing is turned
+    float scale;
+    int B, T, h, h_kv, d, int8;
+    int* status;
+};
+cudaError_t launch_coded_append(const CodedAppendParams& p, bool bf16, cudaStream_t s);
+
+// ------------------------------------------------------------ pages granted and returned
+struct ResizeParams {
+    const int32_t* held;     // [B]
+    const int32_t* want;     // [B]
+    int32_t* table;
+    int64_t table_stride;
+    int max_pages;
+    int32_t* free_pages;     // [n_pages], the first *free_count are free
+    int32_t* free_count;
+    int n_pages;
+    int32_t* lens;           // [B]
+    int32_t* new_lens;       // [B] or nullptr
+    int64_t* slots;          // [B, T] or nullptr
+    int B, T;
+    FastDiv page, by_t;
+    int* status;
+};
+cudaError_t launch_resize(const ResizeParams& p, cudaStream_t s);
+
 // ------------------------------------------------------------ attention under span masks
 struct SpanAttnParams {
     Strided q, k, v, out;

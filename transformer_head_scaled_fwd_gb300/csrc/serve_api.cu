@@ -115,6 +115,25 @@ mha_status_t check_scores(const mha_scores_t* s, int d_k, float* scale, float* c
     return MHA_OK;
 }
 
+// A cache in 8 bits: the pages' view, and what the scales need.
+mha_status_t check_coded(const mha_coded_cache_t* c, int h_kv, int d_k, mha::PagedView* out, mha::FastDiv* block, int64_t* page_scales) {
+    if (c == nullptr) return fail(MHA_ERR_INVALID_ARG, "the cache must not be NULL");
+    if (d_k != 64 && d_k != 128) return fail(MHA_ERR_UNSUPPORTED, "a cache in 8 bits is implemented for d_k = 64 and 128 (d_k = %d)", d_k);
+    mha_status_t st = check_cache(&c->pages, MHA_BF16, out);
+    if (st != MHA_OK) return st;
+    if (c->code != MHA_CODE_E4M3 && c->code != MHA_CODE_INT8) return fail(MHA_ERR_INVALID_ARG, "unknown code %d", c->code);
+    if (c->block <= 0 || c->pages.page_size % c->block != 0)
+        return fail(MHA_ERR_INVALID_ARG, "block must divide page_size (block=%d, page_size=%d)", c->block, c->pages.page_size);
+    if (c->k_scales == nullptr || c->v_scales == nullptr || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
+        return fail(MHA_ERR_INVALID_ARG, "the scales must not be NULL and be aligned to 4 bytes");
+    if (!aligned(c->pages.k_pages, 16) || !aligned(c->pages.v_pages, 16) || c->pages.page_stride % 16 != 0 ||
+        c->pages.slot_stride % 16 != 0 || c->pages.head_stride % 16 != 0)
+        return fail(MHA_ERR_INVALID_ARG, "the pages and their strides must be aligned to 16 bytes");
+    *block = mha::fast_div(static_cast<uint32_t>(c->block));
+    *page_scales = static_cast<int64_t>(c->pages.page_size / c->block) * h_kv;
+    return MHA_OK;
+}
+
 // heads of all tokens that one launch turns or copies (32-bit CTA numbers)
 constexpr int64_t kMostRows = int64_t(1) << 30;
 
@@ -273,6 +292,124 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
     p.status = mha::device_status();
     if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
     return launched(mha::launch_paged_attn(p, dt == MHA_BF16, as_stream(stream)), "paged attention");
+}
+
+mha_status_t mha_paged_resize(const int32_t* held, const int32_t* want, int B, int page_size, int32_t* block_table,
+                              int64_t table_stride, int max_pages, int32_t* free_pages, int n_pages, int32_t* free_count,
+                              int32_t* lens, int32_t* new_lens, int T, int64_t* slots, void* stream) {
+    if (held == nullptr || want == nullptr || block_table == nullptr || free_pages == nullptr || free_count == nullptr || lens == nullptr)
+        return fail(MHA_ERR_INVALID_ARG, "held, want, block_table, free_pages, free_count and lens must not be NULL");
+    if (B <= 0 || page_size <= 0 || max_pages <= 0 || n_pages <= 0 || (slots != nullptr && T <= 0))
+        return fail(MHA_ERR_INVALID_ARG, "sizes must be positive (B=%d page_size=%d max_pages=%d n_pages=%d T=%d)", B, page_size,
+                    max_pages, n_pages, T);
+    if (table_stride < 0 || (B > 1 && table_stride < max_pages))
+        return fail(MHA_ERR_INVALID_ARG, "rows of the block table must not overlap (stride %lld, max_pages=%d)",
+                    static_cast<long long>(table_stride), max_pages);
+    if (slots != nullptr && static_cast<int64_t>(B) * T > 0x7fffffffll) return fail(MHA_ERR_UNSUPPORTED, "B * T must stay below 2^31");
+    for (const void* x : {static_cast<const void*>(held), static_cast<const void*>(want), static_cast<const void*>(block_table),
+                          static_cast<const void*>(free_pages), static_cast<const void*>(free_count), static_cast<const void*>(lens),
+                          static_cast<const void*>(new_lens)})
+        if (!aligned(x, 4)) return fail(MHA_ERR_INVALID_ARG, "int32 arrays must be aligned to 4 bytes");
+    if (!aligned(slots, 8)) return fail(MHA_ERR_INVALID_ARG, "slots must be aligned to 8 bytes");
+    if (lens == held || lens == want || new_lens == held || new_lens == want || lens == new_lens)
+        return fail(MHA_ERR_INVALID_ARG, "lens and new_lens must be arrays of their own");
+    mha::ResizeParams p{};
+    p.held = held; p.want = want;
+    p.table = block_table; p.table_stride = table_stride; p.max_pages = max_pages;
+    p.free_pages = free_pages; p.free_count = free_count; p.n_pages = n_pages;
+    p.lens = lens; p.new_lens = new_lens; p.slots = slots;
+    p.B = B; p.T = slots != nullptr ? T : 1;
+    p.page = mha::fast_div(static_cast<uint32_t>(page_size));
+    p.by_t = mha::fast_div(static_cast<uint32_t>(p.T));
+    p.status = mha::device_status();
+    if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
+    return launched(mha::launch_resize(p, as_stream(stream)), "paged resize");
+}
+
+mha_status_t mha_coded_append(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides, void* q_out,
+                              const mha_strides_t* q_out_strides, const void* k, const mha_strides_t* k_strides,
+                              void* k_out, const mha_strides_t* k_out_strides, const void* v,
+                              const mha_strides_t* v_strides, int B, int T, int h, int h_kv, int d_k,
+                              const int32_t* start, const int32_t* new_lens, const mha_rotary_t* rotary,
+                              const mha_coded_cache_t* cache, void* stream) {
+    mha_status_t st;
+    if ((st = check_dtype(dt)) != MHA_OK || (st = check_bt(B, T, d_k)) != MHA_OK) return st;
+    if (h_kv <= 0 || (q != nullptr && h <= 0))
+        return fail(MHA_ERR_INVALID_ARG, "heads must be positive (h=%d h_kv=%d)", h, h_kv);
+    if (static_cast<int64_t>(B) * T * ((q != nullptr ? static_cast<int64_t>(h) : 0) + 2 * static_cast<int64_t>(h_kv)) > kMostRows)
+        return fail(MHA_ERR_UNSUPPORTED, "B * T * (h + 2 h_kv) must stay below 2^30");
+    if (start == nullptr) return fail(MHA_ERR_INVALID_ARG, "start must not be NULL");
+    if (rotary != nullptr && (st = check_rotary(rotary, d_k)) != MHA_OK) return st;
+    mha::CodedAppendParams p{};
+    if ((st = check_coded(cache, h_kv, d_k, &p.cache, &p.block, &p.page_scales)) != MHA_OK) return st;
+    if (cache->block > 256) return fail(MHA_ERR_UNSUPPORTED, "blocks of up to 256 tokens are appended to (block = %d)", cache->block);
+    struct { const void* p; const mha_strides_t* st; const char* name; mha::Strided* to; } tensors[] = {
+        {k, k_strides, "k", &p.k}, {v, v_strides, "v", &p.v}, {k_out, k_out_strides, "k_out", &p.k_out},
+        {q, q_strides, "q", &p.q}, {q != nullptr ? q_out : nullptr, q_out_strides, "q_out", &p.q_out}};
+    const int64_t chunk = 16 / static_cast<int64_t>(elem(dt));
+    for (auto& x : tensors) {
+        const bool needed = x.to == &p.k || x.to == &p.v || (x.to == &p.q_out && q != nullptr);
+        if (x.p == nullptr && !needed) continue;
+        if ((st = view(x.p, x.st, elem(dt), x.name, x.to)) != MHA_OK) return st;
+        // a dimension of one element has no stride to speak of
+        const int heads = x.to == &p.q || x.to == &p.q_out ? h : h_kv;
+        if (B == 1) x.to->b = 0;
+        if (T == 1) x.to->l = 0;
+        if (heads == 1) x.to->h = 0;
+        if (!aligned(x.p, 16) || x.to->b % chunk != 0 || x.to->l % chunk != 0 || x.to->h % chunk != 0)
+            return fail(MHA_ERR_INVALID_ARG, "%s and its strides must be aligned to 16 bytes", x.name);
+    }
+    if (rotary != nullptr) {
+        p.inv_freq = rotary->inv_freq;
+        p.rot = rotary->rot_dim;
+        p.interleaved = rotary->interleaved;
+        p.scale = rotary->scale;
+    }
+    p.k_scales = cache->k_scales; p.v_scales = cache->v_scales;
+    p.start = start;
+    p.new_lens = new_lens;
+    p.B = B; p.T = T; p.h = q != nullptr ? h : 0; p.h_kv = h_kv; p.d = d_k;
+    p.int8 = cache->code == MHA_CODE_INT8;
+    p.status = mha::device_status();
+    if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
+    return launched(mha::launch_coded_append(p, dt == MHA_BF16, as_stream(stream)), "coded append");
+}
+
+size_t mha_coded_attention_workspace_size(mha_dtype_t dt, int B, int h, int h_kv, int d_k) {
+    if ((dt != MHA_F32 && dt != MHA_BF16) || B <= 0 || h <= 0 || h_kv <= 0 || h % h_kv != 0 || (d_k != 64 && d_k != 128))
+        return 0;
+    return mha::coded_attn_workspace(d_k);
+}
+
+mha_status_t mha_coded_attention(mha_dtype_t dt, const void* q, const mha_strides_t* q_strides, void* out,
+                                 const mha_strides_t* out_strides, int B, int h, int h_kv, int d_k,
+                                 const int32_t* kv_lens, const mha_scores_t* scores, const mha_coded_cache_t* cache,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    mha_status_t st;
+    if ((st = check_dtype(dt)) != MHA_OK) return st;
+    if (B <= 0) return fail(MHA_ERR_INVALID_ARG, "B must be positive (got %d)", B);
+    if ((st = check_heads(h, h_kv)) != MHA_OK) return st;
+    if (B > 65535 || h > 65535) return fail(MHA_ERR_UNSUPPORTED, "B and h up to 65535 (got %d, %d)", B, h);
+    if (kv_lens == nullptr) return fail(MHA_ERR_INVALID_ARG, "kv_lens must not be NULL");
+    mha::PagedAttnParams p{};
+    if ((st = check_coded(cache, h_kv, d_k, &p.cache, &p.scale_block, &p.page_scales)) != MHA_OK) return st;
+    if ((st = check_scores(scores, d_k, &p.scale, &p.cap, &p.slopes)) != MHA_OK) return st;
+    mha::Strided qv, ov;
+    if ((st = view(q, q_strides, elem(dt), "q", &qv)) != MHA_OK) return st;
+    if ((st = view(out, out_strides, elem(dt), "out", &ov)) != MHA_OK) return st;
+    const size_t need = mha_coded_attention_workspace_size(dt, B, h, h_kv, d_k);
+    if (workspace == nullptr || !aligned(workspace, 256))
+        return fail(MHA_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    if (workspace_bytes < need) return fail(MHA_ERR_INVALID_ARG, "workspace too small: %zu < %zu", workspace_bytes, need);
+    p.q = qv.p; p.q_b = qv.b; p.q_h = qv.h;
+    p.out = ov.p; p.o_b = ov.b; p.o_h = ov.h;
+    p.kv_lens = kv_lens;
+    p.k_scales = cache->k_scales; p.v_scales = cache->v_scales;
+    p.B = B; p.h = h; p.h_kv = h_kv; p.d = d_k;
+    p.partial = static_cast<float*>(workspace);
+    p.status = mha::device_status();
+    if (p.status == nullptr) return fail(MHA_ERR_CUDA, "device status word unavailable");
+    return launched(mha::launch_coded_attn(p, dt == MHA_BF16, cache->code == MHA_CODE_INT8, as_stream(stream)), "coded attention");
 }
 
 mha_status_t mha_document_spans(const int32_t* doc_ids, int B, int L, int32_t* spans, void* stream) {
