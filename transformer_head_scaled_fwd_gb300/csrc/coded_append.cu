@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
         const long long first = (blk0 + i) * block;        // position
         BlockInfo x{-1, -1};
         const long long last = min(first + block, start + t1) - 1;
-        if (last >= start + t0) {
+        if (last >= max(first, start + t0)) {
             int page = -1, pg = 0;
             // a block lies in one page, so one look-up does for all its positions
             if (first >= 0 && last <= 0x7fffffffll) {
