@@ -7,7 +7,7 @@
 // HBM-bound: 2 d_k bytes a position and key head, half of a bf16 cache, so the same loads feed twice the keys and the
 // instructions a key count twice as much. Codes become fp16 in registers, which is exact (e4m3 is a subset of fp16, int8 is
 // below 2^8), and the products are fp16 matrix instructions on them. A query row is scaled by a power of two to below 2^15 and
-// enters as one fp16 number an element (bf16: exact down to 2^-29 of the row's largest) or as three (fp32).
+// enters as one fp16 number an element (bf16: exact down to 2^-29 of the row's largest) or as two (fp32: to 2^-22).
 //
 // Scales: ks multiplies a score after its product. vs belongs to a weight, p_j vs_j, whose size is not bounded by that of
 // p_j, and fp16 has no range to spare: the weights have a running maximum of their own, over s_j + log2 of vs_j's power of two,
@@ -61,44 +61,65 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t& a, uint32_t& b) 
 __device__ __forceinline__ float exponent_of(float s) {
     return static_cast<float>(max(static_cast<int>((__float_as_uint(s) >> 23) & 0xffu) - 127, -110));
 }
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
 
 // As in paged_attn.cu, both products are taken transposed: S^T = K q^T (16 keys x d_k times d_k x 8 heads) and
 // o^T = V^T P^T (16 features x 16 keys times 16 keys x 8 heads). An operand's 16-bit elements are made from bytes that lie
 // side by side, so the feature that a row or column of a product stands for is not its number: for K, the k of lane t of
 // four are features 4 t .. 4 t + 3 (q is loaded to match); for V, loaded transposed in units of two bytes, rows g and
 // g + 8 are features 2 g and 2 g + 1.
-template <typename T_, int kD, int kNT, bool kInt8>
+//
+// A row of 128 bytes is a key of d_k = 128, or (kHeads = 2) the same position of two neighbouring key heads of 64, whose query heads
+// are the unit's two tiles: lines of memory are 128 bytes, and with a head of 64 bytes a unit each line came from HBM twice
+// (16 x 8192, 16 heads of 64: 537 MB read for 268).
+template <typename T_, int kD, int kHeads, int kNT, bool kInt8>      // kNT tiles of 8 query heads a key head
 struct WarpCoded {
     using T = T_;
-    using Step = StepOf<kD, 1, 32, kD == 128 ? 3 : 6, true>;
-    static constexpr int kRows = 8 * kNT;
-    static constexpr int kBufs = kNT * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
+    static constexpr int kRow = kD * kHeads;
+    using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads>;
+    static constexpr int kTiles = kNT * kHeads;
+    static_assert(kHeads == 1 || kNT == 1, "one tile for each of two key heads");
+    static constexpr int kRows = 8 * kTiles;
+    static constexpr int kBufs = kTiles * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
     static constexpr int kQFloats = 0;
     static constexpr int kKT = Step::kKeys / 16;
     static constexpr bool kWide = sizeof(T) == 4;
-    static constexpr int kQT = kWide ? 3 : 1;       // fp16 terms of q
+    static constexpr int kQT = kWide ? 2 : 1;       // fp16 terms of q
     static constexpr int kPT = kWide ? 2 : 1;       // and of a weight
-    uint32_t q[kQT][kD / 16][kNT][2];
-    float o[kD / 16][kNT][4];       // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
+    static constexpr float kMost = 32768.0f;        // largest weight: 2^(kGrow + 1 + kBase)
+    uint32_t q[kQT][kD / 16][kTiles][2];
+    float o[kRow / 16][kNT][4];     // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
     // of those two heads: maximum of the scores, and of score + scale's exponent; 2^(m - mo + kBase); this lane's share of the
-    // sum; the bias' slope; what takes a product back to q's size
-    float m[kNT][2], mo[kNT][2], u[kNT][2], l[kNT][2], slope[kNT][2], back[kNT][2];
+    // sum; the bias' slope; what takes a product to a score
+    float m[kTiles][2], mo[kTiles][2], u[kTiles][2], l[kTiles][2], slope[kTiles][2], in[kTiles][2];
+    bool biased;
+    int each;                       // query heads of a key head, kHeads = 2
 
-    static __device__ __forceinline__ int swizzle(int row) { return kD == 128 ? row & 7 : (row >> 1) & 3; }
+    static __device__ __forceinline__ int swizzle(int row) { return kRow == 128 ? row & 7 : (row >> 1) & 3; }
+    // the unit's row of column `col` of a tile, and whether it is one
+    __device__ __forceinline__ int row_of(int nt, int col) const { return kHeads == 2 ? nt * each + col : nt * 8 + col; }
+    __device__ __forceinline__ bool is_row(int nt, int col, int rows) const { return kHeads == 2 ? col < each : nt * 8 + col < rows; }
 
     __device__ __forceinline__ void start(const PagedAttnParams& p, float*, int b, int head0, int rows, int lane) {
+        each = rows / 2;
+        biased = p.slopes != nullptr;
         const T* base = static_cast<const T*>(p.q) + b * p.q_b + head0 * p.q_h;
+        const float form_in = p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e;
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt) {
-            const int row = nt * 8 + (lane >> 2);      // operand column: head lane / 4
-            const T* x = base + row * p.q_h + 4 * (lane & 3);
+        for (int nt = 0; nt < kTiles; ++nt) {
+            const bool mine = is_row(nt, lane >> 2, rows);      // operand column: head lane / 4
+            const T* x = base + row_of(nt, lane >> 2) * p.q_h + 4 * (lane & 3);
             float f[kD / 16][4];
             float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    f[k][e] = row < rows ? load_f(x + 16 * k + e) : 0.0f;
+                    f[k][e] = mine ? load_f(x + 16 * k + e) : 0.0f;
                     top = fmaxf(top, fabsf(f[k][e]));
                 }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -121,47 +142,48 @@ struct WarpCoded {
                     }
                 }
 #pragma unroll
-            for (int k = 0; k < kD / 16; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[k][nt][e] = 0.0f;
-#pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int col = 2 * (lane & 3) + e, hd = nt * 8 + col;
+                const int col = 2 * (lane & 3) + e;
                 const int of_head = __shfl_sync(0xffffffffu, shift, 4 * col);
-                back[nt][e] = __uint_as_float(static_cast<uint32_t>(127 - of_head) << 23);
-                slope[nt][e] = p.slopes != nullptr && hd < rows ? p.slopes[head0 + hd] * kLog2e : 0.0f;
+                in[nt][e] = form_in * __uint_as_float(static_cast<uint32_t>(127 - of_head) << 23);
+                slope[nt][e] = biased && is_row(nt, col, rows) ? p.slopes[head0 + row_of(nt, col)] * kLog2e : 0.0f;
                 m[nt][e] = mo[nt][e] = -CUDART_INF_F;
                 u[nt][e] = l[nt][e] = 0.0f;
             }
         }
+#pragma unroll
+        for (int i = 0; i < kRow / 16; ++i)
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.0f;
     }
 
     // keys key0 .. key0 + 31 in shared memory at k, v, their scales behind v; live: bit i: key0 + i counts
     __device__ __forceinline__ void step(uint32_t k, uint32_t v, int key0, uint32_t live, int n, const ScoreForm& form,
                                          int rows, int lane) {
-        constexpr int kRow = Step::kRow;
         const int r8 = lane & 7, mi = lane >> 3, g = lane >> 2;
         const uint32_t row = (mi & 1) * 8 + r8;
         const uint32_t c0 = static_cast<uint32_t>(((mi >> 1) ^ swizzle(r8)) << 4);
-        float ks[kKT][2], vs[kKT][2];
+        // key 16 t + 8 hf + g of the lane
+        float ks[kHeads][kKT][2], vs[kHeads][kKT][2];
 #pragma unroll
-        for (int t = 0; t < kKT; ++t)
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t a = v + Step::kBytes + 4 * (t * 16 + 8 * hf + g);
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(ks[t][hf]) : "r"(a));
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(vs[t][hf]) : "r"(a + 4 * Step::kKeys));
-            }
-        float s[kKT][kNT][4];
+        for (int i = 0; i < kHeads; ++i) {
+            const uint32_t a = v + Step::kBytes + 128 * i + 16 * g;
+            const float4 x = lds4(a), y = lds4(a + 128 * kHeads);
+            ks[i][0][0] = x.x; ks[i][0][1] = x.y; ks[i][1][0] = x.z; ks[i][1][1] = x.w;
+            vs[i][0][0] = y.x; vs[i][0][1] = y.y; vs[i][1][0] = y.z; vs[i][1][1] = y.w;
+        }
+        float s[kKT][kTiles][4];
 #pragma unroll
         for (int t = 0; t < kKT; ++t) {
             const uint32_t at = k + (t * 16 + row) * kRow;
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < kD / 32; ++kk) {
+            for (int kk = 0; kk < kRow / 32; ++kk) {
                 uint32_t f[4];
                 ldsm4(f, at + (c0 ^ (kk << 5)));
 #pragma unroll
@@ -169,41 +191,85 @@ struct WarpCoded {
                     uint32_t a[4];
                     codes_f16<kInt8, false>(f[2 * hf], a[0], a[2]);
                     codes_f16<kInt8, false>(f[2 * hf + 1], a[1], a[3]);
+                    const int i = (2 * kk + hf) % (kD / 16), head = (2 * kk + hf) / (kD / 16);
 #pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt)
+                    for (int nt = head * kNT; nt < (head + 1) * kNT; ++nt)
 #pragma unroll
-                        for (int x = kQT - 1; x >= 0; --x) mma_f16(s[t][nt], a, q[x][2 * kk + hf][nt][0], q[x][2 * kk + hf][nt][1]);
+                        for (int x = kQT - 1; x >= 0; --x) mma_f16(s[t][nt], a, q[x][i][nt][0], q[x][i][nt][1]);
                 }
             }
         }
-        bool more = false;
 #pragma unroll
         for (int t = 0; t < kKT; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = t * 16 + g + 8 * (e >> 1);
-                const bool ok = (live >> i) & 1u;
-                const float away = static_cast<float>(n - 1 - key0 - i);
-                const float ev = exponent_of(vs[t][e >> 1]);
+            for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-                    const float dot = s[t][nt][e] * (ks[t][e >> 1] * back[nt][e & 1]);
-                    s[t][nt][e] = ok ? form.of<kWide>(dot, slope[nt][e & 1], away) : -CUDART_INF_F;
-                    more |= s[t][nt][e] > m[nt][e & 1] + kGrow || s[t][nt][e] + ev > mo[nt][e & 1] + kGrow;
+                for (int e = 0; e < 4; ++e) s[t][nt][e] *= ks[nt / kNT][t][e >> 1] * in[nt][e & 1];
+        if (form.capped) {
+#pragma unroll
+            for (int t = 0; t < kKT; ++t)
+#pragma unroll
+                for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        s[t][nt][e] = kWide ? form.top * tanhf(s[t][nt][e]) : capped_score(s[t][nt][e], form.top);
+        }
+        if (biased) {
+#pragma unroll
+            for (int t = 0; t < kKT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float away = static_cast<float>(n - 1 - key0 - t * 16 - 8 * (e >> 1) - g);
+#pragma unroll
+                    for (int nt = 0; nt < kTiles; ++nt) s[t][nt][e] = fmaf(-slope[nt][e & 1], away, s[t][nt][e]);
                 }
-            }
-        // The maxima move only when one is passed by kGrow (the first keys always do that): a weight stays below
-        // 2^(kGrow + 1 + kBase) = 2^15, and nothing is rescaled in between.
-        if (__any_sync(0xffffffffu, more)) {
+        }
+        if (live != 0xffffffffu) {
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int t = 0; t < kKT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (!((live >> (t * 16 + 8 * (e >> 1) + g)) & 1u)) {
+#pragma unroll
+                        for (int nt = 0; nt < kTiles; ++nt) s[t][nt][e] = -CUDART_INF_F;
+                    }
+        }
+        float w[kKT][kTiles][4], sum[kTiles][2];
+        auto weigh = [&](float& most_p, float& most_w) {
+            most_p = most_w = 0.0f;
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt) {
+                sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+                for (int t = 0; t < kKT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float p0 = ex2_approx(s[t][nt][e] - m[nt][0]), p1 = ex2_approx(s[t][nt][e + 1] - m[nt][1]);
+                        const float scale = vs[nt / kNT][t][e >> 1];
+                        sum[nt][0] += p0;
+                        sum[nt][1] += p1;
+                        w[t][nt][e] = p0 * u[nt][0] * scale;           // u * scale may be beyond fp32 where p is 0
+                        w[t][nt][e + 1] = p1 * u[nt][1] * scale;
+                        most_p = fmax3(most_p, p0, p1);
+                        most_w = fmax3(most_w, w[t][nt][e], w[t][nt][e + 1]);
+                    }
+            }
+        };
+        // The maxima move only when a weight passes what they allow by 2^kGrow (the first keys always do that: theirs are infinite);
+        // nothing is rescaled in between.
+        float most_p, most_w;
+        weigh(most_p, most_w);
+        if (__any_sync(0xffffffffu, most_p > 256.0f || most_w > kMost)) {
+            static_assert(kGrow == 8.0f && kBase == 6.0f, "the bounds above");
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float top = m[nt][e], most = mo[nt][e];
 #pragma unroll
                     for (int t = 0; t < kKT; ++t) {
                         top = fmax3(top, s[t][nt][e], s[t][nt][e + 2]);
-                        most = fmax3(most, s[t][nt][e] + exponent_of(vs[t][0]), s[t][nt][e + 2] + exponent_of(vs[t][1]));
+                        most = fmax3(most, s[t][nt][e] + exponent_of(vs[nt / kNT][t][0]), s[t][nt][e + 2] + exponent_of(vs[nt / kNT][t][1]));
                     }
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
@@ -216,25 +282,28 @@ struct WarpCoded {
                     m[nt][e] = top;
                     mo[nt][e] = most;
                     u[nt][e] = top == -CUDART_INF_F ? 0.0f : ex2_approx(top - most + kBase);
+                    // the tile's accumulators
 #pragma unroll
                     for (int i = 0; i < kD / 16; ++i) {
-                        o[i][nt][e] *= alpha;
-                        o[i][nt][e + 2] *= alpha;
+                        o[nt / kNT * (kD / 16) + i][nt % kNT][e] *= alpha;
+                        o[nt / kNT * (kD / 16) + i][nt % kNT][e + 2] *= alpha;
                     }
                 }
+            weigh(most_p, most_w);
+        }
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt) {
+            l[nt][0] += sum[nt][0];
+            l[nt][1] += sum[nt][1];
         }
 #pragma unroll
         for (int t = 0; t < kKT; ++t) {
-            uint32_t pt[kPT][kNT][2];
+            uint32_t pt[kPT][kTiles][2];
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt) {
-                const float r0 = m[nt][0] == -CUDART_INF_F ? 0.0f : m[nt][0], r1 = m[nt][1] == -CUDART_INF_F ? 0.0f : m[nt][1];
+            for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const float p0 = ex2_approx(s[t][nt][2 * hf] - r0), p1 = ex2_approx(s[t][nt][2 * hf + 1] - r1);
-                    l[nt][0] += p0;
-                    l[nt][1] += p1;
-                    float w0 = p0 * u[nt][0] * vs[t][hf], w1 = p1 * u[nt][1] * vs[t][hf];
+                    float w0 = w[t][nt][2 * hf], w1 = w[t][nt][2 * hf + 1];
 #pragma unroll
                     for (int x = 0; x < kPT; ++x) {
                         uint32_t h = pack_f16x2(w0, w1);
@@ -246,10 +315,9 @@ struct WarpCoded {
                         asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[x][nt][hf]) : "r"(h));
                     }
                 }
-            }
             const uint32_t at = v + (t * 16 + row) * kRow;
 #pragma unroll
-            for (int i = 0; i < kD / 32; ++i) {
+            for (int i = 0; i < kRow / 32; ++i) {
                 uint32_t f[4];
                 ldsm4t(f, at + (c0 ^ (i << 5)));
 #pragma unroll
@@ -257,10 +325,11 @@ struct WarpCoded {
                     uint32_t a[4];
                     codes_f16<kInt8, true>(f[2 * hf], a[0], a[1]);
                     codes_f16<kInt8, true>(f[2 * hf + 1], a[2], a[3]);
+                    const int head = (2 * i + hf) / (kD / 16);
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                        for (int x = kPT - 1; x >= 0; --x) mma_f16(o[2 * i + hf][nt], a, pt[x][nt][0], pt[x][nt][1]);
+                        for (int x = kPT - 1; x >= 0; --x) mma_f16(o[2 * i + hf][nt], a, pt[x][head * kNT + nt][0], pt[x][head * kNT + nt][1]);
                 }
             }
         }
@@ -269,44 +338,58 @@ struct WarpCoded {
     // the maxima and sums of the heads to shared memory
     __device__ __forceinline__ void put_stats(float* sm_m, float* sm_l, int lane) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 float sum = l[nt][e];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                if (lane < 4) {
-                    sm_m[nt * 8 + 2 * lane + e] = m[nt][e];
-                    sm_l[nt * 8 + 2 * lane + e] = sum;
+                const int col = 2 * lane + e;
+                if (lane < 4 && (kHeads == 1 || col < each)) {
+                    sm_m[row_of(nt, col)] = m[nt][e];
+                    sm_l[row_of(nt, col)] = sum;
                 }
             }
     }
     // o, taken back to the scores' maximum and scaled by f[head], written or added (add = true) to rows of kD floats
     __device__ __forceinline__ void put(float* buf, const float* f, bool add, int rows, int lane) {
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int hd = nt * 8 + 2 * (lane & 3) + e;
-                if (hd >= rows) continue;
+                const int col = 2 * (lane & 3) + e, hd = row_of(nt, col);
+                if (!is_row(nt, col, rows)) continue;
                 const float fr = f[hd], up = m[nt][e] == -CUDART_INF_F ? 0.0f : ex2_approx(mo[nt][e] - m[nt][e] - kBase);
 #pragma unroll
                 for (int i = 0; i < kD / 16; ++i)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         float* y = buf + hd * kD + 16 * i + 2 * (lane >> 2) + hf;
-                        const float x = o[i][nt][e + 2 * hf] * up * fr;
+                        const float x = o[nt / kNT * (kD / 16) + i][nt % kNT][e + 2 * hf] * up * fr;
                         *y = add ? *y + x : x;
                     }
             }
     }
 };
 
-template <int kD, bool kInt8>
-cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
-    if (!bf16) return launch_rows<WarpCoded<float, kD, 1, kInt8>, kD>(p, s);
-    if (p.h / p.h_kv <= 8) return launch_rows<WarpCoded<__nv_bfloat16, kD, 1, kInt8>, kD>(p, s);
-    return launch_rows<WarpCoded<__nv_bfloat16, kD, 2, kInt8>, kD>(p, s);
+template <typename T, bool kInt8>
+cudaError_t launch_t(PagedAttnParams p, cudaStream_t s) {
+    const int group = p.h / p.h_kv;
+    constexpr bool kBf16 = sizeof(T) == 2;
+    if (p.d == 128) {
+        if constexpr (kBf16)
+            if (group > 8) return launch_rows<WarpCoded<T, 128, 1, 2, kInt8>, 128>(p, s);
+        return launch_rows<WarpCoded<T, 128, 1, 1, kInt8>, 128>(p, s);
+    }
+    // heads of 64 that lie side by side go two at a time
+    if (group <= 8 && p.h_kv % 2 == 0 && p.cache.head_stride == 64) {
+        p.h_kv /= 2;
+        p.cache.head_stride = 128;
+        return launch_rows<WarpCoded<T, 64, 2, 1, kInt8>, 64>(p, s);
+    }
+    if constexpr (kBf16)
+        if (group > 8) return launch_rows<WarpCoded<T, 64, 1, 2, kInt8>, 64>(p, s);
+    return launch_rows<WarpCoded<T, 64, 1, 1, kInt8>, 64>(p, s);
 }
 
 }  // namespace
@@ -314,8 +397,8 @@ cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
 size_t coded_attn_workspace(int d) { return line_workspace(d); }
 
 cudaError_t launch_coded_attn(const PagedAttnParams& p, bool bf16, bool int8, cudaStream_t s) {
-    if (p.d == 64) return int8 ? launch_d<64, true>(p, bf16, s) : launch_d<64, false>(p, bf16, s);
-    return int8 ? launch_d<128, true>(p, bf16, s) : launch_d<128, false>(p, bf16, s);
+    if (bf16) return int8 ? launch_t<__nv_bfloat16, true>(p, s) : launch_t<__nv_bfloat16, false>(p, s);
+    return int8 ? launch_t<float, true>(p, s) : launch_t<float, false>(p, s);
 }
 
 }  // namespace mha

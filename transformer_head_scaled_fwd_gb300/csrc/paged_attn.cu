@@ -22,7 +22,7 @@ namespace {
 
 // 4 KB of keys, 4 KB of values a step
 template <typename T, int kD>
-using Halves = StepOf<kD, static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, false>;
+using Halves = StepOf<kD * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, 0>;
 
 // ------------------------------------------------------------ a warp's heads: bf16, matrix instructions
 // Both products are taken transposed, so that the long sides are the matrix instruction's 16 rows and the

@@ -36,16 +36,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWholeBlocks = 4;
 constexpr float kGrow = 8.0f;           // log2 units the maximum may grow before o and l are rescaled
 
-// One step of a warp: kKeys keys, their kBytes bytes of keys and as many of values, elements of kElem bytes; kScales: a
-// float a key besides, for each of the two. Up to 32 keys: lane i looks up key i.
-template <int kD, int kElem_, int kKeys_, int kStages_, bool kScales_>
+// One step of a warp: kKeys keys, their kBytes bytes of keys and as many of values, elements of kElem bytes. kScales: the
+// scales of kScales neighbouring key heads besides, [keys / values][head][key % 8][key / 8]. Up to 32 keys: lane i looks up key i.
+template <int kRow_, int kElem_, int kKeys_, int kStages_, int kScales_>
 struct StepOf {
-    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_;
-    static constexpr bool kScales = kScales_;
-    static constexpr int kRow = kD * kElem;                 // bytes of a key
+    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_, kScales = kScales_;
+    static constexpr int kRow = kRow_;                      // bytes of a key
     static constexpr int kBytes = kKeys * kRow;
     static constexpr int kChunks = kRow / 16;
-    static constexpr int kStage = 2 * kBytes + (kScales ? 2 * 4 * kKeys : 0);
+    static constexpr int kStage = 2 * kBytes + 2 * 4 * kKeys * kScales;
     static_assert(kKeys <= 32 && kChunks <= 32 && kBytes % 512 == 0, "a step of a warp");
 };
 
@@ -341,12 +340,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 cp_async16(dst, src, on);
                 cp_async16(dst + S::kBytes, src + v_minus_k, on);
             }
-            if constexpr (S::kScales) {     // of the lane's key
-                const int64_t at = ok ? static_cast<int64_t>(page) * p.page_scales + p.scale_block.div(slot) * p.h_kv + kvh : 0;
-                const uint32_t to = stage0 + stage * S::kStage + 2 * S::kBytes + 4 * lane;
-                if (lane < S::kKeys) {
-                    cp_async4(to, p.k_scales + at, ok);
-                    cp_async4(to + 4 * S::kKeys, p.v_scales + at, ok);
+            if constexpr (S::kScales > 0) {     // of the lane's key
+                static_assert(S::kKeys == 32, "a key a lane");
+                const int64_t at = ok ? static_cast<int64_t>(page) * p.page_scales + (p.scale_block.div(slot) * p.h_kv + kvh) * S::kScales : 0;
+                const uint32_t to = stage0 + stage * S::kStage + 2 * S::kBytes + 16 * (lane & 7) + 4 * (lane >> 3);
+#pragma unroll
+                for (int i = 0; i < S::kScales; ++i) {
+                    cp_async4(to + 128 * i, p.k_scales + at + i, ok);
+                    cp_async4(to + 128 * (S::kScales + i), p.v_scales + at + i, ok);
                 }
             }
         }
