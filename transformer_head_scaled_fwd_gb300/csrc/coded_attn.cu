@@ -80,7 +80,7 @@ template <typename T_, int kD, int kHeads, int kNT, bool kInt8>      // kNT tile
 struct WarpCoded {
     using T = T_;
     static constexpr int kRow = kD * kHeads;
-    using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads>;
+    using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads, 8, 2>;
     static constexpr int kTiles = kNT * kHeads;
     static_assert(kHeads == 1 || kNT == 1, "one tile for each of two key heads");
     static constexpr int kRows = 8 * kTiles;

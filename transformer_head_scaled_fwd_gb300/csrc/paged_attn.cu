@@ -22,7 +22,7 @@ namespace {
 
 // 4 KB of keys, 4 KB of values a step
 template <typename T, int kD>
-using Halves = StepOf<kD * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, 0>;
+using Halves = StepOf<kD * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, 0, 8, 0>;
 
 // ------------------------------------------------------------ a warp's heads: bf16, matrix instructions
 // Both products are taken transposed, so that the long sides are the matrix instruction's 16 rows and the
@@ -223,7 +223,7 @@ struct WarpF32 {
 
     __device__ __forceinline__ void start(const PagedAttnParams& p, float* shared_q, int b, int head0, int rows, int) {
         const float* x = static_cast<const float*>(p.q) + b * p.q_b + head0 * p.q_h;
-        for (int i = threadIdx.x; i < kR * kD; i += kThreads)
+        for (int i = threadIdx.x; i < kR * kD; i += Step::kThreads)
             shared_q[i] = i < rows * kD ? x[(i / kD) * p.q_h + i % kD] : 0.0f;
         __syncthreads();      // the last unit's readers are behind the barriers of its end
         q = smem_u32(shared_q);

@@ -28,8 +28,6 @@
 namespace mha {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kMaxCtas = 192;           // slots of the workspace
 constexpr int kMaxRows = 16;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -38,9 +36,12 @@ constexpr float kGrow = 8.0f;           // log2 units the maximum may grow befor
 
 // One step of a warp: kKeys keys, their kBytes bytes of keys and as many of values, elements of kElem bytes. kScales: the
 // scales of kScales neighbouring key heads besides, [keys / values][head][key % 8][key / 8]. Up to 32 keys: lane i looks up key i.
-template <int kRow_, int kElem_, int kKeys_, int kStages_, int kScales_>
+// A CTA has kWarps warps, each with kStages steps in shared memory.
+// A unit's end costs as much as kTail blocks.
+template <int kRow_, int kElem_, int kKeys_, int kStages_, int kScales_, int kWarps_, int kTail_>
 struct StepOf {
-    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_, kScales = kScales_;
+    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_, kScales = kScales_, kWarps = kWarps_, kTail = kTail_;
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRow = kRow_;                      // bytes of a key
     static constexpr int kBytes = kKeys * kRow;
     static constexpr int kChunks = kRow / 16;
@@ -96,6 +97,7 @@ struct Cursor {
     int n;              // the sequence's length
 };
 
+template <int kTail>
 struct Lens {
     const int32_t* kv_lens;
     int64_t room;
@@ -105,6 +107,8 @@ struct Lens {
         return static_cast<int>(min(static_cast<int64_t>(n), room));
     }
     __device__ __forceinline__ int blocks(int n) const { return n / block + (n % block != 0); }
+    // of the line: a unit's blocks, and kTail for its end
+    __device__ __forceinline__ int places(int n) const { return n > 0 ? blocks(n) + kTail : 0; }
 };
 
 struct Found {
@@ -112,6 +116,7 @@ struct Found {
     int b;
 };
 
+template <int kWarps>
 struct Shared {
     float m[kWarps][kMaxRows], l[kWarps][kMaxRows], f[kWarps][kMaxRows];
     long long scan[kWarps];
@@ -135,27 +140,27 @@ __device__ __forceinline__ long long warp_scan64(long long v, int lane) {
 }
 
 template <typename W, int kD>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
     using T = typename W::T;
     using S = typename W::Step;
     constexpr int kKeys = S::kKeys;
-    constexpr int kSlot = slot_floats<kD>(), kStages = S::kStages;
+    constexpr int kSlot = slot_floats<kD>(), kStages = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads, kTail = S::kTail;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ Shared sh;
+    __shared__ Shared<kWarps> sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.h / p.h_kv;
     const int head_tiles = (group + W::kRows - 1) / W::kRows;
     const int units = p.h_kv * head_tiles;
     // positions stay below 2^31 with a block to spare
     const int64_t room = min(static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d, static_cast<int64_t>(0x7ffff000));
-    const Lens lens{p.kv_lens, room, kKeys * kWarps};
+    const Lens<kTail> lens{p.kv_lens, room, kKeys * kWarps};
     JoinDesc* join = reinterpret_cast<JoinDesc*>(p.partial + static_cast<int64_t>(kMaxCtas) * 2 * kSlot);
     pdl_trigger();
     pdl_wait();
 
     const int c = blockIdx.x;
     Cursor at;               // the block that is computed
-    long long t0, t1;        // the CTA's blocks of the line
+    long long t0, t1;        // the CTA's places of the line
     int early = -1;          // page of the warp's first key `lane`
     if (p.direct) {
         // a CTA a unit: the first pages are looked up beside the length
@@ -177,13 +182,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             return;
         }
     } else {
-        // ---- total number of blocks, and the sequences that have none. Up to 32 sequences are summed by every warp for
+        // ---- total number of places, and the sequences that have none. Up to 32 sequences are summed by every warp for
         // itself, without a barrier before the first loads.
         const bool few = p.B <= 32;
-        long long total = 0, inc = 0, v = 0;     // few: blocks (of one unit) up to and of sequence `lane`
+        long long total = 0, inc = 0, v = 0;     // few: places (of one unit) up to and of sequence `lane`
         if (few) {
             if (lane < p.B) {
-                v = lens.blocks(lens.len(lane));
+                v = lens.places(lens.len(lane));
                 if (p.kv_lens[lane] > room) atomicCAS(p.status, 0, 0x501);
             }
             inc = warp_scan64(v, lane);
@@ -191,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         } else {
             for (int b = threadIdx.x; b < p.B; b += kThreads) {
                 if (p.kv_lens[b] > room) atomicCAS(p.status, 0, 0x501);
-                v += lens.blocks(lens.len(b));
+                v += lens.places(lens.len(b));
             }
             v = warp_sum64(v);
             if (lane == 0) sh.scan[warp] = v;
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (threadIdx.x == 0 && !p.whole) join[c] = JoinDesc{0, -1, 0, 0, 0};
             return;
         }
-        // CTA c takes blocks [c total / ctas, (c + 1) total / ctas); block t belongs to the last CTA that starts at or before it
+        // CTA c takes places [c total / ctas, (c + 1) total / ctas); place t belongs to the last CTA that starts at or before it
         const bool small = total < (1 << 24);       // kMaxCtas * total fits 32 bits: divisions a quarter as long
         auto start_of = [&](long long i) -> long long {
             return small ? static_cast<uint32_t>(i * total) / static_cast<uint32_t>(ctas) : i * total / ctas;
@@ -227,10 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             found[0] = Found{__shfl_sync(0xffffffffu, lo, b0), b0};
             found[1] = Found{__shfl_sync(0xffffffffu, lo, b1), b1};
         } else {
-            long long acc = 0;   // blocks (of one unit) before sequence b0
+            long long acc = 0;   // places (of one unit) before sequence b0
             for (int b0 = 0; b0 < p.B; b0 += kThreads) {
                 const int b = b0 + threadIdx.x;
-                v = b < p.B ? lens.blocks(lens.len(b)) : 0;
+                v = b < p.B ? lens.places(lens.len(b)) : 0;
                 inc = warp_scan64(v, lane);
                 __syncthreads();
                 if (lane == 31) sh.scan[warp] = inc;
@@ -256,8 +261,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             x.n = lens.len(x.b);
             x.nblk = lens.blocks(x.n);
             const long long rem = t - f.before;
-            x.unit = small ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(x.nblk)) : static_cast<int>(rem / x.nblk);
-            x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * x.nblk);
+            const int each = x.nblk + kTail;
+            x.unit = small ? static_cast<int>(static_cast<uint32_t>(rem) / static_cast<uint32_t>(each)) : static_cast<int>(rem / each);
+            x.blk = static_cast<int>(rem - static_cast<long long>(x.unit) * each);
             return x;
         };
         at = cursor_at(t0, found[0]);
@@ -265,23 +271,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             // units are not split: a CTA takes those that start in its piece of the line
             if (t1 < total) {
                 const Cursor e = cursor_at(t1, found[1]);
-                if (e.blk > 0) t1 += e.nblk - e.blk;
+                if (e.blk > 0) t1 += e.nblk + kTail - e.blk;
             }
         } else if (threadIdx.x == 0) {
             JoinDesc d{0, -1, 0, 0, 0};
-            const long long u0 = t0 - at.blk;       // first block of the unit
-            if (at.blk > 0 && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
+            const long long u0 = t0 - at.blk;       // the unit's first place
+            if (at.blk > 0 && at.blk < at.nblk && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
                 d.c0 = c - 1;
                 d.c1 = owner(u0 + at.nblk - 1);
                 d.b = at.b;
                 d.unit = at.unit;
-                d.first_slot = start_of(c - 1) == u0 ? 0 : 1;
+                d.first_slot = start_of(c - 1) + kTail >= u0 ? 0 : 1;       // in the end of the unit before: nothing of that
             }
             join[c] = d;
         }
     }
-    auto advance = [&](Cursor& x) {
+    auto advance = [&](Cursor& x, long long& t) {
+        ++t;
         if (++x.blk < x.nblk) return;
+        t += kTail;
         x.blk = 0;
         if (++x.unit < units) return;
         x.unit = 0;
@@ -292,10 +300,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         } while (x.n == 0);
     };
 
-    if (p.whole && at.blk > 0) {      // never where a CTA has a unit of its own
-        t0 += at.nblk - at.blk;
+    if (at.blk >= at.nblk || (p.whole && at.blk > 0)) {      // never where a CTA has a unit of its own
+        t0 += at.nblk - 1 - at.blk;
         at.blk = at.nblk - 1;
-        advance(at);
+        advance(at, t0);
     }
 
     // ---- loads: lane i looks up the page of key i of the step one step ahead of its loads
@@ -317,9 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 page = first && p.direct ? early : p.cache.table[ahead.b * p.cache.table_stride + i];
                 inside = true;
             }
-            advance(ahead);
+            advance(ahead, t_ahead);
         }
-        ++t_ahead;
     };
     auto issue = [&](int stage) -> uint32_t {
         const bool ok = inside && page >= 0 && page < p.cache.n_pages;
@@ -367,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     W w;
     bool fresh = true, first_piece = true;
     int piece_blk = at.blk, stage = 0, rows = 0, head0 = 0;
-    for (long long t = t0; t < t1; ++t) {
+    for (long long t = t0; t < t1;) {
         if (fresh) {
             const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
             rows = min(group - ht * W::kRows, W::kRows);
@@ -437,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             fresh = true;
             first_piece = false;
         }
-        advance(at);
+        advance(at, t);
     }
     cp_wait<0>();
 }
@@ -517,8 +524,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 
 template <typename W, int kD>
 cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
+    constexpr int kWarps = W::Step::kWarps, kThreads = W::Step::kThreads;
     constexpr int kSmem = kWarps * W::Step::kStages * W::Step::kStage + (W::kBufs * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
-    static_assert(kSmem + sizeof(Shared) <= 232448, "shared memory budget");
+    static_assert(kSmem + sizeof(Shared<kWarps>) <= 232448, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
