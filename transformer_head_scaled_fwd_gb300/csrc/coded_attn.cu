@@ -74,15 +74,19 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
 // g + 8 are features 2 g and 2 g + 1.
 //
 // A row of 128 bytes is a key of d_k = 128, or (kHeads = 2) the same position of two neighbouring key heads of 64, whose query heads
-// are the unit's two tiles: lines of memory are 128 bytes, and with a head of 64 bytes a unit each line came from HBM twice
+// are the unit's two tiles or, up to four each, the two halves of one (kNT = 0: every column meets both heads'
+// codes, in sums of their own, and what is not of its head is left): lines of memory are 128 bytes, and with a head of 64 bytes a unit each line came from HBM twice
 // (16 x 8192, 16 heads of 64: 537 MB read for 268).
-template <typename T_, int kD, int kHeads, int kNT, bool kInt8>      // kNT tiles of 8 query heads a key head
+template <typename T_, int kD, int kHeads, int kNT, bool kInt8>      // kNT tiles of 8 query heads a key head; 0: one for both
 struct WarpCoded {
     using T = T_;
     static constexpr int kRow = kD * kHeads;
     using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads, 8, 2>;
-    static constexpr int kTiles = kNT * kHeads;
-    static_assert(kHeads == 1 || kNT == 1, "one tile for each of two key heads");
+    static constexpr bool kShared = kNT == 0;       // columns 0 - 3 are of the first key head, 4 - 7 of the second
+    static constexpr int kTiles = kShared ? 1 : kNT * kHeads;
+    static constexpr int kOfChunk = kShared ? 1 : kNT;          // tiles that a chunk of features takes part in
+    static constexpr int kOfKey = kShared ? 1 : kHeads;         // key heads that a lane has scores of
+    static_assert(kHeads == 1 ? kNT >= 1 : kNT <= 1, "at most a tile for each of two key heads");
     static constexpr int kRows = 8 * kTiles;
     static constexpr int kBufs = kTiles * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
     static constexpr int kQFloats = 0;
@@ -92,7 +96,7 @@ struct WarpCoded {
     static constexpr int kPT = kWide ? 2 : 1;       // and of a weight
     static constexpr float kMost = 32768.0f;        // largest weight: 2^(kGrow + 1 + kBase)
     uint32_t q[kQT][kD / 16][kTiles][2];
-    float o[kRow / 16][kNT][4];     // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
+    float o[kRow / 16][kOfChunk][4];     // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
     // of those two heads: maximum of the scores, and of score + scale's exponent; 2^(m - mo + kBase); this lane's share of the
     // sum; the bias' slope; what takes a product to a score
     float m[kTiles][2], mo[kTiles][2], u[kTiles][2], l[kTiles][2], slope[kTiles][2], in[kTiles][2];
@@ -101,25 +105,51 @@ struct WarpCoded {
 
     static __device__ __forceinline__ int swizzle(int row) { return kRow == 128 ? row & 7 : (row >> 1) & 3; }
     // the unit's row of column `col` of a tile, and whether it is one
-    __device__ __forceinline__ int row_of(int nt, int col) const { return kHeads == 2 ? nt * each + col : nt * 8 + col; }
-    __device__ __forceinline__ bool is_row(int nt, int col, int rows) const { return kHeads == 2 ? col < each : nt * 8 + col < rows; }
+    __device__ __forceinline__ int row_of(int nt, int col) const {
+        return kShared ? (col >> 2) * each + (col & 3) : kHeads == 2 ? nt * each + col : nt * 8 + col;
+    }
+    __device__ __forceinline__ bool is_row(int nt, int col, int rows) const {
+        return kShared ? (col & 3) < each : kHeads == 2 ? col < each : nt * 8 + col < rows;
+    }
+    static __device__ __forceinline__ bool second(int lane) { return kShared && (lane & 2); }     // its columns are of the second key head
 
+    // the lane's elements of its query rows, as they lie in memory
+    struct alignas(4 * sizeof(T)) Four {
+        T e[4];
+    };
     __device__ __forceinline__ void start(const PagedAttnParams& p, float*, int b, int head0, int rows, int lane) {
         each = rows / 2;
         biased = p.slopes != nullptr;
         const T* base = static_cast<const T*>(p.q) + b * p.q_b + head0 * p.q_h;
+        const bool wide = reinterpret_cast<uintptr_t>(base) % sizeof(Four) == 0 && p.q_h % 4 == 0;
+        Four raw[kTiles][kD / 16];
+        const T* x[kTiles];      // operand column: head lane / 4; a column without a head reads another's, for nothing
+#pragma unroll
+        for (int nt = 0; nt < kTiles; ++nt)
+            x[nt] = base + (is_row(nt, lane >> 2, rows) ? row_of(nt, lane >> 2) : 0) * p.q_h + 4 * (lane & 3);
+        if (wide) {
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) raw[nt][k] = *reinterpret_cast<const Four*>(x[nt] + 16 * k);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < kTiles; ++nt)
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) raw[nt][k].e[e] = x[nt][16 * k + e];
+        }
         const float form_in = p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e;
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
-            const bool mine = is_row(nt, lane >> 2, rows);      // operand column: head lane / 4
-            const T* x = base + row_of(nt, lane >> 2) * p.q_h + 4 * (lane & 3);
             float f[kD / 16][4];
             float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    f[k][e] = mine ? load_f(x + 16 * k + e) : 0.0f;
+                    f[k][e] = is_row(nt, lane >> 2, rows) ? load_f(&raw[nt][k].e[e]) : 0.0f;
                     top = fmaxf(top, fabsf(f[k][e]));
                 }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -154,7 +184,7 @@ struct WarpCoded {
 #pragma unroll
         for (int i = 0; i < kRow / 16; ++i)
 #pragma unroll
-            for (int nt = 0; nt < kNT; ++nt)
+            for (int nt = 0; nt < kOfChunk; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.0f;
     }
@@ -166,45 +196,59 @@ struct WarpCoded {
         const uint32_t row = (mi & 1) * 8 + r8;
         const uint32_t c0 = static_cast<uint32_t>(((mi >> 1) ^ swizzle(r8)) << 4);
         // key 16 t + 8 hf + g of the lane
-        float ks[kHeads][kKT][2], vs[kHeads][kKT][2];
+        float ks[kOfKey][kKT][2], vs[kOfKey][kKT][2];
 #pragma unroll
-        for (int i = 0; i < kHeads; ++i) {
-            const uint32_t a = v + Step::kBytes + 128 * i + 16 * g;
+        for (int i = 0; i < kOfKey; ++i) {
+            const uint32_t a = v + Step::kBytes + 128 * (second(lane) ? 1 : i) + 16 * g;
             const float4 x = lds4(a), y = lds4(a + 128 * kHeads);
             ks[i][0][0] = x.x; ks[i][0][1] = x.y; ks[i][1][0] = x.z; ks[i][1][1] = x.w;
             vs[i][0][0] = y.x; vs[i][0][1] = y.y; vs[i][1][0] = y.z; vs[i][1][1] = y.w;
         }
-        float s[kKT][kTiles][4];
+        float s[kKT][kTiles][4], other[kShared ? kKT : 1][4];      // shared: the columns' products with the second key head's codes
 #pragma unroll
-        for (int t = 0; t < kKT; ++t) {
-            const uint32_t at = k + (t * 16 + row) * kRow;
+        for (int t = 0; t < kKT; ++t)
 #pragma unroll
-            for (int nt = 0; nt < kTiles; ++nt)
+            for (int e = 0; e < 4; ++e) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.0f;
+                for (int nt = 0; nt < kTiles; ++nt) s[t][nt][e] = 0.0f;
+                if (kShared) other[t][e] = 0.0f;
+            }
+        // the two tiles of keys in turn: their sums are two chains
 #pragma unroll
-            for (int kk = 0; kk < kRow / 32; ++kk) {
-                uint32_t f[4];
-                ldsm4(f, at + (c0 ^ (kk << 5)));
+        for (int kk = 0; kk < kRow / 32; ++kk) {
+            uint32_t f[kKT][4];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {       // the two chunks of 16 features
+            for (int t = 0; t < kKT; ++t) ldsm4(f[t], k + (t * 16 + row) * kRow + (c0 ^ (kk << 5)));
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {       // the two chunks of 16 features
+                const int i = (2 * kk + hf) % (kD / 16), head = (2 * kk + hf) / (kD / 16);
+#pragma unroll
+                for (int t = 0; t < kKT; ++t) {
                     uint32_t a[4];
-                    codes_f16<kInt8, false>(f[2 * hf], a[0], a[2]);
-                    codes_f16<kInt8, false>(f[2 * hf + 1], a[1], a[3]);
-                    const int i = (2 * kk + hf) % (kD / 16), head = (2 * kk + hf) / (kD / 16);
+                    codes_f16<kInt8, false>(f[t][2 * hf], a[0], a[2]);
+                    codes_f16<kInt8, false>(f[t][2 * hf + 1], a[1], a[3]);
 #pragma unroll
-                    for (int nt = head * kNT; nt < (head + 1) * kNT; ++nt)
+                    for (int n = 0; n < kOfChunk; ++n) {
+                        const int nt = kShared ? 0 : head * kOfChunk + n;
 #pragma unroll
-                        for (int x = kQT - 1; x >= 0; --x) mma_f16(s[t][nt], a, q[x][i][nt][0], q[x][i][nt][1]);
+                        for (int x = kQT - 1; x >= 0; --x)
+                            mma_f16(kShared && head == 1 ? other[kShared ? t : 0] : s[t][nt], a, q[x][i][nt][0], q[x][i][nt][1]);
+                    }
                 }
             }
+        }
+        if (second(lane)) {
+#pragma unroll
+            for (int t = 0; t < kKT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[t][0][e] = other[kShared ? t : 0][e];
         }
 #pragma unroll
         for (int t = 0; t < kKT; ++t)
 #pragma unroll
             for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[t][nt][e] *= ks[nt / kNT][t][e >> 1] * in[nt][e & 1];
+                for (int e = 0; e < 4; ++e) s[t][nt][e] *= ks[nt / kOfChunk][t][e >> 1] * in[nt][e & 1];
         if (form.capped) {
 #pragma unroll
             for (int t = 0; t < kKT; ++t)
@@ -245,7 +289,7 @@ struct WarpCoded {
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const float p0 = ex2_approx(s[t][nt][e] - m[nt][0]), p1 = ex2_approx(s[t][nt][e + 1] - m[nt][1]);
-                        const float scale = vs[nt / kNT][t][e >> 1];
+                        const float scale = vs[nt / kOfChunk][t][e >> 1];
                         sum[nt][0] += p0;
                         sum[nt][1] += p1;
                         w[t][nt][e] = p0 * u[nt][0] * scale;           // u * scale may be beyond fp32 where p is 0
@@ -269,7 +313,7 @@ struct WarpCoded {
 #pragma unroll
                     for (int t = 0; t < kKT; ++t) {
                         top = fmax3(top, s[t][nt][e], s[t][nt][e + 2]);
-                        most = fmax3(most, s[t][nt][e] + exponent_of(vs[nt / kNT][t][0]), s[t][nt][e + 2] + exponent_of(vs[nt / kNT][t][1]));
+                        most = fmax3(most, s[t][nt][e] + exponent_of(vs[nt / kOfChunk][t][0]), s[t][nt][e + 2] + exponent_of(vs[nt / kOfChunk][t][1]));
                     }
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) {
@@ -284,9 +328,9 @@ struct WarpCoded {
                     u[nt][e] = top == -CUDART_INF_F ? 0.0f : ex2_approx(top - most + kBase);
                     // the tile's accumulators
 #pragma unroll
-                    for (int i = 0; i < kD / 16; ++i) {
-                        o[nt / kNT * (kD / 16) + i][nt % kNT][e] *= alpha;
-                        o[nt / kNT * (kD / 16) + i][nt % kNT][e + 2] *= alpha;
+                    for (int i = 0; i < kRow / 16 / (kTiles / kOfChunk); ++i) {
+                        o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e] *= alpha;
+                        o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e + 2] *= alpha;
                     }
                 }
             weigh(most_p, most_w);
@@ -325,11 +369,12 @@ struct WarpCoded {
                     uint32_t a[4];
                     codes_f16<kInt8, true>(f[2 * hf], a[0], a[1]);
                     codes_f16<kInt8, true>(f[2 * hf + 1], a[2], a[3]);
-                    const int head = (2 * i + hf) / (kD / 16);
+                    const int head = kShared ? 0 : (2 * i + hf) / (kD / 16);
 #pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt)
+                    for (int nt = 0; nt < kOfChunk; ++nt)
 #pragma unroll
-                        for (int x = kPT - 1; x >= 0; --x) mma_f16(o[2 * i + hf][nt], a, pt[x][head * kNT + nt][0], pt[x][head * kNT + nt][1]);
+                        for (int x = kPT - 1; x >= 0; --x)
+                            mma_f16(o[2 * i + hf][nt], a, pt[x][head * kOfChunk + nt][0], pt[x][head * kOfChunk + nt][1]);
                 }
             }
         }
@@ -345,7 +390,7 @@ struct WarpCoded {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
                 const int col = 2 * lane + e;
-                if (lane < 4 && (kHeads == 1 || col < each)) {
+                if (lane < 4 && is_row(nt, col, kRows)) {
                     sm_m[row_of(nt, col)] = m[nt][e];
                     sm_l[row_of(nt, col)] = sum;
                 }
@@ -365,7 +410,9 @@ struct WarpCoded {
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         float* y = buf + hd * kD + 16 * i + 2 * (lane >> 2) + hf;
-                        const float x = o[nt / kNT * (kD / 16) + i][nt % kNT][e + 2 * hf] * up * fr;
+                        const float mine = second(lane) ? o[(kHeads - 1) * (kD / 16) + i][nt % kOfChunk][e + 2 * hf]
+                                                        : o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e + 2 * hf];
+                        const float x = mine * up * fr;
                         *y = add ? *y + x : x;
                     }
             }
@@ -381,11 +428,11 @@ cudaError_t launch_t(PagedAttnParams p, cudaStream_t s) {
             if (group > 8) return launch_rows<WarpCoded<T, 128, 1, 2, kInt8>, 128>(p, s);
         return launch_rows<WarpCoded<T, 128, 1, 1, kInt8>, 128>(p, s);
     }
-    // heads of 64 that lie side by side go two at a time
-    if (group <= 8 && p.h_kv % 2 == 0 && p.cache.head_stride == 64) {
+    // heads of 64 go two at a time
+    if (group <= 8 && p.h_kv % 2 == 0) {
         p.h_kv /= 2;
-        p.cache.head_stride = 128;
-        return launch_rows<WarpCoded<T, 64, 2, 1, kInt8>, 64>(p, s);
+        p.cache.head_stride *= 2;
+        return group <= 4 ? launch_rows<WarpCoded<T, 64, 2, 0, kInt8>, 64>(p, s) : launch_rows<WarpCoded<T, 64, 2, 1, kInt8>, 64>(p, s);
     }
     if constexpr (kBf16)
         if (group > 8) return launch_rows<WarpCoded<T, 64, 1, 2, kInt8>, 64>(p, s);

@@ -312,7 +312,10 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     int page = -1, slot = 0, kvh = 0;
     bool inside = false;
     const uint32_t stage0 = smem_u32(smem) + warp * (kStages * S::kStage);
-    const char* k_lane = static_cast<const char*>(p.cache.k) + (lane % S::kChunks) * 16;
+    // the lane's chunk of a row; of two key heads each has half of the row, and p.cache.head_stride is that of a pair
+    constexpr int kOfHead = S::kChunks / (S::kScales == 2 ? 2 : 1);
+    const char* k_lane = static_cast<const char*>(p.cache.k) + lane % kOfHead * 16 +
+                         (lane % S::kChunks / kOfHead) * (p.cache.head_stride / 2) * S::kElem;
     const long long v_minus_k = static_cast<const char*>(p.cache.v) - static_cast<const char*>(p.cache.k);
     auto look_up = [&](bool first = false) {
         inside = false;
@@ -361,6 +364,10 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
         cp_commit();
         return live;
     };
+    W w;
+    bool fresh = true, first_piece = true;
+    int piece_blk = at.blk, stage = 0, rows = 0, head0 = 0;
+    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * S::kStage);   // kBufs x [rows][kD], then the query rows (fp32)
     uint32_t live[kStages];
     look_up(true);
 #pragma unroll
@@ -370,10 +377,6 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     }
 
     const ScoreForm form{p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, p.cap > 0.0f};
-    float* buf = reinterpret_cast<float*>(smem + kWarps * kStages * S::kStage);   // kBufs x [rows][kD], then the query rows (fp32)
-    W w;
-    bool fresh = true, first_piece = true;
-    int piece_blk = at.blk, stage = 0, rows = 0, head0 = 0;
     for (long long t = t0; t < t1;) {
         if (fresh) {
             const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
