@@ -145,12 +145,16 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     using S = typename W::Step;
     constexpr int kKeys = S::kKeys;
     constexpr int kSlot = slot_floats<kD>(), kStages = S::kStages, kWarps = S::kWarps, kThreads = S::kThreads, kTail = S::kTail;
+    constexpr bool kSided = S::kScales > 0;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Shared<kWarps> sh;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = p.h / p.h_kv;
     const int head_tiles = (group + W::kRows - 1) / W::kRows;
-    const int units = p.h_kv * head_tiles;
+    // kSided: the line is that of every p.side-th unit, p.side CTAs to a piece
+    const int sides = kSided ? static_cast<int>(p.side.d) : 1;
+    const int units = kSided ? p.side.div(p.h_kv * head_tiles) : p.h_kv * head_tiles;
+    const int c = kSided ? p.side.div(blockIdx.x) : blockIdx.x, my_side = kSided ? static_cast<int>(blockIdx.x) - c * sides : 0;
     // positions stay below 2^31 with a block to spare
     const int64_t room = min(static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d, static_cast<int64_t>(0x7ffff000));
     const Lens<kTail> lens{p.kv_lens, room, kKeys * kWarps};
@@ -158,7 +162,6 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     pdl_trigger();
     pdl_wait();
 
-    const int c = blockIdx.x;
     Cursor at;               // the block that is computed
     long long t0, t1;        // the CTA's places of the line
     int early = -1;          // page of the warp's first key `lane`
@@ -209,9 +212,9 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
             for (int i = threadIdx.x; i < p.h * kD; i += kThreads)
                 store_f(static_cast<T*>(p.out) + b * p.o_b + (i / kD) * p.o_h + i % kD, 0.0f);
         }
-        const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+        const int ctas = static_cast<int>(min(static_cast<long long>(kSided ? p.side.div(gridDim.x) : gridDim.x), total));
         if (c >= ctas) {
-            if (threadIdx.x == 0 && !p.whole) join[c] = JoinDesc{0, -1, 0, 0, 0};
+            if (threadIdx.x == 0 && !p.whole) join[blockIdx.x] = JoinDesc{0, -1, 0, 0, 0};
             return;
         }
         // CTA c takes places [c total / ctas, (c + 1) total / ctas); place t belongs to the last CTA that starts at or before it
@@ -280,10 +283,10 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
                 d.c0 = c - 1;
                 d.c1 = owner(u0 + at.nblk - 1);
                 d.b = at.b;
-                d.unit = at.unit;
+                d.unit = at.unit * sides + my_side;
                 d.first_slot = start_of(c - 1) + kTail >= u0 ? 0 : 1;       // in the end of the unit before: nothing of that
             }
-            join[c] = d;
+            join[blockIdx.x] = d;
         }
     }
     auto advance = [&](Cursor& x, long long& t) {
@@ -321,7 +324,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
         inside = false;
         if (t_ahead < t1) {
             const int key = (ahead.blk * kWarps + warp) * kKeys + lane;
-            kvh = ahead.unit / head_tiles;
+            kvh = (ahead.unit * sides + my_side) / head_tiles;
             if (lane < kKeys && key < ahead.n) {
                 const int i = p.cache.page.div(key);
                 slot = key - i * static_cast<int>(p.cache.page.d);
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     const ScoreForm form{p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e, p.cap * kLog2e, p.cap > 0.0f};
     for (long long t = t0; t < t1;) {
         if (fresh) {
-            const int kh = at.unit / head_tiles, ht = at.unit - kh * head_tiles;
+            const int unit = at.unit * sides + my_side, kh = unit / head_tiles, ht = unit - kh * head_tiles;
             rows = min(group - ht * W::kRows, W::kRows);
             head0 = kh * group + ht * W::kRows;
             w.start(p, buf + W::kBufs * W::kRows * kD, at.b, head0, rows, lane);
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
                 __syncthreads();
             }
             const bool whole = unit_done && piece_blk == 0;
-            float* slot_m = p.partial + (static_cast<int64_t>(c) * 2 + (first_piece ? 0 : 1)) * kSlot;
+            float* slot_m = p.partial + (static_cast<int64_t>(blockIdx.x) * 2 + (first_piece ? 0 : 1)) * kSlot;
             for (int i = threadIdx.x; i < rows * kD; i += kThreads) {
                 const int row = i / kD;
                 float a = 0.0f;
@@ -475,11 +478,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (row >= min(group - ht * rows_tile, rows_tile)) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pieces = d.c1 - d.c0 + 1;
-    const float* slots = p.partial + static_cast<int64_t>(d.c0) * 2 * kSlot;   // piece i at 2 i kSlot, piece 0 at first_slot
-    const float* mine = slots + (tid == 0 ? d.first_slot : 2 * tid) * kSlot;
+    const int sides = p.side.d, step = 2 * sides;
+    // piece i at i step kSlot, piece 0 at first_slot
+    const float* slots = p.partial + (static_cast<int64_t>(d.c0) * sides + (blockIdx.x - p.side.div(blockIdx.x) * sides)) * 2 * kSlot;
+    const float* mine = slots + (tid == 0 ? d.first_slot : step * tid) * kSlot;
     const int g = tid / kCols, x = tid % kCols;
     auto at = [&](int i) {
-        return reinterpret_cast<const float4*>(slots + (i == 0 ? d.first_slot : 2 * i) * kSlot + 2 * kMaxRows + row * kD)[x];
+        return reinterpret_cast<const float4*>(slots + (i == 0 ? d.first_slot : step * i) * kSlot + 2 * kMaxRows + row * kD)[x];
     };
     float4 early[kEarly];      // on their way while the weights are found
 #pragma unroll
@@ -544,13 +549,21 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= kWholeBlocks * kBlock;
     const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + W::kRows - 1) / W::kRows);
     p.direct = p.whole && units <= ctas;
+    // Neighbouring key heads lie side by side in a slot: CTAs that take their units in step read whole rows of memory between them
+    // (24 sequences of 15000, 8 heads of 128, e4m3: 136 -> 120 us). As many as divide the units of a sequence, up to eight; not where units are short.
+    int side = 1;
+    if (W::Step::kScales > 0 && !p.whole)
+        for (int i = 2; i <= 8; ++i)
+            if (units / p.B % i == 0) side = i;
+    p.side = fast_div(static_cast<uint32_t>(side));
     if (p.whole) {
         return launch_pdl(paged_attn_kernel<W, kD>, dim3(static_cast<unsigned>(std::min<int64_t>(units, ctas))), dim3(kThreads),
                           kSmem, s, p);
     }
-    if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(ctas), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
+    const int grid = ctas / side * side;
+    if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(grid), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
     const int rows = std::min(p.h / p.h_kv, W::kRows);
-    return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(ctas, rows), dim3(kJoinThreads), 0, s, p, static_cast<int>(W::kRows));
+    return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(grid, rows), dim3(kJoinThreads), 0, s, p, static_cast<int>(W::kRows));
 }
 }  // namespace
 }  // namespace mha

@@ -87,7 +87,8 @@ struct PagedAttnParams {
     const float* v_scales;
     FastDiv scale_block;     // tokens a scale covers
     int64_t page_scales;
-    int whole;               // set by the launcher: no unit is split
+    FastDiv side;            // set by the launcher: neighbouring units that as many CTAs take side by side
+    int whole;               // ... no unit is split
     int direct;              // ... and each has a CTA of its own
 };
 size_t paged_attn_workspace(bool bf16, int B, int h, int h_kv, int d);
