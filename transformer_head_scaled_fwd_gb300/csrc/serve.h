@@ -131,6 +131,7 @@ struct ResizeParams {
     int B, T;
     FastDiv page, by_t;
     int* status;
+    bool slots_after;        // set by the launcher: by a kernel of their own
 };
 cudaError_t launch_resize(const ResizeParams& p, cudaStream_t s);
 
