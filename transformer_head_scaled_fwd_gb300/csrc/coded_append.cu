@@ -35,6 +35,9 @@ struct TilePlan {
     int tiles;          // of a sequence
     int blocks;         // of a tile
     int parts;          // of the heads
+    int kv_heads;       // of a part
+    FastDiv half;       // pairs that turn
+    FastDiv q_heads;
     int team;           // warps of a task
     int stride;         // floats of a token's row of cos (and of sin)
 };
@@ -98,12 +101,9 @@ template <typename T>
 struct Pair {
     static constexpr int kN = 16 / static_cast<int>(sizeof(T));
     uint4 a, b;
-    __device__ __forceinline__ void load(const T* row, int c0, int c1) {
-        a = *reinterpret_cast<const uint4*>(row + c0);
-        b = *reinterpret_cast<const uint4*>(row + c1);
-    }
-    __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void load_shared(uint32_t at) {
+    __device__ __forceinline__ void load_shared(uint32_t at, bool on) {
+        a = b = make_uint4(0, 0, 0, 0);
+        if (!on) return;
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "r"(at));
         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w) : "r"(at + 512));
     }
@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_chunk(T* p, const float* x) {
 enum Turn { kNone, kNeighbours, kHalves, kStaged };
 
 template <typename T, int kD, int kTurn>
-__global__ void __launch_bounds__(kThreads, 3) coded_append_kernel(const __grid_constant__ CodedAppendParams p, const __grid_constant__ TilePlan plan) {
+__global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_constant__ CodedAppendParams p, const __grid_constant__ TilePlan plan) {
     constexpr int kN = Pair<T>::kN;
     constexpr int kLanes = kD / (2 * kN);          // of a row
     constexpr int kRows = 32 / kLanes;             // of a warp at a time
@@ -156,57 +156,80 @@ __global__ void __launch_bounds__(kThreads, 3) coded_append_kernel(const __grid_
 
     // ---- the lane's chunks of a row
     const int lr = lane / kLanes, li = lane - lr * kLanes;
-    int c0 = li * 2 * kN, c1 = c0 + kN;
+    // neighbouring lanes' first chunks are neighbours, and so are their second ones: whole sectors an access
+    int c0 = li * kN, c1 = c0 + kD / 2;
     if (kTurn == kHalves) {
         const int turning = half / kN;
-        c0 = li < turning ? li * kN : p.rot + (li - turning) * 2 * kN;
-        c1 = li < turning ? c0 + half : c0 + kN;
+        c0 = li < turning ? li * kN : p.rot + (li - turning) * kN;
+        c1 = c0 + (li < turning ? half : (kD - p.rot) / 2);
     }
 
-    // ---- keys and values: a task is a block, a key head, and one of the two; a step of it is kKeep passes of rows. Steps come into shared
-    // memory by asynchronous copies, the next one's while one is worked on; a lane reads what it has copied.
-    const int h0 = static_cast<int>(static_cast<int64_t>(part) * p.h_kv / plan.parts);
-    const int heads = static_cast<int>(static_cast<int64_t>(part + 1) * p.h_kv / plan.parts) - h0;
-    const int tasks = plan.blocks * heads * 2, teams = kWarps / plan.team;
+    // ---- A task is a block, a key head, and its keys or its values; a step of it is kKeep passes of rows. Behind those come steps of rows of
+    // queries. Steps come into shared memory by asynchronous copies, the next one's while one is worked on; a lane reads what it
+    // has copied.
+    const int h0 = part * plan.kv_heads, q0 = part * static_cast<int>(plan.q_heads.d);
+    const int tasks = plan.blocks * plan.kv_heads * 2, teams = kWarps / plan.team;
     const int team = warp / plan.team, member = warp - team * plan.team;
+    const int q_rows = p.q.p != nullptr ? tokens * static_cast<int>(plan.q_heads.d) : 0;
+    enum { kKeys, kValues, kQueries };
     struct Step {
-        int task, step, rounds;     // every round for the maximum, then, from the last one back, for the codes
+        int kind, task;             // kQueries: task is the first row, of all rows of queries
+        int step, rounds;           // every round for the maximum, then, from the last one back, for the codes
         int block, head, from, to;  // of the tile; the block's new tokens
-        bool values;
         __device__ __forceinline__ int round() const { return step < rounds ? step : 2 * rounds - 2 - step; }
     };
     auto settle = [&](Step& x) {       // the first step of x.task, or of the next that has tokens
         for (; x.task < tasks; x.task += teams) {
-            x.values = x.task & 1;
-            x.block = (x.task >> 1) / heads;
-            x.head = h0 + (x.task >> 1) - x.block * heads;
+            x.kind = x.task & 1;
+            const int n = x.task >> 1;
+            x.block = plan.blocks == 1 ? 0 : n / plan.kv_heads;
+            x.head = h0 + n - x.block * plan.kv_heads;
             const long long first = (blk0 + x.block) * block;
             x.from = static_cast<int>(max(first - start, static_cast<long long>(t0)));
             x.to = static_cast<int>(min(first + block - start, static_cast<long long>(t1)));
+            if (x.from >= x.to) continue;
             x.step = 0;
-            const int passes = (x.to - x.from + plan.team * kRows - 1) / (plan.team * kRows);
-            x.rounds = (passes + kKeep - 1) / kKeep;
-            if (x.from < x.to) return;
+            x.rounds = 1;
+            for (int rows = plan.team * kRows * kKeep; x.from + x.rounds * rows < x.to;) ++x.rounds;
+            return;
         }
+        x.kind = kQueries;
+        x.task = warp * kRows * kKeep;
     };
     auto advance = [&](Step& x) {
-        if (++x.step < 2 * x.rounds - 1) return;
-        x.task += teams;
-        settle(x);
+        if (x.kind == kQueries) {
+            x.task += kWarps * kRows * kKeep;
+        } else if (++x.step == 2 * x.rounds - 1) {
+            x.task += teams;
+            settle(x);
+        }
     };
-    auto row_of = [&](const Step& x, int i) { return x.from + ((x.round() * kKeep + i) * plan.team + member) * kRows + lr; };
+    auto pending = [&](const Step& x) { return x.kind != kQueries || x.task < q_rows; };
+    // a lane's token in the first pass of a step of keys or values; the next pass is `apart` tokens further
+    const int apart = plan.team * kRows;
+    auto token_of = [&](const Step& x) { return x.from + (x.round() * kKeep * plan.team + member) * kRows + lr; };
     const uint32_t mine = smem_u32(smem) + warp * (2 * kStep) + lane * 16;
     auto fetch = [&](const Step& x, int buffer) {
-        if (x.task < tasks) {
-            const Strided& in = x.values ? p.v : p.k;
-            const T* src = static_cast<const T*>(in.p) + b * in.b + x.head * in.h;
+        const uint32_t to = mine + buffer * kStep;
+        if (x.kind != kQueries) {
+            const Strided& in = x.kind == kValues ? p.v : p.k;
+            const int t = token_of(x);
+            const T* row = static_cast<const T*>(in.p) + b * in.b + x.head * in.h + t * in.l;
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i, row += apart * in.l) {
+                if (t + i * apart >= x.to) break;
+                cp_async16(to + i * 1024, row + c0, true);
+                cp_async16(to + i * 1024 + 512, row + c1, true);
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                const int t = row_of(x, i);
-                if (t >= x.to) continue;
-                const T* row = src + t * in.l;
-                cp_async16(mine + buffer * kStep + i * 1024, row + c0, true);
-                cp_async16(mine + buffer * kStep + i * 1024 + 512, row + c1, true);
+                const int r = x.task + i * kRows + lr;
+                if (r >= q_rows) break;
+                const int t = plan.q_heads.div(r);
+                const T* row = static_cast<const T*>(p.q.p) + b * p.q.b + (t0 + t) * p.q.l + (q0 + r - t * static_cast<int>(plan.q_heads.d)) * p.q.h;
+                cp_async16(to + i * 1024, row + c0, true);
+                cp_async16(to + i * 1024 + 512, row + c1, true);
             }
         }
         cp_commit();
@@ -263,33 +286,44 @@ __global__ void __launch_bounds__(kThreads, 3) coded_append_kernel(const __grid_
         const float* cs = cosines + t * span;
         const float* sn = sines + t * span;
         if (kTurn == kStaged) {
+            // the pass's rows in shared memory, a pair a lane at a time
             float* row = stage + lr * kD;
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-                row[c0 + i] = x[i];
-                row[c1 + i] = y[i];
+            for (int i = 0; i < kN; i += 4) {
+                *reinterpret_cast<float4*>(row + c0 + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                *reinterpret_cast<float4*>(row + c1 + i) = make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
             }
             __syncwarp();
-            if (!on) return;
+            for (int i0 = 0; i0 < kRows * half; i0 += 32) {
+                const int i = min(i0 + lane, kRows * half - 1), n = plan.half.div(i), e = i - n * half;
+                const int of = __shfl_sync(0xffffffffu, t, n * kLanes);
+                if (i0 + lane >= kRows * half) continue;
+                float* pair = stage + n * kD + e;
+                const float c = cosines[of * span + e], s = sines[of * span + e], u = pair[0], v = pair[half];
+                pair[0] = fmaf(u, c, -(v * s));
+                pair[half] = fmaf(v, c, u * s);
+            }
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 2 * kN; ++i) {
-                const int e = c0 + i;          // c1 = c0 + kN here
-                if (e >= p.rot) break;
-                float& v = i < kN ? x[i % kN] : y[i % kN];
-                const int pr = e < half ? e : e - half;
-                const float other = row[e < half ? e + half : pr];
-                v = e < half ? fmaf(v, cs[pr], -(other * sn[pr])) : fmaf(v, cs[pr], other * sn[pr]);
+            for (int i = 0; i < kN; i += 4) {
+                const float4 a = *reinterpret_cast<const float4*>(row + c0 + i), b = *reinterpret_cast<const float4*>(row + c1 + i);
+                x[i] = a.x; x[i + 1] = a.y; x[i + 2] = a.z; x[i + 3] = a.w;
+                y[i] = b.x; y[i + 1] = b.y; y[i + 2] = b.z; y[i + 3] = b.w;
             }
         } else if (kTurn == kNeighbours) {
-            if (!on || c0 >= p.rot) return;
+            if (!on) return;
 #pragma unroll
-            for (int i = 0; i < 2 * kN; i += 2) {
-                float& u = i < kN ? x[i % kN] : y[i % kN];
-                float& v = i < kN ? x[i % kN + 1] : y[i % kN + 1];
-                const float c = cs[c0 / 2 + i / 2], s = sn[c0 / 2 + i / 2], u0 = u;
-                u = fmaf(u0, c, -(v * s));
-                v = fmaf(v, c, u0 * s);
+            for (int h = 0; h < 2; ++h) {
+                float (&z)[kN] = h == 0 ? x : y;
+                const int at = h == 0 ? c0 : c1;
+                if (at >= p.rot) break;
+#pragma unroll
+                for (int i = 0; i < kN; i += 2) {
+                    const float c = cs[(at + i) / 2], s = sn[(at + i) / 2], u = z[i], v = z[i + 1];
+                    z[i] = fmaf(u, c, -(v * s));
+                    z[i + 1] = fmaf(v, c, u * s);
+                }
             }
         } else {
             if (!on || c0 >= half) return;
@@ -304,100 +338,116 @@ __global__ void __launch_bounds__(kThreads, 3) coded_append_kernel(const __grid_
 
     int flip = 0, buffer = 0;
     float top = 0.0f, scale = 1.0f;
-    while (now.task < tasks) {
+    while (pending(now)) {
         Step next = now;
         advance(next);
         fetch(next, buffer ^ 1);
         cp_wait<1>();
-        const long long first = (blk0 + now.block) * block;
         const uint32_t at = mine + buffer * kStep;
-        if (now.step == 0) top = 0.0f;
-        if (now.step < now.rounds) {
+        if (now.kind == kQueries) {
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                const int t = row_of(now, i);
-                if (kTurn != kStaged && t >= now.to) continue;
+                const int r = now.task + i * kRows + lr;
+                const bool on = r < q_rows;
+                if (kTurn != kStaged && !on) break;
+                const int t = plan.q_heads.div(on ? r : 0);
                 Pair<T> raw;
-                if (t < now.to) raw.load_shared(at + i * 1024);
-                else raw.zero();
+                raw.load_shared(at + i * 1024, on);
                 float x[kN], y[kN];
                 raw.values(x, y);
-                if (!now.values) turn(x, y, min(t, now.to - 1) - t0, t < now.to);
-#pragma unroll
-                for (int e = 0; e < kN; ++e) top = most3(top, x[e], y[e]);
+                turn(x, y, t, on);
+                if (!on) continue;
+                T* row = static_cast<T*>(p.q_out.p) + b * p.q_out.b + (t0 + t) * p.q_out.l + (q0 + r - t * static_cast<int>(plan.q_heads.d)) * p.q_out.h;
+                store_chunk(row + c0, x);
+                store_chunk(row + c1, y);
             }
-        }
-        if (now.step >= now.rounds - 1) {
-            const BlockInfo where = info[now.block];
-            const bool kept = where.slot >= 0;
-            uint8_t* codes = static_cast<uint8_t*>(now.values ? p.cache.v : p.cache.k) + (kept ? where.slot + now.head * p.cache.head_stride : 0);
-            if (now.step == now.rounds - 1) {
-                uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));      // NaN is above all
-                if (plan.team > 1) {
-                    if (lane == 0) peak[flip][warp] = most;
-                    named_bar_sync(1 + team, 32 * plan.team);
-                    for (int i = 0; i < plan.team; ++i) most = max(most, peak[flip][team * plan.team + i]);
-                    flip ^= 1;                             // the other half is free: its readers have passed this barrier
-                }
-                scale = scale_for(int8, most);
-                float* scale_at = (now.values ? p.v_scales : p.k_scales) + (kept ? where.scale + now.head : 0);
-                const int filled = static_cast<int>(start + now.from - first);       // slots of the block that hold earlier tokens
-                if (kept && filled > 0) {
-                    const float old = *scale_at;
-                    if (!(old <= scale)) scale = isnan(scale) ? scale : old;     // the larger; NaN stays
-                    else if (old < scale) {
-                        const float ratio = old / scale;
-                        for (int i = member * kRows + lr; i < filled; i += plan.team * kRows) {
-                            uint8_t* row = codes + i * p.cache.slot_stride;
-#pragma unroll 1
-                            for (int e = 0; e < 2 * kN; e += 4) {
-                                uint32_t* w = reinterpret_cast<uint32_t*>(row + (e < kN ? c0 + e : c1 + e - kN));
-                                const uint32_t c = *w;
-                                *w = code4(int8, value_of(int8, c & 0xffu) * ratio, value_of(int8, (c >> 8) & 0xffu) * ratio,
-                                           value_of(int8, (c >> 16) & 0xffu) * ratio, value_of(int8, c >> 24) * ratio);
+        } else {
+            const long long first = (blk0 + now.block) * block;
+            const int t = token_of(now);
+            float x[kKeep][kN], y[kKeep][kN];
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const bool on = t + i * apart < now.to;
+                Pair<T> raw;
+                raw.load_shared(at + i * 1024, on);
+                raw.values(x[i], y[i]);
+                if (now.kind == kKeys) turn(x[i], y[i], min(t + i * apart, now.to - 1) - t0, on);
+            }
+            if (now.step == 0) top = 0.0f;
+            if (now.step < now.rounds) {
+#pragma unroll
+                for (int i = 0; i < kKeep; ++i)
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) top = most3(top, x[i][e], y[i][e]);
+            }
+            if (now.step >= now.rounds - 1) {
+                const BlockInfo where = info[now.block];
+                const bool kept = where.slot >= 0;
+                uint8_t* codes = static_cast<uint8_t*>(now.kind == kValues ? p.cache.v : p.cache.k) + (kept ? where.slot + now.head * p.cache.head_stride : 0);
+                if (now.step == now.rounds - 1) {
+                    uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));      // NaN is above all
+                    if (plan.team > 1) {
+                        if (lane == 0) peak[flip][warp] = most;
+                        named_bar_sync(1 + team, 32 * plan.team);
+                        for (int i = 0; i < plan.team; ++i) most = max(most, peak[flip][team * plan.team + i]);
+                        flip ^= 1;                             // the other half is free: its readers have passed this barrier
+                    }
+                    scale = scale_for(int8, most);
+                    float* scale_at = (now.kind == kValues ? p.v_scales : p.k_scales) + (kept ? where.scale + now.head : 0);
+                    const int filled = static_cast<int>(start + now.from - first);       // slots of the block that hold earlier tokens
+                    if (kept && filled > 0) {
+                        const float old = *scale_at;
+                        if (!(old <= scale)) scale = isnan(scale) ? scale : old;     // the larger; NaN stays
+                        else if (old < scale) {
+                            const float ratio = old / scale;
+                            for (int i = member * kRows + lr; i < filled; i += plan.team * kRows) {
+                                uint8_t* row = codes + i * p.cache.slot_stride;
+    #pragma unroll 1
+                                for (int e = 0; e < 2 * kN; e += 4) {
+                                    uint32_t* w = reinterpret_cast<uint32_t*>(row + (e < kN ? c0 + e : c1 + e - kN));
+                                    const uint32_t c = *w;
+                                    *w = code4(int8, value_of(int8, c & 0xffu) * ratio, value_of(int8, (c >> 8) & 0xffu) * ratio,
+                                               value_of(int8, (c >> 16) & 0xffu) * ratio, value_of(int8, c >> 24) * ratio);
+                                }
                             }
                         }
                     }
+                    // every warp of the team has read the old scale before one writes the new
+                    if (plan.team > 1 && filled > 0) named_bar_sync(1 + team, 32 * plan.team);
+                    else __syncwarp();
+                    if (kept && member == 0 && lane == 0) *scale_at = scale;
                 }
-                // every warp of the team has read the old scale before one writes the new
-                if (plan.team > 1 && filled > 0) named_bar_sync(1 + team, 32 * plan.team);
-                else __syncwarp();
-                if (kept && member == 0 && lane == 0) *scale_at = scale;
-            }
-            T* const turned = now.values ? nullptr : static_cast<T*>(p.k_out.p);
-            const float inv = 1.0f / scale;
-            const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+                if (now.kind == kKeys && p.k_out.p != nullptr) {
+                    T* row = static_cast<T*>(p.k_out.p) + b * p.k_out.b + now.head * p.k_out.h + t * p.k_out.l;
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-                const int t = row_of(now, i);
-                if (kTurn != kStaged && t >= now.to) continue;
-                Pair<T> raw;
-                if (t < now.to) raw.load_shared(at + i * 1024);
-                else raw.zero();
-                float x[kN], y[kN];
-                raw.values(x, y);
-                if (!now.values) turn(x, y, min(t, now.to - 1) - t0, t < now.to);
-                if (t >= now.to) continue;
-                if (turned != nullptr) {
-                    T* row = turned + b * p.k_out.b + t * p.k_out.l + now.head * p.k_out.h;
-                    store_chunk(row + c0, x);
-                    store_chunk(row + c1, y);
+                    for (int i = 0; i < kKeep; ++i, row += apart * p.k_out.l) {
+                        if (t + i * apart >= now.to) break;
+                        store_chunk(row + c0, x[i]);
+                        store_chunk(row + c1, y[i]);
+                    }
                 }
-                if (!kept) continue;
-                divide(x, y, scale, inv, power);
-                uint8_t* row = codes + static_cast<int>(start + t - first) * p.cache.slot_stride;
-                uint32_t u[kN / 4], v[kN / 4];
+                if (kept) {
+                    const float inv = 1.0f / scale;
+                    const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
+                    uint8_t* row = codes + static_cast<int>(start + t - first) * p.cache.slot_stride;
 #pragma unroll
-                for (int e = 0; e < kN / 4; ++e) {
-                    u[e] = code4(int8, x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
-                    v[e] = code4(int8, y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                }
-                if constexpr (kN == 8) {
-                    *reinterpret_cast<uint2*>(row + c0) = make_uint2(u[0], u[1]);
-                    *reinterpret_cast<uint2*>(row + c1) = make_uint2(v[0], v[1]);
-                } else {
-                    *reinterpret_cast<uint32_t*>(row + c0) = u[0];
-                    *reinterpret_cast<uint32_t*>(row + c1) = v[0];
+                    for (int i = 0; i < kKeep; ++i, row += apart * p.cache.slot_stride) {
+                        if (t + i * apart >= now.to) break;
+                        divide(x[i], y[i], scale, inv, power);
+                        uint32_t u[kN / 4], v[kN / 4];
+#pragma unroll
+                        for (int e = 0; e < kN / 4; ++e) {
+                            u[e] = code4(int8, x[i][4 * e], x[i][4 * e + 1], x[i][4 * e + 2], x[i][4 * e + 3]);
+                            v[e] = code4(int8, y[i][4 * e], y[i][4 * e + 1], y[i][4 * e + 2], y[i][4 * e + 3]);
+                        }
+                        if constexpr (kN == 8) {
+                            *reinterpret_cast<uint2*>(row + c0) = make_uint2(u[0], u[1]);
+                            *reinterpret_cast<uint2*>(row + c1) = make_uint2(v[0], v[1]);
+                        } else {
+                            *reinterpret_cast<uint32_t*>(row + c0) = u[0];
+                            *reinterpret_cast<uint32_t*>(row + c1) = v[0];
+                        }
+                    }
                 }
             }
         }
@@ -405,35 +455,6 @@ __global__ void __launch_bounds__(kThreads, 3) coded_append_kernel(const __grid_
         buffer ^= 1;
     }
     cp_wait<0>();
-
-    // ---- queries
-    if (p.q.p == nullptr) return;
-    const int q0 = static_cast<int>(static_cast<int64_t>(part) * p.h / plan.parts);
-    const int qh = static_cast<int>(static_cast<int64_t>(part + 1) * p.h / plan.parts) - q0;
-    constexpr int kAtOnce = 2;
-    const int all = tokens * qh;
-    for (int r0 = warp * kRows * kAtOnce; r0 < all; r0 += kWarps * kRows * kAtOnce) {
-        Pair<T> raw[kAtOnce];
-        int t[kAtOnce], hd[kAtOnce];
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const int row = r0 + i * kRows + lr;
-            t[i] = row < all ? row / qh : -1;
-            hd[i] = q0 + row - t[i] * qh;
-            if (t[i] >= 0) raw[i].load(static_cast<const T*>(p.q.p) + b * p.q.b + (t0 + t[i]) * p.q.l + hd[i] * p.q.h, c0, c1);
-            else raw[i].zero();
-        }
-#pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            float x[kN], y[kN];
-            raw[i].values(x, y);
-            turn(x, y, max(t[i], 0), t[i] >= 0);
-            if (t[i] < 0) continue;
-            T* row = static_cast<T*>(p.q_out.p) + b * p.q_out.b + (t0 + t[i]) * p.q_out.l + hd[i] * p.q_out.h;
-            store_chunk(row + c0, x);
-            store_chunk(row + c1, y);
-        }
-    }
 }
 
 template <typename T, int kD>
@@ -448,10 +469,14 @@ cudaError_t launch_n(const CodedAppendParams& p, cudaStream_t s) {
     plan.tiles = static_cast<int>((most + plan.blocks - 1) / plan.blocks);
     plan.team = 1;
     while (plan.team < kWarps && std::min(block, p.T) > plan.team * kRows * kKeep) plan.team *= 2;
-    // parts of the heads, while the CTAs are fewer than eight an SM
+    // equal parts of the heads, while the CTAs are fewer than four an SM
     plan.parts = 1;
-    while (plan.parts * 2 <= p.h_kv && static_cast<int64_t>(p.B) * plan.tiles * plan.parts < 152 * 8) plan.parts *= 2;
+    while (p.h_kv % (2 * plan.parts) == 0 && p.h % (2 * plan.parts) == 0 && static_cast<int64_t>(p.B) * plan.tiles * plan.parts < 152 * 4)
+        plan.parts *= 2;
+    plan.kv_heads = p.h_kv / plan.parts;
+    plan.q_heads = fast_div(static_cast<uint32_t>(std::max(p.h / plan.parts, 1)));
     plan.stride = (half + kN - 1) / kN * kN;
+    plan.half = fast_div(static_cast<uint32_t>(std::max(half, 1)));
     const Turn turn = half == 0 ? kNone : p.interleaved != 0 ? kNeighbours : half % kN == 0 ? kHalves : kStaged;
     const size_t smem = kWarps * 2 * kKeep * 1024 + static_cast<size_t>(plan.blocks) * block * plan.stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
     const auto kernel = turn == kNone ? coded_append_kernel<T, kD, kNone> : turn == kNeighbours ? coded_append_kernel<T, kD, kNeighbours>
@@ -471,20 +496,7 @@ cudaError_t launch_t(const CodedAppendParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_coded_append(const CodedAppendParams& p, bool bf16, cudaStream_t s) {
-    CodedAppendParams q = p;
-    if (p.q.p != nullptr && static_cast<int64_t>(p.B) * p.T * p.h * p.d >= (1 << 20)) {
-        // many queries: by the kernel that turns without a cache
-        RotaryParams r{};
-        r.q = p.q; r.q_out = p.q_out;
-        r.start = p.start; r.new_lens = p.new_lens;
-        r.inv_freq = p.inv_freq; r.rot = p.rot; r.interleaved = p.interleaved; r.scale = p.scale;
-        r.B = p.B; r.T = p.T; r.h = p.h; r.d = p.d; r.status = p.status;
-        const cudaError_t e = launch_rotary(r, bf16, s);
-        if (e != cudaSuccess) return e;
-        q.q.p = q.q_out.p = nullptr;
-        q.h = 0;
-    }
-    return bf16 ? launch_t<__nv_bfloat16>(q, s) : launch_t<float>(q, s);
+    return bf16 ? launch_t<__nv_bfloat16>(p, s) : launch_t<float>(p, s);
 }
 
 }  // namespace mha
