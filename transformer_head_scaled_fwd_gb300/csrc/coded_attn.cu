@@ -77,18 +77,20 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
 // are the unit's two tiles or, up to four each, the two halves of one (kNT = 0: every column meets both heads'
 // codes, in sums of their own, and what is not of its head is left): lines of memory are 128 bytes, and with a head of 64 bytes a unit each line came from HBM twice
 // (16 x 8192, 16 heads of 64: 537 MB read for 268).
-template <typename T_, int kD, int kHeads, int kNT, bool kInt8>      // kNT tiles of 8 query heads a key head; 0: one for both
+// kNT tiles of 8 query heads a key head, 0: one for both; kTwo: two CTAs of four warps an SM instead of one of eight
+template <typename T_, int kD, int kHeads, int kNT, bool kInt8, bool kTwo = false>
 struct WarpCoded {
     using T = T_;
     static constexpr int kRow = kD * kHeads;
-    using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads, 8, 2>;
     static constexpr bool kShared = kNT == 0;       // columns 0 - 3 are of the first key head, 4 - 7 of the second
     static constexpr int kTiles = kShared ? 1 : kNT * kHeads;
     static constexpr int kOfChunk = kShared ? 1 : kNT;          // tiles that a chunk of features takes part in
     static constexpr int kOfKey = kShared ? 1 : kHeads;         // key heads that a lane has scores of
     static_assert(kHeads == 1 ? kNT >= 1 : kNT <= 1, "at most a tile for each of two key heads");
     static constexpr int kRows = 8 * kTiles;
-    static constexpr int kBufs = kTiles * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
+    static_assert(!kTwo || (kTiles == 1 && kRow == 128), "what shared memory takes twice");
+    using Step = StepOf<kRow, 1, 32, kRow == 128 ? 3 : 6, kHeads, kTwo ? 4 : 8, kTwo ? 2 : 2, kTwo ? 2 : 1, kTwo ? 8 : 4>;
+    static constexpr int kBufs = kTwo || kTiles * kD > 128 ? 2 : 4;      // of the join, in what shared memory the stages leave
     static constexpr int kQFloats = 0;
     static constexpr int kKT = Step::kKeys / 16;
     static constexpr bool kWide = sizeof(T) == 4;
@@ -419,6 +421,22 @@ struct WarpCoded {
     }
 };
 
+// Many units: two CTAs of four warps an SM, of which one computes and loads while the other ends a unit and begins the next. (8 key
+// heads of 128, four query heads each, lengths up to: 32 x 1000 21.5 -> 17.3 us, 256 x 1000 98 -> 78, 128 x 4000 125 -> 117, 128 x 8000 214 -> 207;
+// 64 x 8000 107 both; but 48 x 15000 143 -> 144, and where units are fewer than SMs, so that each is split: one of 131071 with 2 key heads
+// 22.1 -> 24.6, 4 x 333 with 4 of 64 6.3 -> 7.1.)
+template <typename T, int kD, int kHeads, int kNT, bool kInt8>
+cudaError_t launch_w(const PagedAttnParams& p, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + 7) / 8);
+    const int64_t room = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d;
+    return units >= sms && (room <= 8192 || units >= 3 * sms) ? launch_rows<WarpCoded<T, kD, kHeads, kNT, kInt8, true>, kD>(p, s)
+                                                              : launch_rows<WarpCoded<T, kD, kHeads, kNT, kInt8, false>, kD>(p, s);
+}
+
 template <typename T, bool kInt8>
 cudaError_t launch_t(PagedAttnParams p, cudaStream_t s) {
     const int group = p.h / p.h_kv;
@@ -426,13 +444,13 @@ cudaError_t launch_t(PagedAttnParams p, cudaStream_t s) {
     if (p.d == 128) {
         if constexpr (kBf16)
             if (group > 8) return launch_rows<WarpCoded<T, 128, 1, 2, kInt8>, 128>(p, s);
-        return launch_rows<WarpCoded<T, 128, 1, 1, kInt8>, 128>(p, s);
+        return launch_w<T, 128, 1, 1, kInt8>(p, s);
     }
     // heads of 64 go two at a time
     if (group <= 8 && p.h_kv % 2 == 0) {
         p.h_kv /= 2;
         p.cache.head_stride *= 2;
-        return group <= 4 ? launch_rows<WarpCoded<T, 64, 2, 0, kInt8>, 64>(p, s) : launch_rows<WarpCoded<T, 64, 2, 1, kInt8>, 64>(p, s);
+        return group <= 4 ? launch_w<T, 64, 2, 0, kInt8>(p, s) : launch_rows<WarpCoded<T, 64, 2, 1, kInt8>, 64>(p, s);
     }
     if constexpr (kBf16)
         if (group > 8) return launch_rows<WarpCoded<T, 64, 1, 2, kInt8>, 64>(p, s);
@@ -441,7 +459,7 @@ cudaError_t launch_t(PagedAttnParams p, cudaStream_t s) {
 
 }  // namespace
 
-size_t coded_attn_workspace(int d) { return line_workspace(d); }
+size_t coded_attn_workspace(int d) { return line_workspace(d, 2); }
 
 cudaError_t launch_coded_attn(const PagedAttnParams& p, bool bf16, bool int8, cudaStream_t s) {
     if (bf16) return int8 ? launch_t<__nv_bfloat16, true>(p, s) : launch_t<__nv_bfloat16, false>(p, s);

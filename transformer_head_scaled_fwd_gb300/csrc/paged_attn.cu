@@ -22,7 +22,7 @@ namespace {
 
 // 4 KB of keys, 4 KB of values a step
 template <typename T, int kD>
-using Halves = StepOf<kD * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, 0, 8, 0>;
+using Halves = StepOf<kD * static_cast<int>(sizeof(T)), static_cast<int>(sizeof(T)), 4096 / (kD * static_cast<int>(sizeof(T))), 3, 0, 8, 0, 1, 4>;
 
 // ------------------------------------------------------------ a warp's heads: bf16, matrix instructions
 // Both products are taken transposed, so that the long sides are the matrix instruction's 16 rows and the
@@ -348,7 +348,7 @@ cudaError_t launch_d(const PagedAttnParams& p, bool bf16, cudaStream_t s) {
 }  // namespace
 
 size_t paged_attn_workspace(bool, int, int, int, int d) {
-    return line_workspace(d);
+    return line_workspace(d, 1);
 }
 
 cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t s) {

@@ -28,19 +28,18 @@
 namespace mha {
 namespace {
 
-constexpr int kMaxCtas = 192;           // slots of the workspace
+constexpr int kSlotsPerSm = 192;        // slots of the workspace for a CTA an SM
 constexpr int kMaxRows = 16;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWholeBlocks = 4;
 constexpr float kGrow = 8.0f;           // log2 units the maximum may grow before o and l are rescaled
 
 // One step of a warp: kKeys keys, their kBytes bytes of keys and as many of values, elements of kElem bytes. kScales: the
 // scales of kScales neighbouring key heads besides, [keys / values][head][key % 8][key / 8]. Up to 32 keys: lane i looks up key i.
-// A CTA has kWarps warps, each with kStages steps in shared memory.
+// A CTA has kWarps warps, each with kStages steps in shared memory; kPerSm of them run on an SM.
 // A unit's end costs as much as kTail blocks.
-template <int kRow_, int kElem_, int kKeys_, int kStages_, int kScales_, int kWarps_, int kTail_>
+template <int kRow_, int kElem_, int kKeys_, int kStages_, int kScales_, int kWarps_, int kTail_, int kPerSm_, int kWhole_>
 struct StepOf {
-    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_, kScales = kScales_, kWarps = kWarps_, kTail = kTail_;
+    static constexpr int kElem = kElem_, kKeys = kKeys_, kStages = kStages_, kScales = kScales_, kWarps = kWarps_, kTail = kTail_, kWhole = kWhole_, kPerSm = kPerSm_, kSlots = kPerSm * kSlotsPerSm;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRow = kRow_;                      // bytes of a key
     static constexpr int kBytes = kKeys * kRow;
@@ -59,9 +58,10 @@ struct JoinDesc {
 template <int kD>
 __host__ __device__ constexpr int slot_floats() { return 2 * kMaxRows + kMaxRows * kD; }
 
-inline size_t line_workspace(int d) {
+inline size_t line_workspace(int d, int per_sm) {
+    const size_t slots = static_cast<size_t>(per_sm) * kSlotsPerSm;
     const size_t slot = (2 * kMaxRows + kMaxRows * static_cast<size_t>(d)) * sizeof(float);
-    return (kMaxCtas * 2 * slot + kMaxCtas * sizeof(JoinDesc) + 255) / 256 * 256;
+    return (slots * 2 * slot + slots * sizeof(JoinDesc) + 255) / 256 * 256;
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
@@ -140,7 +140,7 @@ __device__ __forceinline__ long long warp_scan64(long long v, int lane) {
 }
 
 template <typename W, int kD>
-__global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn_kernel(const __grid_constant__ PagedAttnParams p) {
     using T = typename W::T;
     using S = typename W::Step;
     constexpr int kKeys = S::kKeys;
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
     // positions stay below 2^31 with a block to spare
     const int64_t room = min(static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d, static_cast<int64_t>(0x7ffff000));
     const Lens<kTail> lens{p.kv_lens, room, kKeys * kWarps};
-    JoinDesc* join = reinterpret_cast<JoinDesc*>(p.partial + static_cast<int64_t>(kMaxCtas) * 2 * kSlot);
+    JoinDesc* join = reinterpret_cast<JoinDesc*>(p.partial + static_cast<int64_t>(S::kSlots) * 2 * kSlot);
     pdl_trigger();
     pdl_wait();
 
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
             return;
         }
         // CTA c takes places [c total / ctas, (c + 1) total / ctas); place t belongs to the last CTA that starts at or before it
-        const bool small = total < (1 << 24);       // kMaxCtas * total fits 32 bits: divisions a quarter as long
+        const bool small = total < (S::kSlots <= 256 ? 1 << 24 : 1 << 23);       // S::kSlots * total fits 32 bits: divisions a quarter as long
         auto start_of = [&](long long i) -> long long {
             return small ? static_cast<uint32_t>(i * total) / static_cast<uint32_t>(ctas) : i * total / ctas;
         };
@@ -456,20 +456,20 @@ __global__ void __launch_bounds__(W::Step::kThreads, 1) paged_attn_kernel(const 
 }
 
 // Joins the pieces of a unit that several CTAs share: block (c, row). Thread i weighs piece i (there are
-// at most kMaxCtas), then groups of kD / 4 threads sum every kGroups-th piece, 16 bytes a thread.
-constexpr int kJoinThreads = 256;
+// at most kSlots), then groups of kD / 4 threads sum every kGroups-th piece, 16 bytes a thread.
+__host__ __device__ constexpr int join_threads(int slots) { return slots <= 256 ? 256 : 512; }
 constexpr int kEarly = 8;        // loads of a thread that do not wait for the weights (one of 131071: 31.8 -> 30.5 us, of 16000: 12.9 -> 12.1)
-template <typename T, int kD>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
+template <typename T, int kD, int kSlots>
+__global__ void __launch_bounds__(join_threads(kSlots)) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
     constexpr int kSlot = slot_floats<kD>();
     constexpr int kCols = kD / 4;
-    constexpr int kGroups = kJoinThreads / kCols;
-    static_assert(kMaxCtas <= kJoinThreads, "one thread a piece");
+    constexpr int kJoinThreads = join_threads(kSlots), kGroups = kJoinThreads / kCols;
+    static_assert(kSlots <= kJoinThreads, "one thread a piece");
     __shared__ float sh_f[kJoinThreads], sh_x[2][kJoinThreads / 32];
     __shared__ float4 sh_o[kGroups][kCols];
     pdl_trigger();
     pdl_wait();
-    const JoinDesc d = reinterpret_cast<const JoinDesc*>(p.partial + static_cast<int64_t>(kMaxCtas) * 2 * kSlot)[blockIdx.x];
+    const JoinDesc d = reinterpret_cast<const JoinDesc*>(p.partial + static_cast<int64_t>(kSlots) * 2 * kSlot)[blockIdx.x];
     if (d.c1 < d.c0) return;
     const int group = p.h / p.h_kv;
     const int head_tiles = (group + rows_tile - 1) / rows_tile;
@@ -534,19 +534,19 @@ template <typename W, int kD>
 cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     constexpr int kWarps = W::Step::kWarps, kThreads = W::Step::kThreads;
     constexpr int kSmem = kWarps * W::Step::kStages * W::Step::kStage + (W::kBufs * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
-    static_assert(kSmem + sizeof(Shared<kWarps>) <= 232448, "shared memory budget");
+    static_assert((kSmem + sizeof(Shared<kWarps>) + 1024) * W::Step::kPerSm <= 233472, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     int dev = 0, sms = 0;
     if (e == cudaSuccess) e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(sms, kMaxCtas);
-    // Sequences of kWholeBlocks blocks at most are not worth the second kernel: a CTA takes longer over a unit by less
+    const int ctas = std::min(sms, kSlotsPerSm) * W::Step::kPerSm;
+    // Sequences of kWhole blocks at most are not worth the second kernel: a CTA takes longer over a unit by less
     // than the join costs (64 x 300, 32 / 8 heads of 128: 31 against 34 us; one of 500, 16 / 4 heads of 64: 10.8
     // against 13.0 us with the launches). The lengths are on the device, so the host goes by what the table has room for:
     // the same sequences behind a wider table take the two launches.
     constexpr int kBlock = W::Step::kKeys * kWarps;
-    p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= kWholeBlocks * kBlock;
+    p.whole = static_cast<int64_t>(p.cache.max_pages) * p.cache.page.d <= W::Step::kWhole * kBlock;
     const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + W::kRows - 1) / W::kRows);
     p.direct = p.whole && units <= ctas;
     // Neighbouring key heads lie side by side in a slot: CTAs that take their units in step read whole rows of memory between them
@@ -563,7 +563,7 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     const int grid = ctas / side * side;
     if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(grid), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
     const int rows = std::min(p.h / p.h_kv, W::kRows);
-    return launch_pdl(paged_join_kernel<typename W::T, kD>, dim3(grid, rows), dim3(kJoinThreads), 0, s, p, static_cast<int>(W::kRows));
+    return launch_pdl(paged_join_kernel<typename W::T, kD, W::Step::kSlots>, dim3(grid, rows), dim3(join_threads(W::Step::kSlots)), 0, s, p, static_cast<int>(W::kRows));
 }
 }  // namespace
 }  // namespace mha
