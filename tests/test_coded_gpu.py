@@ -323,6 +323,17 @@ ATTEND = [
     (F32, E4, 9, 3, 64, 1, 1, "slots", [66, 2], dict(slopes=True)),
     (F32, I8, 20, 1, 128, 32, 32, "slots", [257, 1], dict(scale=-0.2)),
     (F32, E4, 16, 1, 64, 256, 256, "slots", [3000, 256, 255], {}),
+    # two key heads of 64 at a time: a tile of query columns for both, or one each; pages stored head by head
+    (BF, I8, 8, 4, 64, 16, 16, "slots", [700, 33], dict(slopes=True, cap=8.0)),
+    (BF, E4, 16, 4, 64, 32, 8, "heads", [513, 1, 260], dict(slopes=True)),
+    (BF, E4, 14, 2, 64, 16, 16, "heads", [300, 77], dict(cap=12.0)),
+    (F32, E4, 6, 2, 64, 16, 16, "heads", [300, 77], dict(slopes=True)),
+    (F32, I8, 12, 2, 64, 32, 16, "slots", [900, 2], dict(cap=10.0)),
+    # many units, split and whole: two CTAs an SM
+    (BF, E4, 16, 16, 64, 32, 32, "slots", [random.Random(5).randint(0, 3000) for _ in range(30)], {}),
+    (F32, I8, 32, 8, 64, 32, 32, "slots", [random.Random(6).randint(0, 2500) for _ in range(45)], {}),
+    (F32, E4, 8, 8, 128, 64, 64, "heads", [random.Random(7).randint(0, 900) for _ in range(25)], {}),
+    (BF, I8, 16, 8, 128, 16, 16, "slots", [random.Random(8).randint(0, 1500) for _ in range(60)], dict(cap=25.0, slopes=True)),
 ]
 
 
@@ -402,6 +413,44 @@ def test_attention_tiny_and_zero_value_scales(bnd, dtype):
     got = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
     ref, tol = C.attention(q, kp, ks, vp, vs, table, [n], hk)
     R.check(got, ref, tol, "one tiny block")
+
+
+@pytest.mark.parametrize("dtype,d,hk", [(BF, 128, 1), (F32, 64, 2)])
+@pytest.mark.parametrize("cap", [1e-38, 1e-6, 1e6, 1e25, 3e38])
+def test_attention_caps_of_any_size(bnd, dtype, d, hk, cap):
+    """A cap far above the scores changes nothing, far below it leaves the mean; small and large scales of keys under it."""
+    h, page, n = 4, 16, 900
+    table, n_pages = table_of(2, 1, -(-n // page))
+    kp, ks = pages_of(44, n_pages, page, 16, hk, d, E4)
+    vp, vs = pages_of(45, n_pages, page, 16, hk, d, E4)
+    for up in (1.0, 2.0 ** -40, 2.0 ** 40):
+        q = (randn(46, 1, h, d, dtype=F32) * 3.0 / up).to(dtype)
+        k2 = ks * up
+        got = run_attention(bnd, q, kp, k2, vp, vs, table, [n], hk, cap=cap)
+        # caps beyond 2^100 are taken as 2^100, below 2^-100 as that
+        kept = min(max(cap, 2.0 ** -100), 2.0 ** 100)
+        plain = kept > 1e20      # fp64 itself loses cap * tanh(s / cap) = s far above s
+        ref, tol = C.attention(q, kp, k2, vp, vs, table, [n], hk, cap=0.0 if plain else kept)
+        if cap >= 1e6:           # off by 2^-20 of the score, not of the cap
+            ref2, tol = C.attention(q, kp, k2, vp, vs, table, [n], hk)
+            assert (ref2 - ref).abs().max() <= 1e-9
+            tol = tol + 2.0 ** -19 * 60.0 * vs.max().item() * 448.0
+        R.check(got, ref, tol, str((cap, up)))
+
+
+def test_attention_key_codes_that_are_nan(bnd):
+    """A NaN code of a key reaches its key head's queries only, whichever heads share a tile."""
+    for h, hk in ((4, 4), (8, 2), (12, 2), (2, 1)):
+        d, page, n = 64, 16, 300
+        table, n_pages = table_of(1, 1, -(-n // page))
+        kp, ks = pages_of(64, n_pages, page, 16, hk, d, E4)
+        vp, vs = pages_of(65, n_pages, page, 16, hk, d, E4)
+        q = randn(66, 1, h, d, dtype=BF)
+        clean = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
+        kp.view(torch.uint8)[table[0, 2].long(), 5, 0, 3] = 0x7f
+        got = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
+        g = h // hk
+        assert torch.isnan(got[:, :g]).all() and torch.equal(got[:, g:], clean[:, g:])
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])

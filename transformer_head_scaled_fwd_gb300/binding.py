@@ -488,6 +488,8 @@ def make_coded_cache(k_pages, v_pages, k_scales, v_scales, block_table):
     _want(block_table, "block_table", _i32, block_table.shape, dev)
     if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
         raise ValueError("block_table must be [B, max_pages] with adjacent rows")
+    if k_scales.dim() != 3:
+        raise ValueError("k_scales must be [n_pages, blocks of a page, h_kv]")
     blocks = k_scales.shape[1]
     if blocks < 1 or size % blocks != 0:
         raise ValueError(f"k_scales has {blocks} blocks a page, which do not divide its {size} slots")
@@ -671,6 +673,8 @@ def mha_paged_resize(held, want, *, block_table, page_size: int, free_pages, fre
         raise ValueError("the rows of block_table must be adjacent")
     sp, T = None, 0
     if slots is not None:
+        if slots.dim() != 2:
+            raise ValueError("slots must be [B, T]")
         T = slots.shape[1]
         _want(slots, "slots", _i64, (B, T), dev)
         if not slots.is_contiguous():

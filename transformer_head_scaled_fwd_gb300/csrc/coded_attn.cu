@@ -100,7 +100,7 @@ struct WarpCoded {
     uint32_t q[kQT][kD / 16][kTiles][2];
     float o[kRow / 16][kOfChunk][4];     // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
     // of those two heads: maximum of the scores, and of score + scale's exponent; 2^(m - mo + kBase); this lane's share of the
-    // sum; the bias' slope; what takes a product to a score
+    // sum; the bias' slope; what takes a product to a score (capped: to q.k)
     float m[kTiles][2], mo[kTiles][2], u[kTiles][2], l[kTiles][2], slope[kTiles][2], in[kTiles][2];
     bool biased;
     int each;                       // query heads of a key head, kHeads = 2
@@ -142,7 +142,7 @@ struct WarpCoded {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) raw[nt][k].e[e] = x[nt][16 * k + e];
         }
-        const float form_in = p.cap > 0.0f ? p.scale / p.cap : p.scale * kLog2e;
+        const float form_in = p.cap > 0.0f ? 1.0f : p.scale * kLog2e;        // capped: below, so that scale / cap meets a whole score
 #pragma unroll
         for (int nt = 0; nt < kTiles; ++nt) {
             float f[kD / 16][4];
@@ -258,7 +258,7 @@ struct WarpCoded {
                 for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        s[t][nt][e] = kWide ? form.top * tanhf(s[t][nt][e]) : capped_score(s[t][nt][e], form.top);
+                        s[t][nt][e] = kWide ? form.top * tanhf(s[t][nt][e] * form.in) : capped_score(s[t][nt][e] * form.in, form.top);
         }
         if (biased) {
 #pragma unroll
