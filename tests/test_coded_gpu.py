@@ -87,6 +87,12 @@ APPEND = [
     (F32, E4, 257, 2, 2, 128, 100, False, 256, 256, "heads", [1, 255], None),
     (F32, I8, 100, 1, 3, 64, 62, False, 32, 16, "slots", [17], None),
     (F32, E4, 1, 9, 3, 128, 128, False, 32, 32, "slots", list(range(40)), None),
+    # numbers of heads that do not divide among CTAs
+    (BF, E4, 363, 15, 5, 128, 50, False, 128, 64, "slots", [1, 0, 70], None),
+    (F32, I8, 300, 7, 3, 64, 64, True, 64, 64, "slots", [5], None),
+    (BF, I8, 200, 11, 1, 128, 64, False, 32, 16, "slots", [3, 40], [200, 133]),
+    (F32, E4, 513, 32, 8, 128, 64, False, 64, 64, "heads", [2], None),
+    (BF, E4, 2, 64, 16, 64, 20, False, 256, 256, "slots", [254, 255, 256, 0, 13], None),
 ]
 
 

@@ -6,7 +6,10 @@
 // that is in part filled, whose codes are then rounded again, which in e4m3 is exact but for subnormals. The maximum
 // carries a NaN, so that or an infinity in a block makes its scale NaN.
 //
-// HBM-bound: q and k read and written, v read, codes written: 24.5 KB a token at 32 + 8 heads of 128 in bf16.
+// HBM-bound: q and k read and written, v read, codes written: 24.5 KB a token at 32 + 8 heads of 128 in bf16. Measured, 4 x 8192 of those,
+// blocks of 64: half of each head turned 137-141 us (805 MB, 5.7-5.9 TB/s, 0.86 of measured copy bandwidth), nothing turned 125, all 160, halves
+// of odd length (126) 270; 16 + 16 heads of 64 98 us; blocks of 16 136, of 8 146, of 4 184, of 256 192 (rows read twice). One token 4.5 us,
+// 61 sequences of one token 4.5 us, 7 x 333 in fp32 6.2 us.
 //
 // A CTA takes a tile of neighbouring blocks of one sequence and a part of the heads. It computes the tile's cos and sin into shared
 // memory, then its teams of warps take (block, key head) tasks of keys and of values: a row of d_k elements is
@@ -34,10 +37,11 @@ constexpr float kLeast = 0x1p-120f;     // least scale
 struct TilePlan {
     int tiles;          // of a sequence
     int blocks;         // of a tile
-    int parts;          // of the heads
-    int kv_heads;       // of a part
+    int tokens;         // of a tile, at most
+    int parts;          // of the heads: as many CTAs a tile
+    int kv_heads;       // of a part; the last may have fewer, or none
+    FastDiv q_heads;    // of a part, equal for all
     FastDiv half;       // pairs that turn
-    FastDiv q_heads;
     int team;           // warps of a task
     int stride;         // floats of a token's row of cos (and of sin)
 };
@@ -167,10 +171,11 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
     // ---- A task is a block, a key head, and its keys or its values; a step of it is kKeep passes of rows. Behind those come steps of rows of
     // queries. Steps come into shared memory by asynchronous copies, the next one's while one is worked on; a lane reads what it
     // has copied.
-    const int h0 = part * plan.kv_heads, q0 = part * static_cast<int>(plan.q_heads.d);
-    const int tasks = plan.blocks * plan.kv_heads * 2, teams = kWarps / plan.team;
+    const int h0 = part * plan.kv_heads, kv_heads = max(min(plan.kv_heads, p.h_kv - h0), 0);
+    const int q_heads = static_cast<int>(plan.q_heads.d), q0 = part * q_heads;
+    const int tasks = plan.blocks * kv_heads * 2, teams = kWarps / plan.team;
     const int team = warp / plan.team, member = warp - team * plan.team;
-    const int q_rows = p.q.p != nullptr ? tokens * static_cast<int>(plan.q_heads.d) : 0;
+    const int q_rows = q0 < p.h ? tokens * q_heads : 0;
     enum { kKeys, kValues, kQueries };
     struct Step {
         int kind, task;             // kQueries: task is the first row, of all rows of queries
@@ -182,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
         for (; x.task < tasks; x.task += teams) {
             x.kind = x.task & 1;
             const int n = x.task >> 1;
-            x.block = plan.blocks == 1 ? 0 : n / plan.kv_heads;
-            x.head = h0 + n - x.block * plan.kv_heads;
+            x.block = plan.blocks == 1 ? 0 : n / kv_heads;
+            x.head = h0 + n - x.block * kv_heads;
             const long long first = (blk0 + x.block) * block;
             x.from = static_cast<int>(max(first - start, static_cast<long long>(t0)));
             x.to = static_cast<int>(min(first + block - start, static_cast<long long>(t1)));
@@ -205,19 +210,23 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
         }
     };
     auto pending = [&](const Step& x) { return x.kind != kQueries || x.task < q_rows; };
-    // a lane's token in the first pass of a step of keys or values; the next pass is `apart` tokens further
+    // a lane's token in pass i of a step of keys or values, at or behind x.to where there is none
     const int apart = plan.team * kRows;
-    auto token_of = [&](const Step& x) { return x.from + (x.round() * kKeep * plan.team + member) * kRows + lr; };
+    auto token_of = [&](const Step& x, int i) {
+        return x.from + (x.round() * kKeep * plan.team + member) * kRows + lr + i * apart;
+    };
     const uint32_t mine = smem_u32(smem) + warp * (2 * kStep) + lane * 16;
     auto fetch = [&](const Step& x, int buffer) {
         const uint32_t to = mine + buffer * kStep;
         if (x.kind != kQueries) {
             const Strided& in = x.kind == kValues ? p.v : p.k;
-            const int t = token_of(x);
-            const T* row = static_cast<const T*>(in.p) + b * in.b + x.head * in.h + t * in.l;
+            const T* rows = static_cast<const T*>(in.p) + b * in.b + x.head * in.h;
+            const T* first = rows + token_of(x, 0) * in.l;
 #pragma unroll
-            for (int i = 0; i < kKeep; ++i, row += apart * in.l) {
-                if (t + i * apart >= x.to) break;
+            for (int i = 0; i < kKeep; ++i) {
+                const int t = token_of(x, i);
+                if (t >= x.to) continue;
+                const T* row = first + i * (apart * in.l);
                 cp_async16(to + i * 1024, row + c0, true);
                 cp_async16(to + i * 1024 + 512, row + c1, true);
             }
@@ -227,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
                 const int r = x.task + i * kRows + lr;
                 if (r >= q_rows) break;
                 const int t = plan.q_heads.div(r);
-                const T* row = static_cast<const T*>(p.q.p) + b * p.q.b + (t0 + t) * p.q.l + (q0 + r - t * static_cast<int>(plan.q_heads.d)) * p.q.h;
+                const T* row = static_cast<const T*>(p.q.p) + b * p.q.b + (t0 + t) * p.q.l + (q0 + r - t * q_heads) * p.q.h;
                 cp_async16(to + i * 1024, row + c0, true);
                 cp_async16(to + i * 1024 + 512, row + c1, true);
             }
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
 
     // ---- cos and sin of the tile, [tokens][stride] each; where the blocks lie
     float* cosines = reinterpret_cast<float*>(smem + kWarps * 2 * kStep);
-    float* sines = cosines + plan.blocks * block * plan.stride;
+    float* sines = cosines + plan.tokens * plan.stride;
     const int span = plan.stride;
     if (kTurn != kNone) {
         for (int i = tid; i < tokens * span; i += kThreads) {
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
         info[i] = x;
     }
 
-    float* stage = sines + plan.blocks * block * plan.stride + warp * (kRows * kD);       // kStaged: a pass of rows
+    float* stage = sines + plan.tokens * plan.stride + warp * (kRows * kD);       // kStaged: a pass of rows
     __syncthreads();
 
     auto turn = [&](float (&x)[kN], float (&y)[kN], int t, bool on) {
@@ -338,6 +347,45 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
 
     int flip = 0, buffer = 0;
     float top = 0.0f, scale = 1.0f;
+    // A block's scale, from the largest of its new values: written, and the codes in front of them rounded again where it grows.
+    auto settle_scale = [&](const Step& x, uint32_t most) {
+        if (plan.team > 1) {
+            if (lane == 0) peak[flip][warp] = most;
+            named_bar_sync(1 + team, 32 * plan.team);
+            for (int i = 0; i < plan.team; ++i) most = max(most, peak[flip][team * plan.team + i]);
+            flip ^= 1;                             // the other half is free: its readers have passed this barrier
+        }
+        float s = scale_for(int8, most);
+        const BlockInfo where = info[x.block];
+        const bool kept = where.slot >= 0;
+        float* scale_at = (x.kind == kValues ? p.v_scales : p.k_scales) + (kept ? where.scale + x.head : 0);
+        // slots of the block that hold earlier tokens: only of the tile's first
+        const int filled = static_cast<int>(start + x.from - (blk0 + x.block) * block);
+        if (kept && filled > 0) {
+            const float old = *scale_at;
+            if (!(old <= s)) s = isnan(s) ? s : old;     // the larger; NaN stays
+            else if (old < s) {
+                const float ratio = old / s;
+                uint8_t* codes = static_cast<uint8_t*>(x.kind == kValues ? p.cache.v : p.cache.k) + where.slot + x.head * p.cache.head_stride;
+                for (int i = member * kRows + lr; i < filled; i += apart) {
+                    uint8_t* row = codes + i * p.cache.slot_stride;
+#pragma unroll 1
+                    for (int e = 0; e < 2 * kN; e += 4) {
+                        uint32_t* w = reinterpret_cast<uint32_t*>(row + (e < kN ? c0 + e : c1 + e - kN));
+                        const uint32_t c = *w;
+                        *w = code4(int8, value_of(int8, c & 0xffu) * ratio, value_of(int8, (c >> 8) & 0xffu) * ratio,
+                                   value_of(int8, (c >> 16) & 0xffu) * ratio, value_of(int8, c >> 24) * ratio);
+                    }
+                }
+            }
+        }
+        // every warp of the team has read the old scale before one writes the new
+        if (plan.team > 1 && filled > 0) named_bar_sync(1 + team, 32 * plan.team);
+        else __syncwarp();
+        if (kept && member == 0 && lane == 0) *scale_at = s;
+        return s;
+    };
+
     while (pending(now)) {
         Step next = now;
         advance(next);
@@ -357,96 +405,70 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
                 raw.values(x, y);
                 turn(x, y, t, on);
                 if (!on) continue;
-                T* row = static_cast<T*>(p.q_out.p) + b * p.q_out.b + (t0 + t) * p.q_out.l + (q0 + r - t * static_cast<int>(plan.q_heads.d)) * p.q_out.h;
+                T* row = static_cast<T*>(p.q_out.p) + b * p.q_out.b + (t0 + t) * p.q_out.l + (q0 + r - t * q_heads) * p.q_out.h;
                 store_chunk(row + c0, x);
                 store_chunk(row + c1, y);
             }
         } else {
-            const long long first = (blk0 + now.block) * block;
-            const int t = token_of(now);
             float x[kKeep][kN], y[kKeep][kN];
+            float most[kKeep];
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                const bool on = t + i * apart < now.to;
+                const int t = token_of(now, i);
+                const bool on = t < now.to;
                 Pair<T> raw;
                 raw.load_shared(at + i * 1024, on);
                 raw.values(x[i], y[i]);
-                if (now.kind == kKeys) turn(x[i], y[i], min(t + i * apart, now.to - 1) - t0, on);
+                if (now.kind == kKeys) turn(x[i], y[i], min(t, now.to - 1) - t0, on);
+                float m = 0.0f;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) m = most3(m, x[i][e], y[i][e]);
+                most[i] = m;
             }
             if (now.step == 0) top = 0.0f;
             if (now.step < now.rounds) {
 #pragma unroll
-                for (int i = 0; i < kKeep; ++i)
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) top = most3(top, x[i][e], y[i][e]);
+                for (int i = 0; i < kKeep; ++i) top = most3(top, most[i], 0.0f);
             }
+            if (now.step == now.rounds - 1) scale = settle_scale(now, __reduce_max_sync(0xffffffffu, __float_as_uint(top)));      // NaN is above all
             if (now.step >= now.rounds - 1) {
-                const BlockInfo where = info[now.block];
-                const bool kept = where.slot >= 0;
-                uint8_t* codes = static_cast<uint8_t*>(now.kind == kValues ? p.cache.v : p.cache.k) + (kept ? where.slot + now.head * p.cache.head_stride : 0);
-                if (now.step == now.rounds - 1) {
-                    uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));      // NaN is above all
-                    if (plan.team > 1) {
-                        if (lane == 0) peak[flip][warp] = most;
-                        named_bar_sync(1 + team, 32 * plan.team);
-                        for (int i = 0; i < plan.team; ++i) most = max(most, peak[flip][team * plan.team + i]);
-                        flip ^= 1;                             // the other half is free: its readers have passed this barrier
-                    }
-                    scale = scale_for(int8, most);
-                    float* scale_at = (now.kind == kValues ? p.v_scales : p.k_scales) + (kept ? where.scale + now.head : 0);
-                    const int filled = static_cast<int>(start + now.from - first);       // slots of the block that hold earlier tokens
-                    if (kept && filled > 0) {
-                        const float old = *scale_at;
-                        if (!(old <= scale)) scale = isnan(scale) ? scale : old;     // the larger; NaN stays
-                        else if (old < scale) {
-                            const float ratio = old / scale;
-                            for (int i = member * kRows + lr; i < filled; i += plan.team * kRows) {
-                                uint8_t* row = codes + i * p.cache.slot_stride;
-    #pragma unroll 1
-                                for (int e = 0; e < 2 * kN; e += 4) {
-                                    uint32_t* w = reinterpret_cast<uint32_t*>(row + (e < kN ? c0 + e : c1 + e - kN));
-                                    const uint32_t c = *w;
-                                    *w = code4(int8, value_of(int8, c & 0xffu) * ratio, value_of(int8, (c >> 8) & 0xffu) * ratio,
-                                               value_of(int8, (c >> 16) & 0xffu) * ratio, value_of(int8, c >> 24) * ratio);
-                                }
-                            }
-                        }
-                    }
-                    // every warp of the team has read the old scale before one writes the new
-                    if (plan.team > 1 && filled > 0) named_bar_sync(1 + team, 32 * plan.team);
-                    else __syncwarp();
-                    if (kept && member == 0 && lane == 0) *scale_at = scale;
-                }
+                const int t_first = token_of(now, 0);
                 if (now.kind == kKeys && p.k_out.p != nullptr) {
-                    T* row = static_cast<T*>(p.k_out.p) + b * p.k_out.b + now.head * p.k_out.h + t * p.k_out.l;
+                    T* rows = static_cast<T*>(p.k_out.p) + b * p.k_out.b + now.head * p.k_out.h;
+                    T* first = rows + t_first * p.k_out.l;
 #pragma unroll
-                    for (int i = 0; i < kKeep; ++i, row += apart * p.k_out.l) {
-                        if (t + i * apart >= now.to) break;
+                    for (int i = 0; i < kKeep; ++i) {
+                        const int t = token_of(now, i);
+                        if (t >= now.to) continue;
+                        T* row = first + i * (apart * p.k_out.l);
                         store_chunk(row + c0, x[i]);
                         store_chunk(row + c1, y[i]);
                     }
                 }
-                if (kept) {
-                    const float inv = 1.0f / scale;
-                    const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
-                    uint8_t* row = codes + static_cast<int>(start + t - first) * p.cache.slot_stride;
+                const BlockInfo where = info[now.block];
+                if (where.slot < 0) now.to = 0;          // nothing is stored
+                uint8_t* const pages = static_cast<uint8_t*>(now.kind == kValues ? p.cache.v : p.cache.k) + now.head * p.cache.head_stride;
+                uint8_t* const first = pages + where.slot + static_cast<int>(start + t_first - (blk0 + now.block) * block) * p.cache.slot_stride;
+                const float inv = 1.0f / scale;
+                const bool power = (__float_as_uint(scale) & 0x7fffffu) == 0;
 #pragma unroll
-                    for (int i = 0; i < kKeep; ++i, row += apart * p.cache.slot_stride) {
-                        if (t + i * apart >= now.to) break;
-                        divide(x[i], y[i], scale, inv, power);
-                        uint32_t u[kN / 4], v[kN / 4];
+                for (int i = 0; i < kKeep; ++i) {
+                    const int t = token_of(now, i);
+                    if (t >= now.to) continue;
+                    uint8_t* row = first + i * (apart * p.cache.slot_stride);
+                    divide(x[i], y[i], scale, inv, power);
+                    uint32_t u[kN / 4], v[kN / 4];
 #pragma unroll
-                        for (int e = 0; e < kN / 4; ++e) {
-                            u[e] = code4(int8, x[i][4 * e], x[i][4 * e + 1], x[i][4 * e + 2], x[i][4 * e + 3]);
-                            v[e] = code4(int8, y[i][4 * e], y[i][4 * e + 1], y[i][4 * e + 2], y[i][4 * e + 3]);
-                        }
-                        if constexpr (kN == 8) {
-                            *reinterpret_cast<uint2*>(row + c0) = make_uint2(u[0], u[1]);
-                            *reinterpret_cast<uint2*>(row + c1) = make_uint2(v[0], v[1]);
-                        } else {
-                            *reinterpret_cast<uint32_t*>(row + c0) = u[0];
-                            *reinterpret_cast<uint32_t*>(row + c1) = v[0];
-                        }
+                    for (int e = 0; e < kN / 4; ++e) {
+                        u[e] = code4(int8, x[i][4 * e], x[i][4 * e + 1], x[i][4 * e + 2], x[i][4 * e + 3]);
+                        v[e] = code4(int8, y[i][4 * e], y[i][4 * e + 1], y[i][4 * e + 2], y[i][4 * e + 3]);
+                    }
+                    if constexpr (kN == 8) {
+                        *reinterpret_cast<uint2*>(row + c0) = make_uint2(u[0], u[1]);
+                        *reinterpret_cast<uint2*>(row + c1) = make_uint2(v[0], v[1]);
+                    } else {
+                        *reinterpret_cast<uint32_t*>(row + c0) = u[0];
+                        *reinterpret_cast<uint32_t*>(row + c1) = v[0];
                     }
                 }
             }
@@ -465,22 +487,36 @@ cudaError_t launch_n(const CodedAppendParams& p, cudaStream_t s) {
     // tiles of about kTile tokens, so that cos and sin serve many heads and a CTA has rows for all its warps; of one block where
     // that is longer
     plan.blocks = std::max(1, std::min(kTile, p.T) / block);
+    plan.tokens = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(plan.blocks) * block, p.T));
     const int64_t most = (static_cast<int64_t>(p.T) + block - 2) / block + 1;         // blocks that T tokens touch
     plan.tiles = static_cast<int>((most + plan.blocks - 1) / plan.blocks);
     plan.team = 1;
     while (plan.team < kWarps && std::min(block, p.T) > plan.team * kRows * kKeep) plan.team *= 2;
-    // equal parts of the heads, while the CTAs are fewer than four an SM
-    plan.parts = 1;
-    while (p.h_kv % (2 * plan.parts) == 0 && p.h % (2 * plan.parts) == 0 && static_cast<int64_t>(p.B) * plan.tiles * plan.parts < 152 * 4)
-        plan.parts *= 2;
-    plan.kv_heads = p.h_kv / plan.parts;
-    plan.q_heads = fast_div(static_cast<uint32_t>(std::max(p.h / plan.parts, 1)));
+    // Parts of the heads: where tiles are fewer than one wave of two CTAs an SM, to fill that, and no further for a few tokens a sequence
+    // (61 x 1, 32 / 8 heads of 128: 4.4 us, twice as many CTAs 8.7); where they are more, to three waves, whose ends even out (4 x 8192 ragged, 516
+    // tiles: two parts 105 us, one 113). Short blocks are many tasks a CTA: two waves (9 x 397 in blocks of 4, 16 heads of 64: 57 -> 30 us).
+    constexpr int64_t kWave = 2 * 152;
+    const int64_t alone = static_cast<int64_t>(p.B) * plan.tiles;
+    const int64_t wanted = alone >= kWave ? (3 * kWave + alone - 1) / alone
+                           : p.T < kTile  ? kWave / alone
+                                          : ((block <= kRows ? 2 : 1) * kWave + alone - 1) / alone;
+    const int heads = std::max(p.h_kv, p.h), parts = static_cast<int>(std::min<int64_t>(wanted, heads));
+    auto each = [&](int h, int n) { return (h + n - 1) / n; };
+    plan.kv_heads = each(p.h_kv, std::min(parts, p.h_kv));
+    // equal numbers of query heads: the next divisor of theirs, unless that is far
+    int q_parts = std::min(parts, std::max(p.h, 1));
+    while (p.h % q_parts != 0 && q_parts < 4 * parts) ++q_parts;
+    while (p.h % q_parts != 0) --q_parts;
+    plan.q_heads = fast_div(static_cast<uint32_t>(std::max(p.h / q_parts, 1)));
+    plan.parts = std::max(each(p.h_kv, plan.kv_heads), p.h > 0 ? q_parts : 1);
     plan.stride = (half + kN - 1) / kN * kN;
     plan.half = fast_div(static_cast<uint32_t>(std::max(half, 1)));
     const Turn turn = half == 0 ? kNone : p.interleaved != 0 ? kNeighbours : half % kN == 0 ? kHalves : kStaged;
-    const size_t smem = kWarps * 2 * kKeep * 1024 + static_cast<size_t>(plan.blocks) * block * plan.stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
-    const auto kernel = turn == kNone ? coded_append_kernel<T, kD, kNone> : turn == kNeighbours ? coded_append_kernel<T, kD, kNeighbours>
-                        : turn == kHalves ? coded_append_kernel<T, kD, kHalves> : coded_append_kernel<T, kD, kStaged>;
+    const size_t smem = kWarps * 2 * kKeep * 1024 + static_cast<size_t>(plan.tokens) * plan.stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
+    const auto kernel = turn == kNone         ? coded_append_kernel<T, kD, kNone>
+                        : turn == kNeighbours ? coded_append_kernel<T, kD, kNeighbours>
+                        : turn == kHalves     ? coded_append_kernel<T, kD, kHalves>
+                                              : coded_append_kernel<T, kD, kStaged>;
     {        // up to 211 KB: 256 tokens, 64 pairs
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
