@@ -15,6 +15,12 @@
 // result), for an fp32 result taken as two fp16 terms (2^-22). p_j itself is summed in fp32.
 //
 // Work split, loads and join: paged_line.cuh; a step is 32 keys.
+//
+// Measured: 16 sequences of 8192, 16 heads of 64, e4m3, 268 MB: 52 us, 5.2 TB/s (0.77 of measured copy bandwidth; a bf16 cache takes 89); 24 of 15000,
+// 32 / 8 heads of 128, 737 MB: 120 us (0.92); 48 ragged ones up to 15000, int8, capped, 790 MB: 142 us (0.83); one of 131071, 16 / 2 heads: 22 us,
+// of which 10 are its traffic. A step costs a warp 2700 cycles, 1000 of them to issue its copies and 1400 to compute; at eight warps
+// an SM that is what HBM delivers, so long streams run at its rate and the rest is what any call has: the look-ups 1.7 + 3 us, the queries 1, a
+// unit's end 1.7, the second launch and the join 3.7.
 #include "paged_line.cuh"
 
 namespace mha {
