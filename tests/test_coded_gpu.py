@@ -481,6 +481,72 @@ def test_attention_queries_of_any_size(bnd, dtype):
         R.check(got, ref, tol, str(up))
 
 
+@pytest.mark.parametrize("dtype,h,hk,d", [(BF, 4, 2, 64), (F32, 3, 1, 128)])
+def test_attention_codes_and_scales_of_other_origin(bnd, dtype, h, hk, d):
+    """The code -128, key scales of 0 (equal scores) beside others, lengths below 0, another stream."""
+    page, n = 16, 200
+    table, n_pages = table_of(3, 3, -(-n // page))
+    kp, ks = pages_of(47, n_pages, page, 16, hk, d, I8)
+    vp, vs = pages_of(48, n_pages, page, 16, hk, d, I8)
+    kp[kp > 60] = -128
+    vp[vp > 60] = -128
+    ks[::3] = 0.0
+    q = randn(49, 3, h, d, dtype=dtype)
+    lens = [n, -7, 33]
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, lens, hk)
+    ref, tol = C.attention(q, kp, ks, vp, vs, table, lens, hk)
+    R.check(got, ref, tol, "other origin")
+    assert not got[1].any()
+    side, out = torch.cuda.Stream(), torch.full_like(q, float("nan"))
+    dt = bnd.MHA_BF16 if dtype == BF else bnd.MHA_F32
+    ws = torch.zeros(bnd.coded_attention_workspace_size(dt, 3, h, hk, d), dtype=torch.uint8, device="cuda")
+    cache, kv_lens = bnd.make_coded_cache(kp, vp, ks, vs, table), ints(lens)
+    torch.cuda.synchronize()
+    bnd.mha_coded_attention(q, kv_lens, cache=cache, out=out, workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(out, got)
+    # appended to: codes rounded again from -128
+    x = randn(50, 3, 1, hk, d, dtype=dtype) * 1e4
+    before = C.values(kp, ks)
+    held = [199, 0, 33]
+    bnd.mha_coded_append(x, x, ints(held), cache=cache, new_lens=ints([1, 0, 1]), stream=side)
+    side.synchronize()
+    for b in (0, 2):
+        pg, sl = table[b, held[b] // page].item(), held[b] % page
+        now = C.values(kp, ks)[pg]
+        R.check(now[:sl], before[pg, :sl], (ks[pg].double() / 2)[..., None].expand(sl, hk, d), "rounded again")
+        R.check(now[sl], x[b, 0].double(), C.half_step(x[b, 0].double(), ks[pg, 0].double()[:, None], I8), "appended")
+
+
+def test_two_calls_at_once(bnd):
+    """Attention and append of two batches on two streams, a workspace each: as one after the other."""
+    B, h, hk, d, page, n = 6, 8, 2, 128, 16, 3000
+    sets = []
+    for i in range(2):
+        table, n_pages = table_of(i, B, -(-n // page) + 1)
+        kp, ks = pages_of(60 + i, n_pages, page, 16, hk, d, E4)
+        vp, vs = pages_of(70 + i, n_pages, page, 16, hk, d, E4)
+        ws = torch.zeros(bnd.coded_attention_workspace_size(bnd.MHA_BF16, B, h, hk, d), dtype=torch.uint8, device="cuda")
+        q, x = randn(80 + i, B, h, d, dtype=BF), randn(90 + i, B, 1, hk, d, dtype=BF)
+        sets.append((bnd.make_coded_cache(kp, vp, ks, vs, table), q, x, ints([n - 37 * b for b in range(B)]), ws, torch.zeros_like(q)))
+    def both(streams):
+        for (cache, q, x, lens, ws, out), s in zip(sets, streams):
+            bnd.mha_coded_append(x, x, lens, cache=cache, stream=s)
+            bnd.mha_coded_attention(q, lens, cache=cache, out=out, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    both(streams)
+    torch.cuda.synchronize()
+    first = [s[5].clone() for s in sets]
+    for _ in range(5):
+        both(streams)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, s[5]) for a, s in zip(first, sets))
+    for (cache, q, x, lens, ws, out), f in zip(sets, first):
+        bnd.mha_coded_attention(q, lens, cache=cache, out=out, workspace=ws)
+        assert torch.equal(out, f)
+
+
 def test_attention_large_scores_and_shared_pages(bnd):
     h, hk, d, page = 4, 2, 64, 16
     kp, ks = pages_of(50, 40, page, 16, hk, d, E4)
@@ -602,6 +668,7 @@ RESIZE = [
     # B, room, pages, page size, T, most new, steps
     (1, 1, 1, 1, 1, 1, 6), (1, 40, 30, 16, 1, 1, 40), (3, 8, 11, 4, 5, 9, 30), (16, 70, 400, 16, 1, 1, 25), (5, 100, 300, 7, 33, 300, 20),
     (512, 9, 2000, 8, 2, 20, 6), (513, 9, 2000, 8, 3, 20, 6), (1500, 5, 4000, 24, 1, 60, 6), (64, 300, 9000, 16, 700, 3000, 4), (2, 5000, 9000, 1, 4000, 4500, 5),
+    (40, 300, 6000, 16, 3500, 3400, 3), (1, 3000, 2900, 64, 140000, 150000, 3), (700, 12, 5000, 16, 190, 200, 3),       # slots by a kernel of their own
 ]
 
 
@@ -643,6 +710,29 @@ def test_resize_the_pool_runs_dry_in_order(bnd):
     assert pool.step([0] * 5, [4, 8, 8, 1, 0], 9) == [4, 8, 0, 0, 0]        # one page is left: two are wanted, then one
     assert pool.step([4, 8, 0, 0, 0], [4, 7, 0, 4, 0], 4) == [4, 7, 0, 4, 0]
     assert pool.step([4, 7, 0, 4, 0], [0, 8, 4, 4, 5], 4) == [0, 8, 4, 4, 0]   # the page given back serves; two more do not fit
+
+
+def test_resize_many_slots_with_a_bad_page(bnd):
+    """The slots of many tokens are a second kernel's: a page number outside the pool gives none there either."""
+    pool = Pool(bnd, 3, 400, 1200, 128, free=1100)
+    pool.table[1, 0] = 5000
+    pool.step([0, 100, 0], [51200, 51000, 1], 51200)
+    assert bnd.mha_check_device_status(reset=True) == bnd.MHA_PAGED_BAD_PAGE
+
+
+def test_resize_on_another_stream(bnd):
+    """The same step in the default stream and, by the stream argument, in another; held and want may be one array."""
+    got = []
+    for stream in (None, torch.cuda.Stream()):
+        pool = Pool(bnd, 4, 8, 20, 4)
+        want, slots = ints([3, 9, 0, 31]), torch.zeros(4, 5, dtype=torch.int64, device="cuda")
+        torch.cuda.synchronize()
+        for held in (ints([0, 0, 0, 0]), want):
+            bnd.mha_paged_resize(held, want, block_table=pool.table, page_size=4, free_pages=pool.stack, free_count=pool.count, lens=pool.lens,
+                                 new_lens=pool.new, slots=slots if held is not want else None, stream=stream)
+        torch.cuda.synchronize()
+        got.append((pool.table.tolist(), pool.count.item(), pool.lens.tolist(), pool.new.tolist(), slots.tolist()))
+    assert got[0] == got[1] and got[0][1:4] == (8, [3, 9, 0, 31], [0, 0, 0, 0])
 
 
 def test_resize_reports_what_is_out_of_range(bnd):
