@@ -443,7 +443,7 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
 
 /*
  * The block table of a paged cache as sequences grow, shrink and end, on the device: sequence b goes from held[b] to want[b]
- * positions (device int32 [B]; below 0: 0), so from ceil(held / page_size) to ceil(want / page_size) pages.
+ * positions (device int32 [B], B <= 2^24; below 0: 0), so from ceil(held / page_size) to ceil(want / page_size) pages.
  *   free_pages  device int32 [n_pages], a stack: entries 0 .. *free_count - 1 are the free pages; the two are updated.
  *   Sequences that shrink (want 0: end) give their last pages back: entry by entry pushed so that the first sequence's first
  *   page ends on top, and -1 in the table. Then those that grow take pages from the top in the order of the sequences, the first
@@ -457,7 +457,7 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
  * A call with held and want exchanged takes a step back, the stack included. Entries of the table that a call does not name, and
  * of the stack above the pages given back, are left as they were. A page number outside [0, n_pages) moves as it is, gives no slot
  * and records MHA_PAGED_BAD_PAGE, and so does a stack that pages given back would overflow (the ones beyond n_pages are
- * dropped). lens and new_lens are neither held nor want. Calls that share a table or a stack are ordered by the caller.
+ * dropped). lens and new_lens overlap neither held nor want nor each other. Calls that share a table or a stack are ordered by the caller.
  */
 mha_status_t mha_paged_resize(const int32_t* held, const int32_t* want, int B, int page_size,
                               int32_t* block_table, int64_t table_stride, int max_pages,

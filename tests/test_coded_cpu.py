@@ -98,6 +98,20 @@ def test_resize_refusals(lib):
     assert call(new=at(1 << 19)) == INV
 
 
+def test_resize_refuses_arrays_that_overlap_and_too_many_sequences(lib):
+    def call(held, want, lens, new, B_=4):
+        return lib.mha_paged_resize(held, want, B_, 16, at(1 << 28), 8, 8, at(1 << 17), 100, at(1 << 18), lens, new, 0, None, None)
+    base = 1 << 19
+    for off in (4, 12):
+        for sign in (1, -1):
+            near = at(base + sign * off)
+            assert call(at(base), at(8192), near, None) == INV and b"of their own" in lib.mha_last_error(), (off, sign)
+            assert call(at(8192), at(base), near, None) == INV
+            assert call(at(base), at(8192), at(1 << 20), near) == INV
+            assert call(at(8192), at(16384), at(base), near) == INV
+    assert call(at(1 << 29), at(1 << 30), at(1 << 31), None, B_=(1 << 24) + 1) == UNS
+
+
 def test_native_front_declines_what_is_no_call():
     if B.build_front() is None:
         pytest.skip("the headers of Python or torch are missing")

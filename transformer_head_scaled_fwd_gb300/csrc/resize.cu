@@ -7,7 +7,7 @@
 // the one at F - 1 - (U + i) of the F that are then free, so a step back returns the same stack. Served are those whose U + up is
 // at most F; needs are positive, so they are the first ones.
 //
-// A latency, not a bandwidth: a step of one token moves a few hundred bytes. One launch: the CTAs of a cluster each
+// A latency, not a bandwidth: a step of one token moves a few hundred bytes. One launch (a second for the slots of very many tokens): the CTAs of a cluster each
 // sum the lengths of all sequences for themselves (two loads and two scans a kThreads sequences), divide the pages and slots among them,
 // and meet at one cluster barrier: after the pages that went back are on the stack, if any did, else before the new
 // count is written. Pages are found from the flat number of a grant by bisection in the sums, so a sequence of 10^5 positions

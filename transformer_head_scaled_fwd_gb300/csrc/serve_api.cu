@@ -1,5 +1,6 @@
 // serve_api.cu -- C ABI of the serving operators declared in include/mha.h: argument checks,
 // parameter blocks and launches. Every check runs before anything is enqueued.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -311,8 +312,14 @@ mha_status_t mha_paged_resize(const int32_t* held, const int32_t* want, int B, i
                           static_cast<const void*>(new_lens)})
         if (!aligned(x, 4)) return fail(MHA_ERR_INVALID_ARG, "int32 arrays must be aligned to 4 bytes");
     if (!aligned(slots, 8)) return fail(MHA_ERR_INVALID_ARG, "slots must be aligned to 8 bytes");
-    if (lens == held || lens == want || new_lens == held || new_lens == want || lens == new_lens)
-        return fail(MHA_ERR_INVALID_ARG, "lens and new_lens must be arrays of their own");
+    if (B > 1 << 24) return fail(MHA_ERR_UNSUPPORTED, "up to 2^24 sequences (got %d)", B);
+    const int32_t* const arrays[] = {held, want, lens, new_lens};       // of B numbers; the last two are written
+    for (int i = 0; i < 4; ++i)
+        for (int j = std::max(i + 1, 2); j < 4; ++j) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i]), y = reinterpret_cast<uintptr_t>(arrays[j]);
+            if (y != 0 && (x > y ? x - y : y - x) < sizeof(int32_t) * static_cast<uintptr_t>(B))
+                return fail(MHA_ERR_INVALID_ARG, "lens and new_lens must be arrays of their own");
+        }
     mha::ResizeParams p{};
     p.held = held; p.want = want;
     p.table = block_table; p.table_stride = table_stride; p.max_pages = max_pages;
