@@ -221,6 +221,27 @@ def test_append_shows_what_is_not_finite(bnd, code):
     assert math.isnan(ks[1, 1, 1].item()) and ks[1, 1, 0].item() > 0
 
 
+@pytest.mark.parametrize("dtype,d,rot,interleaved", [(BF, 64, 22, True), (BF, 128, 36, True), (F32, 64, 6, True), (F32, 128, 70, True),
+                                                     (BF, 64, 22, False), (F32, 128, 64, False), (F32, 64, 6, False)])
+def test_append_leaves_what_does_not_turn(bnd, dtype, d, rot, interleaved):
+    """Elements behind rot_dim come out bit for bit, infinities, negative zeros and their neighbours too; a NaN is one."""
+    T, h, hk = 5, 3, 2
+    q, k = randn(1, 1, T, h, d, dtype=dtype), randn(2, 1, T, hk, d, dtype=dtype)
+    for x in (q, k):
+        for i, odd in enumerate((math.inf, -math.inf, math.nan, -0.0)):
+            x[0, i, :, rot + i] = odd
+            x[0, i, :, d - 1] = odd
+    kp, ks = torch.zeros(1, 8, hk, d, device="cuda").to(E4), torch.zeros(1, 2, hk, device="cuda")
+    vp, vs = kp.clone(), ks.clone()
+    qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+    bnd.mha_coded_append(k, k, ints([1]), cache=bnd.make_coded_cache(kp, vp, ks, vs, ints([[0]])), q=q, q_out=qo, k_out=ko,
+                         rotary=bnd.make_rotary(freqs(rot), interleaved))
+    for got, x in ((qo[..., rot:], q[..., rot:]), (ko[..., rot:], k[..., rot:])):
+        assert torch.equal(torch.isnan(got), torch.isnan(x))        # bf16: of whatever bits, conversions write their own
+        assert same(torch.nan_to_num(got, 0.0, math.inf, -math.inf), torch.nan_to_num(x, 0.0, math.inf, -math.inf))
+    assert torch.isfinite(qo[..., :rot]).all() and torch.isfinite(ko[..., :rot]).all()
+
+
 def test_append_of_extreme_sizes(bnd):
     """Values at the ends of fp32's range, and nothing but zeros."""
     page = block = 4

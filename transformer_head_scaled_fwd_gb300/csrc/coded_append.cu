@@ -251,18 +251,13 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
     // ---- cos and sin of the tile, [tokens][stride] each; where the blocks lie
     float* cosines = reinterpret_cast<float*>(smem + kWarps * 2 * kStep);
     float* sines = cosines + plan.tokens * plan.stride;
-    const int span = plan.stride;
+    const int span = half;
     if (kTurn != kNone) {
         for (int i = tid; i < tokens * span; i += kThreads) {
             const int t = i / span, e = i - t * span;
-            float2 cs = make_float2(1.0f, 0.0f);       // behind the pairs that turn
-            if (e < half) {
-                cs = turn_of(static_cast<int>(start + t0 + t), p.inv_freq[e]);
-                cs.x *= p.scale;
-                cs.y *= p.scale;
-            }
-            cosines[i] = cs.x;
-            sines[i] = cs.y;
+            const float2 cs = turn_of(static_cast<int>(start + t0 + t), p.inv_freq[e]);
+            cosines[i] = cs.x * p.scale;
+            sines[i] = cs.y * p.scale;
         }
     }
     for (int i = tid; i < plan.blocks; i += kThreads) {
@@ -326,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 2) coded_append_kernel(const __grid_
             for (int h = 0; h < 2; ++h) {
                 float (&z)[kN] = h == 0 ? x : y;
                 const int at = h == 0 ? c0 : c1;
-                if (at >= p.rot) break;
 #pragma unroll
                 for (int i = 0; i < kN; i += 2) {
+                    if (at + i >= p.rot) break;          // what does not turn stays, beside an infinity too
                     const float c = cs[(at + i) / 2], s = sn[(at + i) / 2], u = z[i], v = z[i + 1];
                     z[i] = fmaf(u, c, -(v * s));
                     z[i + 1] = fmaf(v, c, u * s);
