@@ -473,7 +473,7 @@ typedef struct {
     mha_paged_cache_t pages;   /* pages and strides aligned to 16 bytes */
     mha_code_t code;
     int block;                 /* tokens that a scale covers: divides page_size; up to 256 for the append */
-    float* k_scales;           /* device fp32 [n_pages, page_size / block, h_kv], contiguous */
+    float* k_scales;           /* device fp32 [n_pages, page_size / block, h_kv], contiguous, below 2^31 a page */
     float* v_scales;
 } mha_coded_cache_t;
 

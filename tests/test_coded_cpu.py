@@ -83,6 +83,12 @@ def test_attention_refusals(lib):
         assert lib.mha_coded_attention_workspace_size(*args) == 0
 
 
+def test_pages_of_too_many_scales_are_refused(lib):
+    big = cache_t(page_size=1 << 30, block=1, slot_stride=256)
+    assert lib.mha_coded_attention(1, P, st(), P, st(), 2, 8, 4, 64, P, None, big, P, 1 << 30, None) == UNS and b"scales" in lib.mha_last_error()
+    assert lib.mha_coded_append(1, None, None, None, None, P, st(), None, None, P, st(), 2, 3, 0, 4, 64, P, None, None, big, None) == UNS
+
+
 def test_resize_refusals(lib):
     def call(held=P, want=at(8192), B_=4, page=16, table=at(1 << 16), stride=8, most=8, free=at(1 << 17), n=100, count=at(1 << 18),
              lens=at(1 << 19), new=at(1 << 20), T=4, slots=at(1 << 21)):

@@ -132,6 +132,7 @@ mha_status_t check_coded(const mha_coded_cache_t* c, int h_kv, int d_k, mha::Pag
         return fail(MHA_ERR_INVALID_ARG, "the pages and their strides must be aligned to 16 bytes");
     *block = mha::fast_div(static_cast<uint32_t>(c->block));
     *page_scales = static_cast<int64_t>(c->pages.page_size / c->block) * h_kv;
+    if (*page_scales > 0x7fffffffll) return fail(MHA_ERR_UNSUPPORTED, "scales of a page must stay below 2^31 (%lld)", static_cast<long long>(*page_scales));
     return MHA_OK;
 }
 
