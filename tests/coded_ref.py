@@ -100,10 +100,12 @@ def attend_tol(o, mag, size, most, n, d, dtype, *, cap=0.0, far=0.0):
     """Bound of |kernel - o|: the output's half step; every weight off by a relative e^delta - 1, delta twice the error of a score: d
     products summed by the matrix instruction in fp32, whose sums may be cut where additions round (2 d 2^-24 of sum |q k|), six roundings of
     the score itself, an fp32 query as two fp16 terms (2^-22 of it), the cap's tanh to 2^-20; exp2 to 2^-21, the scale and the running maximum's factors (2^-21 each); the weight rounded
-    to fp16 (bf16 result: 2^-12; fp32: two terms, 2^-22), or, where it is subnormal there, off by 2^-25 while the largest is at least
+    to fp16 (bf16 result: 2^-11, since fp16 keeps ten bits behind the leading one: its steps in [2^e, 2^(e + 1)) are 2^(e - 10), a rounding is
+    off by half of one, 2^(e - 11), and the weight is at least 2^e; fp32: a second term holds what the first left, 2^-11 of it, and is off by
+    2^-11 of that, 2^-22), or, where it is subnormal there, off by 2^-25 while the largest is at least
     2^6 (2^-31 of `most` a key); n weights and products summed in fp32, cut or rounded (2 n 2^-24 each)."""
     delta = 2 * ((2 * d + 10) * 2.0 ** -24 * size + 6 * 2.0 ** -24 * far + cap * 2.0 ** -20)
-    weight = 2.0 ** -12 if dtype == torch.bfloat16 else 2.0 ** -22
+    weight = 2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -22
     rel = torch.expm1(delta) + 3 * 2.0 ** -20 + weight + 4 * (n + 16) * 2.0 ** -24
     return R.HALF[dtype] * o.abs() + rel * mag + n * 2.0 ** -31 * most + 1e-30
 

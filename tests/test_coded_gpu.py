@@ -617,6 +617,71 @@ def test_attention_never_follows_a_bad_page(bnd):
     R.check(got, ref, tol, "cut to the table")
 
 
+MANY = [
+    # dtype, code, B, h, h_kv, d, page, pages of a sequence, scores: many units, a table with little room
+    (BF, E4, 50, 32, 8, 128, 32, 1, {}),
+    (BF, I8, 200, 6, 2, 128, 24, 4, dict(cap=20.0)),
+    (F32, E4, 90, 8, 4, 128, 64, 2, dict(slopes=True)),
+    (F32, I8, 60, 16, 16, 128, 32, 16, {}),                   # room for 512
+    (BF, I8, 130, 36, 3, 128, 128, 1, dict(slopes=True)),     # twelve query heads a key head
+    (F32, E4, 100, 24, 2, 128, 16, 8, dict(cap=10.0)),
+    (BF, E4, 70, 24, 8, 64, 256, 1, {}),                      # pairs of heads, one tile
+    (F32, I8, 120, 12, 12, 64, 8, 12, dict(slopes=True, cap=9.0)),
+    (BF, I8, 60, 64, 8, 64, 32, 3, {}),                       # pairs of heads, a tile each
+    (F32, E4, 160, 32, 4, 64, 1, 77, {}),
+    (BF, E4, 50, 35, 5, 64, 100, 2, dict(cap=30.0)),          # an odd number of key heads
+    (F32, E4, 180, 5, 1, 64, 16, 2, dict(scale=0.4)),
+    (BF, I8, 100, 36, 3, 64, 64, 2, dict(slopes=True)),
+    (BF, E4, 1000, 10, 1, 64, 16, 32, {}),
+    (BF, E4, 300, 30, 10, 128, 16, 1, {}),                    # more units than run at a time, many times over
+]
+
+
+@pytest.mark.parametrize("dtype,code,B,h,hk,d,page,per,sc,order", [c + ("heads" if i % 2 else "slots",) for i, c in enumerate(MANY)])
+def test_attention_many_short(bnd, dtype, code, B, h, hk, d, page, per, sc, order):
+    room = page * per
+    rng = random.Random(B + d)
+    lens = [rng.choice([0, 1, room, rng.randint(0, room), rng.randint(0, room)]) for _ in range(B)]
+    block = next(b for b in (16, 8, 25, 4, 1) if page % b == 0)
+    table, n_pages = table_of(61, B, per)
+    kp, ks = pages_of(62, n_pages, page, block, hk, d, code, order)
+    vp, vs = pages_of(63, n_pages, page, block, hk, d, code, order)
+    poison(kp, ks, vp, vs, table, lens, block)
+    q = randn(64, h, B, d, dtype=dtype).transpose(0, 1) * 2.0
+    sc = dict(sc)
+    if sc.get("slopes"):
+        sc["slopes"] = slopes_of(h)
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, lens, hk, **sc)
+    ref, tol = C.attention(q, kp, ks, vp, vs, table, lens, hk, **sc)
+    R.check(got, ref, tol, "attention")
+    assert torch.equal(got, run_attention(bnd, q, kp, ks, vp, vs, table, lens, hk, **sc))
+    empty = [b for b, n in enumerate(lens) if n == 0]
+    assert not got[empty].any()
+    assert bnd.mha_check_device_status() == 0
+
+
+def test_attention_many_short_and_bad_pages(bnd):
+    """Bad pages, lengths beyond the table and below 0, among more units than SMs hold."""
+    B, h, hk, d, page = 400, 3, 1, 128, 16
+    rows = [[0, -1, 1], [2, 99, 3], [-5, -5, -5], [1, 2, 0]]
+    lens = [40, 48, 20, 3]
+    table = ints([rows[b % 4] for b in range(B)])
+    kp, ks = pages_of(70, 4, page, 16, hk, d, I8)
+    vp, vs = pages_of(71, 4, page, 16, hk, d, I8)
+    q = randn(72, B, h, d, dtype=BF)
+    n = [lens[b % 4] for b in range(B)]
+    bad = [(b, j) for b in range(B) for j in (range(16, 32) if b % 4 < 2 else range(20) if b % 4 == 2 else ())]
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, n, hk)
+    assert bnd.mha_check_device_status(reset=True) == bnd.MHA_PAGED_BAD_PAGE
+    ref, tol = C.attention(q, kp, ks, vp, vs, table, n, hk, bad=bad)
+    R.check(got, ref, tol, "bad pages left out")
+    good = ints([rows[3]] * B)
+    got = run_attention(bnd, q, kp, ks, vp, vs, good, [49 if b % 2 else -7 for b in range(B)], hk)
+    assert bnd.mha_check_device_status(reset=True) == bnd.MHA_PAGED_BAD_PAGE
+    ref, tol = C.attention(q, kp, ks, vp, vs, good, [48 if b % 2 else 0 for b in range(B)], hk)
+    R.check(got, ref, tol, "cut to the table")
+
+
 def test_attention_strided_query_and_output(bnd):
     """q a slice of a projection, a broadcast q, an output between other data, which stays."""
     B, h, hk, d, page, n = 3, 4, 2, 64, 16, 90

@@ -35,6 +35,7 @@ struct WarpBf16 {
     using Step = Halves<T, kD>;
     static constexpr int kRows = 8 * kNT, kBufs = 4;
     static constexpr int kQFloats = 0;      // shared memory for the query rows (they stay in registers)
+    static constexpr bool kSplits = true;   // units among CTAs
     static constexpr int kKeys = Step::kKeys;
     static constexpr int kKT = kKeys / 16;
     uint32_t q[kD / 16][kNT][2];
@@ -209,6 +210,7 @@ struct WarpF32 {
     using Step = Halves<T, kD>;
     static constexpr int kRows = kR, kBufs = 4;
     static constexpr int kQFloats = kR * kD;
+    static constexpr bool kSplits = true;
     static constexpr int kKeys = Step::kKeys;      // 8 or 16
     static constexpr int kLanes = 32 / kKeys;             // lanes that share a key's dot product: 4 or 2
     static constexpr int kDims = kD / kLanes;             // features a lane multiplies: 32

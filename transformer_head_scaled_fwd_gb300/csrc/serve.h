@@ -97,6 +97,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams& p, bool bf16, cudaStream_t 
 // ------------------------------------------------------------ a cache in 8 bits
 size_t coded_attn_workspace(int d);
 cudaError_t launch_coded_attn(const PagedAttnParams& p, bool bf16, bool int8, cudaStream_t s);
+cudaError_t launch_coded_attn_f32(const PagedAttnParams& p, bool int8, cudaStream_t s);
 
 struct CodedAppendParams {
     Strided q, q_out, k, k_out, v;    // q.p, k_out.p may be nullptr
