@@ -94,6 +94,12 @@ APPEND = [
     (F32, E4, 513, 32, 8, 128, 64, False, 64, 64, "heads", [2], None),
     (BF, E4, 2, 64, 16, 64, 20, False, 256, 256, "slots", [254, 255, 256, 0, 13], None),
 ]
+# blocks of one pass of rows and of two, in few and in many tiles; each way of turning
+for _i, (_dt, _d, _b) in enumerate([(BF, 128, 4), (BF, 64, 8), (F32, 128, 2), (F32, 64, 4), (BF, 128, 8), (BF, 64, 16), (F32, 128, 4), (F32, 64, 8)]):
+    for _j, (_rot, _inter) in enumerate([(0, False), (24, True), (_d // 2, False), (22, False)]):
+        _rng, _n = random.Random(4 * _i + _j), 80 if _j == _i % 4 else 9
+        APPEND.append((_dt, (E4, I8)[(_i + _j) % 2], 33 + _i, 3 + _j, 1 + _j % 2, _d, _rot, _inter, 16, _b, ("slots", "heads")[_j % 2],
+                       [_rng.randint(0, 40) for _ in range(_n)], [_rng.randint(0, 33 + _i) for _ in range(_n)] if _j > 1 else None))
 
 
 def run_append(bnd, dtype, code, T, h, hk, d, rot, inter, page, block, order, start, lens, big=4.0, first=8):

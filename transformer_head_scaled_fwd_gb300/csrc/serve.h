@@ -115,6 +115,7 @@ struct CodedAppendParams {
     int* status;
 };
 cudaError_t launch_coded_append(const CodedAppendParams& p, bool bf16, cudaStream_t s);
+cudaError_t launch_coded_append_f32(const CodedAppendParams& p, cudaStream_t s);
 
 // ------------------------------------------------------------ pages granted and returned
 struct ResizeParams {
