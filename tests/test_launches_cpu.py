@@ -1,0 +1,94 @@
+"""What the host side of the 8-bit cache's operators launches, and on what conditions, without a GPU: the library's objects are linked
+with a stand-in for the CUDA runtime (launch_record.c) that records launches."""
+import ctypes
+import glob
+import os
+import shutil
+import subprocess
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from transformer_head_scaled_fwd_gb300 import binding as bnd  # noqa: E402
+from transformer_head_scaled_fwd_gb300 import build as B  # noqa: E402
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+P = ctypes.c_void_p(4096)
+
+
+class Record(ctypes.Structure):
+    _fields_ = [("name", ctypes.c_char_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3), ("cluster", ctypes.c_uint),
+                ("smem", ctypes.c_int), ("allowed", ctypes.c_int), ("portable", ctypes.c_int)]
+
+
+@pytest.fixture(scope="module")
+def linked(tmp_path_factory):
+    if shutil.which("g++") is None or shutil.which("gcc") is None:
+        pytest.skip("no host compiler")
+    B.build()
+    objects = sorted(glob.glob(os.path.join(B.BUILD, "*.cu.o")))
+    if [os.path.basename(o)[:-2] for o in objects] != [os.path.basename(s) for s in B._sources()]:
+        B.build(force=True)
+        objects = sorted(glob.glob(os.path.join(B.BUILD, "*.cu.o")))
+    at = tmp_path_factory.mktemp("launches")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(B._nvcc()))), "include")
+    subprocess.run(["gcc", "-O1", "-fPIC", "-I", cuda, "-c", os.path.join(HERE, "launch_record.c"), "-o", str(at / "record.o")], check=True)
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", str(at / "lib.so"), *objects, str(at / "record.o"), "-Wl,-z,defs"], check=True)
+    return at
+
+
+class Recorded:
+    """A library of its own, so that what it keeps a device is asked again."""
+
+    def __init__(self, at, name, sms=152, cluster=16):
+        path = str(at / f"{name}.so")
+        shutil.copy(str(at / "lib.so"), path)
+        self.lib = ctypes.CDLL(path)
+        os.remove(path)
+        self.lib.fake_device(sms, cluster)
+        vp, i, i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
+        self.lib.mha_last_error.restype = ctypes.c_char_p
+        self.lib.mha_coded_append.argtypes = [i] + [vp] * 10 + [i] * 5 + [vp] * 5
+        self.lib.mha_paged_resize.argtypes = [vp, vp, i, i, vp, i64, i, vp, i, vp, vp, vp, i, vp, vp]
+
+    def _launched(self, status):
+        assert status == 0, self.lib.mha_last_error()
+        at = ctypes.POINTER(Record)()
+        n = self.lib.fake_records(ctypes.byref(at))
+        got = [Record.from_buffer_copy(at[j]) for j in range(n)]
+        self.lib.fake_clear()
+        return got
+
+    def append(self, dt=1, n=4, T=64, h=8, h_kv=2, d=128, rot=64, interleaved=0, block=16, code=0):
+        page = max(block, 64 // block * block)
+        strides = ctypes.byref(bnd.StridesT(T * 4096, 4096, 128))
+        pages = bnd.PagedCacheT(4096, 4096, page * 4096, 4096, 128, 1000, page, 4096, 64, 64)
+        cache = ctypes.byref(bnd.CodedCacheT(pages, code, block, 4096, 4096))
+        rotary = ctypes.byref(bnd.RotaryT(inv_freq=4096, rot_dim=rot, interleaved=interleaved, scale=1.0)) if rot else None
+        got = self._launched(self.lib.mha_coded_append(dt, P, strides, P, strides, P, strides, None, None, P, strides, n, T, h, h_kv, d, P,
+                                                       None, rotary, cache, None))
+        assert len(got) == 1
+        return got[0]
+
+
+def test_an_appends_shared_memory_limit_is_never_lowered(linked):
+    """The limit is state of the kernel in the whole process: a call that sets less than another one needs makes that one's launch fail,
+    if its own setting came before and its launch comes after."""
+    r = Recorded(linked, "limit")
+    limits, most = {}, {}
+    for dt in (0, 1):
+        for d in (64, 128):
+            for rot in sorted({0, 8, 16, 22, 62, 64, d - 2, d}):
+                for interleaved in (0, 1):
+                    for T, n in ((1, 3), (33, 2), (300, 2), (33, 200)):
+                        for block in (1, 4, 8, 16, 25, 64, 128, 255, 256):
+                            got = r.append(dt=dt, d=d, rot=rot if rot else 0, interleaved=interleaved, T=T, n=n, block=block)
+                            limits.setdefault(got.name, set()).add(got.allowed)
+                            most[got.name] = max(most.get(got.name, 0), got.smem)
+    assert all(len(x) == 1 for x in limits.values()), "a kernel's limit depends on the call"
+    assert r.lib.fake_lowered() == 0
+    # every instance is met, and no limit is a guess: steps of four passes are launched with all of theirs
+    assert len(limits) == 2 * 2 * 4 * 5
+    big = {n: (max(limits[n]), most[n]) for n in limits if most[n] > 150 << 10}
+    assert big and all(allowed == used for allowed, used in big.values())

@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 32;               // tokens of a tile, unless a block is longer
+constexpr int kLongest = 256;           // tokens of a block: what cos and sin of a tile have room for
 constexpr float kLeast = 0x1p-120f;     // least scale
 
 struct TilePlan {
@@ -477,6 +478,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm) coded_append_kernel(const __
     cp_wait<0>();
 }
 
+// Of steps, cos and sin of `tokens` rows of `stride` floats each, and a pass of rows that turn in shared memory: up to 208 KB (256 tokens,
+// halves of 57 to 63 pairs).
+template <typename T, int kD, int kKeep>
+constexpr size_t shared_bytes(int turn, int tokens, int stride) {
+    constexpr int kRows = 64 * Pair<T>::kN / kD;
+    return kWarps * 2 * kKeep * 1024 + static_cast<size_t>(tokens) * stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
+}
+
 template <typename T, int kD, int kKeep, int kPerSm>
 cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, cudaStream_t s) {
     constexpr int kN = Pair<T>::kN, kRows = 64 * kN / kD;
@@ -502,16 +511,19 @@ cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, cudaStream_t s) 
     plan.parts = std::max(each(p.h_kv, plan.kv_heads), p.h > 0 ? q_parts : 1);
     plan.stride = (half + kN - 1) / kN * kN;
     plan.half = fast_div(static_cast<uint32_t>(std::max(half, 1)));
-    const Turn turn = half == 0 ? kNone : p.interleaved != 0 ? kNeighbours : half % kN == 0 ? kHalves : kStaged;
-    const size_t smem = kWarps * 2 * kKeep * 1024 + static_cast<size_t>(plan.tokens) * plan.stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
+    const int turn = half == 0 ? kNone : p.interleaved != 0 ? kNeighbours : half % kN == 0 ? kHalves : kStaged;
     const auto kernel = turn == kNone         ? coded_append_kernel<T, kD, kNone, kKeep, kPerSm>
                         : turn == kNeighbours ? coded_append_kernel<T, kD, kNeighbours, kKeep, kPerSm>
                         : turn == kHalves     ? coded_append_kernel<T, kD, kHalves, kKeep, kPerSm>
                                               : coded_append_kernel<T, kD, kStaged, kKeep, kPerSm>;
-    {        // up to 211 KB: 256 tokens, 64 pairs
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    // The limit is the kernel's in the whole process, and another thread's call may come between this and the launch: it is the most that
+    // any call of this kernel needs, never what this one does.
+    constexpr int kTokens = kKeep == 4 ? kLongest : kTile;
+    static_assert(shared_bytes<T, kD, kKeep>(kStaged, kLongest, kD / 2) + 1024 <= 227 * 1024, "shared memory budget");
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(shared_bytes<T, kD, kKeep>(turn, kTokens, turn == kNone ? 0 : kD / 2)));
+    if (e != cudaSuccess) return e;
+    const size_t smem = shared_bytes<T, kD, kKeep>(turn, plan.tokens, plan.stride);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * plan.tiles), plan.parts), dim3(kThreads), smem, s, p, plan);
 }
 
