@@ -108,7 +108,7 @@ struct Lens {
     }
     __device__ __forceinline__ int blocks(int n) const { return n / block + (n % block != 0); }
     // of the line: a unit's blocks, and kTail for its end
-    __device__ __forceinline__ int places(int n) const { return n > 0 ? blocks(n) + kTail : 0; }
+    __device__ __forceinline__ int places(int n) const { return kTail == 0 ? blocks(n) : n > 0 ? blocks(n) + kTail : 0; }
 };
 
 struct Found {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn
         } else if (threadIdx.x == 0) {
             JoinDesc d{0, -1, 0, 0, 0};
             const long long u0 = t0 - at.blk;       // the unit's first place
-            if (at.blk > 0 && at.blk < at.nblk && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
+            if (at.blk > 0 && (kTail == 0 || at.blk < at.nblk) && owner(u0) == c - 1) {  // the first of the CTAs that continue it describes the join
                 d.c0 = c - 1;
                 d.c1 = owner(u0 + at.nblk - 1);
                 d.b = at.b;
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn
         } while (x.n == 0);
     };
 
-    if (at.blk >= at.nblk || (p.whole && at.blk > 0)) {      // never where a CTA has a unit of its own
+    if ((kTail > 0 && at.blk >= at.nblk) || (p.whole && at.blk > 0)) {      // never where a CTA has a unit of its own
         t0 += at.nblk - 1 - at.blk;
         at.blk = at.nblk - 1;
         advance(at, t0);
@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn
                 inside = true;
             }
             advance(ahead, t_ahead);
+        } else if (kTail == 0) {
+            ++t_ahead;           // without tails it stays a step count ahead of the block that is computed, and needs no registers of its own
         }
     };
     auto issue = [&](int stage) -> uint32_t {
@@ -415,10 +417,11 @@ __global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn
                 sh.f[warp][lane] = mw == -CUDART_INF_F ? 0.0f : ex2_approx(mw - M);
             }
             __syncwarp();
-            float* own = buf + warp % W::kBufs * (W::kRows * kD);
+            static_assert((W::kBufs & (W::kBufs - 1)) == 0, "a mask");
+            float* own = buf + (warp & (W::kBufs - 1)) * (W::kRows * kD);
 #pragma unroll
             for (int r = kWarps / W::kBufs - 1; r >= 0; --r) {
-                if (warp / W::kBufs == r) w.put(own, sh.f[warp], r != kWarps / W::kBufs - 1, rows, lane);
+                if ((r == 0 || warp >= r * W::kBufs) && (r + 1 == kWarps / W::kBufs || warp < (r + 1) * W::kBufs)) w.put(own, sh.f[warp], r != kWarps / W::kBufs - 1, rows, lane);
                 __syncthreads();
             }
             const bool whole = unit_done && piece_blk == 0;
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(W::Step::kThreads, W::Step::kPerSm) paged_attn
 // at most kSlots), then groups of kD / 4 threads sum every kGroups-th piece, 16 bytes a thread.
 __host__ __device__ constexpr int join_threads(int slots) { return slots <= 256 ? 256 : 512; }
 constexpr int kEarly = 8;        // loads of a thread that do not wait for the weights (one of 131071: 31.8 -> 30.5 us, of 16000: 12.9 -> 12.1)
-template <typename T, int kD, int kSlots>
+template <typename T, int kD, int kSlots, bool kSided>
 __global__ void __launch_bounds__(join_threads(kSlots)) paged_join_kernel(const __grid_constant__ PagedAttnParams p, int rows_tile) {
     constexpr int kSlot = slot_floats<kD>();
     constexpr int kCols = kD / 4;
@@ -478,9 +481,10 @@ __global__ void __launch_bounds__(join_threads(kSlots)) paged_join_kernel(const 
     if (row >= min(group - ht * rows_tile, rows_tile)) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int pieces = d.c1 - d.c0 + 1;
-    const int sides = p.side.d, step = 2 * sides;
+    const int sides = kSided ? static_cast<int>(p.side.d) : 1, step = 2 * sides;
+    const int my_side = kSided ? static_cast<int>(blockIdx.x) - p.side.div(blockIdx.x) * sides : 0;
     // piece i at i step kSlot, piece 0 at first_slot
-    const float* slots = p.partial + (static_cast<int64_t>(d.c0) * sides + (blockIdx.x - p.side.div(blockIdx.x) * sides)) * 2 * kSlot;
+    const float* slots = p.partial + (static_cast<int64_t>(d.c0) * sides + my_side) * 2 * kSlot;
     const float* mine = slots + (tid == 0 ? d.first_slot : step * tid) * kSlot;
     const int g = tid / kCols, x = tid % kCols;
     auto at = [&](int i) {
@@ -564,7 +568,7 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
         const int grid = ctas / side * side;
         if ((e = launch_pdl(paged_attn_kernel<W, kD>, dim3(grid), dim3(kThreads), kSmem, s, p)) != cudaSuccess) return e;
         const int rows = std::min(p.h / p.h_kv, W::kRows);
-        return launch_pdl(paged_join_kernel<typename W::T, kD, W::Step::kSlots>, dim3(grid, rows), dim3(join_threads(W::Step::kSlots)), 0, s, p, static_cast<int>(W::kRows));
+        return launch_pdl(paged_join_kernel<typename W::T, kD, W::Step::kSlots, (W::Step::kScales > 0)>, dim3(grid, rows), dim3(join_threads(W::Step::kSlots)), 0, s, p, static_cast<int>(W::kRows));
     } else {
         return cudaErrorInvalidConfiguration;       // its launcher has none that are not whole
     }
