@@ -1,11 +1,14 @@
-"""The operators around a cache in 8 bits on the GPU: calls from several host threads."""
+"""The operators around a cache in 8 bits on the GPU: calls from several host threads, weights of very different sizes."""
+import math
 import threading
 
 import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_coded_gpu import BF, E4, bnd, clean_status, freqs, ints, pages_of, randn, same, table_of  # noqa: E402, F401
+import coded_ref as C  # noqa: E402
+from test_coded_gpu import (BF, E4, F32, I8, bnd, clean_status, freqs, ints, pages_of, randn, run_attention, same,  # noqa: E402, F401
+                            table_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +58,53 @@ def test_appends_from_two_host_threads(bnd):
     assert not errors, errors
     for _, outs, want, _ in jobs:
         assert all(same(a, b) for a, b in zip(outs, want))
+
+
+# ------------------------------------------------------------------------------------------ attention
+def norm_error(got, ref):
+    return ((got.double() - ref).norm() / ref.norm()).item()
+
+
+# A first key of nearly all of the weight and of no value, scores of one product each. fp32: a weight is off by 2^-22 of itself, its score
+# of up to 20 by four roundings, twice as it also enters the sum (2 * 20 * 4 * 2^-24 = 1e-5), exp2 and the factors of the running maximum by
+# 4 * 2^-21 = 2e-6; the sum of values takes a product of 16 of a warp's n / 8 keys after the other, each cut at 2^-23 of what the sum came
+# to, the sum of weights one of 32 of them, rounded. bf16: what rounding the exact result gives, r, and twice the error e in front of the
+# rounding: |round(x + e) - x| is |round(x) - x| unless a border lies between x and x + e, where the first is at most half a step + e and
+# the second at least half a step - e. (Of r itself no more than 1.66e-3 of the norm in the mean is known, and 128 values do not keep to
+# that within a twentieth.) e: weights rounded to 2^-11 (2^-11 / sqrt 3 = 2.8e-4), or to 2^-25 where the largest is 2^10 or more, of which
+# the others have share / (1 - share) / n in the mean and e^(1/2) of that in the root mean square: 2^-35 / sqrt 3 of the largest each, for
+# the warp with the first key, which has every eighth step (4.7e-4 at 131071 keys and a share of 1 / 1000); a twentieth for samples.
+@pytest.mark.parametrize("code", [E4, I8])
+@pytest.mark.parametrize("dtype,hk,d,group", [(BF, 1, 128, 1), (F32, 1, 128, 3), (F32, 2, 64, 1), (F32, 2, 64, 5), (F32, 1, 64, 2)])
+@pytest.mark.parametrize("n,share", [(400, 0.001), (8192, 0.1), (8192, 0.001), (32768, 0.01), (131071, 0.001)])
+def test_attention_beside_a_key_of_nearly_all_the_weight(bnd, dtype, code, hk, d, group, n, share):
+    """Sequences of the same pages, as many as keep each in one CTA, where a warp has every eighth step of it."""
+    B, page, h = 400 // hk, 16, hk * group
+    per = -(-n // page)
+    table = torch.arange(per, device="cuda", dtype=torch.int32).repeat(B, 1)
+    vp, vs = pages_of(47, per, page, 1, hk, d, code)
+    kp, ks = pages_of(48, per, page, 1, hk, d, code)
+    vs.fill_(2.0 ** -5)
+    vp[0, 0] = 0
+    one = 64.0
+    first = torch.randn(per, page, hk, generator=torch.Generator(device="cuda").manual_seed(49), device="cuda") * one
+    kp[..., 0] = first.round().clamp(-127, 127).to(kp.dtype)
+    kp[0, 0, :, 0] = torch.tensor(one, device="cuda").to(kp.dtype)
+    ks.fill_(1.0 / one)
+    for g in range(hk):
+        s = kp[..., g, 0].double().flatten()[1:n] / one
+        ks[0, 0, g] = (torch.logsumexp(s, 0) + math.log((1 - share) / share)).item() / one
+    q = torch.zeros(B, h, d, device="cuda", dtype=dtype)
+    q[..., 0] = 1.0
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, [n] * B, hk, scale=1.0)
+    want = torch.zeros(h, d, dtype=torch.float64, device="cuda")
+    kv, vv = C.values(kp, ks).flatten(0, 1)[:n], C.values(vp, vs).flatten(0, 1)[:n]
+    for i in range(h):
+        want[i] = torch.softmax(kv[:, i // group, 0], 0) @ vv[:, i // group]
+    bound = 1.3e-5 + n / 8 / 16 * 2.0 ** -23 + n / 8 / 32 * 2.0 ** -24
+    if dtype == BF:
+        small = (1 - share) / share * n * 2.0 ** -35 / math.sqrt(3) / math.exp(0.5) / math.sqrt(8)
+        bound = norm_error(want.to(BF), want) + 2 * 1.05 * math.hypot(2.8e-4, small)
+    worst = max(norm_error(got[b], want) for b in (0, B // 3, B - 1))
+    assert worst <= bound, (worst, bound)
+    assert all(norm_error(got[b], want) <= bound for b in range(B))

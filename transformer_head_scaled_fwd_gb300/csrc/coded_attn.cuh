@@ -11,8 +11,14 @@
 //
 // Scales: ks multiplies a score after its product. vs belongs to a weight, p_j vs_j, whose size is not bounded by that of
 // p_j, and fp16 has no range to spare: the weights have a running maximum of their own, over s_j + log2 of vs_j's power of two,
-// so that the largest lies in 2^6 .. 2^15 whatever the scales are. They are rounded to fp16 (2^-11, against 2^-8 of a bf16
-// result), for an fp32 result taken as two fp16 terms (2^-22). p_j itself is summed in fp32.
+// so that the largest that a warp has met lies in 2^10 .. 2^15 whatever the scales are. They are rounded to fp16: to 2^-11 of themselves
+// (against 2^-8 of a bf16 result), or, where fp16 ends, to 2^-25, that is 2^-35 of the largest. A second term would take that to what an fp32
+// result has, for 1 to 7 % of the time (16 x 8192 50.8 -> 52.3 us, 48 ragged capped 135.7 -> 145.6), and bring the error of a bf16 result
+// against 64 bits to that of rounding it, which it is within 0.6 % of (12 x 9000 int8, capped, 1.650e-3 of the norm for 1.641e-3; 16 x 8192 1.627e-3 for
+// 1.623e-3): for that it is not taken. For an fp32 result there are two: the second is
+// the first one's rest times 2^12, whose products have sums of their own, so a weight is good to 2^-22 of itself or
+// to 2^-37, 2^-47 of the largest. (With the rest on the first one's scale, and the largest from 2^6 on, a key of 99 % of the weight and no value
+// left the other 32768 keys seven bits each: 2e-4 of the result's norm.) p_j itself is summed in fp32.
 //
 // Work split, loads and join: paged_line.cuh; a step is 32 keys.
 //
@@ -28,7 +34,7 @@
 namespace mha {
 namespace {
 
-constexpr float kBase = 6.0f;       // log2 of the least the largest weight is taken to
+constexpr float kBase = 10.0f;      // log2 of the least the largest weight is taken to
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -65,9 +71,11 @@ __device__ __forceinline__ void codes_f16(uint32_t x, uint32_t& a, uint32_t& b) 
     }
 }
 
-// Exponent of a scale, at least -110: that of the weights' maximum stays within fp32's range of the scores'.
+// Exponent of a scale, at least kLeastExponent: what then takes a weight of 2^kGrow to the weights' maximum stays in fp32.
+constexpr int kLeastExponent = -106;
+static_assert(kGrow - kLeastExponent + kBase < 127.0f, "2^127 is fp32's largest power of two");
 __device__ __forceinline__ float exponent_of(float s) {
-    return static_cast<float>(max(static_cast<int>((__float_as_uint(s) >> 23) & 0xffu) - 127, -110));
+    return static_cast<float>(max(static_cast<int>((__float_as_uint(s) >> 23) & 0xffu) - 127, kLeastExponent));
 }
 __device__ __forceinline__ float4 lds4(uint32_t a) {
     float4 v;
@@ -109,9 +117,10 @@ struct WarpCoded {
     static constexpr bool kWide = sizeof(T) == 4;
     static constexpr int kQT = kWide ? 2 : 1;       // fp16 terms of q
     static constexpr int kPT = kWide ? 2 : 1;       // and of a weight
-    static constexpr float kMost = 32768.0f;        // largest weight: 2^(kGrow + 1 + kBase)
+    static constexpr float kMost = 32768.0f;        // largest weight: it may grow 2^4 beyond the power of two that it was taken to
+    static constexpr float kRest = 4096.0f;         // factor of a weight's second term: that of 2^15 is up to 2^3 and has to stay below 2^16
     uint32_t q[kQT][kD / 16][kTiles][2];
-    float o[kRow / 16][kOfChunk][4];     // features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
+    float o[kPT][kRow / 16][kOfChunk][4];     // of a weight's terms; features 2 (lane / 4) (+ 1), heads 2 (lane % 4) + {0, 1}
     // of those two heads: maximum of the scores, and of score + scale's exponent; 2^(m - mo + kBase); this lane's share of the
     // sum; the bias' slope; what takes a product to a score (capped: to q.k)
     float m[kTiles][2], mo[kTiles][2], u[kTiles][2], l[kTiles][2], slope[kTiles][2], in[kTiles][2];
@@ -201,7 +210,9 @@ struct WarpCoded {
 #pragma unroll
             for (int nt = 0; nt < kOfChunk; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.0f;
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int x = 0; x < kPT; ++x) o[x][i][nt][e] = 0.0f;
     }
 
     // keys key0 .. key0 + 31 in shared memory at k, v, their scales behind v; live: bit i: key0 + i counts
@@ -319,7 +330,7 @@ struct WarpCoded {
         float most_p, most_w;
         weigh(most_p, most_w);
         if (__any_sync(0xffffffffu, most_p > 256.0f || most_w > kMost)) {
-            static_assert(kGrow == 8.0f && kBase == 6.0f, "the bounds above");
+            static_assert(kGrow == 8.0f && kBase == 10.0f, "the bounds above");
 #pragma unroll
             for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
@@ -343,10 +354,12 @@ struct WarpCoded {
                     u[nt][e] = top == -CUDART_INF_F ? 0.0f : ex2_approx(top - most + kBase);
                     // the tile's accumulators
 #pragma unroll
-                    for (int i = 0; i < kRow / 16 / (kTiles / kOfChunk); ++i) {
-                        o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e] *= alpha;
-                        o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e + 2] *= alpha;
-                    }
+                    for (int i = 0; i < kRow / 16 / (kTiles / kOfChunk); ++i)
+#pragma unroll
+                        for (int x = 0; x < kPT; ++x) {
+                            o[x][nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e] *= alpha;
+                            o[x][nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e + 2] *= alpha;
+                        }
                 }
             weigh(most_p, most_w);
         }
@@ -368,8 +381,8 @@ struct WarpCoded {
                         uint32_t h = pack_f16x2(w0, w1);
                         if (x + 1 < kPT) {
                             const float2 got = unpack_f16x2(h);
-                            w0 -= got.x;
-                            w1 -= got.y;
+                            w0 = (w0 - got.x) * kRest;
+                            w1 = (w1 - got.y) * kRest;
                         }
                         asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(pt[x][nt][hf]) : "r"(h));
                     }
@@ -388,8 +401,8 @@ struct WarpCoded {
 #pragma unroll
                     for (int nt = 0; nt < kOfChunk; ++nt)
 #pragma unroll
-                        for (int x = kPT - 1; x >= 0; --x)
-                            mma_f16(o[2 * i + hf][nt], a, pt[x][head * kOfChunk + nt][0], pt[x][head * kOfChunk + nt][1]);
+                        for (int x = 0; x < kPT; ++x)
+                            mma_f16(o[x][2 * i + hf][nt], a, pt[x][head * kOfChunk + nt][0], pt[x][head * kOfChunk + nt][1]);
                 }
             }
         }
@@ -425,8 +438,11 @@ struct WarpCoded {
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         float* y = buf + hd * kD + 16 * i + 2 * (lane >> 2) + hf;
-                        const float mine = second(lane) ? o[(kHeads - 1) * (kD / 16) + i][nt % kOfChunk][e + 2 * hf]
-                                                        : o[nt / kOfChunk * (kD / 16) + i][nt % kOfChunk][e + 2 * hf];
+                        auto sum = [&](int chunk) {
+                            const float first = o[0][chunk][nt % kOfChunk][e + 2 * hf];
+                            return kPT == 1 ? first : fmaf(o[kPT - 1][chunk][nt % kOfChunk][e + 2 * hf], 1.0f / kRest, first);
+                        };
+                        const float mine = second(lane) ? sum((kHeads - 1) * (kD / 16) + i) : sum(nt / kOfChunk * (kD / 16) + i);
                         const float x = mine * up * fr;
                         *y = add ? *y + x : x;
                     }
