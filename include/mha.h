@@ -498,9 +498,11 @@ mha_status_t mha_coded_append(mha_dtype_t dt, const void* q, const mha_strides_t
 
 /*
  * mha_paged_attention over such a cache: the attention over the values c * scale, for q and out of type dt. Scales are
- * 0 or between 2^-120 and 2^120, of any mantissa. q enters as it is (bf16: exact down to 2^-29 of its row's largest element; fp32:
+ * 0 or between 2^-120 and 2^122, of any mantissa, and |c * scale| of the values sums to less than 2^120 over a sequence. q enters as it is (bf16: exact down to 2^-29 of its row's largest element; fp32:
  * to 2^-22 of itself or 2^-39 of that); weights (a softmax numerator times its value's scale) are rounded to 2^-11 of themselves or 2^-35 of the row's
- * largest for a bf16 result, to 2^-22 or 2^-47 for an fp32 one; products and sums are fp32.
+ * largest for a bf16 result, to 2^-22 or 2^-47 for an fp32 one (the second bounds where the largest's scale is from 2^-106 to 2^112, and rising
+ * to 2^-21 and 2^-33 at 2^-120, 2^-38 at 2^122); products and sums are fp32. A key whose softmax numerator is below 2^-126 of the row's largest may
+ * count as none, whatever the scale of its value.
  * What lies behind a sequence's end is not used; a block's scale is, for the block's other slots.
  * workspace >= mha_coded_attention_workspace_size(...); kv_lens, scores, bad pages, order: as for mha_paged_attention.
  */

@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import coded_ref as C  # noqa: E402
+import serving_ref as R  # noqa: E402
 from test_coded_gpu import (BF, E4, F32, I8, bnd, clean_status, freqs, ints, pages_of, randn, run_attention, same,  # noqa: E402, F401
                             table_of)
 
@@ -108,3 +109,53 @@ def test_attention_beside_a_key_of_nearly_all_the_weight(bnd, dtype, code, hk, d
     worst = max(norm_error(got[b], want) for b in (0, B // 3, B - 1))
     assert worst <= bound, (worst, bound)
     assert all(norm_error(got[b], want) <= bound for b in range(B))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("code", [E4, I8])
+@pytest.mark.parametrize("n,far", [(20, 9), (300, 40), (300, 299), (20000, 3), (20000, 19000)])
+@pytest.mark.parametrize("below", [90, 110, 125])
+def test_attention_value_scales_that_outweigh_the_softmax(bnd, dtype, code, n, far, below):
+    """A first key with nearly all of the softmax and values of scale 2^-120, one whose numerator is 2^-below of its and whose values, of scale 2^110
+    (448 times that is 2^118.9: the sums' limit is 2^120), are the result: in one warp, in two, in two CTAs. The other keys lie in between and add nothing. Below 2^-126 the key may
+    count as none: the result is then the exact one or that without it."""
+    h, hk, d, page = 4, 2, 64, 16
+    table, n_pages = table_of(1, 1, -(-n // page))
+    kp, ks = pages_of(52, n_pages, page, 1, hk, d, code)
+    vp, vs = pages_of(53, n_pages, page, 1, hk, d, code)
+    where = table[0].long().repeat_interleave(page)[:n], torch.arange(n, device="cuda") % page
+    kp[..., 0] = torch.tensor(1.0, device="cuda").to(code)
+    score = torch.full((n,), -100.0, device="cuda")
+    score[0] = 0.0
+    vs[where] = 2.0 ** -120
+    q = torch.zeros(1, h, d, device="cuda", dtype=dtype)
+    q[..., 0] = 1.0
+    for gap in (below, 126 + below):
+        score[far] = -gap
+        ks[where] = -score[:, None].expand(n, hk)           # codes of 1 and a scale of scores, which are powers of two's logarithms
+        vs[where[0][far], where[1][far]] = 2.0 ** 110
+        got = run_attention(bnd, -q, kp, ks, vp, vs, table, [n], hk, scale=math.log(2.0))
+        ref, tol = C.attention(-q, kp, ks, vp, vs, table, [n], hk, scale=math.log(2.0))
+        if gap > 126:
+            vs[where[0][far], where[1][far]] = 0.0
+            none, none_tol = C.attention(-q, kp, ks, vp, vs, table, [n], hk, scale=math.log(2.0))
+            assert torch.isfinite(got).all()
+            assert (((got.double() - ref).abs() <= tol) | ((got.double() - none).abs() <= none_tol)).all()
+        else:
+            assert (ref.abs() > 2.0 ** (105 - gap)).any()
+            R.check(got, ref, tol, "outweighed")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attention_values_of_the_largest_scale(bnd, dtype):
+    """Scales of 2^122, the largest that an append makes, with codes small enough for the sums."""
+    h, hk, d, page, n = 4, 2, 128, 16, 8
+    table, n_pages = table_of(1, 1, 1)
+    kp, ks = pages_of(54, n_pages, page, 16, hk, d, E4)
+    vp, vs = pages_of(55, n_pages, page, 16, hk, d, E4)
+    vp = (vp.float().sign() * 2.0 ** -6).to(E4)
+    vs.fill_(2.0 ** 122)
+    q = randn(56, 1, h, d, dtype=dtype)
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
+    ref, tol = C.attention(q, kp, ks, vp, vs, table, [n], hk)
+    R.check(got, ref, tol, "2^122")

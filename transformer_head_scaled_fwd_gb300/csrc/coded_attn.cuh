@@ -9,16 +9,17 @@
 // below 2^8), and the products are fp16 matrix instructions on them. A query row is scaled by a power of two to below 2^15 and
 // enters as one fp16 number an element (bf16: exact down to 2^-29 of the row's largest) or as two (fp32: to 2^-22).
 //
-// Scales: ks multiplies a score after its product. vs belongs to a weight, p_j vs_j, whose size is not bounded by that of
-// p_j, and fp16 has no range to spare: the weights have a running maximum of their own, over s_j + log2 of vs_j's power of two,
-// so that the largest that a warp has met lies in 2^10 .. 2^15 whatever the scales are. They are rounded to fp16: to 2^-11 of themselves
-// (against 2^-8 of a bf16 result), or, where fp16 ends, to 2^-25, that is 2^-35 of the largest. A second term would take that to what an fp32
-// result has, for 1 to 7 % of the time (16 x 8192 50.8 -> 52.3 us, 48 ragged capped 135.7 -> 145.6), and bring the error of a bf16 result
-// against 64 bits to that of rounding it, which it is within 0.6 % of (12 x 9000 int8, capped, 1.650e-3 of the norm for 1.641e-3; 16 x 8192 1.627e-3 for
-// 1.623e-3): for that it is not taken. For an fp32 result there are two: the second is
-// the first one's rest times 2^12, whose products have sums of their own, so a weight is good to 2^-22 of itself or
-// to 2^-37, 2^-47 of the largest. (With the rest on the first one's scale, and the largest from 2^6 on, a key of 99 % of the weight and no value
-// left the other 32768 keys seven bits each: 2e-4 of the result's norm.) p_j itself is summed in fp32.
+// Scales: ks multiplies a score after its product. vs belongs to a weight, p_j vs_j, whose size is not bounded by that of p_j, and fp16 has no
+// range to spare: the weights have a running maximum of their own, over s_j + log2 of vs_j's power of two, so that the largest that a warp has
+// met lies in 2^10 .. 2^15 for scales from 2^-106 on. (p_j is fp32 relative to the largest: below 2^-126 of that it is 0, here and in the
+// joins, and its value counts for nothing whatever its scale.) They are rounded to fp16: to 2^-11 of themselves (against 2^-8 of a bf16
+// result), or, where fp16 ends, to 2^-25, that is 2^-35 of the largest. A second term would take that to what an fp32 result has, for 1 to 7 %
+// of the time (16 x 8192 50.8 -> 52.3 us, 48 ragged capped 135.7 -> 145.6), and bring the error of a bf16 result against 64 bits to that of
+// rounding it, which it is within 0.6 % of (12 x 9000 int8, capped, 1.650e-3 of the norm for 1.641e-3; 16 x 8192 1.627e-3 for 1.623e-3): for
+// that it is not taken. For an fp32 result there are two: the second is the first one's rest times 2^12, whose products have sums of their
+// own, so a weight is good to 2^-22 of itself or to 2^-37, 2^-47 of the largest. (With the rest on the first one's scale, and the largest from
+// 2^6 on, a key of 99 % of the weight and no value left the other 32768 keys seven bits each: 2e-4 of the result's norm.) p_j itself is summed
+// in fp32.
 //
 // Work split, loads and join: paged_line.cuh; a step is 32 keys.
 //
