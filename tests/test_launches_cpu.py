@@ -92,3 +92,22 @@ def test_an_appends_shared_memory_limit_is_never_lowered(linked):
     assert len(limits) == 2 * 2 * 4 * 5
     big = {n: (max(limits[n]), most[n]) for n in limits if most[n] > 150 << 10}
     assert big and all(allowed == used for allowed, used in big.values())
+
+
+def resize(r, n, T=1, slots=True):
+    """Launches of a step of n sequences and T slots each."""
+    B_, t = 1 << 40, ctypes.c_void_p
+    arrays = [t(B_ + i * (1 << 32)) for i in range(4)]
+    return r._launched(r.lib.mha_paged_resize(arrays[0], arrays[1], n, 16, t(4096), 64, 64, t(4096), 1000, t(4096), arrays[2], arrays[3], T,
+                                              t(4096) if slots else None, None))
+
+
+@pytest.mark.parametrize("largest", [16, 8, 4, 2, 1])
+@pytest.mark.parametrize("n", [1, 512, 513])
+def test_a_resize_takes_the_largest_cluster_that_fits(linked, largest, n):
+    """A part of a device, or another one, may have no room for 16 CTAs side by side: the call is then made with fewer."""
+    r = Recorded(linked, f"cluster{largest}_{n}", cluster=largest)
+    for _ in range(2):
+        got = resize(r, n)
+        assert len(got) == 1 and got[0].cluster == largest and got[0].grid[0] == largest
+        assert got[0].block[0] == (512 if n <= 512 else 1024)

@@ -4,8 +4,6 @@
 
 #include <math_constants.h>
 
-#include <atomic>
-
 #include "launch.h"
 #include "mha_internal.h"
 #include "ptx_pair.cuh"
@@ -269,33 +267,6 @@ __device__ __forceinline__ void join_parts(const SpanAttnParams& p, int b, int h
     else if (pieces == 4) join_by<T, kD, kUnit, kThr, 4>(p, b, head, q0, piece, m_at, o_at);
     else join_by<T, kD, kUnit, kThr, 8>(p, b, head, q0, piece, m_at, o_at);
 }
-
-// Clusters of a kernel, allowed `smem` bytes by the caller, that the current device runs at once; asked once a device and
-// size, for it is a property of the device.
-struct ClusterRoom {
-    static constexpr int kDevices = 64;
-    std::atomic<int> known[kDevices][4] = {};      // by log2(size); 0: not asked, else 1 + the answer
-    template <typename Kernel>
-    int at_once(Kernel kernel, int threads, size_t smem, int size) {
-        const int lg = size == 8 ? 3 : size == 4 ? 2 : 1;
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
-        if (const int k = known[dev][lg].load(std::memory_order_relaxed)) return k - 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(size);
-        cfg.blockDim = dim3(threads);
-        cfg.dynamicSmemBytes = smem;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
-        known[dev][lg].store(n + 1, std::memory_order_relaxed);
-        return n;
-    }
-};
 
 }  // namespace
 

@@ -3,6 +3,8 @@
 // kernel calls pdl_wait() (ptx.cuh) before reading anything that work produced.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_runtime.h>
 
 namespace mha {
@@ -41,5 +43,32 @@ cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block,
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
+
+// Clusters of a kernel, allowed `smem` bytes by the caller, that the current device runs at once; asked once a device and
+// size, for it is a property of the device.
+struct ClusterRoom {
+    static constexpr int kDevices = 64;
+    std::atomic<int> known[kDevices][5] = {};      // by log2(size); 0: not asked, else 1 + the answer
+    template <typename Kernel>
+    int at_once(Kernel kernel, int threads, size_t smem, int size) {
+        const int lg = size == 16 ? 4 : size == 8 ? 3 : size == 4 ? 2 : 1;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+        if (const int k = known[dev][lg].load(std::memory_order_relaxed)) return k - 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {static_cast<unsigned>(size), 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+        known[dev][lg].store(n + 1, std::memory_order_relaxed);
+        return n;
+    }
+};
 
 }  // namespace mha

@@ -295,12 +295,19 @@ cudaError_t launch_resize(const ResizeParams& p, cudaStream_t s) {
     ResizeParams q = p;
     const int64_t slots = p.slots != nullptr ? static_cast<int64_t>(p.B) * p.T : 0;
     q.slots_after = slots >= kFewSlots;
-    const auto kernel = p.B <= 512 ? resize_kernel<512> : resize_kernel<1024>;
+    const bool few = p.B <= 512;
+    const int threads = few ? 512 : 1024;
+    const auto kernel = few ? resize_kernel<512> : resize_kernel<1024>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) e = launch_pdl_cluster(kernel, dim3(kCtas), dim3(p.B <= 512 ? 512 : 1024), kCtas, 0, s, q);
+    if (e != cudaSuccess) return e;
+    // a part of a device, or a smaller one, may have no room for 16 side by side; the kernel takes any number
+    static ClusterRoom rooms[2];
+    int ctas = kCtas;
+    while (ctas > 1 && rooms[few].at_once(kernel, threads, 0, ctas) < 1) ctas /= 2;
+    e = launch_pdl_cluster(kernel, dim3(ctas), dim3(threads), ctas, 0, s, q);
     if (e != cudaSuccess || !q.slots_after) return e;
-    const int64_t ctas = std::min<int64_t>(8 * 152, (slots + kSlots * kSlotThreads - 1) / (kSlots * kSlotThreads));
-    return launch_pdl(slots_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kSlotThreads), 0, s, q);
+    const int64_t wide = std::min<int64_t>(8 * 152, (slots + kSlots * kSlotThreads - 1) / (kSlots * kSlotThreads));
+    return launch_pdl(slots_kernel, dim3(static_cast<unsigned>(wide)), dim3(kSlotThreads), 0, s, q);
 }
 
 }  // namespace mha
