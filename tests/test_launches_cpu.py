@@ -111,3 +111,19 @@ def test_a_resize_takes_the_largest_cluster_that_fits(linked, largest, n):
         got = resize(r, n)
         assert len(got) == 1 and got[0].cluster == largest and got[0].grid[0] == largest
         assert got[0].block[0] == (512 if n <= 512 else 1024)
+
+
+def test_sizes_of_grids_go_by_the_devices_sms(linked):
+    """Waves and rules of as many CTAs as SMs are those of the device that runs them."""
+    half, whole = Recorded(linked, "half", sms=76), Recorded(linked, "whole", sms=152)
+    # fewer tiles than a wave of either: parts of the heads fill it, on both alike
+    shape = dict(h=64, h_kv=64, n=4, T=64, block=32)
+    a, b = half.append(**shape), whole.append(**shape)
+    assert a.grid[0] == b.grid[0] and 0 < a.grid[1] < b.grid[1]
+    # as many tiles as 76 SMs, but not as 152: "many" for one, and the kernel of more CTAs an SM
+    shape = dict(n=50, T=64, block=4)
+    a, b = half.append(**shape), whole.append(**shape)
+    assert 76 <= a.grid[0] < 152 and a.grid[0] == b.grid[0] and a.name != b.name
+    # the slots of many tokens
+    a, b = resize(half, 64, T=1 << 16), resize(whole, 64, T=1 << 16)
+    assert len(a) == len(b) == 2 and a[1].grid[0] == 8 * 76 and b[1].grid[0] == 8 * 152

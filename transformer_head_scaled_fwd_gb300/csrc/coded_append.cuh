@@ -487,7 +487,7 @@ constexpr size_t shared_bytes(int turn, int tokens, int stride) {
 }
 
 template <typename T, int kD, int kKeep, int kPerSm>
-cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, cudaStream_t s) {
+cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, int sms, cudaStream_t s) {
     constexpr int kN = Pair<T>::kN, kRows = 64 * kN / kD;
     const int block = static_cast<int>(p.block.d), half = p.rot / 2;
     plan.team = 1;
@@ -495,11 +495,11 @@ cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, cudaStream_t s) 
     // Parts of the heads: where tiles are fewer than one wave, to fill that, and no further for a few tokens a sequence
     // (61 x 1, 32 / 8 heads of 128: 4.4 us, twice as many CTAs 8.7); where they are more, to three waves, whose ends even out (4 x 8192 ragged, 516
     // tiles: two parts 105 us, one 113). Short blocks are many tasks a CTA: two waves (9 x 397 in blocks of 4, 16 heads of 64: 57 -> 30 us).
-    constexpr int64_t kWave = kPerSm * 152;
+    const int64_t wave = static_cast<int64_t>(kPerSm) * sms;
     const int64_t alone = static_cast<int64_t>(p.B) * plan.tiles;
-    const int64_t wanted = alone >= kWave ? (3 * kWave + alone - 1) / alone
-                           : p.T < kTile  ? kWave / alone
-                                          : ((block <= kRows ? 2 : 1) * kWave + alone - 1) / alone;
+    const int64_t wanted = alone >= wave ? (3 * wave + alone - 1) / alone
+                           : p.T < kTile ? wave / alone
+                                         : ((block <= kRows ? 2 : 1) * wave + alone - 1) / alone;
     const int heads = std::max(p.h_kv, p.h), parts = static_cast<int>(std::min<int64_t>(wanted, heads));
     auto each = [&](int h, int n) { return (h + n - 1) / n; };
     plan.kv_heads = each(p.h_kv, std::min(parts, p.h_kv));
@@ -542,10 +542,12 @@ cudaError_t launch_d(const CodedAppendParams& p, cudaStream_t s) {
     plan.tokens = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(plan.blocks) * block, p.T));
     const int64_t most = (static_cast<int64_t>(p.T) + block - 2) / block + 1;         // blocks that T tokens touch
     plan.tiles = static_cast<int>((most + plan.blocks - 1) / plan.blocks);
-    const bool many = static_cast<int64_t>(p.B) * plan.tiles >= 152 && p.T >= kTile;
-    if (rows <= kRows) return many ? launch_n<T, kD, 1, 4>(p, plan, s) : launch_n<T, kD, 1, 3>(p, plan, s);
-    if (rows <= 2 * kRows) return many ? launch_n<T, kD, 2, 3>(p, plan, s) : launch_n<T, kD, 2, 2>(p, plan, s);
-    return launch_n<T, kD, 4, 2>(p, plan, s);
+    int sms = 0;
+    if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
+    const bool many = static_cast<int64_t>(p.B) * plan.tiles >= sms && p.T >= kTile;
+    if (rows <= kRows) return many ? launch_n<T, kD, 1, 4>(p, plan, sms, s) : launch_n<T, kD, 1, 3>(p, plan, sms, s);
+    if (rows <= 2 * kRows) return many ? launch_n<T, kD, 2, 3>(p, plan, sms, s) : launch_n<T, kD, 2, 2>(p, plan, sms, s);
+    return launch_n<T, kD, 4, 2>(p, plan, sms, s);
 }
 
 template <typename T>

@@ -463,10 +463,8 @@ struct WarpCoded {
 // 16 heads 28.0 -> 20.9; 30 x 240, 8 heads of twelve query heads, two tiles each, 16.4 -> 20.9.)
 template <typename T, int kD, int kHeads, int kNT, bool kInt8>
 cudaError_t launch_w(const PagedAttnParams& p, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    int sms = 0;
+    if (const cudaError_t e = sm_count(&sms); e != cudaSuccess) return e;
     using One = WarpCoded<T, kD, kHeads, kNT, kInt8>;
     constexpr bool kHalves = One::kTiles == 1 && One::kRow == 128;
     const int64_t units = static_cast<int64_t>(p.B) * p.h_kv * ((p.h / p.h_kv + One::kRows - 1) / One::kRows);

@@ -44,6 +44,13 @@ cudaError_t launch_pdl_cluster(void (*kernel)(Params...), dim3 grid, dim3 block,
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...);
 }
 
+// SMs of the current device.
+inline cudaError_t sm_count(int* sms) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    return e != cudaSuccess ? e : cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+}
+
 // Clusters of a kernel, allowed `smem` bytes by the caller, that the current device runs at once; asked once a device and
 // size, for it is a property of the device.
 struct ClusterRoom {

@@ -540,9 +540,8 @@ cudaError_t launch_rows(PagedAttnParams p, cudaStream_t s) {
     constexpr int kSmem = kWarps * W::Step::kStages * W::Step::kStage + (W::kBufs * W::kRows * kD + W::kQFloats) * static_cast<int>(sizeof(float));
     static_assert((kSmem + sizeof(Shared<kWarps>) + 1024) * W::Step::kPerSm <= 233472, "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<W, kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    int dev = 0, sms = 0;
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    if (e == cudaSuccess) e = sm_count(&sms);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(sms, kSlotsPerSm) * W::Step::kPerSm;
     // Sequences of kWhole blocks at most are not worth the second kernel: a CTA takes longer over a unit by less

@@ -306,7 +306,9 @@ cudaError_t launch_resize(const ResizeParams& p, cudaStream_t s) {
     while (ctas > 1 && rooms[few].at_once(kernel, threads, 0, ctas) < 1) ctas /= 2;
     e = launch_pdl_cluster(kernel, dim3(ctas), dim3(threads), ctas, 0, s, q);
     if (e != cudaSuccess || !q.slots_after) return e;
-    const int64_t wide = std::min<int64_t>(8 * 152, (slots + kSlots * kSlotThreads - 1) / (kSlots * kSlotThreads));
+    int sms = 0;
+    if ((e = sm_count(&sms)) != cudaSuccess) return e;
+    const int64_t wide = std::min<int64_t>(8 * sms, (slots + kSlots * kSlotThreads - 1) / (kSlots * kSlotThreads));
     return launch_pdl(slots_kernel, dim3(static_cast<unsigned>(wide)), dim3(kSlotThreads), 0, s, q);
 }
 
