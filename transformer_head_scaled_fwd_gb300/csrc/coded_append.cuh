@@ -46,7 +46,7 @@ struct TilePlan {
     FastDiv q_heads;    // of a part, equal for all
     FastDiv half;       // pairs that turn
     int team;           // warps of a task
-    int stride;         // floats of a token's row of cos (and of sin)
+    int room;           // floats a token of cos (and of sin): half, rounded up so that the rows behind them are aligned to 16 bytes
 };
 
 // Where a block lies: elements from the pages' start to its first slot, or -1; its place among the scales, without the head.
@@ -251,13 +251,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) coded_append_kernel(const __
     settle(now);
     fetch(now, 0);
 
-    // ---- cos and sin of the tile, [tokens][stride] each; where the blocks lie
+    // ---- cos and sin of the tile, [tokens][half] each; where the blocks lie
     float* cosines = reinterpret_cast<float*>(smem + kWarps * 2 * kStep);
-    float* sines = cosines + plan.tokens * plan.stride;
-    const int span = half;
+    float* sines = cosines + plan.tokens * plan.room;
     if (kTurn != kNone) {
-        for (int i = tid; i < tokens * span; i += kThreads) {
-            const int t = i / span, e = i - t * span;
+        for (int i = tid; i < tokens * half; i += kThreads) {
+            const int t = i / half, e = i - t * half;
             const float2 cs = turn_of(static_cast<int>(start + t0 + t), p.inv_freq[e]);
             cosines[i] = cs.x * p.scale;
             sines[i] = cs.y * p.scale;
@@ -285,13 +284,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) coded_append_kernel(const __
         info[i] = x;
     }
 
-    float* stage = sines + plan.tokens * plan.stride + warp * (kRows * kD);       // kStaged: a pass of rows
+    float* stage = sines + plan.tokens * plan.room + warp * (kRows * kD);       // kStaged: a pass of rows
     __syncthreads();
 
     auto turn = [&](float (&x)[kN], float (&y)[kN], int t, bool on) {
         if (kTurn == kNone) return;
-        const float* cs = cosines + t * span;
-        const float* sn = sines + t * span;
+        const float* cs = cosines + t * half;
+        const float* sn = sines + t * half;
         if (kTurn == kStaged) {
             // the pass's rows in shared memory, a pair a lane at a time; a short block leaves passes empty (6 x 468 in blocks of 8: 24.0 -> 22.9 us)
             if (__ballot_sync(0xffffffffu, on) == 0) return;
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) coded_append_kernel(const __
                 const int of = __shfl_sync(0xffffffffu, t, n * kLanes);
                 if (i0 + lane >= kRows * half) continue;
                 float* pair = stage + n * kD + e;
-                const float c = cosines[of * span + e], s = sines[of * span + e], u = pair[0], v = pair[half];
+                const float c = cosines[of * half + e], s = sines[of * half + e], u = pair[0], v = pair[half];
                 pair[0] = fmaf(u, c, -(v * s));
                 pair[half] = fmaf(v, c, u * s);
             }
@@ -478,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm) coded_append_kernel(const __
     cp_wait<0>();
 }
 
-// Of steps, cos and sin of `tokens` rows of `stride` floats each, and a pass of rows that turn in shared memory: up to 208 KB (256 tokens,
+// Of steps, cos and sin of `tokens` tokens with room for `room` floats each, and a pass of rows that turn in shared memory: up to 208 KB (256 tokens,
 // halves of 57 to 63 pairs).
 template <typename T, int kD, int kKeep>
-constexpr size_t shared_bytes(int turn, int tokens, int stride) {
+constexpr size_t shared_bytes(int turn, int tokens, int room) {
     constexpr int kRows = 64 * Pair<T>::kN / kD;
-    return kWarps * 2 * kKeep * 1024 + static_cast<size_t>(tokens) * stride * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
+    return kWarps * 2 * kKeep * 1024 + static_cast<size_t>(tokens) * room * 2 * sizeof(float) + (turn == kStaged ? kWarps * kRows * kD * sizeof(float) : 0);
 }
 
 template <typename T, int kD, int kKeep, int kPerSm>
@@ -509,7 +508,7 @@ cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, int sms, cudaStr
     while (p.h % q_parts != 0) --q_parts;
     plan.q_heads = fast_div(static_cast<uint32_t>(std::max(p.h / q_parts, 1)));
     plan.parts = std::max(each(p.h_kv, plan.kv_heads), p.h > 0 ? q_parts : 1);
-    plan.stride = (half + kN - 1) / kN * kN;
+    plan.room = (half + kN - 1) / kN * kN;
     plan.half = fast_div(static_cast<uint32_t>(std::max(half, 1)));
     const int turn = half == 0 ? kNone : p.interleaved != 0 ? kNeighbours : half % kN == 0 ? kHalves : kStaged;
     const auto kernel = turn == kNone         ? coded_append_kernel<T, kD, kNone, kKeep, kPerSm>
@@ -523,7 +522,7 @@ cudaError_t launch_n(const CodedAppendParams& p, TilePlan plan, int sms, cudaStr
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(shared_bytes<T, kD, kKeep>(turn, kTokens, turn == kNone ? 0 : kD / 2)));
     if (e != cudaSuccess) return e;
-    const size_t smem = shared_bytes<T, kD, kKeep>(turn, plan.tokens, plan.stride);
+    const size_t smem = shared_bytes<T, kD, kKeep>(turn, plan.tokens, plan.room);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(static_cast<int64_t>(p.B) * plan.tiles), plan.parts), dim3(kThreads), smem, s, p, plan);
 }
 
