@@ -458,6 +458,9 @@ mha_status_t mha_paged_attention(mha_dtype_t dt, const void* q, const mha_stride
  * of the stack above the pages given back, are left as they were. A page number outside [0, n_pages) moves as it is, gives no slot
  * and records MHA_PAGED_BAD_PAGE, and so does a stack that pages given back would overflow (the ones beyond n_pages are
  * dropped). lens and new_lens overlap neither held nor want nor each other. Calls that share a table or a stack are ordered by the caller.
+ * A page has one owner: it stands once among the rows' held pages and the free ones, and that is not looked at. A page of several rows (a
+ * common prefix, which the attention reads as any other) would be given back by each of them and then granted twice; of whole pages that are
+ * shared, give the call the table's columns behind them, and held and want without their positions.
  */
 mha_status_t mha_paged_resize(const int32_t* held, const int32_t* want, int B, int page_size,
                               int32_t* block_table, int64_t table_stride, int max_pages,

@@ -159,3 +159,27 @@ def test_attention_values_of_the_largest_scale(bnd, dtype):
     got = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
     ref, tol = C.attention(q, kp, ks, vp, vs, table, [n], hk)
     R.check(got, ref, tol, "2^122")
+
+
+# ------------------------------------------------------------------------------------------ pages granted
+def test_resize_behind_a_shared_prefix(bnd):
+    """Three sequences whose first two pages are the same: the call gets the table's columns behind those, so that they are neither given
+    back nor granted when the sequences end."""
+    B, page, room, n_pages, shared = 3, 4, 8, 20, 2
+    table = torch.full((B, room), -1, dtype=torch.int32, device="cuda")
+    table[:, 0], table[:, 1] = 18, 7
+    free = [p for p in range(n_pages) if p not in (18, 7)]
+    stack, count = ints(free + [-1] * shared), ints([len(free)])
+    at = [shared * page + x for x in (5, 0, 9)]                  # of the whole sequence
+    lens, new_lens = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(2))
+    slots = torch.zeros(B, 9, dtype=torch.int64, device="cuda")
+    zero, behind = ints([0] * B), ints([x - shared * page for x in at])
+    kw = dict(block_table=table[:, shared:], page_size=page, free_pages=stack, free_count=count, lens=lens, new_lens=new_lens)
+    bnd.mha_paged_resize(zero, behind, slots=slots, **kw)
+    want = C.resize([0] * B, [5, 0, 9], page, [[-1] * (room - shared)] * B, free + [-1] * shared, len(free), 9)
+    assert lens.tolist() == want[0] and new_lens.tolist() == want[1] and slots.tolist() == want[2]
+    assert table[:, shared:].tolist() == want[3] and stack.tolist() == want[4] and count.item() == want[5]
+    granted = [p for row in table[:, shared:].tolist() for p in row if p >= 0]
+    assert not {18, 7} & set(granted) and table[:, :shared].tolist() == [[18, 7]] * B
+    bnd.mha_paged_resize(behind, zero, **kw)
+    assert count.item() == len(free) and sorted(stack.tolist()[:len(free)]) == free and table[:, :shared].tolist() == [[18, 7]] * B
