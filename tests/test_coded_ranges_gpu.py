@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 import coded_ref as C  # noqa: E402
 import serving_ref as R  # noqa: E402
 from test_coded_gpu import (BF, E4, F32, I8, bnd, clean_status, freqs, ints, pages_of, randn, run_attention, same,  # noqa: E402, F401
-                            table_of)
+                            slopes_of, table_of)
 
 pytestmark = pytest.mark.gpu
 
@@ -159,6 +159,64 @@ def test_attention_values_of_the_largest_scale(bnd, dtype):
     got = run_attention(bnd, q, kp, ks, vp, vs, table, [n], hk)
     ref, tol = C.attention(q, kp, ks, vp, vs, table, [n], hk)
     R.check(got, ref, tol, "2^122")
+
+
+# fp32: scores of up to 16 (16 sums in the matrix instruction, each cut at 2^-23, and four roundings, twice as they also enter the sum of
+# weights: 2 (16 2^-23 + 4 2^-24) 16 = 6.9e-5), sums of at most 5000 keys a warp-wise 32 at a time (1e-5); the cap's tanh to 2^-20 of it, twice. bf16: what
+# rounding the exact result gives and twice the error in front of it, weights rounded to 2^-11 (2^-11 / sqrt 3 = 2.8e-4) and the same of scores.
+@pytest.mark.parametrize("dtype,code,B,h,hk,d,n,page,block,sc", [
+    (BF, E4, 1, 16, 2, 128, 70001, 64, 16, {}), (BF, I8, 2, 4, 4, 64, 30000, 128, 128, {}), (BF, E4, 16, 8, 8, 64, 1000, 16, 16, dict(cap=30.0)),
+    (BF, I8, 64, 16, 4, 64, 200, 16, 8, {}), (BF, E4, 3, 20, 1, 128, 5000, 100, 25, dict(slopes=True)), (BF, I8, 12, 32, 8, 128, 3000, 32, 32, {}),
+    (BF, E4, 30, 48, 8, 64, 2000, 64, 64, {}), (BF, E4, 200, 32, 8, 128, 90, 32, 16, {}),
+    (F32, E4, 1, 4, 1, 64, 40001, 64, 16, {}), (F32, I8, 8, 8, 2, 128, 700, 16, 16, dict(cap=30.0)), (F32, E4, 9, 24, 8, 128, 5000, 64, 32, {}),
+    (F32, I8, 3, 16, 16, 64, 4000, 64, 64, dict(slopes=True)), (F32, E4, 5, 10, 2, 64, 3000, 24, 24, {}), (F32, I8, 130, 12, 4, 64, 100, 16, 16, {})])
+def test_attention_error_of_the_norm(bnd, dtype, code, B, h, hk, d, n, page, block, sc):
+    sc = dict(sc, slopes=slopes_of(h)) if sc.get("slopes") else sc
+    lens = [max(n - 7 * b, 1) for b in range(B)]
+    table, n_pages = table_of(32, B, -(-n // page))
+    kp, ks = pages_of(33, n_pages, page, block, hk, d, code)
+    vp, vs = pages_of(34, n_pages, page, block, hk, d, code)
+    q = randn(35, B, h, d, dtype=dtype)
+    got = run_attention(bnd, q, kp, ks, vp, vs, table, lens, hk, **sc)
+    ref, _ = C.attention(q, kp, ks, vp, vs, table, lens, hk, **sc)
+    off = 8e-5 + 2 * 2.0 ** -20 * sc.get("cap", 0.0)
+    bound = off if dtype == F32 else norm_error(ref.to(BF), ref) + 2 * 1.05 * math.hypot(2.8e-4, off)
+    assert norm_error(got, ref) <= bound
+
+
+@pytest.mark.parametrize("dtype,code,h,hk,d,lens,page", [
+    (BF, E4, 4, 2, 64, [40001], 64), (BF, I8, 16, 2, 128, [30000, 5], 128), (BF, E4, 16, 8, 128, [9000, 12000, 1], 64),
+    (BF, I8, 6, 3, 64, [5000] * 3, 16), (BF, E4, 2, 2, 64, [1000] * 3, 16), (BF, E4, 8, 8, 128, [4000, 0, 3999] * 8, 32),
+    (BF, I8, 24, 1, 128, [3000, 7], 104), (BF, E4, 48, 8, 64, [2500, 40], 64), (BF, I8, 8, 4, 64, [100, 33, 1, 97] * 40, 16),
+    (F32, E4, 4, 1, 64, [20001], 64), (F32, I8, 2, 2, 128, [513, 8000, 64], 24), (F32, E4, 16, 16, 64, [3000, 2999], 64),
+    (F32, I8, 12, 2, 64, [4097], 16), (F32, E4, 4, 4, 128, [250, 3] * 60, 16)])
+def test_attention_takes_every_key_once(bnd, dtype, code, h, hk, d, lens, page):
+    """Equal scores, values that are zero but at d keys at a time, each with a feature of its own: that feature of the output is 1 / n, and 0 or 2 / n
+    if the key is left out or taken twice. Every key is looked at. Codes of 1, 2, 4 under scales of 1, 1/2, 1/4: weights are powers of two
+    and sums whole numbers of the least of them, exact in fp32 up to 2^24; left are the quotient and the output's rounding."""
+    B, n = len(lens), max(lens)
+    table, n_pages = table_of(40, B, -(-n // page))
+    kp, ks = pages_of(41, n_pages, page, 8, hk, d, code)
+    vp, _ = pages_of(42, n_pages, page, 8, hk, d, code)
+    down = torch.randint(0, 3, (n_pages, page // 8, hk), generator=torch.Generator(device="cuda").manual_seed(43), device="cuda")
+    vs = torch.exp2(-down.float())
+    ones = torch.exp2(down.float()).repeat_interleave(8, dim=1)               # codes that stand for 1, [n_pages, page, hk]
+    q = torch.zeros(B, h, d, device="cuda", dtype=dtype)
+    at = torch.arange(n, device="cuda")
+    held = torch.tensor(lens, device="cuda")[:, None] > at                    # [B, n]
+    pages, slots = table.long()[:, at // page], (at % page).expand(B, n)
+    whole = torch.zeros(vp.shape, device="cuda")
+    for first in range(0, n, d):
+        live = held[:, first:first + d]
+        f = torch.arange(d, device="cuda").expand(B, d)[:, :live.shape[1]][live]
+        pg, sl = pages[:, first:first + d][live], slots[:, first:first + d][live]
+        whole.zero_()
+        whole[pg, sl, :, f] = ones[pg, sl]
+        vp.copy_(whole.to(code))
+        want = torch.zeros(B, h, d, dtype=torch.float64, device="cuda")
+        want[:, :, :live.shape[1]] = (live.double() / torch.tensor(lens, device="cuda").clamp_min(1)[:, None])[:, None]
+        got = run_attention(bnd, q, kp, ks, vp, vs, table, lens, hk)
+        R.check(got, want, want * (R.HALF[dtype] + 2.0 ** -22), "every key once")
 
 
 # ------------------------------------------------------------------------------------------ pages granted
