@@ -8,7 +8,8 @@
 //
 // HBM-bound: q and k read and written, v read, codes written: 24.5 KB a token at 32 + 8 heads of 128 in bf16. Measured, 4 x 8192 of those,
 // blocks of 64: half of each head turned 137-141 us (805 MB, 5.7-5.9 TB/s, 0.86 of measured copy bandwidth), nothing turned 125, all 160, halves
-// of odd length (126) 270; 16 + 16 heads of 64 98 us; blocks of 16 136, of 8 132, of 4 143, of 256 192 (rows read twice). One token 4.5 us,
+// of odd length (126) 270; 16 + 16 heads of 64 98 us; blocks of 16 136, of 8 132, of 4 143, of 256 192 (rows read twice, and cos and
+// sin of 256 tokens leave one CTA an SM). int8 the same (131 us for 131, calls captured). fp32, 43 KB a token: 219 us, 1.41 GB, 6.4 TB/s in both codes. One token 4.5 us,
 // 61 sequences of one token 4.5 us, 7 x 333 in fp32 5.8 us.
 //
 // A CTA takes a tile of neighbouring blocks of one sequence and a part of the heads. It computes the tile's cos and sin into shared

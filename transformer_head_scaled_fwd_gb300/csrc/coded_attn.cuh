@@ -25,7 +25,7 @@
 //
 // Measured: 16 sequences of 8192, 16 heads of 64, e4m3, 268 MB: 52 us, 5.2 TB/s (0.77 of measured copy bandwidth; a bf16 cache takes 89); 24 of 15000,
 // 32 / 8 heads of 128, 737 MB: 120 us (0.92); 48 ragged ones up to 15000, int8, capped, 790 MB: 142 us (0.83); one of 131071, 16 / 2 heads: 22 us,
-// of which 10 are its traffic. A step costs a warp 2700 cycles, 1000 of them to issue its copies and 1400 to compute; at eight warps
+// of which 10 are its traffic; fp32 queries 16 x 8192 55 us (int8 59), 9 ragged up to 5000, 24 / 8 heads of 128 20 us. A step costs a warp 2700 cycles, 1000 of them to issue its copies and 1400 to compute; at eight warps
 // an SM that is what HBM delivers, so long streams run at its rate and the rest is what any call has: the look-ups 1.7 + 3 us, the queries 1, a
 // unit's end 1.7, the second launch and the join 3.7.
 #pragma once
@@ -456,7 +456,7 @@ struct WarpCoded {
 // 64 x 8000 107 both; but 48 x 15000 143 -> 144, and where units are fewer than SMs, so that each is split: one of 131071 with 2 key heads
 // 22.1 -> 24.6, 4 x 333 with 4 of 64 6.3 -> 7.1.)
 //
-// Many units of a table with room for little: a warp a unit, seven CTAs of one an SM, which the hardware hands out. What such calls wait for is latency (queries, first keys, the
+// Many units of a table with room for little (the host does not know the lengths: the same units behind a wide table take the forms above, 200 x 20 25 us for 12.5): a warp a unit, seven CTAs of one an SM, which the hardware hands out. What such calls wait for is latency (queries, first keys, the
 // unit's end), and that of seven units runs side by side. (Shapes above -> this: 8 key heads of 128, four query heads each, room for 32: 41 x 20 10.0 -> 7.0,
 // 200 x 20 22.7 -> 13.0; room for 128, full: 54 10.9 both, 200 28.7 -> 23.0; for 256, full: 54 14.1 -> 15.9, 200 36.2 -> 32.6; 64 x 500, 16 heads 34.6 -> 27.7; but 41 x 500 19.7 -> 25.3, 30 x 20
 // 5.5 -> 6.9. What has no two CTAs an SM: pairs of heads of 64, eight query heads each, 49 x 20, 4 pairs 12.4 -> 9.5, full in 128 12.5 -> 12.8, in 256 13.3 -> 17.2. fp32: 64 x 240,
