@@ -1,5 +1,9 @@
-"""The operators around a cache in 8 bits on the GPU: calls from several host threads, weights of very different sizes."""
+"""The operators around a cache in 8 bits on the GPU: calls from several host threads, weights of very different sizes, nothing lost
+and nothing doubled, calls captured first."""
 import math
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -241,3 +245,60 @@ def test_resize_behind_a_shared_prefix(bnd):
     assert not {18, 7} & set(granted) and table[:, :shared].tolist() == [[18, 7]] * B
     bnd.mha_paged_resize(behind, zero, **kw)
     assert count.item() == len(free) and sorted(stack.tolist()[:len(free)]) == free and table[:, :shared].tolist() == [[18, 7]] * B
+
+
+# ------------------------------------------------------------------------------------------ a run of them
+def serving_step(bnd, B=5, T=3, h=8, hk=2, d=128, page=16, room=6):
+    """Pages granted, T new tokens appended and the last one attending, from empty rows; what the step writes."""
+    n_pages = B * room + 2
+    table = torch.full((B, room), -1, dtype=torch.int32, device="cuda")
+    stack, count = ints(list(range(n_pages))), ints([n_pages])
+    kp, ks = pages_of(60, n_pages, page, 8, hk, d, E4)
+    vp, vs = pages_of(61, n_pages, page, 8, hk, d, E4)
+    q, k, v = (randn(62 + i, B, T, (h, hk, hk)[i], d, dtype=BF) for i in range(3))
+    held, want, lens, new_lens = ints([0] * B), ints([T, 1, 0, 2, T]), ints([0] * B), ints([0] * B)
+    slots, q1, out = torch.zeros(B, T, dtype=torch.int64, device="cuda"), torch.zeros_like(q), torch.zeros(B, h, d, device="cuda", dtype=BF)
+    cache, rotary = bnd.make_coded_cache(kp, vp, ks, vs, table), bnd.make_rotary(freqs(64))
+    ws = torch.zeros(bnd.coded_attention_workspace_size(bnd.MHA_BF16, B, h, hk, d), dtype=torch.uint8, device="cuda")
+    state = (table, stack, count, kp, vp, ks, vs, lens, new_lens, slots, q1, out)
+    begin = [t.clone() for t in state]
+
+    def restart():
+        for t, b in zip(state, begin):
+            t.copy_(b)
+
+    def step():
+        bnd.mha_paged_resize(held, want, block_table=table, page_size=page, free_pages=stack, free_count=count, lens=lens, new_lens=new_lens,
+                             slots=slots)
+        bnd.mha_coded_append(k, v, held, cache=cache, q=q, q_out=q1, new_lens=new_lens, rotary=rotary)
+        bnd.mha_coded_attention(q1[:, 0], lens, cache=cache, out=out, workspace=ws)
+    return step, restart, state
+
+
+def test_first_step_may_be_captured():
+    """A fresh process whose first calls are captured into a graph: what a device has room for may be asked for there."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import test_coded_ranges_gpu as T
+from transformer_head_scaled_fwd_gb300 import binding as bnd
+step, restart, state = T.serving_step(bnd)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in state]
+assert got[2].item() == 32 - 4 and got[11].float().abs().sum() > 0
+restart()
+step()
+torch.cuda.synchronize()
+assert all(T.same(a, b) for a, b in zip(got, state))
+assert bnd.mha_check_device_status() == 0
+print("captured first")
+""" % (os.path.dirname(here), here)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
